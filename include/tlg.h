@@ -364,6 +364,111 @@ tlg_status tlg_gemm_workspace_size_op(int64_t M, int64_t N, int64_t K,
                                       const void *C, int64_t ldc, tlg_out out,
                                       const tlg_config *config, size_t *bytes);
 
+/* ---------------------------------------------------------------- microscaled formats
+ *
+ * Matrices in 4 or 8 bits with one power-of-two scale for every 32 elements
+ * along a row (the microscaling, MX, formats of the Open Compute Project), for
+ * 4-bit products and 8-bit activation checkpoints.  (These entry points have
+ * no counterpart on the pages; they exist for users who train and serve the
+ * layers tlg_gemm_fused and tlg_gemm_op compute.)
+ *
+ * An MX matrix of rows x cols is two buffers:
+ *
+ *  - Q, the elements, row-major with a row stride of ldq BYTES.  A row holds
+ *    ceil(cols / 32) whole blocks (16 bytes each for E2M1, 32 for E4M3); the
+ *    elements past cols are 0.  E2M1: element 2i in the low half of byte i,
+ *    2i + 1 in the high half.  Q must be 16-byte aligned and ldq a multiple
+ *    of 16, at least the row bytes tlg_mx_size gives.
+ *  - S, one E8M0 byte b per block, which stands for 2^(b - 127), 0xFF for
+ *    NaN.  The bytes lie in tiles of 128 rows x 4 blocks, 512 bytes each: with
+ *    tiles_x = ceil(ceil(cols / 32) / 4), the scale of (row, block) is byte
+ *      ((row / 128) * tiles_x + block / 4) * 512
+ *        + (row % 32) * 16 + ((row % 128) / 32) * 4 + block % 4.
+ *    S must be 16-byte aligned and hold the bytes tlg_mx_size gives.  The
+ *    bytes of blocks past the last one (up to a multiple of 4) are written as
+ *    0 and must not be 0xFF in a matrix built elsewhere; the bytes of rows
+ *    past the last one (up to a multiple of 128) are neither written nor used.
+ *
+ * An element's value is its E2M1 or E4M3 value times its block's scale.
+ * Quantising a block whose largest magnitude is amax:
+ *  - E2M1: scale 2^(floor(log2 amax) - 2); magnitudes above 6 scales saturate;
+ *  - E4M3: the smallest power of two with amax <= 448 scales; nothing
+ *    saturates;
+ * with exponents held to [-127, 127] (-127 for an all-zero block), and each
+ * element the nearest representable value, ties to even.  A block that holds
+ * a NaN or an infinity gets the scale 0xFF: all of it reads back as NaN.
+ *
+ * Sizes: 0 <= rows, cols <= 2^31 - 257, strides at most 2^36, every matrix
+ * below 2^60 bytes (TLG_ERR_UNSUPPORTED beyond).  Rows or cols of 0: nothing
+ * is written, TLG_OK (tlg_act_backward_mx still writes dbias = 0 for rows of
+ * 0).  Other matrices need only element alignment; those whose base and row
+ * stride are multiples of 16 bytes are accessed 16 bytes at a time.  Inputs
+ * must not overlap outputs except where an entry point says so, and every
+ * buffer is device memory of the current device.  These calls launch as
+ * programmatic dependents of the kernel before them in the stream: only their
+ * launch overlaps it; they touch memory after it has completed.  All may be
+ * captured into CUDA graphs.
+ */
+
+/* Element types of ordinary matrices (f32 and f16 as in tlg_out). */
+typedef enum tlg_type { TLG_TYPE_F32 = 0, TLG_TYPE_F16 = 1, TLG_TYPE_BF16 = 2 } tlg_type;
+
+/* Element formats of MX matrices: 4 bits (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives) and 8 bits (4 exponent and 3 mantissa bits, up to 448). */
+typedef enum tlg_mx_format { TLG_MX_E2M1 = 0, TLG_MX_E4M3 = 1 } tlg_mx_format;
+
+/* Bytes of one row of Q, and of S, for a rows x cols MX matrix.  Host only. */
+tlg_status tlg_mx_size(tlg_mx_format format, int64_t rows, int64_t cols,
+                       int64_t *q_row_bytes, size_t *s_bytes);
+
+/*
+ * Quantises a matrix.  op == TLG_OP_N: X is rows x cols, row-major, ldx >= cols.
+ * op == TLG_OP_T: X is stored cols x rows, ldx >= rows, and its transpose is
+ * quantised, the blocks running down X's columns: what the backward products
+ * of a 4-bit layer need of its weights, activations and gradients.
+ */
+tlg_status tlg_mx_quantize(tlg_mx_format format, int64_t rows, int64_t cols,
+                           tlg_op op, tlg_type type, const void *X, int64_t ldx,
+                           void *Q, int64_t ldq, void *S, void *stream);
+
+/* X (rows x cols) = the values of an MX matrix, rounded once to X's type. */
+tlg_status tlg_mx_dequantize(tlg_mx_format format, int64_t rows, int64_t cols,
+                             const void *Q, int64_t ldq, const void *S,
+                             tlg_type type, void *X, int64_t ldx, void *stream);
+
+/*
+ * Y = act(Z), and Z saved for the backward pass as an E4M3 MX matrix, in one
+ * pass over Z.  Y may be Z itself (same base and row stride).  Computed in
+ * fp32 and rounded once; the activations and their accuracy are
+ * tlg_gemm_fused's (a bf16 Y takes the 16-bit form of GELU).
+ */
+tlg_status tlg_act_forward_mx(int64_t rows, int64_t cols, tlg_activation activation,
+                              tlg_type type, const void *Z, int64_t ldz,
+                              void *Y, int64_t ldy, void *Q, int64_t ldq, void *S,
+                              void *stream);
+
+/*
+ * The backward pass of act on a saved input: dZ = dY * act'(Z), with Z the
+ * values of the E4M3 MX matrix (Q, S), and, when dbias is not NULL, dbias[c] =
+ * the sum over the rows of dZ[., c] (cols fp32 values), summed in fp32 before
+ * dZ is rounded, in an order that does not depend on timing.  dZ may be dY
+ * itself.  act' is computed in fp32 with an error below 1e-6; ReLU's is 0 at
+ * 0, and a NaN in Z makes dZ NaN.
+ * workspace: tlg_act_backward_mx_workspace_size() bytes of device memory,
+ * 256-byte aligned, needed when dbias is not NULL (TLG_ERR_INVALID_ARG when too
+ * small; the size may be 0).  Its contents on entry do not matter; calls that
+ * overlap in time must not share one.
+ */
+tlg_status tlg_act_backward_mx(int64_t rows, int64_t cols, tlg_activation activation,
+                               tlg_type type, const void *dY, int64_t lddy,
+                               const void *Q, int64_t ldq, const void *S,
+                               void *dZ, int64_t lddz, float *dbias,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of tlg_act_backward_mx with a dbias, for the current device. */
+tlg_status tlg_act_backward_mx_workspace_size(int64_t rows, int64_t cols, tlg_type type,
+                                              size_t *bytes);
+
 /*
  * Resolve a configuration for this shape.  On input *config (never NULL)
  * holds the requested fields, zero meaning "choose for me" (all zero: the

@@ -15,11 +15,16 @@ Functions (same names as the C entry points):
 * ``tlg_gemm_ex(...)``                     any of the above with an explicit configuration
 * ``tlg_gemm_op(...)``                     operands stored transposed
 * ``tlg_gemm_fused(...)``                  C = act(op(A).op(B) + bias) + residual
+* ``tlg_mx_quantize(X, ...)``, ``tlg_mx_dequantize(Q, S, cols, ...)``  4- and 8-bit
+  microscaled (MX) matrices
+* ``tlg_act_forward_mx(Z, activation)``, ``tlg_act_backward_mx(dY, Q, S, activation)``
+  an activation whose input is saved in 8 bits, and its backward pass
 * ``tlg_choose_config``, ``tlg_device_error``, ``tlg_selftest_timeout``,
   ``tlg_status_string``, ``tlg_version``
 
 A and B are 2-D fp16 tensors with unit stride along their last dimension
-(row-major); their row strides become lda / ldb.
+(row-major); their row strides become lda / ldb.  An MX matrix is a pair of uint8
+tensors: Q (rows x row bytes) and S (flat scale bytes; layout in ``include/tlg.h``).
 """
 
 from __future__ import annotations
@@ -46,6 +51,12 @@ TLG_OP_N, TLG_OP_T = 0, 1
 TLG_ACT_NONE, TLG_ACT_RELU, TLG_ACT_GELU, TLG_ACT_SILU, TLG_ACT_GELU_TANH = 0, 1, 2, 3, 4
 _ACT = {"none": TLG_ACT_NONE, "relu": TLG_ACT_RELU, "gelu": TLG_ACT_GELU, "silu": TLG_ACT_SILU,
         "gelu_tanh": TLG_ACT_GELU_TANH}
+TLG_TYPE_F32, TLG_TYPE_F16, TLG_TYPE_BF16 = 0, 1, 2
+TLG_MX_E2M1, TLG_MX_E4M3 = 0, 1
+_TYPES = {"f32": (TLG_TYPE_F32, torch.float32), "f16": (TLG_TYPE_F16, torch.float16),
+          "bf16": (TLG_TYPE_BF16, torch.bfloat16)}
+_TYPE_OF = {dt: code for code, dt in _TYPES.values()}
+_FORMATS = {"e2m1": (TLG_MX_E2M1, 16), "e4m3": (TLG_MX_E4M3, 32)}  # code, bytes of a block
 
 EXPORTED = ("tlg_gemm_f16f32", "tlg_gemm_f16f16", "tlg_gemm_bias_relu_f16", "tlg_gemm_ex",
             "tlg_gemm_op", "tlg_gemm_fused", "tlg_gemm_ex_noalloc", "tlg_gemm_workspace_size",
@@ -91,7 +102,14 @@ _lib.tlg_selftest_timeout.argtypes = [ctypes.c_uint32, _p]
 _lib.tlg_status_string.argtypes = [_i32]
 _lib.tlg_status_string.restype = ctypes.c_char_p
 _lib.tlg_version.restype = ctypes.c_int32
-for _name in ("tlg_gemm_f16f32", "tlg_gemm_f16f16", "tlg_gemm_bias_relu_f16", "tlg_gemm_ex",
+_lib.tlg_mx_size.argtypes = [_i32, _i64, _i64, ctypes.POINTER(_i64), ctypes.POINTER(_sz)]
+_lib.tlg_mx_quantize.argtypes = [_i32, _i64, _i64, _i32, _i32, _p, _i64, _p, _i64, _p, _p]
+_lib.tlg_mx_dequantize.argtypes = [_i32, _i64, _i64, _p, _i64, _p, _i32, _p, _i64, _p]
+_lib.tlg_act_forward_mx.argtypes = [_i64, _i64, _i32, _i32, _p, _i64, _p, _i64, _p, _i64, _p, _p]
+_lib.tlg_act_backward_mx.argtypes = [_i64, _i64, _i32, _i32, _p, _i64, _p, _i64, _p, _p, _i64, _p, _p, _sz, _p]
+_lib.tlg_act_backward_mx_workspace_size.argtypes = [_i64, _i64, _i32, ctypes.POINTER(_sz)]
+for _name in ("tlg_mx_size", "tlg_mx_quantize", "tlg_mx_dequantize", "tlg_act_forward_mx", "tlg_act_backward_mx",
+              "tlg_act_backward_mx_workspace_size", "tlg_gemm_f16f32", "tlg_gemm_f16f16", "tlg_gemm_bias_relu_f16", "tlg_gemm_ex",
               "tlg_gemm_op", "tlg_gemm_fused", "tlg_gemm_ex_noalloc", "tlg_gemm_workspace_size", "tlg_gemm_workspace_size_op", "tlg_choose_config", "tlg_device_error", "tlg_selftest_timeout"):
     getattr(_lib, _name).restype = _i32
 
@@ -367,6 +385,167 @@ def tlg_device_error(clear: bool = True):
 
 def tlg_selftest_timeout(limit_us: int, stream=None):
     _check(_lib.tlg_selftest_timeout(int(limit_us), _stream_handle(stream)), "tlg_selftest_timeout")
+
+
+# ------------------------------------------------------------------ microscaled formats
+
+
+def _format(format: str):
+    if format not in _FORMATS:
+        raise ValueError(f"format must be one of {sorted(_FORMATS)}")
+    return _FORMATS[format]
+
+
+def _type_code(t: torch.Tensor, name: str) -> int:
+    code = _TYPE_OF.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be fp32, fp16 or bf16")
+    return code
+
+
+def _same_device(*tensors):
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
+
+
+def _mx_scale_bytes(rows: int, row_bytes: int, block_bytes: int) -> int:
+    return -(-rows // 128) * -(-(row_bytes // block_bytes) // 4) * 512
+
+
+def _mx(Q: torch.Tensor, S: torch.Tensor, rows: int, row_bytes: int, block_bytes: int, name: str = ""):
+    """Checks an MX matrix's two buffers; returns the arguments (Q, ldq, S)."""
+    if Q.dtype != torch.uint8 or Q.dim() != 2 or Q.size(0) != rows or Q.size(1) != row_bytes:
+        raise ValueError(f"Q{name} must be a uint8 tensor of shape ({rows}, {row_bytes})")
+    if S.dtype != torch.uint8 or not S.is_contiguous() or S.numel() < _mx_scale_bytes(rows, row_bytes, block_bytes):
+        raise ValueError(f"S{name} must be a contiguous uint8 tensor of at least "
+                         f"{_mx_scale_bytes(rows, row_bytes, block_bytes)} bytes")
+    q, ldq = _mat(Q, f"Q{name}")
+    return q, ldq, S.data_ptr()
+
+
+def _mx_out(Q, S, rows: int, cols: int, block_bytes: int, like: torch.Tensor):
+    row_bytes = -(-cols // 32) * block_bytes
+    if Q is None:
+        Q = torch.empty((rows, row_bytes), dtype=torch.uint8, device=like.device)
+    if S is None:
+        S = torch.empty(_mx_scale_bytes(rows, row_bytes, block_bytes), dtype=torch.uint8, device=like.device)
+    return Q, S, row_bytes
+
+
+def tlg_mx_size(format: str, rows: int, cols: int):
+    """(bytes of one row of Q, bytes of S) of a rows x cols MX matrix."""
+    q, s = ctypes.c_int64(0), _sz(0)
+    _check(_lib.tlg_mx_size(_format(format)[0], rows, cols, ctypes.byref(q), ctypes.byref(s)), "tlg_mx_size")
+    return int(q.value), int(s.value)
+
+
+def tlg_mx_quantize(X: torch.Tensor, format: str = "e2m1", op: str = "N", Q: torch.Tensor | None = None,
+                    S: torch.Tensor | None = None, stream=None):
+    """(Q, S): X (fp32, fp16 or bf16) in blocks of 32 along its rows; ``op="T"`` quantises X's
+    transpose, in blocks down its columns.  ``format``: "e2m1" (4 bits) or "e4m3" (8 bits)."""
+    fmt, block_bytes = _format(format)
+    code = _type_code(X, "X")
+    px, ldx = _mat(X, "X")
+    t = op.upper() == "T"
+    cols, rows = X.shape if t else (X.shape[1], X.shape[0])
+    Q, S, row_bytes = _mx_out(Q, S, rows, cols, block_bytes, X)
+    q, ldq, s = _mx(Q, S, rows, row_bytes, block_bytes)
+    _same_device(X, Q, S)
+    _check(_lib.tlg_mx_quantize(fmt, rows, cols, TLG_OP_T if t else TLG_OP_N, code, px, ldx, q, ldq, s,
+                                _stream_handle(stream, X)), "tlg_mx_quantize")
+    return Q, S
+
+
+def tlg_mx_dequantize(Q: torch.Tensor, S: torch.Tensor, cols: int, format: str = "e2m1", out: str = "f16",
+                      X: torch.Tensor | None = None, stream=None):
+    """The values of an MX matrix with ``cols`` columns, as "f32", "f16" or "bf16"."""
+    fmt, block_bytes = _format(format)
+    if out not in _TYPES:
+        raise ValueError(f"out must be one of {sorted(_TYPES)}")
+    code, dtype = _TYPES[out]
+    rows = Q.shape[0]
+    q, ldq, s = _mx(Q, S, rows, -(-cols // 32) * block_bytes, block_bytes)
+    if X is None:
+        X = torch.empty((rows, cols), dtype=dtype, device=Q.device)
+    elif X.dtype != dtype or tuple(X.shape) != (rows, cols):
+        raise ValueError(f"X must be {dtype} of shape ({rows}, {cols})")
+    px, ldx = _mat(X, "X")
+    _same_device(X, Q, S)
+    _check(_lib.tlg_mx_dequantize(fmt, rows, cols, q, ldq, s, code, px, ldx, _stream_handle(stream, Q)),
+           "tlg_mx_dequantize")
+    return X
+
+
+def _activation(activation: str) -> int:
+    if activation not in _ACT:
+        raise ValueError(f"activation must be one of {sorted(_ACT)}")
+    return _ACT[activation]
+
+
+def tlg_act_forward_mx(Z: torch.Tensor, activation: str, Y: torch.Tensor | None = None,
+                       Q: torch.Tensor | None = None, S: torch.Tensor | None = None, stream=None):
+    """(Y, Q, S): Y = act(Z) in Z's type (``Y`` may be ``Z`` itself), and Z saved in 8 bits (E4M3)."""
+    act = _activation(activation)
+    code = _type_code(Z, "Z")
+    pz, ldz = _mat(Z, "Z")
+    rows, cols = Z.shape
+    if Y is None:
+        Y = torch.empty((rows, cols), dtype=Z.dtype, device=Z.device)
+    elif Y.dtype != Z.dtype or Y.shape != Z.shape:
+        raise ValueError(f"Y must be {Z.dtype} of shape ({rows}, {cols})")
+    py, ldy = _mat(Y, "Y")
+    Q, S, row_bytes = _mx_out(Q, S, rows, cols, 32, Z)
+    q, ldq, s = _mx(Q, S, rows, row_bytes, 32)
+    _same_device(Z, Y, Q, S)
+    _check(_lib.tlg_act_forward_mx(rows, cols, act, code, pz, ldz, py, ldy, q, ldq, s, _stream_handle(stream, Z)),
+           "tlg_act_forward_mx")
+    return Y, Q, S
+
+
+def tlg_act_backward_mx_workspace_size(rows: int, cols: int, type: str = "f16") -> int:
+    n = _sz(0)
+    _check(_lib.tlg_act_backward_mx_workspace_size(rows, cols, _TYPES[type][0], ctypes.byref(n)),
+           "tlg_act_backward_mx_workspace_size")
+    return int(n.value)
+
+
+def tlg_act_backward_mx(dY: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, activation: str,
+                        dZ: torch.Tensor | None = None, dbias: torch.Tensor | None = None, bias_grad: bool = True,
+                        workspace: torch.Tensor | None = None, stream=None):
+    """(dZ, dbias): dZ = dY * act'(Z) in dY's type (``dZ`` may be ``dY`` itself), Z read from its 8-bit
+    checkpoint, and the fp32 column sums of dZ (None with ``bias_grad=False``).  ``workspace``: a
+    device buffer of tlg_act_backward_mx_workspace_size bytes; allocated here when not given."""
+    act = _activation(activation)
+    code = _type_code(dY, "dY")
+    py, ldy = _mat(dY, "dY")
+    rows, cols = dY.shape
+    q, ldq, s = _mx(Q, S, rows, -(-cols // 32) * 32, 32)
+    if dZ is None:
+        dZ = torch.empty((rows, cols), dtype=dY.dtype, device=dY.device)
+    elif dZ.dtype != dY.dtype or dZ.shape != dY.shape:
+        raise ValueError(f"dZ must be {dY.dtype} of shape ({rows}, {cols})")
+    pz, ldz = _mat(dZ, "dZ")
+    pb, ws_ptr, ws_bytes = None, None, 0
+    handle = _stream_handle(stream, dY)
+    if bias_grad or dbias is not None:
+        if dbias is None:
+            dbias = torch.empty((cols,), dtype=torch.float32, device=dY.device)
+        elif dbias.dtype != torch.float32 or dbias.dim() != 1 or dbias.numel() != cols or not dbias.is_contiguous():
+            raise ValueError(f"dbias must be a contiguous fp32 vector of length {cols}")
+        pb = dbias.data_ptr()
+        if workspace is None:
+            n = _sz(0)
+            _check(_lib.tlg_act_backward_mx_workspace_size(rows, cols, code, ctypes.byref(n)),
+                   "tlg_act_backward_mx_workspace_size")
+            if n.value:
+                workspace = torch.empty(n.value, dtype=torch.uint8, device=dY.device)
+        if workspace is not None:
+            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _same_device(dY, Q, S, dZ, dbias, workspace)
+    _check(_lib.tlg_act_backward_mx(rows, cols, act, code, py, ldy, q, ldq, s, pz, ldz, pb, ws_ptr, ws_bytes, handle),
+           "tlg_act_backward_mx")
+    return dZ, dbias
 
 
 def raw_library():

@@ -11,25 +11,15 @@
 #include <mutex>
 
 #include "tlg.h"
+#include "tlg_host.cuh"
 #include "tlg_variants.cuh"
 
-namespace {
-
-using namespace tlg;
-
-constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s per pipeline wait
-constexpr size_t kCounterBytes = 4096;            // slice counters at the start of a workspace
-constexpr size_t kWorkspaceAlign = 256;
-
-struct DeviceInfo {
-  bool probed = false;
-  bool supported = false;
-  int sm_count = 0;
-};
+namespace tlg {
 
 std::mutex g_mutex;
-DeviceInfo g_devices[kMaxDevices];
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+static DeviceInfo g_devices[kMaxDevices];
+static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 tlg_status current_device(int *dev, DeviceInfo *info) {
   if (cudaGetDevice(dev) != cudaSuccess) {
@@ -87,6 +77,29 @@ void extent(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t esz, 
 }
 
 bool overlaps(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) { return a0 < b1 && b0 < a1; }
+
+bool encode_2d(CUtensorMap *tm, CUtensorMapDataType dtype, const void *base, uint64_t inner,
+               uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+               CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  const cuuint32_t estride[2] = {1, 1};
+  const CUresult r = g_encode(tm, dtype, 2, const_cast<void *>(base), dims, strides, box, estride,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+}  // namespace tlg
+
+namespace {
+
+using namespace tlg;
+
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s per pipeline wait
+constexpr size_t kCounterBytes = 4096;            // slice counters at the start of a workspace
+constexpr size_t kWorkspaceAlign = 256;
 
 // --------------------------------------------------------------------------- kernel variants
 
@@ -294,18 +307,6 @@ tlg_status resolve(int dev, int sms, int64_t M, int64_t N, int64_t K, bool f16, 
 }
 
 // --------------------------------------------------------------------------- launch
-
-bool encode_2d(CUtensorMap *tm, CUtensorMapDataType dtype, const void *base, uint64_t inner,
-               uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estride[2] = {1, 1};
-  const CUresult r = g_encode(tm, dtype, 2, const_cast<void *>(base), dims, strides, box, estride,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
 
 static_assert(kActNone == TLG_ACT_NONE && kActRelu == TLG_ACT_RELU && kActGelu == TLG_ACT_GELU &&
                   kActSilu == TLG_ACT_SILU && kActGeluTanh == TLG_ACT_GELU_TANH,

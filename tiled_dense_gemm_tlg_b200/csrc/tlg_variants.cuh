@@ -9,10 +9,9 @@
 
 #include "tlg.h"
 #include "tlg_gemm_kernel.cuh"
+#include "tlg_host.cuh"
 
 namespace tlg {
-
-constexpr int kMaxDevices = 64;
 
 // Per device and instantiation: kernel attributes set, co-resident work units.
 struct LaunchState {
