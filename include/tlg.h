@@ -437,6 +437,37 @@ tlg_status tlg_mx_dequantize(tlg_mx_format format, int64_t rows, int64_t cols,
                              tlg_type type, void *X, int64_t ldx, void *stream);
 
 /*
+ * C = act(A . B^T + bias) + residual over 4-bit operands: A is an M x K and B
+ * an N x K E2M1 MX matrix (K runs along the rows of both, as weights are
+ * stored), C is M x N row-major of type out.  Every product of two elements
+ * and their scales is exact, sums are fp32, and the result is rounded once.
+ * M may be 1: a single token against a layer's weights.
+ *
+ * The backward products are the same call on transposed quantisations: with
+ * C = A . B^T, dA = dC . B takes dC and B^T (tlg_mx_quantize with TLG_OP_T on
+ * B), and dB = dC^T . A takes dC^T and A^T.
+ *
+ * epilogue as for tlg_gemm_fused, NULL for none: the bias holds N fp16 values
+ * (bf16 when C is bf16), the residual has C's type and may be C itself.
+ * config: NULL or zero fields choose automatically; block_n, cta_group,
+ * stages, raster_group and max_ctas as for tlg_gemm_ex, split_k and k_split 0
+ * or 1, overlap_prev is always on.  No workspace.  K == 0 gives C = act(bias)
+ * + residual.  Sizes and errors as tlg_gemm_fused's; lda and ldb are in BYTES
+ * (ldq above).  A pipeline wait past its time limit is reported by
+ * tlg_device_error().
+ */
+tlg_status tlg_gemm_mxfp4(int64_t M, int64_t N, int64_t K,
+                          const void *A, int64_t lda, const void *SA,
+                          const void *B, int64_t ldb, const void *SB,
+                          const tlg_fused_epilogue *epilogue,
+                          void *C, int64_t ldc, tlg_type out,
+                          const tlg_config *config, void *stream);
+
+/* tlg_choose_config for tlg_gemm_mxfp4. */
+tlg_status tlg_choose_config_mxfp4(int64_t M, int64_t N, int64_t K, tlg_type out,
+                                   tlg_config *config);
+
+/*
  * Y = act(Z), and Z saved for the backward pass as an E4M3 MX matrix, in one
  * pass over Z.  Y may be Z itself (same base and row stride).  Computed in
  * fp32 and rounded once; the activations and their accuracy are

@@ -166,6 +166,46 @@ def test_activation_refusals(tlg):
     assert lib.tlg_act_backward_mx_workspace_size(8, 8, 1, None) == bad
 
 
+def test_product_refusals(tlg):
+    lib = tlg.raw_library()
+
+    def call(M=8, N=8, K=64, Am=A, lda=32, SA=2 * A, B=3 * A, ldb=32, SB=4 * A, epi=None, C=5 * A, ldc=8, out=1):
+        return lib.tlg_gemm_mxfp4(M, N, K, Am, lda, SA, B, ldb, SB, ctypes.byref(epi) if epi else None, C, ldc, out,
+                                  None, None)
+
+    E = tlg.tlg_fused_epilogue
+    bad, align, unsup = tlg.TLG_ERR_INVALID_ARG, tlg.TLG_ERR_ALIGNMENT, tlg.TLG_ERR_UNSUPPORTED
+    assert call(M=-1) == bad and call(out=3) == bad and call(K=2 ** 31) == unsup and call(M=2 ** 31 - 300, N=2 ** 20) == unsup
+    assert call(Am=None) == bad and call(SB=None) == bad and call(C=None) == bad
+    assert call(lda=16) == bad and call(ldb=31) == bad and call(ldc=7) == bad
+    assert call(lda=40) == align and call(B=3 * A + 8) == align and call(SA=2 * A + 8) == align
+    assert call(C=5 * A + 1) == align and call(C=5 * A + 2, out=0) == align
+    assert call(C=A) == bad and call(C=4 * A) == bad  # C over A, over B's scales
+    assert call(epi=E(None, 5, None, 0)) == bad and call(epi=E(6 * A + 1, 0, None, 0)) == align
+    assert call(epi=E(5 * A, 0, None, 0)) == bad and call(epi=E(None, 0, 5 * A, 16)) == bad
+    assert call(epi=E(None, 0, 6 * A, 7)) == bad and call(epi=E(None, 0, 6 * A + 1, 8)) == align
+    assert call(M=0) == tlg.TLG_OK and call(N=0) == tlg.TLG_OK
+    assert lib.tlg_choose_config_mxfp4(8, 8, 8, 1, None) == bad
+
+
+def test_product_binding_refusals(tlg):
+    Q, S = torch.zeros((4, 32), dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        tlg.tlg_gemm_mxfp4(Q, S, Q[:, :16], S)
+    with pytest.raises(ValueError):
+        tlg.tlg_gemm_mxfp4(Q[:, :24], S, Q[:, :24], S)
+    with pytest.raises(ValueError):
+        tlg.tlg_gemm_mxfp4(Q, S[:256], Q, S)
+    with pytest.raises(ValueError):
+        tlg.tlg_gemm_mxfp4(Q, S, Q, S, out="bf16", bias=torch.zeros(4, dtype=torch.float16))
+    with pytest.raises(ValueError):
+        tlg.tlg_gemm_mxfp4(Q, S, Q, S, residual=torch.zeros((4, 4)))
+    with pytest.raises(ValueError):
+        tlg.tlg_gemm_mxfp4(Q, S, Q, S, activation="swish")
+    with pytest.raises(tlg.TlgError):
+        tlg.tlg_gemm_mxfp4(Q, S, Q, S)
+
+
 def test_binding_refusals(tlg):
     X = torch.zeros((4, 40), dtype=torch.float16)
     Q, S = torch.zeros((4, 32), dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)

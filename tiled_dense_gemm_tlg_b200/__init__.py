@@ -17,6 +17,7 @@ Functions (same names as the C entry points):
 * ``tlg_gemm_fused(...)``                  C = act(op(A).op(B) + bias) + residual
 * ``tlg_mx_quantize(X, ...)``, ``tlg_mx_dequantize(Q, S, cols, ...)``  4- and 8-bit
   microscaled (MX) matrices
+* ``tlg_gemm_mxfp4(A, SA, B, SB, ...)``    C = act(A.B^T + bias) + residual over 4-bit operands
 * ``tlg_act_forward_mx(Z, activation)``, ``tlg_act_backward_mx(dY, Q, S, activation)``
   an activation whose input is saved in 8 bits, and its backward pass
 * ``tlg_choose_config``, ``tlg_device_error``, ``tlg_selftest_timeout``,
@@ -108,7 +109,10 @@ _lib.tlg_mx_dequantize.argtypes = [_i32, _i64, _i64, _p, _i64, _p, _i32, _p, _i6
 _lib.tlg_act_forward_mx.argtypes = [_i64, _i64, _i32, _i32, _p, _i64, _p, _i64, _p, _i64, _p, _p]
 _lib.tlg_act_backward_mx.argtypes = [_i64, _i64, _i32, _i32, _p, _i64, _p, _i64, _p, _p, _i64, _p, _p, _sz, _p]
 _lib.tlg_act_backward_mx_workspace_size.argtypes = [_i64, _i64, _i32, ctypes.POINTER(_sz)]
-for _name in ("tlg_mx_size", "tlg_mx_quantize", "tlg_mx_dequantize", "tlg_act_forward_mx", "tlg_act_backward_mx",
+_lib.tlg_gemm_mxfp4.argtypes = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, ctypes.POINTER(tlg_fused_epilogue),
+                                _p, _i64, _i32, ctypes.POINTER(tlg_config), _p]
+_lib.tlg_choose_config_mxfp4.argtypes = [_i64, _i64, _i64, _i32, ctypes.POINTER(tlg_config)]
+for _name in ("tlg_gemm_mxfp4", "tlg_choose_config_mxfp4", "tlg_mx_size", "tlg_mx_quantize", "tlg_mx_dequantize", "tlg_act_forward_mx", "tlg_act_backward_mx",
               "tlg_act_backward_mx_workspace_size", "tlg_gemm_f16f32", "tlg_gemm_f16f16", "tlg_gemm_bias_relu_f16", "tlg_gemm_ex",
               "tlg_gemm_op", "tlg_gemm_fused", "tlg_gemm_ex_noalloc", "tlg_gemm_workspace_size", "tlg_gemm_workspace_size_op", "tlg_choose_config", "tlg_device_error", "tlg_selftest_timeout"):
     getattr(_lib, _name).restype = _i32
@@ -475,6 +479,51 @@ def tlg_mx_dequantize(Q: torch.Tensor, S: torch.Tensor, cols: int, format: str =
     _check(_lib.tlg_mx_dequantize(fmt, rows, cols, q, ldq, s, code, px, ldx, _stream_handle(stream, Q)),
            "tlg_mx_dequantize")
     return X
+
+
+def tlg_gemm_mxfp4(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch.Tensor,
+                   bias: torch.Tensor | None = None, activation: str = "none",
+                   residual: torch.Tensor | None = None, C: torch.Tensor | None = None, out: str = "f16",
+                   config: dict | None = None, stream=None):
+    """C = act(A.B^T + bias[col]) + residual[row, col]: A (M x K) and B (N x K) are 4-bit MX matrices
+    (``tlg_mx_quantize(..., format="e2m1")``), C is "f32", "f16" or "bf16".  The bias is fp16, or
+    bf16 for a bf16 C; the residual has C's type and may be ``C`` itself."""
+    M, N, kb = A.shape[0], B.shape[0], A.shape[1]
+    if B.dim() != 2 or B.shape[1] != kb or kb % 16:
+        raise ValueError(f"A and B must hold whole blocks of one K: {tuple(A.shape)} and {tuple(B.shape)} bytes")
+    if out not in _TYPES:
+        raise ValueError(f"out must be one of {sorted(_TYPES)}")
+    code, dtype = _TYPES[out]
+    pa, lda, psa = _mx(A, SA, M, kb, 16, "A")
+    pb, ldb, psb = _mx(B, SB, N, kb, 16, "B")
+    C = _out(C, M, N, dtype, A)
+    pc, ldc = _mat(C, "C")
+    epi = None
+    if bias is not None or residual is not None or activation != "none":
+        epi = tlg_fused_epilogue(None, _activation(activation), None, 0)
+        if bias is not None:
+            bdt = torch.bfloat16 if out == "bf16" else torch.float16
+            if bias.dtype != bdt or bias.dim() != 1 or bias.numel() != N or (N > 1 and bias.stride(0) != 1):
+                raise ValueError(f"bias must be a contiguous {bdt} vector of length {N}")
+            epi.bias = bias.data_ptr()
+        if residual is not None:
+            if residual.dtype != dtype or tuple(residual.shape) != (M, N):
+                raise ValueError(f"residual must be {dtype} of shape ({M}, {N})")
+            epi.residual, epi.ldr = _mat(residual, "residual")
+    _same_device(A, SA, B, SB, C, bias, residual)
+    cfg = tlg_config(**{k: int(v) for k, v in config.items()}) if config is not None else None
+    _check(_lib.tlg_gemm_mxfp4(M, N, kb * 2, pa, lda, psa, pb, ldb, psb,
+                               ctypes.byref(epi) if epi is not None else None, pc, ldc, code,
+                               ctypes.byref(cfg) if cfg is not None else None, _stream_handle(stream, A)),
+           "tlg_gemm_mxfp4")
+    return C
+
+
+def tlg_choose_config_mxfp4(M: int, N: int, K: int, out: str = "f16", request: dict | None = None) -> dict:
+    """The configuration tlg_gemm_mxfp4 would run for this shape (request fields of 0 = automatic)."""
+    cfg = tlg_config(**{k: int(v) for k, v in (request or {}).items()})
+    _check(_lib.tlg_choose_config_mxfp4(M, N, K, _TYPES[out][0], ctypes.byref(cfg)), "tlg_choose_config_mxfp4")
+    return cfg.as_dict()
 
 
 def _activation(activation: str) -> int:

@@ -1161,7 +1161,7 @@ tlg_status tlg_device_error(int clear, uint32_t *code_out) {
   // Every translation unit's kernels report into that unit's own word.
   tlg_status (*const readers[])(bool, uint32_t *) = {tlg::error_word_host, tlg::error_word_nn,
                                                      tlg::error_word_nt, tlg::error_word_tn,
-                                                     tlg::error_word_tt};
+                                                     tlg::error_word_tt, tlg::error_word_mxgemm};
   uint32_t v = 0;
   for (auto read : readers) {
     uint32_t w = 0;

@@ -1,0 +1,297 @@
+// Host side of tlg_gemm_mxfp4: argument checks, the tile choice and the launch.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include "tlg.h"
+#include "tlg_mx_host.cuh"
+#include "tlg_mxgemm_kernel.cuh"
+#include "tlg_variants.cuh"
+
+namespace tlg {
+
+namespace {
+
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s per pipeline wait
+
+// --------------------------------------------------------------------------- launches
+
+struct MxMaps {
+  CUtensorMap a = {}, b = {}, sa = {}, sb = {}, c = {};
+};
+
+template <int CG, int BN, int STAGES, int OUT, bool EPI>
+struct MxVariant {
+  using Plan = MxPlan<CG, BN, STAGES>;
+  static constexpr auto kKernel = mxgemm_kernel<CG, BN, STAGES, OUT, EPI>;
+
+  static void fill(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int ctas, cudaStream_t s) {
+    *cfg = {};
+    cfg->gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg->blockDim = dim3(kThreads);
+    cfg->dynamicSmemBytes = Plan::kDynamicBytes;
+    cfg->stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg->attrs = attr;
+    cfg->numAttrs = CG > 1 ? 2 : 1;
+  }
+
+  static tlg_status units(int dev, int sms, int *out) {
+    static LaunchState state[kMaxDevices];
+    static std::mutex mutex;
+    std::lock_guard<std::mutex> lock(mutex);
+    LaunchState &st = state[dev];
+    if (!st.ready) {
+      if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan::kDynamicBytes) !=
+          cudaSuccess) {
+        cudaGetLastError();
+        return TLG_ERR_CUDA;
+      }
+      int n = sms;
+      if (CG > 1) {
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        fill(&cfg, attr, CG * (sms / CG), nullptr);
+        if (cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg) != cudaSuccess || n < 1) {
+          cudaGetLastError();
+          return TLG_ERR_CUDA;
+        }
+      }
+      st.units = n;
+      st.ready = true;
+    }
+    *out = st.units;
+    return TLG_OK;
+  }
+
+  static tlg_status launch(int units, const MxMaps &m, const MxGemmParams &p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    fill(&cfg, attr, units * CG, s);
+    if (cudaLaunchKernelEx(&cfg, kKernel, m.a, m.b, m.sa, m.sb, m.c, p) != cudaSuccess) {
+      cudaGetLastError();
+      return TLG_ERR_CUDA;
+    }
+    return TLG_OK;
+  }
+};
+
+struct MxFns {
+  tlg_status (*units)(int, int, int *);
+  tlg_status (*launch)(int, const MxMaps &, const MxGemmParams &, cudaStream_t);
+};
+
+template <int CG, int BN, int STAGES, int OUT, bool EPI>
+constexpr MxFns fns() {
+  return {MxVariant<CG, BN, STAGES, OUT, EPI>::units, MxVariant<CG, BN, STAGES, OUT, EPI>::launch};
+}
+
+struct MxTile {
+  int cta_group, block_n, stages;
+  double eff;   // sustained fraction of the MMA peak, relative
+  MxFns fns[3][2];  // [tlg_type][epilogue]
+};
+
+#define TLG_MX_TILE(CG, BN, ST, EFF)                                                                   \
+  {                                                                                                    \
+    CG, BN, ST, EFF, {                                                                                 \
+      {fns<CG, BN, ST, kTypeF32, false>(), fns<CG, BN, ST, kTypeF32, true>()},                         \
+          {fns<CG, BN, ST, kTypeF16, false>(), fns<CG, BN, ST, kTypeF16, true>()},                     \
+          {fns<CG, BN, ST, kTypeBF16, false>(), fns<CG, BN, ST, kTypeBF16, true>()},                   \
+    }                                                                                                  \
+  }
+
+// Tiles the library is built with: 128 * cta_group rows by block_n columns.
+const MxTile kTiles[] = {
+    TLG_MX_TILE(1, 64, 6, 0.5),
+    TLG_MX_TILE(1, 128, 5, 0.8),
+    TLG_MX_TILE(2, 192, 5, 1.0),
+};
+
+// --------------------------------------------------------------------------- tile choice
+
+struct MxChoice {
+  const MxTile *tile;
+  int units;
+  tlg_config cfg;
+};
+
+tlg_status choose(int dev, int sms, int64_t M, int64_t N, int type, bool epi, const tlg_config *req, MxChoice *out) {
+  tlg_config r = {};
+  if (req != nullptr) r = *req;
+  if (r.raster_group < 0 || r.raster_group > 64 || r.max_ctas < 0 || r.stages < 0 || r.block_n < 0 ||
+      r.cta_group < 0 || (r.overlap_prev != 0 && r.overlap_prev != 1) || (r.split_k != 0 && r.split_k != 1) ||
+      (r.k_split != 0 && r.k_split != 1))
+    return TLG_ERR_UNSUPPORTED;
+  double best = 0;
+  out->tile = nullptr;
+  for (const MxTile &t : kTiles) {
+    if ((r.cta_group != 0 && r.cta_group != t.cta_group) || (r.block_n != 0 && r.block_n != t.block_n) ||
+        (r.stages != 0 && r.stages != t.stages))
+      continue;
+    int units = 0;
+    const tlg_status us = t.fns[type][epi].units(dev, sms, &units);
+    if (us != TLG_OK) return us;
+    if (r.max_ctas > 0) units = std::max(1, std::min(units, r.max_ctas / t.cta_group));
+    const int64_t tm = 128 * t.cta_group;
+    const int64_t tiles = ((M + tm - 1) / tm) * ((N + t.block_n - 1) / t.block_n);
+    units = static_cast<int>(std::min<int64_t>(units, tiles));
+    const double cost = static_cast<double>((tiles + units - 1) / units) * t.block_n / t.eff;
+    if (out->tile == nullptr || cost < best) {
+      best = cost;
+      out->tile = &t;
+      out->units = units;
+    }
+  }
+  if (out->tile == nullptr) return TLG_ERR_UNSUPPORTED;
+  tlg_config &c = out->cfg;
+  c.block_n = out->tile->block_n;
+  c.stages = out->tile->stages;
+  c.cta_group = out->tile->cta_group;
+  c.raster_group = r.raster_group != 0 ? r.raster_group : 8;
+  c.max_ctas = out->units * c.cta_group;
+  c.split_k = 1;
+  c.overlap_prev = 1;
+  c.k_split = 1;
+  return TLG_OK;
+}
+
+tlg_status check_sizes(int64_t M, int64_t N, int64_t K, int out) {
+  if (!valid_type(out) || M < 0 || N < 0 || K < 0) return TLG_ERR_INVALID_ARG;
+  if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent) return TLG_ERR_UNSUPPORTED;
+  if (((M + 127) / 128) * ((N + 63) / 64) > kMaxExtent) return TLG_ERR_UNSUPPORTED;
+  return TLG_OK;
+}
+
+}  // namespace
+
+TLG_DEFINE_ERROR_WORD_READER(error_word_mxgemm)
+
+}  // namespace tlg
+
+using namespace tlg;
+
+extern "C" {
+
+tlg_status tlg_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *SA, const void *B,
+                          int64_t ldb, const void *SB, const tlg_fused_epilogue *epilogue, void *C, int64_t ldc,
+                          tlg_type out, const tlg_config *config, void *stream) {
+  tlg_status st = check_sizes(M, N, K, out);
+  if (st != TLG_OK) return st;
+  tlg_fused_epilogue e = {};
+  if (epilogue != nullptr) e = *epilogue;
+  if (!valid_activation(e.activation)) return TLG_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return TLG_OK;
+  const int64_t osz = type_bytes(out);
+  Range rc, rr, ra, rsa, rb, rsb;
+  st = check_matrix(C, M, N, ldc, osz, &rc);
+  if (st != TLG_OK) return st;
+  if (K > 0) {
+    st = check_mx(TLG_MX_E2M1, M, K, A, lda, SA, &ra, &rsa);
+    if (st != TLG_OK) return st;
+    st = check_mx(TLG_MX_E2M1, N, K, B, ldb, SB, &rb, &rsb);
+    if (st != TLG_OK) return st;
+    if (meets(rc, ra) || meets(rc, rsa) || meets(rc, rb) || meets(rc, rsb)) return TLG_ERR_INVALID_ARG;
+  }
+  if (e.bias != nullptr) {
+    if (reinterpret_cast<uintptr_t>(e.bias) % 2 != 0) return TLG_ERR_ALIGNMENT;
+    const uintptr_t b0 = reinterpret_cast<uintptr_t>(e.bias);
+    if (meets(rc, Range{b0, b0 + static_cast<uintptr_t>(2 * N)})) return TLG_ERR_INVALID_ARG;
+  }
+  if (e.residual != nullptr) {
+    st = check_matrix(e.residual, M, N, e.ldr, osz, &rr);
+    if (st != TLG_OK) return st;
+    if (meets(rc, rr) && !(e.residual == C && e.ldr == ldc)) return TLG_ERR_INVALID_ARG;
+  }
+  int dev = 0;
+  DeviceInfo info;
+  st = current_device(&dev, &info);
+  if (st != TLG_OK) return st;
+  for (const void *q : {static_cast<const void *>(C), K > 0 ? A : nullptr, K > 0 ? SA : nullptr, K > 0 ? B : nullptr,
+                        K > 0 ? SB : nullptr, e.bias, e.residual})
+    if (q != nullptr && !device_accessible(q, dev)) return TLG_ERR_INVALID_ARG;
+
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool epi = e.bias != nullptr || e.activation != TLG_ACT_NONE || e.residual != nullptr;
+  MxGemmParams p = {};
+  p.C = C;
+  p.ldc = ldc;
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.num_kb = static_cast<int>((K + kMxBK - 1) / kMxBK);
+  p.n_aligned = (N * osz) % 16 == 0 ? 1 : 0;
+  p.c_plain = (!aligned16(C) || (ldc * osz) % 16 != 0) ? 1 : 0;
+  p.limit_ns = kWaitLimitNs;
+  p.bias = e.bias;
+  p.act = e.activation;
+  p.R = e.residual;
+  p.ldr = e.ldr;
+  p.r_vec = (e.residual != nullptr && aligned16(e.residual) && (e.ldr * osz) % 16 == 0) ? 1 : 0;
+  if (K == 0) {
+    const int64_t total = M * N;
+    const int blocks = static_cast<int>(std::min<int64_t>((total + 255) / 256, 4096));
+    if (out == TLG_TYPE_F32)
+      mx_fill_empty_k_kernel<kTypeF32><<<blocks, 256, 0, s>>>(p);
+    else if (out == TLG_TYPE_F16)
+      mx_fill_empty_k_kernel<kTypeF16><<<blocks, 256, 0, s>>>(p);
+    else
+      mx_fill_empty_k_kernel<kTypeBF16><<<blocks, 256, 0, s>>>(p);
+    if (cudaPeekAtLastError() != cudaSuccess) {
+      cudaGetLastError();
+      return TLG_ERR_CUDA;
+    }
+    return TLG_OK;
+  }
+
+  MxChoice c;
+  st = choose(dev, info.sm_count, M, N, out, epi, config, &c);
+  if (st != TLG_OK) return st;
+  p.raster_group = c.cfg.raster_group;
+  // Boxes (inner x outer): A 128 bytes (256 k) x 128 rows, B 128 bytes x the CTA's rows, scales
+  // two tiles (256 words) x the 128-row groups a tile meets, C 128 bytes x 32 rows.
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  const CUtensorMapDataType ct = out == TLG_TYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : out == TLG_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t kbytes = static_cast<uint64_t>(row_bytes(TLG_MX_E2M1, K));
+  const uint64_t tx = static_cast<uint64_t>(scale_tiles_x(K));
+  const int bn = c.cfg.block_n;
+  MxMaps m;
+  if (!encode_2d(&m.a, u8, A, kbytes, static_cast<uint64_t>(M), static_cast<uint64_t>(lda), 128, 128) ||
+      !encode_2d(&m.b, u8, B, kbytes, static_cast<uint64_t>(N), static_cast<uint64_t>(ldb), 128,
+                 static_cast<uint32_t>(bn / c.cfg.cta_group)) ||
+      !encode_2d(&m.sa, u32, SA, tx * 128, static_cast<uint64_t>((M + 127) / 128), tx * 512, 256, 1,
+                 CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_2d(&m.sb, u32, SB, tx * 128, static_cast<uint64_t>((N + 127) / 128), tx * 512, 256, bn <= 128 ? 1 : 2,
+                 CU_TENSOR_MAP_SWIZZLE_NONE))
+    return TLG_ERR_CUDA;
+  if (!p.c_plain && !encode_2d(&m.c, ct, C, static_cast<uint64_t>(N), static_cast<uint64_t>(M),
+                               static_cast<uint64_t>(ldc * osz), static_cast<uint32_t>(128 / osz), 32))
+    return TLG_ERR_CUDA;
+  return c.tile->fns[out][epi].launch(c.units, m, p, s);
+}
+
+tlg_status tlg_choose_config_mxfp4(int64_t M, int64_t N, int64_t K, tlg_type out, tlg_config *config) {
+  if (config == nullptr) return TLG_ERR_INVALID_ARG;
+  tlg_status st = check_sizes(M, N, K, out);
+  if (st != TLG_OK) return st;
+  int dev = 0;
+  DeviceInfo info;
+  st = current_device(&dev, &info);
+  if (st != TLG_OK) return st;
+  MxChoice c;
+  const tlg_config req = *config;
+  st = choose(dev, info.sm_count, std::max<int64_t>(M, 1), std::max<int64_t>(N, 1), out, true, &req, &c);
+  if (st == TLG_OK) *config = c.cfg;
+  return st;
+}
+
+}  // extern "C"

@@ -1,0 +1,526 @@
+// Persistent, warp-specialised product of E2M1 (4-bit) MX matrices for sm_100a:
+// C = act(A . B^T + bias) + residual, A M x K and B N x K, both with K contiguous and one E8M0
+// scale per 32 k.  The tensor core applies the scales itself (tcgen05.mma.kind::mxf4 with
+// block scaling): each product a * b * 2^(ea + eb) is exact and the sum is kept in fp32.
+//
+// The roles are the fp16 kernel's (tlg_gemm_kernel.cuh): a TMA producer lane, an MMA lane and
+// four epilogue warps over a ring of operand slots and two TMEM accumulators.  What differs:
+//
+//  - A k-block is 256 elements, 128 bytes a row (one 128-byte swizzle row of 4-bit elements),
+//    and four MMAs of 64 k.
+//  - Beside the operand tiles a slot holds their scales: 1 KB per 128 rows (two scale tiles of
+//    128 rows x 4 blocks).  The MMA lane copies them to TMEM (tcgen05.cp, which spreads a
+//    tile's 512 bytes over 32 lanes x 4 columns and repeats them for the four lane groups)
+//    right before the MMAs that use them.
+//  - Every ring slot has TMEM columns of its own for its scales, so the wait for the slot's
+//    bytes, which the producer only requested once the slot's earlier MMAs were done, also
+//    covers overwriting the scales those MMAs read.
+//
+// Tiles are 128 * CG rows by BN columns.  A tile's columns start at a multiple of 64, its
+// scales at a multiple of 128 rows of B: for a start in the second half of a scale tile the
+// MMA's scale address skips the two columns (of 32 rows of B each) before it.
+#pragma once
+
+#include "tlg_mx_device.cuh"
+
+namespace tlg {
+
+constexpr int kMxBK = 256;  // elements of a k-block
+constexpr uint32_t kSfTileBytes = 512;  // 128 rows x 4 blocks
+
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr) {
+  // No swizzle; 8-row core matrices of 16-byte rows, 128 bytes apart.
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(128u >> 4) << 16 |
+         static_cast<uint64_t>(128u >> 4) << 32 | static_cast<uint64_t>(1u) << 46;
+}
+
+// Copies one scale tile (512 bytes of shared memory) to four TMEM columns.  With CG == 2 each
+// CTA of the pair copies from its own shared memory to its own TMEM.
+template <int CG>
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// D[tmem] (+)= (A x scales) . (B x scales) over 64 k; E2M1 operands, a scale per 32 k.
+template <int CG>
+__device__ __forceinline__ void mma_mxf4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of tcgen05.mma.kind::mxf4 with block scaling, both operands K-major:
+//   bits 4-5 which bytes of a TMEM scale word B uses (0: blocks 0 and 1; 2: blocks 2 and 3),
+//   7-9 A format (1 = E2M1), 10-11 B format, 17-22 N >> 3, bit 23 scale format (1 = E8M0),
+//   27-28 M >> 7, 29-30 as bits 4-5, for A.
+__host__ __device__ constexpr uint32_t make_idesc_mxf4(int m, int n, int sf) {
+  return (static_cast<uint32_t>(sf) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (1u << 23) | (static_cast<uint32_t>(m >> 7) << 27) | (static_cast<uint32_t>(sf) << 29);
+}
+
+struct MxGemmParams {
+  void *C;
+  int64_t ldc;
+  int M, N;
+  int num_kb;        // k-blocks of 256
+  int raster_group;  // tile rows walked together
+  int n_aligned;     // N * sizeof(out) is a multiple of 16: every box may go through TMA
+  int c_plain;       // C cannot be written by TMA
+  uint64_t limit_ns;
+  const void *bias;  // 16-bit: bf16 for a bf16 C, else fp16
+  int act;
+  const void *R;     // residual in C's type, or nullptr; may be C itself (same ldc)
+  int64_t ldr;
+  int r_vec;         // R's base and row stride are 16-byte aligned
+};
+
+template <int CG, int BN, int STAGES>
+struct MxPlan {
+  static constexpr int kBNc = BN / CG;                 // B rows held by one CTA
+  static constexpr int kGroups = BN <= 128 ? 1 : 2;    // 128-row groups of B's scales a tile meets
+  static constexpr uint32_t kABytes = kBM * 128;
+  static constexpr uint32_t kBBytes = kBNc * 128;
+  static constexpr uint32_t kSfaBytes = 2 * kSfTileBytes;
+  static constexpr uint32_t kSfbBytes = kGroups * 2 * kSfTileBytes;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
+  static constexpr uint32_t kBOffset = STAGES * kABytes;
+  static constexpr uint32_t kSfOffset = kBOffset + STAGES * kBBytes;
+  static constexpr uint32_t kOutOffset = kSfOffset + STAGES * (kSfaBytes + kSfbBytes);
+  static constexpr uint32_t kBiasOffset = kOutOffset + kEpiWarps * 2 * kStageOutBytes;
+  static constexpr uint32_t kBarOffset = kBiasOffset + 2 * BN * 4;  // two tiles' bias in fp32
+  static constexpr uint32_t kNumBars = 2 * STAGES + 4 + 1;
+  static constexpr uint32_t kMiscOffset = kBarOffset + kNumBars * 8;
+  static constexpr uint32_t kDynamicBytes = kMiscOffset + 16 + 1024;
+  static constexpr int kSfCols = 8 + 8 * kGroups;      // TMEM columns of one slot's scales
+  static constexpr int kSf0 = 2 * BN;
+  static constexpr uint32_t kTmemCols = kSf0 + STAGES * kSfCols <= 256 ? 256 : 512;
+  static_assert(kSf0 + STAGES * kSfCols <= 512, "accumulators and scales must fit in TMEM");
+  static_assert(kBBytes % 1024 == 0, "operand tiles are 1024-byte aligned");
+  static_assert(BN % 64 == 0 && BN <= 192, "tile columns start in the first or second half of a scale tile");
+  static_assert(kDynamicBytes <= 232448, "shared memory per CTA exceeded");
+};
+
+template <int OUT>
+__device__ __forceinline__ float load_elem(const void *p, int64_t i) {
+  if constexpr (OUT == kTypeF32) {
+    return static_cast<const float *>(p)[i];
+  } else if constexpr (OUT == kTypeF16) {
+    return __half2float(static_cast<const __half *>(p)[i]);
+  } else {
+    return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+  }
+}
+
+template <int OUT>
+__device__ __forceinline__ void store_elem(void *p, int64_t i, float v) {
+  if constexpr (OUT == kTypeF32)
+    static_cast<float *>(p)[i] = v;
+  else if constexpr (OUT == kTypeF16)
+    static_cast<__half *>(p)[i] = __float2half_rn(v);
+  else
+    static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// Type of the bias beside a C of type OUT.
+template <int OUT>
+constexpr int kBiasType = OUT == kTypeBF16 ? kTypeBF16 : kTypeF16;
+
+// v[j] += R[row, col0 + j], j < 32 (R may be C: ordinary loads).
+template <int OUT>
+__device__ __forceinline__ void mx_add_residual_32(const MxGemmParams &p, int row, int col0, float (&v)[32]) {
+  if (row >= p.M) return;
+  const int64_t at = static_cast<int64_t>(row) * p.ldr + col0;
+  if (p.r_vec && col0 + 32 <= p.N) {
+    if constexpr (OUT == kTypeF32) {
+      const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p.R) + at);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float4 w = q[c];
+        f2_add_to(v[4 * c], v[4 * c + 1], w.x, w.y);
+        f2_add_to(v[4 * c + 2], v[4 * c + 3], w.z, w.w);
+      }
+    } else {
+      const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.R) + at);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 w = q[c];
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float lo, hi;
+          unpack2<OUT>(x[i], lo, hi);
+          f2_add_to(v[c * 8 + 2 * i], v[c * 8 + 2 * i + 1], lo, hi);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (col0 + j < p.N) v[j] += load_elem<OUT>(p.R, at + j);
+  }
+}
+
+// Plain predicated stores of one thread's 128-byte row piece (see store_row_tail).
+template <int OUT>
+__device__ __forceinline__ void mx_store_row(const MxGemmParams &p, int row, int col0, const uint32_t (&w)[32]) {
+  if (row >= p.M) return;
+  const int64_t at = static_cast<int64_t>(row) * p.ldc + col0;
+  if constexpr (OUT == kTypeF32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (col0 + j < p.N) static_cast<uint32_t *>(p.C)[at + j] = w[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+      if (col0 + j < p.N) static_cast<uint16_t *>(p.C)[at + j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+  }
+}
+
+template <int CG, int BN, int STAGES, int OUT, bool EPI>
+__global__ void __launch_bounds__(kThreads, 1)
+    mxgemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                  const __grid_constant__ CUtensorMap tmC, const MxGemmParams p) {
+  using Plan = MxPlan<CG, BN, STAGES>;
+  constexpr int kTileM = kBM * CG;
+  constexpr int G = Plan::kGroups;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const uint32_t s0 = smem_u32(smem);
+  auto a_slot = [&](int s) { return s0 + s * Plan::kABytes; };
+  auto b_slot = [&](int s) { return s0 + Plan::kBOffset + s * Plan::kBBytes; };
+  auto sfa_slot = [&](int s) { return s0 + Plan::kSfOffset + s * (Plan::kSfaBytes + Plan::kSfbBytes); };
+  const uint32_t bar0 = s0 + Plan::kBarOffset;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+  uint32_t *misc = reinterpret_cast<uint32_t *>(smem + Plan::kMiscOffset);
+  volatile uint32_t *abort_flag = misc + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = (CG == 2) ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int unit = CG == 2 ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int num_units = CG == 2 ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+  const int num_m = (p.M + kTileM - 1) / kTileM;
+  const int num_n = (p.N + BN - 1) / BN;
+  const int tiles = num_m * num_n;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), kEpiWarps * CG);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+    if (!p.c_plain) tma_prefetch_desc(&tmC);
+  }
+  if (warp == 1) {
+    tmem_alloc<CG>(smem_u32(misc), Plan::kTmemCols);
+    tmem_relinquish<CG>();
+  }
+  tc_fence_before_sync();
+  __syncwarp();
+  if constexpr (CG == 2)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(misc);
+  grid_dependency_wait();  // global memory is touched only after this
+  grid_launch_dependents();
+
+  if (warp == 0 && lane == 0) {
+    // ---------------------------------------------------------------- producer (every CTA)
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t issued_mask = 0, issued_parity = 0;
+    bool ok = true;
+    for (int t = unit; t < tiles && ok; t += num_units) {
+      int mb, nb;
+      tile_coords(t, num_m, num_n, p.raster_group, mb, nb);
+      const int a_row = mb * kTileM + static_cast<int>(rank) * kBM;
+      const int b_row = nb * BN + static_cast<int>(rank) * Plan::kBNc;
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!mbar_wait_spin(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns, kRoleProducer, &g_device_error,
+                            4096)) {
+          ok = false;
+          break;
+        }
+        uint32_t bar;
+        if constexpr (CG == 1) {
+          bar = full_bar(stage);
+          mbar_arrive_expect_tx(bar, Plan::kStageBytes);
+        } else {
+          if (leader) mbar_arrive_expect_tx(full_bar(stage), 2 * Plan::kStageBytes);
+          bar = mapa_shared(full_bar(stage), 0);
+        }
+        auto load = [&](uint32_t dst, const CUtensorMap *tm, int32_t x, int32_t y) {
+          if constexpr (CG == 1)
+            tma_load_2d(dst, tm, bar, x, y);
+          else
+            tma_load_2d_pair(dst, tm, bar, x, y);
+        };
+        load(a_slot(stage), &tmA, kb * 128, a_row);
+        load(b_slot(stage), &tmB, kb * 128, b_row);
+        load(sfa_slot(stage), &tmSA, kb * 256, a_row / 128);  // 256 words: two scale tiles
+        load(sfa_slot(stage) + Plan::kSfaBytes, &tmSB, kb * 256, nb * BN / 128);
+        issued_mask |= 1u << stage;
+        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (ok) {
+      // Wait until every slot has been released: no commit-arrive is still on its way.
+      for (int i = 0; i < STAGES; ++i) {
+        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns, kRoleProducer, &g_device_error)) {
+          ok = false;
+          break;
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && leader) {
+      // Let the copies already issued land before shared memory goes away.
+      for (int s = 0; s < STAGES; ++s)
+        if (issued_mask & (1u << s))
+          mbar_wait(full_bar(s), (issued_parity >> s) & 1u, nullptr, p.limit_ns, kRoleProducer, &g_device_error);
+    }
+  } else if (warp == 1 && lane == 0 && leader) {
+    // ---------------------------------------------------------------- MMA issuer (leader CTA)
+    constexpr uint32_t idesc[2] = {make_idesc_mxf4(kTileM, BN, 0), make_idesc_mxf4(kTileM, BN, 2)};
+    int stage = 0;
+    uint32_t phase = 0;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int t = unit; t < tiles && ok; t += num_units) {
+      int mb, nb;
+      tile_coords(t, num_m, num_n, p.raster_group, mb, nb);
+      const uint32_t skip = static_cast<uint32_t>((nb * BN) % 128 / 32);
+      if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.limit_ns, kRoleMma, &g_device_error)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!mbar_wait_spin(full_bar(stage), phase, abort_flag, p.limit_ns, kRoleMma, &g_device_error, 4096)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t sfa = tmem_base + static_cast<uint32_t>(Plan::kSf0 + stage * Plan::kSfCols);
+        const uint32_t sfb = sfa + 8;
+        const uint64_t sf_desc = smem_desc_plain(sfa_slot(stage));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // the two scale tiles (128 k each)
+          tmem_copy_scales<CG>(sfa + 4 * h, sf_desc + h * (kSfTileBytes / 16));
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            tmem_copy_scales<CG>(sfb + 4 * (h * G + g),
+                                 sf_desc + (Plan::kSfaBytes + (g * 2 + h) * kSfTileBytes) / 16);
+        }
+        const uint64_t ad = smem_desc_sw128(a_slot(stage), 16, 1024);
+        const uint64_t bd = smem_desc_sw128(b_slot(stage), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)  // 64 k: 32 bytes along the swizzled row
+          mma_mxf4_ss<CG>(d_tmem, ad + kk * 2, bd + kk * 2, idesc[kk & 1], sfa + 4 * (kk >> 1),
+                          sfb + 4 * G * (kk >> 1) + skip, (kb > 0 || kk > 0) ? 1u : 0u);
+        mma_commit<CG>(empty_bar(stage));
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      mma_commit<CG>(tfull_bar(acc));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (!ok) {
+      mma_commit_local<CG>(drain_bar);
+      mbar_wait(drain_bar, 0, nullptr, p.limit_ns, kRoleMma, &g_device_error);
+    }
+  } else if (warp >= 2) {
+    // ---------------------------------------------------------------- epilogue (every CTA)
+    // Warp w drains TMEM lanes 32*(w%4) .. +31, 64 columns at a time, into two 4 KB boxes.
+    const int quarter = warp & 3;
+    const int ew = warp - 2;
+    const uint32_t box0 = s0 + Plan::kOutOffset + static_cast<uint32_t>(ew * 2) * kStageOutBytes;
+    const uint32_t release_bar0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
+    constexpr int kBoxCols = OUT == kTypeF32 ? 32 : 64;
+    int acc = 0;
+    uint32_t acc_phase = 0, boxes_used = 0;
+    int bias_buf = 0;
+    const uint64_t tile_limit_ns = p.limit_ns + static_cast<uint64_t>(p.num_kb) * kWaitPerKBlockNs;
+    for (int t = unit; t < tiles; t += num_units) {
+      int mb, nb;
+      tile_coords(t, num_m, num_n, p.raster_group, mb, nb);
+      const int row0 = mb * kTileM + static_cast<int>(rank) * kBM + quarter * 32;
+      const int row = row0 + lane;
+      const uint32_t sbias = s0 + Plan::kBiasOffset + static_cast<uint32_t>(bias_buf * BN * 4);
+      if (EPI && p.bias != nullptr) {
+        // The tile's bias in fp32, in the buffer of the tile before last (whose readers have
+        // passed the barrier of the last tile).
+        float *sb = reinterpret_cast<float *>(smem + Plan::kBiasOffset) + bias_buf * BN;
+        for (int c = ew * 32 + lane; c < BN; c += 32 * kEpiWarps) {
+          const int col = nb * BN + c;
+          sb[c] = col < p.N ? load_elem<kBiasType<OUT>>(p.bias, col) : 0.0f;
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+        bias_buf ^= 1;
+      }
+      // On a timeout the warp stops reading tiles but keeps meeting the bias barrier, so no
+      // other epilogue warp waits at it for good.
+      bool ok = *abort_flag == 0u;
+      if (ok && !mbar_wait(tfull_bar(acc), acc_phase, abort_flag, tile_limit_ns, kRoleEpilogue, &g_device_error))
+        ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after_sync();
+#pragma unroll 1
+        for (int tc = 0; tc < BN; tc += 64) {
+          const int col0 = nb * BN + tc;
+          uint32_t ra[32], rb[32];
+          __syncwarp();
+          tmem_load_2x32cols(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                 static_cast<uint32_t>(acc * BN + tc),
+                             ra, rb);
+          if (tc + 64 >= BN) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (CG == 2)
+                mbar_arrive_cluster(release_bar0 + 8u * acc);
+              else
+                mbar_arrive(release_bar0 + 8u * acc);
+            }
+          }
+          if (row0 >= p.M || col0 >= p.N) continue;
+          float va[32], vb[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            va[j] = __uint_as_float(ra[j]);
+            vb[j] = __uint_as_float(rb[j]);
+          }
+          auto finish = [&](float(&v)[32], int half) {
+            if constexpr (EPI) {
+              if (p.bias != nullptr) add_bias_smem_32(sbias, tc + 32 * half, v);
+              activate_lane<OUT, 32>(p.act, v);
+              if (p.R != nullptr) mx_add_residual_32<OUT>(p, row, col0 + 32 * half, v);
+            }
+          };
+          auto put = [&](const uint32_t(&w)[32], int col) {
+            if (p.c_plain || (!p.n_aligned && col + kBoxCols > p.N)) {
+              mx_store_row<OUT>(p, row, col, w);
+              return;
+            }
+            const uint32_t box = box0 + (boxes_used & 1u) * kStageOutBytes;
+            if (lane == 0) bulk_wait_group_read<1>();
+            __syncwarp();
+            st_box_row(box, lane, w, 0);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tmC, box, col, row0);
+              bulk_commit_group();
+            }
+            ++boxes_used;
+          };
+          if constexpr (OUT == kTypeF32) {
+            uint32_t w[32];
+            finish(va, 0);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(va[j]);
+            put(w, col0);
+            if (col0 + 32 < p.N) {
+              finish(vb, 1);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(vb[j]);
+              put(w, col0 + 32);
+            }
+          } else {
+            uint32_t w[32];
+            finish(va, 0);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = pack2<OUT>(va[2 * j], va[2 * j + 1]);
+            finish(vb, 1);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[16 + j] = pack2<OUT>(vb[2 * j], vb[2 * j + 1]);
+            put(w, col0);
+          }
+        }
+      }
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+  }
+
+  tc_fence_before_sync();
+  __syncwarp();
+  if constexpr (CG == 2)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc<CG>(tmem_base, Plan::kTmemCols);
+  }
+}
+
+// K == 0: C = act(bias[col]) + R[row, col] (each element read and written by one thread).
+template <int OUT>
+__global__ void mx_fill_empty_k_kernel(const MxGemmParams p) {
+  grid_dependency_wait();
+  const int64_t total = static_cast<int64_t>(p.M) * p.N;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t r = i / p.N, c = i % p.N;
+    float v = p.bias != nullptr ? load_elem<kBiasType<OUT>>(p.bias, c) : 0.0f;
+    v = activate<OUT != kTypeF32>(p.act, v);
+    if (p.R != nullptr) v += load_elem<OUT>(p.R, r * p.ldr + c);
+    store_elem<OUT>(p.C, r * p.ldc + c, v);
+  }
+}
+
+}  // namespace tlg

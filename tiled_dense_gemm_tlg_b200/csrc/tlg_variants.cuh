@@ -173,6 +173,7 @@ tlg_status error_word_nn(bool clear, uint32_t *out);
 tlg_status error_word_nt(bool clear, uint32_t *out);
 tlg_status error_word_tn(bool clear, uint32_t *out);
 tlg_status error_word_tt(bool clear, uint32_t *out);
+tlg_status error_word_mxgemm(bool clear, uint32_t *out);  // tlg_mxgemm.cu
 
 #define TLG_DEFINE_ERROR_WORD_READER(NAME)                                            \
   tlg_status NAME(bool clear, uint32_t *out) {                                        \
