@@ -19,7 +19,7 @@ from oracle import mx
 pytestmark = pytest.mark.gpu
 
 TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
-TILES = [(1, 64), (1, 128), (2, 192)]
+TILES = [(1, 64), (1, 128), (2, 192), (2, 256)]
 SHAPES = [(1, 1, 1), (1, 8, 32), (3, 65, 33), (128, 64, 256), (129, 129, 257), (200, 333, 1000), (257, 400, 2000),
           (512, 768, 512), (5, 1000, 700), (300, 17, 96)]
 

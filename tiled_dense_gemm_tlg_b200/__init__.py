@@ -137,25 +137,35 @@ def _check(rc: int, where: str):
         raise TlgError(rc, where)
 
 
+# torch's current stream as a bare handle: a thirtieth of the time of building a Stream object
+# (0.07 us against 2.3 us), which is a large part of a small call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(index: int) -> int:
+        return int(torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream_handle(stream, *tensors) -> int:
     if stream is not None:
         return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
     for t in tensors:
         if t is not None and t.is_cuda:
-            return int(torch.cuda.current_stream(t.device).cuda_stream)
+            return _raw_stream(t.get_device())
     return 0
 
 
 def _mat(t: torch.Tensor, name: str):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
-    if t.size(1) > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if cols > 1 and unit != 1:
         raise ValueError(f"{name} must be row-major (unit stride along its last dimension)")
-    if t.size(0) > 1 and t.stride(0) < t.size(1):
+    if rows > 1 and ld < cols:
         # a broadcast or overlapping view: its rows are not `stride(0)` elements apart in a
         # buffer of rows x stride(0) elements, which is what the library would read
-        raise ValueError(f"{name} has overlapping rows (row stride {t.stride(0)} < {t.size(1)} columns)")
-    return t.data_ptr(), max(t.stride(0), t.size(1))
+        raise ValueError(f"{name} has overlapping rows (row stride {ld} < {cols} columns)")
+    return t.data_ptr(), ld if ld > cols else cols
 
 
 def _shapes(A, B):
@@ -400,6 +410,24 @@ def _format(format: str):
     return _FORMATS[format]
 
 
+def _out_type(out: str):
+    if out not in _TYPES:
+        raise ValueError(f"the type must be one of {sorted(_TYPES)}")
+    return _TYPES[out]
+
+
+def _activation(activation: str) -> int:
+    if activation not in _ACT:
+        raise ValueError(f"activation must be one of {sorted(_ACT)}")
+    return _ACT[activation]
+
+
+def _stream_of(stream, device: int) -> int:
+    if stream is not None:
+        return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    return _raw_stream(device) if device >= 0 else 0
+
+
 def _type_code(t: torch.Tensor, name: str) -> int:
     code = _TYPE_OF.get(t.dtype)
     if code is None:
@@ -407,34 +435,45 @@ def _type_code(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _same_device(*tensors):
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
+def _same_device(device: int, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("all tensors must be on one device")
 
 
-def _mx_scale_bytes(rows: int, row_bytes: int, block_bytes: int) -> int:
-    return -(-rows // 128) * -(-(row_bytes // block_bytes) // 4) * 512
+def _mx_scale_bytes(rows: int, blocks: int) -> int:
+    return -(-rows // 128) * -(-blocks // 4) * 512
 
 
-def _mx(Q: torch.Tensor, S: torch.Tensor, rows: int, row_bytes: int, block_bytes: int, name: str = ""):
+def _mx(Q: torch.Tensor, S: torch.Tensor, rows: int, blocks: int, block_bytes: int, name: str = ""):
     """Checks an MX matrix's two buffers; returns the arguments (Q, ldq, S)."""
-    if Q.dtype != torch.uint8 or Q.dim() != 2 or Q.size(0) != rows or Q.size(1) != row_bytes:
-        raise ValueError(f"Q{name} must be a uint8 tensor of shape ({rows}, {row_bytes})")
-    if S.dtype != torch.uint8 or not S.is_contiguous() or S.numel() < _mx_scale_bytes(rows, row_bytes, block_bytes):
-        raise ValueError(f"S{name} must be a contiguous uint8 tensor of at least "
-                         f"{_mx_scale_bytes(rows, row_bytes, block_bytes)} bytes")
     q, ldq = _mat(Q, f"Q{name}")
+    if Q.dtype != torch.uint8 or Q.shape != (rows, blocks * block_bytes):
+        raise ValueError(f"Q{name} must be a uint8 tensor of shape ({rows}, {blocks * block_bytes})")
+    if S.dtype != torch.uint8 or not S.is_contiguous() or S.numel() < _mx_scale_bytes(rows, blocks):
+        raise ValueError(f"S{name} must be a contiguous uint8 tensor of at least "
+                         f"{_mx_scale_bytes(rows, blocks)} bytes")
     return q, ldq, S.data_ptr()
 
 
-def _mx_out(Q, S, rows: int, cols: int, block_bytes: int, like: torch.Tensor):
-    row_bytes = -(-cols // 32) * block_bytes
+def _new(rows: int, cols: int, dtype, device):
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
+def _mx_out(Q, S, rows: int, cols: int, block_bytes: int, like: torch.Tensor, device: int):
+    """The MX matrix an operator writes, allocated where not given: (Q, S) and its arguments."""
+    blocks = (cols + 31) // 32
+    if Q is None and S is None:
+        row_bytes = blocks * block_bytes
+        Q = _new(rows, row_bytes, torch.uint8, like.device)
+        S = torch.empty_strided((_mx_scale_bytes(rows, blocks),), (1,), dtype=torch.uint8, device=like.device)
+        return Q, S, Q.data_ptr(), row_bytes, S.data_ptr()
     if Q is None:
-        Q = torch.empty((rows, row_bytes), dtype=torch.uint8, device=like.device)
+        Q = _new(rows, blocks * block_bytes, torch.uint8, like.device)
     if S is None:
-        S = torch.empty(_mx_scale_bytes(rows, row_bytes, block_bytes), dtype=torch.uint8, device=like.device)
-    return Q, S, row_bytes
+        S = torch.empty(_mx_scale_bytes(rows, blocks), dtype=torch.uint8, device=like.device)
+    _same_device(device, Q, S)
+    return (Q, S) + _mx(Q, S, rows, blocks, block_bytes)
 
 
 def tlg_mx_size(format: str, rows: int, cols: int):
@@ -449,15 +488,14 @@ def tlg_mx_quantize(X: torch.Tensor, format: str = "e2m1", op: str = "N", Q: tor
     """(Q, S): X (fp32, fp16 or bf16) in blocks of 32 along its rows; ``op="T"`` quantises X's
     transpose, in blocks down its columns.  ``format``: "e2m1" (4 bits) or "e4m3" (8 bits)."""
     fmt, block_bytes = _format(format)
-    code = _type_code(X, "X")
     px, ldx = _mat(X, "X")
-    t = op.upper() == "T"
+    code = _type_code(X, "X")
+    t = op == "T" or op == "t"
     cols, rows = X.shape if t else (X.shape[1], X.shape[0])
-    Q, S, row_bytes = _mx_out(Q, S, rows, cols, block_bytes, X)
-    q, ldq, s = _mx(Q, S, rows, row_bytes, block_bytes)
-    _same_device(X, Q, S)
-    _check(_lib.tlg_mx_quantize(fmt, rows, cols, TLG_OP_T if t else TLG_OP_N, code, px, ldx, q, ldq, s,
-                                _stream_handle(stream, X)), "tlg_mx_quantize")
+    device = X.get_device()
+    Q, S, q, ldq, s = _mx_out(Q, S, rows, cols, block_bytes, X, device)
+    _check(_lib.tlg_mx_quantize(fmt, rows, cols, t, code, px, ldx, q, ldq, s, _stream_of(stream, device)),
+           "tlg_mx_quantize")
     return Q, S
 
 
@@ -465,18 +503,19 @@ def tlg_mx_dequantize(Q: torch.Tensor, S: torch.Tensor, cols: int, format: str =
                       X: torch.Tensor | None = None, stream=None):
     """The values of an MX matrix with ``cols`` columns, as "f32", "f16" or "bf16"."""
     fmt, block_bytes = _format(format)
-    if out not in _TYPES:
-        raise ValueError(f"out must be one of {sorted(_TYPES)}")
-    code, dtype = _TYPES[out]
+    code, dtype = _out_type(out)
     rows = Q.shape[0]
-    q, ldq, s = _mx(Q, S, rows, -(-cols // 32) * block_bytes, block_bytes)
+    device = Q.get_device()
+    q, ldq, s = _mx(Q, S, rows, (cols + 31) // 32, block_bytes)
     if X is None:
-        X = torch.empty((rows, cols), dtype=dtype, device=Q.device)
-    elif X.dtype != dtype or tuple(X.shape) != (rows, cols):
-        raise ValueError(f"X must be {dtype} of shape ({rows}, {cols})")
-    px, ldx = _mat(X, "X")
-    _same_device(X, Q, S)
-    _check(_lib.tlg_mx_dequantize(fmt, rows, cols, q, ldq, s, code, px, ldx, _stream_handle(stream, Q)),
+        X = _new(rows, cols, dtype, Q.device)
+        px, ldx = X.data_ptr(), cols
+    else:
+        if X.dtype != dtype or X.shape != (rows, cols):
+            raise ValueError(f"X must be {dtype} of shape ({rows}, {cols})")
+        px, ldx = _mat(X, "X")
+    _same_device(device, X, S)
+    _check(_lib.tlg_mx_dequantize(fmt, rows, cols, q, ldq, s, code, px, ldx, _stream_of(stream, device)),
            "tlg_mx_dequantize")
     return X
 
@@ -488,73 +527,73 @@ def tlg_gemm_mxfp4(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch
     """C = act(A.B^T + bias[col]) + residual[row, col]: A (M x K) and B (N x K) are 4-bit MX matrices
     (``tlg_mx_quantize(..., format="e2m1")``), C is "f32", "f16" or "bf16".  The bias is fp16, or
     bf16 for a bf16 C; the residual has C's type and may be ``C`` itself."""
-    M, N, kb = A.shape[0], B.shape[0], A.shape[1]
-    if B.dim() != 2 or B.shape[1] != kb or kb % 16:
+    M, kb = A.shape
+    N, kb2 = B.shape
+    if kb2 != kb or kb % 16:
         raise ValueError(f"A and B must hold whole blocks of one K: {tuple(A.shape)} and {tuple(B.shape)} bytes")
-    if out not in _TYPES:
-        raise ValueError(f"out must be one of {sorted(_TYPES)}")
-    code, dtype = _TYPES[out]
-    pa, lda, psa = _mx(A, SA, M, kb, 16, "A")
-    pb, ldb, psb = _mx(B, SB, N, kb, 16, "B")
-    C = _out(C, M, N, dtype, A)
-    pc, ldc = _mat(C, "C")
+    code, dtype = _out_type(out)
+    device = A.get_device()
+    pa, lda, psa = _mx(A, SA, M, kb // 16, 16, "A")
+    pb, ldb, psb = _mx(B, SB, N, kb // 16, 16, "B")
+    if C is None:
+        C = _new(M, N, dtype, A.device)
+        pc, ldc = C.data_ptr(), N
+    else:
+        if C.dtype != dtype or C.shape != (M, N):
+            raise ValueError(f"C must be {dtype} of shape ({M}, {N})")
+        pc, ldc = _mat(C, "C")
     epi = None
     if bias is not None or residual is not None or activation != "none":
         epi = tlg_fused_epilogue(None, _activation(activation), None, 0)
         if bias is not None:
             bdt = torch.bfloat16 if out == "bf16" else torch.float16
-            if bias.dtype != bdt or bias.dim() != 1 or bias.numel() != N or (N > 1 and bias.stride(0) != 1):
+            if bias.dtype != bdt or bias.shape != (N,) or (N > 1 and bias.stride(0) != 1):
                 raise ValueError(f"bias must be a contiguous {bdt} vector of length {N}")
             epi.bias = bias.data_ptr()
         if residual is not None:
-            if residual.dtype != dtype or tuple(residual.shape) != (M, N):
+            if residual.dtype != dtype or residual.shape != (M, N):
                 raise ValueError(f"residual must be {dtype} of shape ({M}, {N})")
             epi.residual, epi.ldr = _mat(residual, "residual")
-    _same_device(A, SA, B, SB, C, bias, residual)
-    cfg = tlg_config(**{k: int(v) for k, v in config.items()}) if config is not None else None
-    _check(_lib.tlg_gemm_mxfp4(M, N, kb * 2, pa, lda, psa, pb, ldb, psb,
-                               ctypes.byref(epi) if epi is not None else None, pc, ldc, code,
-                               ctypes.byref(cfg) if cfg is not None else None, _stream_handle(stream, A)),
-           "tlg_gemm_mxfp4")
+        epi = ctypes.byref(epi)
+    _same_device(device, SA, B, SB, C, bias, residual)
+    cfg = ctypes.byref(tlg_config(**{k: int(v) for k, v in config.items()})) if config is not None else None
+    _check(_lib.tlg_gemm_mxfp4(M, N, kb * 2, pa, lda, psa, pb, ldb, psb, epi, pc, ldc, code, cfg,
+                               _stream_of(stream, device)), "tlg_gemm_mxfp4")
     return C
 
 
 def tlg_choose_config_mxfp4(M: int, N: int, K: int, out: str = "f16", request: dict | None = None) -> dict:
     """The configuration tlg_gemm_mxfp4 would run for this shape (request fields of 0 = automatic)."""
     cfg = tlg_config(**{k: int(v) for k, v in (request or {}).items()})
-    _check(_lib.tlg_choose_config_mxfp4(M, N, K, _TYPES[out][0], ctypes.byref(cfg)), "tlg_choose_config_mxfp4")
+    _check(_lib.tlg_choose_config_mxfp4(M, N, K, _out_type(out)[0], ctypes.byref(cfg)), "tlg_choose_config_mxfp4")
     return cfg.as_dict()
-
-
-def _activation(activation: str) -> int:
-    if activation not in _ACT:
-        raise ValueError(f"activation must be one of {sorted(_ACT)}")
-    return _ACT[activation]
 
 
 def tlg_act_forward_mx(Z: torch.Tensor, activation: str, Y: torch.Tensor | None = None,
                        Q: torch.Tensor | None = None, S: torch.Tensor | None = None, stream=None):
     """(Y, Q, S): Y = act(Z) in Z's type (``Y`` may be ``Z`` itself), and Z saved in 8 bits (E4M3)."""
     act = _activation(activation)
-    code = _type_code(Z, "Z")
     pz, ldz = _mat(Z, "Z")
+    code = _type_code(Z, "Z")
     rows, cols = Z.shape
+    device = Z.get_device()
     if Y is None:
-        Y = torch.empty((rows, cols), dtype=Z.dtype, device=Z.device)
-    elif Y.dtype != Z.dtype or Y.shape != Z.shape:
-        raise ValueError(f"Y must be {Z.dtype} of shape ({rows}, {cols})")
-    py, ldy = _mat(Y, "Y")
-    Q, S, row_bytes = _mx_out(Q, S, rows, cols, 32, Z)
-    q, ldq, s = _mx(Q, S, rows, row_bytes, 32)
-    _same_device(Z, Y, Q, S)
-    _check(_lib.tlg_act_forward_mx(rows, cols, act, code, pz, ldz, py, ldy, q, ldq, s, _stream_handle(stream, Z)),
+        Y = _new(rows, cols, Z.dtype, Z.device)
+        py, ldy = Y.data_ptr(), cols
+    else:
+        if Y.dtype != Z.dtype or Y.shape != Z.shape:
+            raise ValueError(f"Y must be {Z.dtype} of shape ({rows}, {cols})")
+        py, ldy = _mat(Y, "Y")
+        _same_device(device, Y)
+    Q, S, q, ldq, s = _mx_out(Q, S, rows, cols, 32, Z, device)
+    _check(_lib.tlg_act_forward_mx(rows, cols, act, code, pz, ldz, py, ldy, q, ldq, s, _stream_of(stream, device)),
            "tlg_act_forward_mx")
     return Y, Q, S
 
 
 def tlg_act_backward_mx_workspace_size(rows: int, cols: int, type: str = "f16") -> int:
     n = _sz(0)
-    _check(_lib.tlg_act_backward_mx_workspace_size(rows, cols, _TYPES[type][0], ctypes.byref(n)),
+    _check(_lib.tlg_act_backward_mx_workspace_size(rows, cols, _out_type(type)[0], ctypes.byref(n)),
            "tlg_act_backward_mx_workspace_size")
     return int(n.value)
 
@@ -566,21 +605,23 @@ def tlg_act_backward_mx(dY: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, acti
     checkpoint, and the fp32 column sums of dZ (None with ``bias_grad=False``).  ``workspace``: a
     device buffer of tlg_act_backward_mx_workspace_size bytes; allocated here when not given."""
     act = _activation(activation)
-    code = _type_code(dY, "dY")
     py, ldy = _mat(dY, "dY")
+    code = _type_code(dY, "dY")
     rows, cols = dY.shape
-    q, ldq, s = _mx(Q, S, rows, -(-cols // 32) * 32, 32)
+    device = dY.get_device()
+    q, ldq, s = _mx(Q, S, rows, (cols + 31) // 32, 32)
     if dZ is None:
-        dZ = torch.empty((rows, cols), dtype=dY.dtype, device=dY.device)
-    elif dZ.dtype != dY.dtype or dZ.shape != dY.shape:
-        raise ValueError(f"dZ must be {dY.dtype} of shape ({rows}, {cols})")
-    pz, ldz = _mat(dZ, "dZ")
+        dZ = _new(rows, cols, dY.dtype, dY.device)
+        pz, ldz = dZ.data_ptr(), cols
+    else:
+        if dZ.dtype != dY.dtype or dZ.shape != dY.shape:
+            raise ValueError(f"dZ must be {dY.dtype} of shape ({rows}, {cols})")
+        pz, ldz = _mat(dZ, "dZ")
     pb, ws_ptr, ws_bytes = None, None, 0
-    handle = _stream_handle(stream, dY)
     if bias_grad or dbias is not None:
         if dbias is None:
-            dbias = torch.empty((cols,), dtype=torch.float32, device=dY.device)
-        elif dbias.dtype != torch.float32 or dbias.dim() != 1 or dbias.numel() != cols or not dbias.is_contiguous():
+            dbias = torch.empty_strided((cols,), (1,), dtype=torch.float32, device=dY.device)
+        elif dbias.dtype != torch.float32 or dbias.shape != (cols,) or not dbias.is_contiguous():
             raise ValueError(f"dbias must be a contiguous fp32 vector of length {cols}")
         pb = dbias.data_ptr()
         if workspace is None:
@@ -588,12 +629,12 @@ def tlg_act_backward_mx(dY: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, acti
             _check(_lib.tlg_act_backward_mx_workspace_size(rows, cols, code, ctypes.byref(n)),
                    "tlg_act_backward_mx_workspace_size")
             if n.value:
-                workspace = torch.empty(n.value, dtype=torch.uint8, device=dY.device)
+                workspace = torch.empty_strided((n.value,), (1,), dtype=torch.uint8, device=dY.device)
         if workspace is not None:
             ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _same_device(dY, Q, S, dZ, dbias, workspace)
-    _check(_lib.tlg_act_backward_mx(rows, cols, act, code, py, ldy, q, ldq, s, pz, ldz, pb, ws_ptr, ws_bytes, handle),
-           "tlg_act_backward_mx")
+    _same_device(device, Q, S, dZ, dbias, workspace)
+    _check(_lib.tlg_act_backward_mx(rows, cols, act, code, py, ldy, q, ldq, s, pz, ldz, pb, ws_ptr, ws_bytes,
+                                    _stream_of(stream, device)), "tlg_act_backward_mx")
     return dZ, dbias
 
 

@@ -31,7 +31,7 @@ struct MxVariant {
   static void fill(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int ctas, cudaStream_t s) {
     *cfg = {};
     cfg->gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg->blockDim = dim3(kThreads);
+    cfg->blockDim = dim3(kMxThreads);
     cfg->dynamicSmemBytes = Plan::kDynamicBytes;
     cfg->stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -114,6 +114,7 @@ const MxTile kTiles[] = {
     TLG_MX_TILE(1, 64, 6, 0.5),
     TLG_MX_TILE(1, 128, 5, 0.8),
     TLG_MX_TILE(2, 192, 5, 1.0),
+    TLG_MX_TILE(2, 256, 5, 1.0),
 };
 
 // --------------------------------------------------------------------------- tile choice

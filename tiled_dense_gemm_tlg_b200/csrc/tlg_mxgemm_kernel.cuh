@@ -3,8 +3,9 @@
 // scale per 32 k.  The tensor core applies the scales itself (tcgen05.mma.kind::mxf4 with
 // block scaling): each product a * b * 2^(ea + eb) is exact and the sum is kept in fp32.
 //
-// The roles are the fp16 kernel's (tlg_gemm_kernel.cuh): a TMA producer lane, an MMA lane and
-// four epilogue warps over a ring of operand slots and two TMEM accumulators.  What differs:
+// The roles are the fp16 kernel's (tlg_gemm_kernel.cuh): a TMA producer warp, an MMA warp and
+// epilogue warps (eight here) over a ring of operand slots and two TMEM accumulators.  What
+// differs:
 //
 //  - A k-block is 256 elements, 128 bytes a row (one 128-byte swizzle row of 4-bit elements),
 //    and four MMAs of 64 k.
@@ -15,6 +16,10 @@
 //  - Every ring slot has TMEM columns of its own for its scales, so the wait for the slot's
 //    bytes, which the producer only requested once the slot's earlier MMAs were done, also
 //    covers overwriting the scales those MMAs read.
+//
+//  - The 256-column accumulators overlap: TMEM holds two of 256 columns 128 apart and the
+//    scales of five slots.  The epilogue drains the shared 128 columns first and hands them
+//    back; the next tile's MMAs, into the other accumulator, start then.
 //
 // Tiles are 128 * CG rows by BN columns.  A tile's columns start at a multiple of 64, its
 // scales at a multiple of 128 rows of B: for a start in the second half of a scale tile the
@@ -91,6 +96,16 @@ struct MxGemmParams {
   int r_vec;         // R's base and row stride are 16-byte aligned
 };
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+constexpr int kMxEpiWarps = 8;  // two to a quarter of the tile's rows, taking its 64-column pieces in turn
+constexpr int kMxThreads = 32 * (2 + kMxEpiWarps);
+
 template <int CG, int BN, int STAGES>
 struct MxPlan {
   static constexpr int kBNc = BN / CG;                 // B rows held by one CTA
@@ -103,17 +118,20 @@ struct MxPlan {
   static constexpr uint32_t kBOffset = STAGES * kABytes;
   static constexpr uint32_t kSfOffset = kBOffset + STAGES * kBBytes;
   static constexpr uint32_t kOutOffset = kSfOffset + STAGES * (kSfaBytes + kSfbBytes);
-  static constexpr uint32_t kBiasOffset = kOutOffset + kEpiWarps * 2 * kStageOutBytes;
+  static constexpr uint32_t kBiasOffset = kOutOffset + kMxEpiWarps * kStageOutBytes;
   static constexpr uint32_t kBarOffset = kBiasOffset + 2 * BN * 4;  // two tiles' bias in fp32
   static constexpr uint32_t kNumBars = 2 * STAGES + 4 + 1;
   static constexpr uint32_t kMiscOffset = kBarOffset + kNumBars * 8;
   static constexpr uint32_t kDynamicBytes = kMiscOffset + 16 + 1024;
   static constexpr int kSfCols = 8 + 8 * kGroups;      // TMEM columns of one slot's scales
-  static constexpr int kSf0 = 2 * BN;
+  static constexpr bool kOverlap = BN == 256;          // the two accumulators share columns
+  static constexpr int kAccStride = kOverlap ? 128 : BN;
+  static constexpr int kAccBars = kOverlap ? 1 : 2;
+  static constexpr int kSf0 = kAccStride + BN;
   static constexpr uint32_t kTmemCols = kSf0 + STAGES * kSfCols <= 256 ? 256 : 512;
   static_assert(kSf0 + STAGES * kSfCols <= 512, "accumulators and scales must fit in TMEM");
   static_assert(kBBytes % 1024 == 0, "operand tiles are 1024-byte aligned");
-  static_assert(BN % 64 == 0 && BN <= 192, "tile columns start in the first or second half of a scale tile");
+  static_assert(BN % 64 == 0 && BN <= 256, "tile columns start in the first or second half of a scale tile");
   static_assert(kDynamicBytes <= 232448, "shared memory per CTA exceeded");
 };
 
@@ -194,7 +212,7 @@ __device__ __forceinline__ void mx_store_row(const MxGemmParams &p, int row, int
 }
 
 template <int CG, int BN, int STAGES, int OUT, bool EPI>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kMxThreads, 1)
     mxgemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                   const __grid_constant__ CUtensorMap tmC, const MxGemmParams p) {
@@ -217,9 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t *misc = reinterpret_cast<uint32_t *>(smem + Plan::kMiscOffset);
   volatile uint32_t *abort_flag = misc + 1;
 
-  const int warp = threadIdx.x >> 5;
+  // Shuffled from lane 0: the same in every lane, and known to be.
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = (CG == 2) ? cluster_ctarank() : 0u;
+  const uint32_t rank = (CG == 2) ? __shfl_sync(0xffffffffu, cluster_ctarank(), 0) : 0u;
   const bool leader = rank == 0;
   const int unit = CG == 2 ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
   const int num_units = CG == 2 ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
@@ -234,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), kEpiWarps * CG);
+      mbar_init(tempty_bar(a), kMxEpiWarps * CG);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0u;
@@ -260,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();  // global memory is touched only after this
   grid_launch_dependents();
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ---------------------------------------------------------------- producer (every CTA)
     int stage = 0;
     uint32_t phase = 0;
@@ -272,29 +291,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int a_row = mb * kTileM + static_cast<int>(rank) * kBM;
       const int b_row = nb * BN + static_cast<int>(rank) * Plan::kBNc;
       for (int kb = 0; kb < p.num_kb; ++kb) {
-        if (!mbar_wait_spin(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns, kRoleProducer, &g_device_error,
-                            4096)) {
-          ok = false;
-          break;
+        ok = __all_sync(0xffffffffu, mbar_wait_spin(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns,
+                                                    kRoleProducer, &g_device_error, 4096));
+        if (!ok) break;
+        if (elect_one()) {
+          uint32_t bar;
+          if constexpr (CG == 1) {
+            bar = full_bar(stage);
+            mbar_arrive_expect_tx(bar, Plan::kStageBytes);
+          } else {
+            if (leader) mbar_arrive_expect_tx(full_bar(stage), 2 * Plan::kStageBytes);
+            bar = mapa_shared(full_bar(stage), 0);
+          }
+          auto load = [&](uint32_t dst, const CUtensorMap *tm, int32_t x, int32_t y) {
+            if constexpr (CG == 1)
+              tma_load_2d(dst, tm, bar, x, y);
+            else
+              tma_load_2d_pair(dst, tm, bar, x, y);
+          };
+          load(a_slot(stage), &tmA, kb * 128, a_row);
+          load(b_slot(stage), &tmB, kb * 128, b_row);
+          load(sfa_slot(stage), &tmSA, kb * 256, a_row / 128);  // 256 words: two scale tiles
+          load(sfa_slot(stage) + Plan::kSfaBytes, &tmSB, kb * 256, nb * BN / 128);
         }
-        uint32_t bar;
-        if constexpr (CG == 1) {
-          bar = full_bar(stage);
-          mbar_arrive_expect_tx(bar, Plan::kStageBytes);
-        } else {
-          if (leader) mbar_arrive_expect_tx(full_bar(stage), 2 * Plan::kStageBytes);
-          bar = mapa_shared(full_bar(stage), 0);
-        }
-        auto load = [&](uint32_t dst, const CUtensorMap *tm, int32_t x, int32_t y) {
-          if constexpr (CG == 1)
-            tma_load_2d(dst, tm, bar, x, y);
-          else
-            tma_load_2d_pair(dst, tm, bar, x, y);
-        };
-        load(a_slot(stage), &tmA, kb * 128, a_row);
-        load(b_slot(stage), &tmB, kb * 128, b_row);
-        load(sfa_slot(stage), &tmSA, kb * 256, a_row / 128);  // 256 words: two scale tiles
-        load(sfa_slot(stage) + Plan::kSfaBytes, &tmSB, kb * 256, nb * BN / 128);
+        __syncwarp();
         issued_mask |= 1u << stage;
         issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == STAGES) {
@@ -305,11 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok) {
       // Wait until every slot has been released: no commit-arrive is still on its way.
-      for (int i = 0; i < STAGES; ++i) {
-        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns, kRoleProducer, &g_device_error)) {
-          ok = false;
-          break;
-        }
+      for (int i = 0; i < STAGES && ok; ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns, kRoleProducer,
+                                               &g_device_error));
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -322,75 +340,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (issued_mask & (1u << s))
           mbar_wait(full_bar(s), (issued_parity >> s) & 1u, nullptr, p.limit_ns, kRoleProducer, &g_device_error);
     }
-  } else if (warp == 1 && lane == 0 && leader) {
+  } else if (warp == 1 && leader) {
     // ---------------------------------------------------------------- MMA issuer (leader CTA)
     constexpr uint32_t idesc[2] = {make_idesc_mxf4(kTileM, BN, 0), make_idesc_mxf4(kTileM, BN, 2)};
     int stage = 0;
     uint32_t phase = 0;
     int acc = 0;
-    uint32_t acc_phase = 0;
+    uint32_t j = 0;  // tiles done
     bool ok = true;
-    for (int t = unit; t < tiles && ok; t += num_units) {
+    for (int t = unit; t < tiles && ok; t += num_units, ++j) {
       int mb, nb;
       tile_coords(t, num_m, num_n, p.raster_group, mb, nb);
       const uint32_t skip = static_cast<uint32_t>((nb * BN) % 128 / 32);
-      if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.limit_ns, kRoleMma, &g_device_error)) {
-        ok = false;
-        break;
-      }
+      // Two accumulators apart: each waits for its own last drain.  Overlapping ones: tile j
+      // waits for the shared columns of tile j - 1, and so for everything before them.
+      ok = __all_sync(0xffffffffu, mbar_wait(tempty_bar(j % Plan::kAccBars), ((j / Plan::kAccBars) & 1u) ^ 1u,
+                                             abort_flag, p.limit_ns, kRoleMma, &g_device_error));
+      if (!ok) break;
       tc_fence_after_sync();
-      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * Plan::kAccStride);
       for (int kb = 0; kb < p.num_kb; ++kb) {
-        if (!mbar_wait_spin(full_bar(stage), phase, abort_flag, p.limit_ns, kRoleMma, &g_device_error, 4096)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait_spin(full_bar(stage), phase, abort_flag, p.limit_ns, kRoleMma,
+                                                    &g_device_error, 4096));
+        if (!ok) break;
         tc_fence_after_sync();
-        const uint32_t sfa = tmem_base + static_cast<uint32_t>(Plan::kSf0 + stage * Plan::kSfCols);
-        const uint32_t sfb = sfa + 8;
-        const uint64_t sf_desc = smem_desc_plain(sfa_slot(stage));
+        if (elect_one()) {
+          const uint32_t sfa = tmem_base + static_cast<uint32_t>(Plan::kSf0 + stage * Plan::kSfCols);
+          const uint32_t sfb = sfa + 8;
+          const uint64_t sf_desc = smem_desc_plain(sfa_slot(stage));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // the two scale tiles (128 k each)
-          tmem_copy_scales<CG>(sfa + 4 * h, sf_desc + h * (kSfTileBytes / 16));
+          for (int h = 0; h < 2; ++h) {  // the two scale tiles (128 k each)
+            tmem_copy_scales<CG>(sfa + 4 * h, sf_desc + h * (kSfTileBytes / 16));
 #pragma unroll
-          for (int g = 0; g < G; ++g)
-            tmem_copy_scales<CG>(sfb + 4 * (h * G + g),
-                                 sf_desc + (Plan::kSfaBytes + (g * 2 + h) * kSfTileBytes) / 16);
+            for (int g = 0; g < G; ++g)
+              tmem_copy_scales<CG>(sfb + 4 * (h * G + g),
+                                   sf_desc + (Plan::kSfaBytes + (g * 2 + h) * kSfTileBytes) / 16);
+          }
+          const uint64_t ad = smem_desc_sw128(a_slot(stage), 16, 1024);
+          const uint64_t bd = smem_desc_sw128(b_slot(stage), 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 64 k: 32 bytes along the swizzled row
+            mma_mxf4_ss<CG>(d_tmem, ad + kk * 2, bd + kk * 2, idesc[kk & 1], sfa + 4 * (kk >> 1),
+                            sfb + 4 * G * (kk >> 1) + skip, (kb > 0 || kk > 0) ? 1u : 0u);
+          mma_commit<CG>(empty_bar(stage));
         }
-        const uint64_t ad = smem_desc_sw128(a_slot(stage), 16, 1024);
-        const uint64_t bd = smem_desc_sw128(b_slot(stage), 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // 64 k: 32 bytes along the swizzled row
-          mma_mxf4_ss<CG>(d_tmem, ad + kk * 2, bd + kk * 2, idesc[kk & 1], sfa + 4 * (kk >> 1),
-                          sfb + 4 * G * (kk >> 1) + skip, (kb > 0 || kk > 0) ? 1u : 0u);
-        mma_commit<CG>(empty_bar(stage));
+        __syncwarp();
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
         }
       }
       if (!ok) break;
-      mma_commit<CG>(tfull_bar(acc));
+      if (elect_one()) mma_commit<CG>(tfull_bar(j % Plan::kAccBars));
+      __syncwarp();
       acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
     }
     if (!ok) {
-      mma_commit_local<CG>(drain_bar);
+      if (elect_one()) mma_commit_local<CG>(drain_bar);
+      __syncwarp();
       mbar_wait(drain_bar, 0, nullptr, p.limit_ns, kRoleMma, &g_device_error);
     }
   } else if (warp >= 2) {
     // ---------------------------------------------------------------- epilogue (every CTA)
-    // Warp w drains TMEM lanes 32*(w%4) .. +31, 64 columns at a time, into two 4 KB boxes.
+    // Warp w drains TMEM lanes 32*(w%4) .. +31, 64 columns at a time, by way of a 4 KB box.  The
+    // two warps of a quarter take its pieces in turn.
     const int quarter = warp & 3;
     const int ew = warp - 2;
-    const uint32_t box0 = s0 + Plan::kOutOffset + static_cast<uint32_t>(ew * 2) * kStageOutBytes;
+    const int side = ew >> 2;
+    constexpr int kPieces = BN / 64;
+    const uint32_t box = s0 + Plan::kOutOffset + static_cast<uint32_t>(ew) * kStageOutBytes;
     const uint32_t release_bar0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
     constexpr int kBoxCols = OUT == kTypeF32 ? 32 : 64;
     int acc = 0;
-    uint32_t acc_phase = 0, boxes_used = 0;
     int bias_buf = 0;
+    uint32_t j = 0;
     const uint64_t tile_limit_ns = p.limit_ns + static_cast<uint64_t>(p.num_kb) * kWaitPerKBlockNs;
-    for (int t = unit; t < tiles; t += num_units) {
+    for (int t = unit; t < tiles; t += num_units, ++j) {
       int mb, nb;
       tile_coords(t, num_m, num_n, p.raster_group, mb, nb);
       const int row0 = mb * kTileM + static_cast<int>(rank) * kBM + quarter * 32;
@@ -400,45 +425,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The tile's bias in fp32, in the buffer of the tile before last (whose readers have
         // passed the barrier of the last tile).
         float *sb = reinterpret_cast<float *>(smem + Plan::kBiasOffset) + bias_buf * BN;
-        for (int c = ew * 32 + lane; c < BN; c += 32 * kEpiWarps) {
+        for (int c = ew * 32 + lane; c < BN; c += 32 * kMxEpiWarps) {
           const int col = nb * BN + c;
           sb[c] = col < p.N ? load_elem<kBiasType<OUT>>(p.bias, col) : 0.0f;
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kMxEpiWarps) : "memory");
         bias_buf ^= 1;
       }
       // On a timeout the warp stops reading tiles but keeps meeting the bias barrier, so no
       // other epilogue warp waits at it for good.
       bool ok = *abort_flag == 0u;
-      if (ok && !mbar_wait(tfull_bar(acc), acc_phase, abort_flag, tile_limit_ns, kRoleEpilogue, &g_device_error))
+      if (ok && !mbar_wait(tfull_bar(j % Plan::kAccBars), (j / Plan::kAccBars) & 1u, abort_flag, tile_limit_ns,
+                           kRoleEpilogue, &g_device_error))
         ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         tc_fence_after_sync();
+        auto release = [&]() {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CG == 2)
+              mbar_arrive_cluster(release_bar0 + 8u * (j % Plan::kAccBars));
+            else
+              mbar_arrive(release_bar0 + 8u * (j % Plan::kAccBars));
+          }
+        };
+        if (side >= kPieces) release();
 #pragma unroll 1
-        for (int tc = 0; tc < BN; tc += 64) {
+        for (int i = side; i < kPieces; i += 2) {
+          // Overlapping accumulators: the shared columns (the upper half of accumulator 0, the
+          // lower of accumulator 1) first.
+          const int tc = 64 * (Plan::kOverlap && acc == 0 ? (i + 2) % 4 : i);
           const int col0 = nb * BN + tc;
           uint32_t ra[32], rb[32];
           __syncwarp();
           tmem_load_2x32cols(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                 static_cast<uint32_t>(acc * BN + tc),
+                                 static_cast<uint32_t>(acc * Plan::kAccStride + tc),
                              ra, rb);
-          if (tc + 64 >= BN) {
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (CG == 2)
-                mbar_arrive_cluster(release_bar0 + 8u * acc);
-              else
-                mbar_arrive(release_bar0 + 8u * acc);
-            }
-          }
+          if (Plan::kOverlap ? i < 2 : i + 2 >= kPieces) release();
           if (row0 >= p.M || col0 >= p.N) continue;
           float va[32], vb[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            va[j] = __uint_as_float(ra[j]);
-            vb[j] = __uint_as_float(rb[j]);
+          for (int c = 0; c < 32; ++c) {
+            va[c] = __uint_as_float(ra[c]);
+            vb[c] = __uint_as_float(rb[c]);
           }
           auto finish = [&](float(&v)[32], int half) {
             if constexpr (EPI) {
@@ -452,8 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mx_store_row<OUT>(p, row, col, w);
               return;
             }
-            const uint32_t box = box0 + (boxes_used & 1u) * kStageOutBytes;
-            if (lane == 0) bulk_wait_group_read<1>();
+            if (lane == 0) bulk_wait_group_read<0>();  // this box's previous store has read it
             __syncwarp();
             st_box_row(box, lane, w, 0);
             fence_proxy_async_shared();
@@ -462,7 +492,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_store_2d(&tmC, box, col, row0);
               bulk_commit_group();
             }
-            ++boxes_used;
           };
           if constexpr (OUT == kTypeF32) {
             uint32_t w[32];
@@ -489,7 +518,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
     }
     if (lane == 0) bulk_wait_group<0>();
     __syncwarp();
