@@ -1,7 +1,7 @@
 // Microscaled (MX) elementwise operators: quantisation of a matrix or its transpose,
 // dequantisation, the activation that saves its input in 8 bits and the backward pass that
 // reads it.  All of them are bound by HBM traffic: every kernel reads each input byte once
-// and writes each output byte once, 16 or 32 bytes a lane.
+// and writes each output byte once, 16 bytes a lane where rows are aligned.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -25,121 +25,107 @@ static_assert(kE2M1 == TLG_MX_E2M1 && kE4M3 == TLG_MX_E4M3,
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 
-// A lane holds 32 bytes of a row: E elements; a warp 32 * E of them (a chunk: 512 columns of
-// a 16-bit type, 256 of fp32, so whole groups of four blocks).
+// A lane holds 16 bytes of a row: E elements; a warp 32 * E of them (a chunk: 256 columns of
+// a 16-bit type, 128 of fp32, so whole groups of four blocks).  16 bytes, not 32: a warp's
+// store then covers 512 consecutive bytes, where two stores of 16 bytes 32 apart would each
+// fill half of every sector (8192 x 8192 E2M1 to bf16: 53 us with 32 bytes a lane).
 template <int T>
-constexpr int kLaneElems = T == kTypeF32 ? 8 : 16;
+constexpr int kLaneElems = 16 / kTypeBytes<T>;
 
-// One matrix of a row kernel: base, row stride in elements, and whether rows may be accessed
-// 16 bytes at a time.
+// One matrix of a row kernel: base and row stride in elements.  Kernels are built with VEC (every
+// matrix of the call has a base and row stride that are multiples of 16 bytes) and without.
 struct RowMat {
   const void *p;
   int64_t ld;
-  int vec;
 };
 
-// Elements [c0, c0 + 32 E) of a row, E to a lane; zeros from column `cols` on.  Rows whose
-// address is not a multiple of 16 bytes are read element by element, neighbouring lanes on
-// neighbouring elements, and rearranged through `stage` (1 KB per warp).
-template <int T>
-__device__ __forceinline__ void load_lane(const RowMat &m, int64_t row, int64_t c0, int64_t cols,
-                                          int lane, uint32_t *stage, uint32_t (&w)[8]) {
+// Elements [c0, c0 + 32 E) of a row, E to a lane; zeros from column `cols` on.  Without VEC they
+// are read element by element, neighbouring lanes on neighbouring elements (lane l: elements l,
+// l + 32, ...); finish_load rearranges them.
+// FULL: the whole piece lies before `cols`.
+template <int T, bool VEC, bool FULL>
+__device__ __forceinline__ void issue_load(const char *base, int left, int lane, uint32_t (&w)[4]) {
   constexpr int E = kLaneElems<T>;
-  constexpr int B = kTypeBytes<T>;
-  const char *base = static_cast<const char *>(m.p) + (row * m.ld + c0) * B;
-  const int64_t left = cols - c0;  // > 0
-  if (m.vec) {
-    const int at = lane * E;
-    if (at + E <= left) {
-      const uint4 *q = reinterpret_cast<const uint4 *>(base + lane * 32);
-      const uint4 a = q[0], b = q[1];
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-      return;
-    }
-    const int n = static_cast<int>(max(left - at, int64_t(0)));
-    if constexpr (T == kTypeF32) {
-      const uint32_t *q = reinterpret_cast<const uint32_t *>(base) + at;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = j < n ? q[j] : 0u;
-    } else {
-      const unsigned short *q = reinterpret_cast<const unsigned short *>(base) + at;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t lo = 2 * j < n ? q[2 * j] : 0u;
-        const uint32_t hi = 2 * j + 1 < n ? q[2 * j + 1] : 0u;
-        w[j] = lo | (hi << 16);
-      }
-    }
+  if (VEC && (FULL || (lane + 1) * E <= left)) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(base + lane * 16);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
     return;
   }
-  __syncwarp();
+  const int first = VEC ? lane * E : lane;
+  constexpr int step = VEC ? 1 : 32;
   if constexpr (T == kTypeF32) {
     const uint32_t *q = reinterpret_cast<const uint32_t *>(base);
-    uint32_t x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i * 32 + lane < left ? q[i * 32 + lane] : 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) stage[i * 32 + lane] = x[i];
+    for (int j = 0; j < 4; ++j) w[j] = FULL || first + j * step < left ? q[first + j * step] : 0u;
   } else {
     const unsigned short *q = reinterpret_cast<const unsigned short *>(base);
-    unsigned short x[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = i * 32 + lane < left ? q[i * 32 + lane] : (unsigned short)0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) reinterpret_cast<unsigned short *>(stage)[i * 32 + lane] = x[i];
+    for (int j = 0; j < 4; ++j) {
+      const int c = first + 2 * j * step;
+      const uint32_t lo = FULL || c < left ? q[c] : 0u;
+      const uint32_t hi = FULL || c + step < left ? q[c + step] : 0u;
+      w[j] = lo | (hi << 16);
+    }
   }
-  __syncwarp();
-  const uint4 a = reinterpret_cast<const uint4 *>(stage)[lane * 2];
-  const uint4 b = reinterpret_cast<const uint4 *>(stage)[lane * 2 + 1];
-  w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-  w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
-// The reverse of load_lane: columns from `cols` on are not written.
-template <int T>
-__device__ __forceinline__ void store_lane(const RowMat &m, int64_t row, int64_t c0, int64_t cols,
-                                           int lane, uint32_t *stage, const uint32_t (&w)[8]) {
-  constexpr int E = kLaneElems<T>;
-  constexpr int B = kTypeBytes<T>;
-  char *base = static_cast<char *>(const_cast<void *>(m.p)) + (row * m.ld + c0) * B;
-  const int64_t left = cols - c0;
-  if (m.vec) {
-    const int at = lane * E;
-    if (at + E <= left) {
-      uint4 *q = reinterpret_cast<uint4 *>(base + lane * 32);
-      q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      q[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      return;
-    }
-    const int n = static_cast<int>(max(left - at, int64_t(0)));
+// `stage`: 512 bytes of shared memory per warp.
+template <int T, bool VEC>
+__device__ __forceinline__ void finish_load(int lane, uint32_t *stage, uint32_t (&w)[4]) {
+  if constexpr (!VEC) {
+    __syncwarp();
     if constexpr (T == kTypeF32) {
-      uint32_t *q = reinterpret_cast<uint32_t *>(base) + at;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) q[j] = w[j];
+      for (int j = 0; j < 4; ++j) stage[j * 32 + lane] = w[j];
     } else {
-      unsigned short *q = reinterpret_cast<unsigned short *>(base) + at;
+      unsigned short *h = reinterpret_cast<unsigned short *>(stage);
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (j < n) q[j] = static_cast<unsigned short>(w[j / 2] >> (16 * (j & 1)));
+      for (int j = 0; j < 4; ++j) {
+        h[2 * j * 32 + lane] = static_cast<unsigned short>(w[j]);
+        h[(2 * j + 1) * 32 + lane] = static_cast<unsigned short>(w[j] >> 16);
+      }
     }
+    __syncwarp();
+    const uint4 a = reinterpret_cast<const uint4 *>(stage)[lane];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+  }
+}
+
+// The reverse: columns from `left` on are not written.
+template <int T, bool VEC, bool FULL>
+__device__ __forceinline__ void store_lane(char *base, int left, int lane, uint32_t *stage, const uint32_t (&w)[4]) {
+  constexpr int E = kLaneElems<T>;
+  if (VEC && (FULL || (lane + 1) * E <= left)) {
+    *reinterpret_cast<uint4 *>(base + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     return;
   }
-  __syncwarp();
-  reinterpret_cast<uint4 *>(stage)[lane * 2] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4 *>(stage)[lane * 2 + 1] = make_uint4(w[4], w[5], w[6], w[7]);
-  __syncwarp();
+  uint32_t x[4] = {w[0], w[1], w[2], w[3]};
+  if constexpr (!VEC) {
+    __syncwarp();
+    reinterpret_cast<uint4 *>(stage)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (T == kTypeF32) {
+        x[j] = stage[j * 32 + lane];
+      } else {
+        const unsigned short *h = reinterpret_cast<const unsigned short *>(stage);
+        x[j] = h[2 * j * 32 + lane] | (static_cast<uint32_t>(h[(2 * j + 1) * 32 + lane]) << 16);
+      }
+    }
+  }
+  const int first = VEC ? lane * E : lane;
+  constexpr int step = VEC ? 1 : 32;
   if constexpr (T == kTypeF32) {
     uint32_t *q = reinterpret_cast<uint32_t *>(base);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i * 32 + lane < left) q[i * 32 + lane] = stage[i * 32 + lane];
+    for (int j = 0; j < 4; ++j)
+      if (FULL || first + j * step < left) q[first + j * step] = x[j];
   } else {
     unsigned short *q = reinterpret_cast<unsigned short *>(base);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i * 32 + lane < left) q[i * 32 + lane] = reinterpret_cast<const unsigned short *>(stage)[i * 32 + lane];
+    for (int j = 0; j < 8; ++j)
+      if (FULL || first + j * step < left) q[first + j * step] = static_cast<unsigned short>(x[j / 2] >> (16 * (j & 1)));
   }
 }
 
@@ -155,132 +141,191 @@ struct MxMat {
 
 template <int FMT, int E>
 __device__ __forceinline__ void load_q(const uint8_t *p, uint32_t (&q)[kQWords<FMT, E>]) {
-  constexpr int N = kQWords<FMT, E>;
-  if constexpr (N == 4) {
-    const uint4 x = *reinterpret_cast<const uint4 *>(p);
-    q[0] = x.x; q[1] = x.y; q[2] = x.z; q[3] = x.w;
-  } else if constexpr (N == 2) {
+  constexpr int N = kQBytes<FMT, E>;
+  if constexpr (N == 8) {
     const uint2 x = *reinterpret_cast<const uint2 *>(p);
     q[0] = x.x; q[1] = x.y;
-  } else {
+  } else if constexpr (N == 4) {
     q[0] = *reinterpret_cast<const uint32_t *>(p);
+  } else {
+    q[0] = *reinterpret_cast<const uint16_t *>(p);
   }
 }
 
 template <int FMT, int E>
 __device__ __forceinline__ void store_q(uint8_t *p, const uint32_t (&q)[kQWords<FMT, E>]) {
-  constexpr int N = kQWords<FMT, E>;
-  if constexpr (N == 4)
-    *reinterpret_cast<uint4 *>(p) = make_uint4(q[0], q[1], q[2], q[3]);
-  else if constexpr (N == 2)
+  constexpr int N = kQBytes<FMT, E>;
+  if constexpr (N == 8)
     *reinterpret_cast<uint2 *>(p) = make_uint2(q[0], q[1]);
-  else
+  else if constexpr (N == 4)
     *reinterpret_cast<uint32_t *>(p) = q[0];
+  else
+    *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(q[0]);
 }
 
-// Quantises a lane's elements (w as stored, v their values) and writes elements and scale.
-// The lanes of a block (2 of 16-bit elements, 4 of fp32) agree on its largest magnitude by
-// shuffles.
-template <int T, int FMT>
-__device__ __forceinline__ void quantize_lane(const MxMat &o, int64_t row, int64_t c0, int lane,
-                                              const uint32_t (&w)[8],
-                                              const float (&v)[kLaneElems<T>]) {
-  constexpr int E = kLaneElems<T>;
-  constexpr int kLanesPerBlock = kMxBlock / E;
-  uint32_t m = amax_bits<T, 8>(w);
-#pragma unroll
-  for (int d = 1; d < kLanesPerBlock; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-  const uint32_t byte = scale_byte<FMT>(m);
+// A lane's elements of one row of an MX matrix and their scale byte; zeros past the last block.
+template <int FMT, int E>
+struct MxLane {
   uint32_t q[kQWords<FMT, E>];
-  encode<FMT, E>(v, inverse_scale(byte), q);
-  const int block = static_cast<int>(c0 / kMxBlock) + lane / kLanesPerBlock;
-  if (block < o.blocks) {
-    uint8_t *dst = const_cast<uint8_t *>(o.q) + row * o.ldq +
-                   static_cast<int64_t>(block) * kBlockBytes<FMT> + (lane % kLanesPerBlock) * kQWords<FMT, E> * 4;
-    store_q<FMT, E>(dst, q);
+  uint32_t byte;
+};
+
+// q: the lane's element bytes; s: its scale byte (read only where `in` holds).
+template <int FMT, int E>
+__device__ __forceinline__ void issue_load_mx(const uint8_t *q, const uint8_t *s, bool in, MxLane<FMT, E> &x) {
+#pragma unroll
+  for (int j = 0; j < kQWords<FMT, E>; ++j) x.q[j] = 0;
+  x.byte = 0;
+  if (in) {
+    load_q<FMT, E>(q, x.q);
+    x.byte = *s;
   }
-  // blocks past the last one, up to a whole group of four, hold no elements: their scale is 0
-  if (lane % kLanesPerBlock == 0 && (block >> 2) < o.tiles_x)
-    const_cast<uint8_t *>(o.s)[scale_offset(row, block, o.tiles_x)] = static_cast<uint8_t>(byte);
 }
 
-// Rows x chunks of a matrix walked by warps, `step` apart, without a division per item.
-struct ChunkIter {
-  int64_t row;
-  int chunk;
-  int64_t step_rows;
-  int step_chunks, chunks;
-  __device__ __forceinline__ ChunkIter(int64_t at, int64_t step, int chunks_) : chunks(chunks_) {
-    row = at / chunks_;
-    chunk = static_cast<int>(at - row * chunks_);
-    step_rows = step / chunks_;
-    step_chunks = static_cast<int>(step - step_rows * chunks_);
+// The row kernels: a CTA owns a stripe of U * 32 * E columns (U pieces of 32 * E) and the rows
+// [blockIdx.y * rows_per, +rows_per); its warps take the rows in turn.  Of one row a warp loads
+// all U pieces before it works on the first (16 * U bytes a lane in flight); with the columns
+// fixed, each row costs a few pointer steps, and the pieces of a row are constant distances
+// apart in every matrix.  (An item-at-a-time walk over rows and pieces spent 13 instructions an
+// element on quantising, most of them on addresses.)
+template <int T, int U>
+struct Stripe {
+  static constexpr int E = kLaneElems<T>;
+  static constexpr int kPiece = 32 * E;              // columns of a piece
+  static constexpr int kPieceScales = kPiece / kMxBlock / 4 * 512;  // bytes between two pieces' scales
+  uint32_t c0;    // first column
+  int left;       // columns from c0 on
+  int block;      // this lane's block in piece 0
+  uint32_t r0, r1;
+  __device__ __forceinline__ Stripe(uint32_t rows, uint32_t cols, uint32_t rows_per, int lane) {
+    c0 = blockIdx.x * (kPiece * U);
+    left = static_cast<int>(min(cols - c0, uint32_t(kPiece * U)));
+    block = static_cast<int>(c0 / kMxBlock) + lane * E / kMxBlock;
+    r0 = blockIdx.y * rows_per;
+    r1 = min(rows, r0 + rows_per);
   }
-  __device__ __forceinline__ void next() {
-    row += step_rows;
-    chunk += step_chunks;
-    if (chunk >= chunks) {
-      chunk -= chunks;
-      ++row;
-    }
+  // Bytes of this lane's elements in a row of an ordinary matrix / of an MX matrix.
+  __device__ __forceinline__ int64_t at(int lane, bool vec) const {
+    return static_cast<int64_t>(c0) * kTypeBytes<T> + (vec ? lane * 16 : 0);
+  }
+  template <int FMT>
+  __device__ __forceinline__ int64_t q_at(int lane) const {
+    return static_cast<int64_t>(c0 / E) * kQBytes<FMT, E> + lane * kQBytes<FMT, E>;
   }
 };
 
-// Quantises X row by row; with ACT also writes Y = act(X).
-template <int T, int FMT, bool ACT>
-__global__ void __launch_bounds__(kRowThreads)
-    quantize_rows_kernel(const RowMat x, const MxMat o, const RowMat y, int act, int64_t rows,
-                         int64_t cols, int chunks) {
-  constexpr int E = kLaneElems<T>;
-  __shared__ __align__(16) uint32_t stage[kRowWarps][256];
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kRowWarps;
-  for (ChunkIter it(static_cast<int64_t>(blockIdx.x) * kRowWarps + warp, nwarps, chunks);
-       it.row < rows; it.next()) {
-    const int64_t c0 = static_cast<int64_t>(it.chunk) * (32 * E);
-    uint32_t w[8];
-    float v[E];
-    load_lane<T>(x, it.row, c0, cols, lane, stage[warp], w);
-    to_floats<T, E>(w, v);
-    quantize_lane<T, FMT>(o, it.row, c0, lane, w, v);
-    if constexpr (ACT) {
-      activate_lane<T, E>(act, v);
-      from_floats<T, E>(v, w);
-      store_lane<T>(y, it.row, c0, cols, lane, stage[warp], w);
-    }
-  }
+// Scale offset of (row, block 0 of its tile row), the part that depends on the row.
+__device__ __forceinline__ int64_t scale_row(uint32_t row, int64_t tile_row_bytes) {
+  return (row >> 7) * tile_row_bytes + ((row & 31) * 16 + ((row >> 5) & 3) * 4);
 }
 
-template <int T, int FMT>
-__global__ void __launch_bounds__(kRowThreads)
-    dequantize_rows_kernel(const MxMat in, const RowMat x, int64_t rows, int64_t cols, int chunks) {
-  constexpr int E = kLaneElems<T>;
+// Quantises X row by row; with ACT also writes Y = act(X).  The lanes of a block (4 of 16-bit
+// elements, 8 of fp32) agree on its largest magnitude by shuffles.
+template <int T, int FMT, bool ACT, bool VEC, int U>
+__global__ void __launch_bounds__(kRowThreads, 4)
+    quantize_rows_kernel(const RowMat x, const MxMat o, const RowMat y, int act, uint32_t rows,
+                         uint32_t cols, uint32_t rows_per) {
+  using St = Stripe<T, U>;
+  constexpr int E = St::E, B = kTypeBytes<T>;
   constexpr int kLanesPerBlock = kMxBlock / E;
-  __shared__ __align__(16) uint32_t stage[kRowWarps][256];
+  __shared__ __align__(16) uint32_t stage[VEC ? 1 : kRowWarps][128];
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kRowWarps;
-  for (ChunkIter it(static_cast<int64_t>(blockIdx.x) * kRowWarps + warp, nwarps, chunks);
-       it.row < rows; it.next()) {
-    const int64_t c0 = static_cast<int64_t>(it.chunk) * (32 * E);
-    const int block = static_cast<int>(c0 / kMxBlock) + lane / kLanesPerBlock;
-    uint32_t q[kQWords<FMT, E>] = {};
-    uint32_t byte = 0;
-    if (block < in.blocks) {
-      load_q<FMT, E>(in.q + it.row * in.ldq + static_cast<int64_t>(block) * kBlockBytes<FMT> +
-                         (lane % kLanesPerBlock) * kQWords<FMT, E> * 4,
-                     q);
-      byte = in.s[scale_offset(it.row, block, in.tiles_x)];
+  uint32_t *st = stage[VEC ? 0 : warp];
+  const St s(rows, cols, rows_per, lane);
+  const int64_t tile_row = o.tiles_x * 512;
+  const char *src = static_cast<const char *>(x.p) + static_cast<int64_t>(s.r0 + warp) * x.ld * B + s.at(0, false);
+  char *dst = static_cast<char *>(const_cast<void *>(y.p)) + static_cast<int64_t>(s.r0 + warp) * y.ld * B + s.at(0, false);
+  uint8_t *oq = const_cast<uint8_t *>(o.q) + static_cast<int64_t>(s.r0 + warp) * o.ldq + s.template q_at<FMT>(lane);
+  uint8_t *os = const_cast<uint8_t *>(o.s) + scale_offset(0, s.block, o.tiles_x);
+  // Whole stripes (all but the last) need no column checks.
+  auto run = [&](auto full) {
+    constexpr bool kFull = decltype(full)::value;
+    for (uint32_t r = s.r0 + warp; r < s.r1; r += kRowWarps) {
+      uint32_t w[U][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (kFull || u * St::kPiece < s.left) issue_load<T, VEC, kFull>(src + u * (St::kPiece * B), s.left - u * St::kPiece, lane, w[u]);
+      const int64_t sr = scale_row(r, tile_row);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (kFull || u * St::kPiece < s.left) {
+          float v[E];
+          finish_load<T, VEC>(lane, st, w[u]);
+          to_floats<T, E>(w[u], v);
+          uint32_t m = amax_bits<T, 4>(w[u]);
+#pragma unroll
+          for (int d = 1; d < kLanesPerBlock; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+          const uint32_t byte = scale_byte<FMT>(m);
+          uint32_t q[kQWords<FMT, E>];
+          encode<FMT, E>(v, inverse_scale(byte), q);
+          const int block = s.block + u * (St::kPiece / kMxBlock);
+          if (kFull || block < o.blocks) store_q<FMT, E>(oq + u * (32 * kQBytes<FMT, E>), q);
+          // blocks past the last one, up to a whole group of four, hold no elements: their scale is 0
+          if (lane % kLanesPerBlock == 0 && (kFull || (block >> 2) < o.tiles_x))
+            os[sr + u * St::kPieceScales] = static_cast<uint8_t>(byte);
+          if constexpr (ACT) {
+            activate_lane<T, E>(act, v);
+            from_floats<T, E>(v, w[u]);
+            store_lane<T, VEC, kFull>(dst + u * (St::kPiece * B), s.left - u * St::kPiece, lane, st, w[u]);
+          }
+        }
+      }
+      src += kRowWarps * x.ld * B;
+      oq += kRowWarps * o.ldq;
+      if constexpr (ACT) dst += kRowWarps * y.ld * B;
     }
-    float v[E];
-    decode<FMT, E>(q, scale_value(byte), v);
-    uint32_t w[8];
-    from_floats<T, E>(v, w);
-    store_lane<T>(x, it.row, c0, cols, lane, stage[warp], w);
-  }
+  };
+  if (s.left == St::kPiece * U)
+    run(std::true_type());
+  else
+    run(std::false_type());
+}
+
+template <int T, int FMT, bool VEC, int U>
+__global__ void __launch_bounds__(kRowThreads, 4)
+    dequantize_rows_kernel(const MxMat in, const RowMat x, uint32_t rows, uint32_t cols, uint32_t rows_per) {
+  using St = Stripe<T, U>;
+  constexpr int E = St::E, B = kTypeBytes<T>;
+  __shared__ __align__(16) uint32_t stage[VEC ? 1 : kRowWarps][128];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t *st = stage[VEC ? 0 : warp];
+  const St s(rows, cols, rows_per, lane);
+  const int64_t tile_row = in.tiles_x * 512;
+  char *dst = static_cast<char *>(const_cast<void *>(x.p)) + static_cast<int64_t>(s.r0 + warp) * x.ld * B + s.at(0, false);
+  const uint8_t *iq = in.q + static_cast<int64_t>(s.r0 + warp) * in.ldq + s.template q_at<FMT>(lane);
+  const uint8_t *is = in.s + scale_offset(0, s.block, in.tiles_x);
+  // Whole stripes (all but the last) need no column checks.
+  auto run = [&](auto full) {
+    constexpr bool kFull = decltype(full)::value;
+    for (uint32_t r = s.r0 + warp; r < s.r1; r += kRowWarps) {
+      MxLane<FMT, E> q[U];
+      const int64_t sr = scale_row(r, tile_row);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        issue_load_mx<FMT, E>(iq + u * (32 * kQBytes<FMT, E>), is + sr + u * St::kPieceScales,
+                              kFull || s.block + u * (St::kPiece / kMxBlock) < in.blocks, q[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (kFull || u * St::kPiece < s.left) {
+          float v[E];
+          uint32_t w[4];
+          decode<FMT, E>(q[u].q, scale_value(q[u].byte), v);
+          from_floats<T, E>(v, w);
+          store_lane<T, VEC, kFull>(dst + u * (St::kPiece * B), s.left - u * St::kPiece, lane, st, w);
+        }
+      }
+      dst += kRowWarps * x.ld * B;
+      iq += kRowWarps * in.ldq;
+    }
+  };
+  if (s.left == St::kPiece * U)
+    run(std::true_type());
+  else
+    run(std::false_type());
 }
 
 // ------------------------------------------------------------------ transposed quantisation
@@ -311,23 +356,23 @@ __global__ void __launch_bounds__(T == kTypeF32 ? 512 : 256)
     const int64_t tr = t % tiles_r, tc = t / tiles_r;
     const int64_t n0 = tr * 128 + n_in, k0 = tc * 128 + blk * 32;
     uint32_t w[32];
-    if constexpr (T == kTypeF32) {
+    if ((T == kTypeF32 || pair_aligned) && tr * 128 + 128 <= rows && tc * 128 + 128 <= cols) {
+      // A whole tile: no element is checked.
+      const char *src = static_cast<const char *>(X) + (k0 * ldx + n0) * kTypeBytes<T>;
+      const int64_t step = ldx * kTypeBytes<T>;
+#pragma unroll
+      for (int k = 0; k < 32; ++k, src += step) w[k] = *reinterpret_cast<const uint32_t *>(src);
+    } else if constexpr (T == kTypeF32) {
       const uint32_t *src = static_cast<const uint32_t *>(X) + k0 * ldx + n0;
 #pragma unroll
       for (int k = 0; k < 32; ++k) w[k] = n0 < rows && k0 + k < cols ? src[k * ldx] : 0u;
     } else {
       const unsigned short *src = static_cast<const unsigned short *>(X) + k0 * ldx + n0;
-      if (pair_aligned && n0 + 1 < rows) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          w[k] = k0 + k < cols ? *reinterpret_cast<const uint32_t *>(src + k * ldx) : 0u;
-      } else {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const uint32_t lo = n0 < rows && k0 + k < cols ? src[k * ldx] : 0u;
-          const uint32_t hi = n0 + 1 < rows && k0 + k < cols ? src[k * ldx + 1] : 0u;
-          w[k] = lo | (hi << 16);
-        }
+      for (int k = 0; k < 32; ++k) {
+        const uint32_t lo = n0 < rows && k0 + k < cols ? src[k * ldx] : 0u;
+        const uint32_t hi = n0 + 1 < rows && k0 + k < cols ? src[k * ldx + 1] : 0u;
+        w[k] = lo | (hi << 16);
       }
     }
 #pragma unroll
@@ -380,82 +425,195 @@ __global__ void __launch_bounds__(T == kTypeF32 ? 512 : 256)
 
 // ------------------------------------------------------------------ backward
 
+// Copies 16 bytes to shared memory asynchronously, in this thread's current group.
+__device__ __forceinline__ void copy_async_16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows a warp of the backward kernel has on their way while it works on one.
+constexpr int kAhead = 2;
+
 // dZ = dY act'(Z), Z from its 8-bit checkpoint, and the column sums of dZ before rounding.
-// A CTA owns one chunk of columns and the rows [blockIdx.y * rows_per, +rows_per); its warps
-// take rows in turn and keep the sums of their columns in registers.  The warps' sums are
+// Each warp keeps the sums of its stripe's columns in registers.  The warps' sums are
 // added in warp order and written to part[blockIdx.y][cols] (or straight to dbias when one
 // CTA covers all rows), so the result does not depend on timing.
-template <int T, bool SUM>
-__global__ void __launch_bounds__(kRowThreads)
-    act_backward_kernel(const RowMat dy, const MxMat z, const RowMat dz, int act, int64_t rows,
-                        int64_t cols, int64_t rows_per, float *part) {
-  constexpr int E = kLaneElems<T>;
-  constexpr int kLanesPerBlock = kMxBlock / E;
-  __shared__ __align__(16) uint32_t stage[kRowWarps][256];
-  __shared__ __align__(16) float sums[SUM ? kRowWarps : 1][SUM ? 32 * E : 4];
+//
+// Two input streams, the sums and the derivative leave no registers for loads in flight, so
+// whole stripes of aligned rows come through shared memory, 16 bytes a lane of the next kAhead
+// rows copied asynchronously (8192 x 8192 bf16, SiLU: 74 us loading to registers, 1.4 times the
+// time of its bytes).  The scales, a byte for 32 elements, are loaded a row ahead.
+template <int T, bool SUM, bool VEC, int U>
+__global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
+    act_backward_kernel(const RowMat dy, const MxMat z, const RowMat dz, int act, uint32_t rows,
+                        uint32_t cols, uint32_t rows_per, float *part) {
+  using St = Stripe<T, U>;
+  constexpr int E = St::E, B = kTypeBytes<T>;
+  constexpr int kQ = kQBytes<kE4M3, E>;
+  constexpr int kCols = St::kPiece * U;
+  struct Ahead {
+    uint4 dy[kAhead + 1][U][kRowThreads];
+    uint8_t q[kAhead + 1][kRowWarps][U * 32 * kQ];
+  };
+  union Shared {
+    Ahead ahead[VEC ? 1 : 0];
+    uint32_t stage[VEC ? 0 : kRowWarps][128];
+    float sums[kRowWarps][SUM ? kCols : 4];
+  };
+  __shared__ __align__(16) Shared sh;
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * (32 * E);
-  const int block = static_cast<int>(c0 / kMxBlock) + lane / kLanesPerBlock;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows_per;
-  const int64_t r1 = min(rows, r0 + rows_per);
-  float acc[E];
+  const St s(rows, cols, rows_per, lane);
+  const int64_t tile_row = z.tiles_x * 512;
+  const char *src = static_cast<const char *>(dy.p) + static_cast<int64_t>(s.r0 + warp) * dy.ld * B + s.at(0, false);
+  char *dst = static_cast<char *>(const_cast<void *>(dz.p)) + static_cast<int64_t>(s.r0 + warp) * dz.ld * B + s.at(0, false);
+  const uint8_t *zq = z.q + static_cast<int64_t>(s.r0 + warp) * z.ldq + s.template q_at<kE4M3>(lane);
+  float acc[U][E];
 #pragma unroll
-  for (int j = 0; j < E; ++j) acc[j] = 0.0f;
-  for (int64_t r = r0 + warp; r < r1; r += kRowWarps) {
-    uint32_t w[8];
-    uint32_t q[kQWords<kE4M3, E>] = {};
-    uint32_t byte = 0;
-    if (block < z.blocks) {
-      load_q<kE4M3, E>(z.q + r * z.ldq + static_cast<int64_t>(block) * kBlockBytes<kE4M3> +
-                           (lane % kLanesPerBlock) * kQWords<kE4M3, E> * 4,
-                       q);
-      byte = z.s[scale_offset(r, block, z.tiles_x)];
-    }
-    load_lane<T>(dy, r, c0, cols, lane, stage[warp], w);
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int j = 0; j < E; ++j) acc[u][j] = 0.0f;
+  // One piece of a row: w holds dY's elements, q and byte Z's.
+  auto work = [&](int u, uint32_t(&w)[4], const uint32_t(&q)[kQWords<kE4M3, E>], uint32_t byte) {
     float v[E], d[E];
     decode<kE4M3, E>(q, scale_value(byte), v);
     to_floats<T, E>(w, d);
     slope_lane<E>(act, v, d);
     if constexpr (SUM) {
 #pragma unroll
-      for (int j = 0; j < E; j += 2) f2_add_to(acc[j], acc[j + 1], d[j], d[j + 1]);
+      for (int j = 0; j < E; j += 2) f2_add_to(acc[u][j], acc[u][j + 1], d[j], d[j + 1]);
     }
     from_floats<T, E>(d, w);
-    store_lane<T>(dz, r, c0, cols, lane, stage[warp], w);
+  };
+  if (VEC && s.left == kCols) {
+    if constexpr (VEC) {
+      Ahead &a = sh.ahead[0];
+      const int tid = threadIdx.x;
+      const uint8_t *zs = z.s + scale_offset(0, s.block, z.tiles_x);
+      const char *fsrc = src + lane * 16;  // of the row to fetch next
+      const uint8_t *fq = zq - lane * kQ + lane * 16;
+      uint32_t fr = s.r0 + warp;
+      auto fetch = [&](int slot) {
+        if (fr < s.r1) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) copy_async_16(&a.dy[slot][u][tid], fsrc + u * (St::kPiece * B));
+          if (lane * 16 < U * 32 * kQ) copy_async_16(&a.q[slot][warp][lane * 16], fq);
+        }
+        copy_async_commit();
+        fr += kRowWarps;
+        fsrc += kRowWarps * dy.ld * B;
+        fq += kRowWarps * z.ldq;
+      };
+      uint32_t bytes[U];
+      auto fetch_scales = [&](uint32_t r) {
+        if (r < s.r1) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) bytes[u] = zs[scale_row(r, tile_row) + u * St::kPieceScales];
+        }
+      };
+      int slot = 0;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) fetch(i);
+      fetch_scales(s.r0 + warp);
+      for (uint32_t r = s.r0 + warp; r < s.r1; r += kRowWarps) {
+        copy_async_wait<kAhead - 1>();
+        __syncwarp();  // every lane's copies of this row have landed, and the row before is read
+        fetch(slot == 0 ? kAhead : slot - 1);  // into the slot of the row before
+        uint32_t now[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) now[u] = bytes[u];
+        fetch_scales(r + kRowWarps);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint4 x = a.dy[slot][u][tid];
+          uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t q[kQWords<kE4M3, E>];
+          load_q<kE4M3, E>(&a.q[slot][warp][(u * 32 + lane) * kQ], q);
+          work(u, w, q, now[u]);
+          store_lane<T, true, true>(dst + u * (St::kPiece * B), kCols, lane, nullptr, w);
+        }
+        dst += kRowWarps * dz.ld * B;
+        slot = slot == kAhead ? 0 : slot + 1;
+      }
+      copy_async_wait<0>();
+    }
+  } else {
+    uint32_t *st = VEC ? nullptr : sh.stage[VEC ? 0 : warp];
+    const uint8_t *zs = z.s + scale_offset(0, s.block, z.tiles_x);
+    for (uint32_t r = s.r0 + warp; r < s.r1; r += kRowWarps) {
+      uint32_t w[U][4];
+      MxLane<kE4M3, E> q[U];
+      const int64_t sr = scale_row(r, tile_row);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        issue_load_mx<kE4M3, E>(zq + u * (32 * kQ), zs + sr + u * St::kPieceScales,
+                                s.block + u * (St::kPiece / kMxBlock) < z.blocks, q[u]);
+        if (u * St::kPiece < s.left)
+          issue_load<T, VEC, false>(src + u * (St::kPiece * B), s.left - u * St::kPiece, lane, w[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u * St::kPiece < s.left) {
+          finish_load<T, VEC>(lane, st, w[u]);
+          work(u, w[u], q[u].q, q[u].byte);
+          store_lane<T, VEC, false>(dst + u * (St::kPiece * B), s.left - u * St::kPiece, lane, st, w[u]);
+        }
+      }
+      src += kRowWarps * dy.ld * B;
+      dst += kRowWarps * dz.ld * B;
+      zq += kRowWarps * z.ldq;
+    }
   }
+  if constexpr (SUM) __syncthreads();  // every warp is done with its part of the shared memory
   if constexpr (SUM) {
 #pragma unroll
-    for (int j = 0; j < E; j += 4)
-      *reinterpret_cast<float4 *>(&sums[warp][lane * E + j]) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-    __syncthreads();
-    for (int c = threadIdx.x; c < 32 * E && c0 + c < cols; c += kRowThreads) {
-      float s = sums[0][c];
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 1; i < kRowWarps; ++i) s += sums[i][c];
-      part[static_cast<int64_t>(blockIdx.y) * cols + c0 + c] = s;
+      for (int j = 0; j < E; j += 4)
+        *reinterpret_cast<float4 *>(&sh.sums[warp][u * St::kPiece + lane * E + j]) =
+            make_float4(acc[u][j], acc[u][j + 1], acc[u][j + 2], acc[u][j + 3]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < s.left; c += kRowThreads) {
+      float t = sh.sums[0][c];
+#pragma unroll
+      for (int i = 1; i < kRowWarps; ++i) t += sh.sums[i][c];
+      part[static_cast<int64_t>(blockIdx.y) * cols + (s.c0 + c)] = t;
     }
   }
 }
 
-// dbias[c] = the sum over `parts` partial sums, in order.
-__global__ void __launch_bounds__(128) column_sum_kernel(const float *part, int parts, int64_t cols, float *dbias) {
+// dbias[c] = the sum over `parts` partial sums: a warp takes every eighth one of 32 columns, and
+// the eight sums are added in order.
+__global__ void __launch_bounds__(kRowThreads) column_sum_kernel(const float *part, int parts, int64_t cols, float *dbias) {
+  __shared__ float sums[kRowWarps][32];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-  if (c >= cols) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.0f;
+  if (c < cols) {
 #pragma unroll 8
-  for (int i = 0; i < parts; ++i) s += part[i * cols + c];
-  dbias[c] = s;
+    for (int i = warp; i < parts; i += kRowWarps) s += part[i * cols + c];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < cols) {
+#pragma unroll
+    for (int i = 1; i < kRowWarps; ++i) s += sums[i][lane];
+    dbias[c] = s;
+  }
 }
 
 // ------------------------------------------------------------------ host side
 
-RowMat row_mat(const void *p, int64_t ld, int type) {
-  return {p, ld, aligned16(p) && (ld * type_bytes(type)) % 16 == 0 ? 1 : 0};
-}
+bool vec_rows(const void *p, int64_t ld, int type) { return aligned16(p) && (ld * type_bytes(type)) % 16 == 0; }
 
 MxMat mx_mat(const void *Q, int64_t ldq, const void *S, int64_t cols) {
   return {static_cast<const uint8_t *>(Q), ldq, static_cast<const uint8_t *>(S), scale_tiles_x(cols),
@@ -494,27 +652,55 @@ tlg_status with_type(int type, F f) {
 }
 
 template <typename F>
+tlg_status with_flag(bool flag, F f) {
+  return flag ? f(std::true_type()) : f(std::false_type());
+}
+
+template <typename F>
 tlg_status with_format(int format, F f) {
   return format == TLG_MX_E2M1 ? f(std::integral_constant<int, kE2M1>()) : f(std::integral_constant<int, kE4M3>());
 }
 
-// Column chunks of a row kernel, and its grid: one warp an item up to eight 256-thread blocks
-// an SM, then each warp takes several.
-int chunks_of(int type, int64_t cols) {
-  const int64_t c = 32 * 32 / type_bytes(type);
-  return static_cast<int>((cols + c - 1) / c);
+// Pieces of a row a warp loads at once: several where there are rows enough to fill the
+// device all the same, one in small calls.
+constexpr int kWide = 4, kWideBackward = 2;
+
+// A row kernel's grid: column stripes x row splits, about `per_sm` CTAs an SM, each warp with a
+// few rows.
+struct RowGrid {
+  int u;
+  dim3 grid;
+  uint32_t rows_per;
+};
+
+RowGrid row_grid(int64_t rows, int64_t cols, int type, bool vec, int wide, int sms, int per_sm) {
+  const int64_t piece = 32 * 16 / type_bytes(type);
+  const int64_t row_groups = (rows + kRowWarps - 1) / kRowWarps;  // a row to each warp of a CTA
+  RowGrid g;
+  if (!vec && type != TLG_TYPE_F32) wide = 1;  // element loads: eight a piece are enough in flight
+  g.u = row_groups * ((cols + piece * wide - 1) / (piece * wide)) >= 2 * int64_t(sms) ? wide : 1;
+  const int64_t stripes = (cols + piece * g.u - 1) / (piece * g.u);
+  int64_t splits = std::max<int64_t>(1, std::min<int64_t>({(int64_t(sms) * per_sm + stripes - 1) / stripes, row_groups, 65535}));
+  g.rows_per = static_cast<uint32_t>((row_groups + splits - 1) / splits * kRowWarps);
+  splits = (rows + g.rows_per - 1) / g.rows_per;
+  g.grid = dim3(static_cast<unsigned>(stripes), static_cast<unsigned>(splits));
+  return g;
 }
 
-dim3 row_grid(int64_t rows, int chunks, int sms) {
-  const int64_t blocks = (rows * chunks + kRowWarps - 1) / kRowWarps;
-  return dim3(static_cast<unsigned>(std::min<int64_t>(blocks, int64_t(sms) * 8)));
+// The same for the backward kernel, whose splits each leave a partial column sum: at least two
+// rows to a warp.
+RowGrid backward_grid(int64_t rows, int64_t cols, int type, int sms) {
+  RowGrid g = row_grid(rows, cols, type, true, kWideBackward, sms, 4);
+  if (g.rows_per < 2 * kRowWarps) {
+    g.rows_per = 2 * kRowWarps;
+    g.grid.y = static_cast<unsigned>((rows + g.rows_per - 1) / g.rows_per);
+  }
+  return g;
 }
 
-// Row splits of the backward kernel: enough CTAs to fill the device, each warp with a few rows.
-int backward_splits(int64_t rows, int chunks, int sms) {
-  const int64_t want = (int64_t(sms) * 4 + chunks - 1) / chunks;
-  const int64_t most = (rows + 4 * kRowWarps - 1) / (4 * kRowWarps);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, 65535})));
+template <typename F>
+tlg_status with_width(int u, F f) {
+  return u == 1 ? f(std::integral_constant<int, 1>()) : f(std::integral_constant<int, kWide>());
 }
 
 }  // namespace
@@ -562,9 +748,14 @@ tlg_status tlg_mx_quantize(tlg_mx_format format, int64_t rows, int64_t cols, tlg
         return launch(quantize_cols_kernel<kT, kF>, dim3(static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 30))),
                       kT == kTypeF32 ? 512 : 256, s, X, ldx, pair, o, rows, cols, tiles_r, tiles);
       }
-      const int chunks = chunks_of(type, cols);
-      return launch(quantize_rows_kernel<kT, kF, false>, row_grid(rows, chunks, info.sm_count), kRowThreads, s,
-                    row_mat(X, ldx, type), o, RowMat{}, 0, rows, cols, chunks);
+      const bool vec = vec_rows(X, ldx, type);
+      const RowGrid g = row_grid(rows, cols, type, vec, kWide, info.sm_count, 4);
+      return with_flag(vec, [&](auto V) {
+        return with_width(g.u, [&](auto U) {
+          return launch(quantize_rows_kernel<kT, kF, false, decltype(V)::value, decltype(U)::value>, g.grid,
+                        kRowThreads, s, RowMat{X, ldx}, o, RowMat{}, 0, rows, cols, g.rows_per);
+        });
+      });
     });
   });
 }
@@ -584,12 +775,17 @@ tlg_status tlg_mx_dequantize(tlg_mx_format format, int64_t rows, int64_t cols, c
   st = device_ready({X, Q, S}, &info);
   if (st != TLG_OK) return st;
   const MxMat in = mx_mat(Q, ldq, S, cols);
-  const int chunks = chunks_of(type, cols);
+  const bool vec = vec_rows(X, ldx, type);
+  const RowGrid g = row_grid(rows, cols, type, vec, kWide, info.sm_count, 4);
   return with_type(type, [&](auto T) {
     return with_format(format, [&](auto F) {
-      return launch(dequantize_rows_kernel<decltype(T)::value, decltype(F)::value>,
-                    row_grid(rows, chunks, info.sm_count), kRowThreads, static_cast<cudaStream_t>(stream), in,
-                    row_mat(X, ldx, type), rows, cols, chunks);
+      return with_flag(vec, [&](auto V) {
+        return with_width(g.u, [&](auto U) {
+          return launch(
+              dequantize_rows_kernel<decltype(T)::value, decltype(F)::value, decltype(V)::value, decltype(U)::value>,
+              g.grid, kRowThreads, static_cast<cudaStream_t>(stream), in, RowMat{X, ldx}, rows, cols, g.rows_per);
+        });
+      });
     });
   });
 }
@@ -612,11 +808,16 @@ tlg_status tlg_act_forward_mx(int64_t rows, int64_t cols, tlg_activation activat
   st = device_ready({Z, Y, Q, S}, &info);
   if (st != TLG_OK) return st;
   const MxMat o = mx_mat(Q, ldq, S, cols);
-  const int chunks = chunks_of(type, cols);
+  const bool vec = vec_rows(Z, ldz, type) && vec_rows(Y, ldy, type);
+  const RowGrid g = row_grid(rows, cols, type, vec, kWide, info.sm_count, 4);
   return with_type(type, [&](auto T) {
-    return launch(quantize_rows_kernel<decltype(T)::value, kE4M3, true>, row_grid(rows, chunks, info.sm_count),
-                  kRowThreads, static_cast<cudaStream_t>(stream), row_mat(Z, ldz, type), o, row_mat(Y, ldy, type),
-                  static_cast<int>(activation), rows, cols, chunks);
+    return with_flag(vec, [&](auto V) {
+      return with_width(g.u, [&](auto U) {
+        return launch(quantize_rows_kernel<decltype(T)::value, kE4M3, true, decltype(V)::value, decltype(U)::value>,
+                      g.grid, kRowThreads, static_cast<cudaStream_t>(stream), RowMat{Z, ldz}, o, RowMat{Y, ldy},
+                      static_cast<int>(activation), rows, cols, g.rows_per);
+      });
+    });
   });
 }
 
@@ -630,7 +831,7 @@ tlg_status tlg_act_backward_mx_workspace_size(int64_t rows, int64_t cols, tlg_ty
   DeviceInfo info;
   const tlg_status ds = current_device(&dev, &info);
   if (ds != TLG_OK) return ds;
-  const int splits = backward_splits(rows, chunks_of(type, cols), info.sm_count);
+  const unsigned splits = backward_grid(rows, cols, type, info.sm_count).grid.y;
   *bytes = splits > 1 ? static_cast<size_t>(splits) * static_cast<size_t>(cols) * 4 : 0;
   return TLG_OK;
 }
@@ -678,9 +879,8 @@ tlg_status tlg_act_backward_mx(int64_t rows, int64_t cols, tlg_activation activa
   if (dbias != nullptr && workspace != nullptr && meets(rb, rw)) return TLG_ERR_INVALID_ARG;
   st = device_ready({dY, Q, S, dZ, dbias, workspace}, &info);
   if (st != TLG_OK) return st;
-  const int chunks = chunks_of(type, cols);
-  const int splits = backward_splits(rows, chunks, info.sm_count);
-  const int64_t rows_per = (rows + splits - 1) / splits;
+  const RowGrid g = backward_grid(rows, cols, type, info.sm_count);
+  const int splits = static_cast<int>(g.grid.y);
   float *part = dbias;
   if (dbias != nullptr && splits > 1) {
     if (workspace == nullptr || workspace_bytes < static_cast<size_t>(splits) * static_cast<size_t>(cols) * 4)
@@ -688,17 +888,21 @@ tlg_status tlg_act_backward_mx(int64_t rows, int64_t cols, tlg_activation activa
     part = static_cast<float *>(workspace);
   }
   const MxMat z = mx_mat(Q, ldq, S, cols);
-  const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(splits));
   st = with_type(type, [&](auto T) {
     constexpr int kT = decltype(T)::value;
-    const RowMat dy = row_mat(dY, lddy, type), dz = row_mat(dZ, lddz, type);
-    return dbias != nullptr ? launch(act_backward_kernel<kT, true>, grid, kRowThreads, s, dy, z, dz,
-                                     static_cast<int>(activation), rows, cols, rows_per, part)
-                            : launch(act_backward_kernel<kT, false>, grid, kRowThreads, s, dy, z, dz,
-                                     static_cast<int>(activation), rows, cols, rows_per, part);
+    return with_flag(dbias != nullptr, [&](auto SUM) {
+      return with_flag(vec_rows(dY, lddy, type) && vec_rows(dZ, lddz, type), [&](auto V) {
+        auto run = [&](auto U) {
+          return launch(act_backward_kernel<kT, decltype(SUM)::value, decltype(V)::value, decltype(U)::value>, g.grid,
+                        kRowThreads, s, RowMat{dY, lddy}, z, RowMat{dZ, lddz}, static_cast<int>(activation), rows,
+                        cols, g.rows_per, part);
+        };
+        return g.u == 1 ? run(std::integral_constant<int, 1>()) : run(std::integral_constant<int, kWideBackward>());
+      });
+    });
   });
   if (st != TLG_OK || part == dbias) return st;
-  return launch(column_sum_kernel, dim3(static_cast<unsigned>((cols + 127) / 128)), 128, s, part, splits, cols, dbias);
+  return launch(column_sum_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), kRowThreads, s, part, splits, cols, dbias);
 }
 
 }  // extern "C"

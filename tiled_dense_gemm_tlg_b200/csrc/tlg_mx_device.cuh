@@ -62,26 +62,26 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// A lane's 32 bytes as fp32 values, and back (one rounding).
+// A lane's 16 bytes as fp32 values, and back (one rounding).
 template <int T, int E>
-__device__ __forceinline__ void to_floats(const uint32_t (&w)[8], float (&v)[E]) {
+__device__ __forceinline__ void to_floats(const uint32_t (&w)[4], float (&v)[E]) {
   if constexpr (T == kTypeF32) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+    for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(w[j]);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) unpack2<T>(w[j], v[2 * j], v[2 * j + 1]);
+    for (int j = 0; j < 4; ++j) unpack2<T>(w[j], v[2 * j], v[2 * j + 1]);
   }
 }
 
 template <int T, int E>
-__device__ __forceinline__ void from_floats(const float (&v)[E], uint32_t (&w)[8]) {
+__device__ __forceinline__ void from_floats(const float (&v)[E], uint32_t (&w)[4]) {
   if constexpr (T == kTypeF32) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[j]);
+    for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(v[j]);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = pack2<T>(v[2 * j], v[2 * j + 1]);
+    for (int j = 0; j < 4; ++j) w[j] = pack2<T>(v[2 * j], v[2 * j + 1]);
   }
 }
 
@@ -148,7 +148,18 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 
 // ------------------------------------------------------------------ conversions
 
-// Eight values to E2M1, round to nearest even, saturating: element 2i in the low half of byte i.
+// Four values to E2M1 (16 bits), round to nearest even, saturating: element 2i in the low half of byte i.
+__device__ __forceinline__ uint32_t to_e2m1x4(const float *v) {
+  uint16_t r;
+  asm("{\n\t.reg .b8 a, b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "mov.b16 %0, {a, b};\n\t}"
+      : "=h"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t to_e2m1x8(const float *v) {
   uint32_t r;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
@@ -185,7 +196,17 @@ __device__ __forceinline__ void from_e4m3x4(uint32_t w, float *v) {
   unpack2<kTypeF16>(hi, v[2], v[3]);
 }
 
-// Eight E2M1 elements to fp32.
+// Four E2M1 elements (the low 16 bits of w) to fp32.
+__device__ __forceinline__ void from_e2m1x4(uint32_t w, float *v) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b8 a, b;\n\tmov.b16 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "h"(static_cast<uint16_t>(w)));
+  unpack2<kTypeF16>(lo, v[0], v[1]);
+  unpack2<kTypeF16>(hi, v[2], v[3]);
+}
+
 __device__ __forceinline__ void from_e2m1x8(uint32_t w, float *v) {
   uint32_t p[4];
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
@@ -197,9 +218,11 @@ __device__ __forceinline__ void from_e2m1x8(uint32_t w, float *v) {
   for (int i = 0; i < 4; ++i) unpack2<kTypeF16>(p[i], v[2 * i], v[2 * i + 1]);
 }
 
-// Words a lane's E elements take in Q.
+// Bytes a lane's E elements take in Q, and the words that hold them (4 E2M1 elements: half a word).
 template <int FMT, int E>
-constexpr int kQWords = FMT == kE2M1 ? E / 8 : E / 4;
+constexpr int kQBytes = FMT == kE2M1 ? E / 2 : E;
+template <int FMT, int E>
+constexpr int kQWords = (kQBytes<FMT, E> + 3) / 4;
 
 // v times 2^-e, rounded to the format.  The product is exact, or so small that it rounds to 0.
 template <int FMT, int E>
@@ -210,10 +233,12 @@ __device__ __forceinline__ void encode(const float (&v)[E], float inv, uint32_t 
     f2_unpack(f2_mul(f2_pack(v[j], v[j + 1]), f2_splat(inv)), t[j], t[j + 1]);
 #pragma unroll
   for (int j = 0; j < kQWords<FMT, E>; ++j) {
-    if constexpr (FMT == kE2M1)
-      q[j] = to_e2m1x8(t + 8 * j);
-    else
+    if constexpr (FMT == kE4M3)
       q[j] = to_e4m3x4(t + 4 * j);
+    else if constexpr (E == 4)
+      q[j] = to_e2m1x4(t);
+    else
+      q[j] = to_e2m1x8(t + 8 * j);
   }
 }
 
@@ -221,10 +246,12 @@ template <int FMT, int E>
 __device__ __forceinline__ void decode(const uint32_t (&q)[kQWords<FMT, E>], float scale, float (&v)[E]) {
 #pragma unroll
   for (int j = 0; j < kQWords<FMT, E>; ++j) {
-    if constexpr (FMT == kE2M1)
-      from_e2m1x8(q[j], v + 8 * j);
-    else
+    if constexpr (FMT == kE4M3)
       from_e4m3x4(q[j], v + 4 * j);
+    else if constexpr (E == 4)
+      from_e2m1x4(q[j], v);
+    else
+      from_e2m1x8(q[j], v + 8 * j);
   }
 #pragma unroll
   for (int j = 0; j < E; j += 2)
@@ -250,12 +277,19 @@ __device__ __forceinline__ void activate_lane(int act, float (&v)[E]) {
   }
 }
 
-// min and max that keep a NaN.
+// The larger of the two; a NaN stays.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
+// x held to [-limit, limit]; a NaN stays.
 __device__ __forceinline__ float clamp_nan(float x, float limit) {
   float r;
-  asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, %2;\n\tneg.f32 %0, %2;\n\tmax.NaN.f32 %0, t, %0;\n\t}"
-      : "=&f"(r)
-      : "f"(x), "f"(limit));
+  asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, %2;\n\tmax.NaN.f32 %0, t, %3;\n\t}"
+      : "=f"(r)
+      : "f"(x), "f"(limit), "f"(-limit));
   return r;
 }
 
@@ -289,38 +323,33 @@ __device__ __forceinline__ void gelu_slope_2(float x0, float x1, float &s0, floa
   f2_unpack(f2_add(f2_pack(h0, h1), f2_splat(0.5f)), s0, s1);
 }
 
-// The derivative of x sigmoid(u), u = c1 x + c3 x^3 (SiLU, tanh GELU; see SigmoidForm):
-// s + x s (1 - s) (c1 + 3 c3 x^2), with s = 1 / (1 + t), 1 - s = t s, t = 2^(-u log2 e).
-// |x| is held below the point where the derivative is 0 or 1 to fp32's last place and t still
-// finite, so no product is 0 times infinity; a NaN stays.
-struct SlopeForm {
-  SigmoidForm f;    // times -log2(e)
-  float d1, d3;     // c1, 3 c3
-  float limit;
-};
-
-__device__ __forceinline__ SlopeForm slope_form(int act) {
-  constexpr float kTanhC1 = 1.5957691216057308f;  // 2 sqrt(2/pi)
-  SlopeForm s;
-  s.f = sigmoid_form(act);
-  const bool silu = act == kActSilu;
-  s.d1 = silu ? 1.0f : kTanhC1;
-  s.d3 = silu ? 0.0f : 3.0f * 0.044715f * kTanhC1;
-  s.limit = silu ? 80.0f : 9.5f;
-  return s;
-}
-
-__device__ __forceinline__ void sigmoid_slope_2(const SlopeForm &f, float x0, float x1, float &s0,
-                                                float &s1) {
-  const uint64_t x = f2_pack(clamp_nan(x0, f.limit), clamp_nan(x1, f.limit));
-  const uint64_t xx = f2_mul(x, x);
+// The derivative of x sigmoid(u): s + x s (1 - s) u'(x), with s = 1 / (1 + t), 1 - s = t s,
+// t = 2^(-u log2 e).  x is held to where the derivative is 0 or 1 to fp32's last place and t
+// still finite, so no product is 0 times infinity; a NaN stays.
+//   SiLU: u = x.  Only negative x needs holding (above, t underflows to 0 and x t s to 0).
+__device__ __forceinline__ void silu_slope_2(float x0, float x1, float &s0, float &s1) {
+  const uint64_t x = f2_pack(max_nan(x0, -80.0f), max_nan(x1, -80.0f));
   float z0, z1;
-  f2_unpack(f2_mul(x, f2_fma(f2_splat(f.f.c3), xx, f2_splat(f.f.c1))), z0, z1);
+  f2_unpack(f2_mul(x, f2_splat(-1.4426950408889634f)), z0, z1);
   const uint64_t t = f2_pack(ex2_approx(z0), ex2_approx(z1));
   float d0, d1;
   f2_unpack(f2_add(t, f2_splat(1.0f)), d0, d1);
   const uint64_t s = f2_pack(rcp_approx(d0), rcp_approx(d1));
-  const uint64_t du = f2_mul(x, f2_fma(f2_splat(f.d3), xx, f2_splat(f.d1)));
+  f2_unpack(f2_fma(f2_mul(x, s), f2_mul(t, s), s), s0, s1);
+}
+
+//   tanh GELU: u = c (x + 0.044715 x^3), c = 2 sqrt(2/pi); |x| held to 9.5 (u < 77).
+__device__ __forceinline__ void gelu_tanh_slope_2(float x0, float x1, float &s0, float &s1) {
+  constexpr float kC1 = 1.5957691216057308f, kC3 = 0.044715f * kC1, kNegLog2e = -1.4426950408889634f;
+  const uint64_t x = f2_pack(clamp_nan(x0, 9.5f), clamp_nan(x1, 9.5f));
+  const uint64_t xx = f2_mul(x, x);
+  float z0, z1;
+  f2_unpack(f2_mul(x, f2_fma(f2_splat(kC3 * kNegLog2e), xx, f2_splat(kC1 * kNegLog2e))), z0, z1);
+  const uint64_t t = f2_pack(ex2_approx(z0), ex2_approx(z1));
+  float d0, d1;
+  f2_unpack(f2_add(t, f2_splat(1.0f)), d0, d1);
+  const uint64_t s = f2_pack(rcp_approx(d0), rcp_approx(d1));
+  const uint64_t du = f2_mul(x, f2_fma(f2_splat(3.0f * kC3), xx, f2_splat(kC1)));
   f2_unpack(f2_fma(f2_mul(du, s), f2_mul(t, s), s), s0, s1);
 }
 
@@ -330,7 +359,7 @@ template <int E>
 __device__ __forceinline__ void slope_lane(int act, const float (&z)[E], float (&d)[E]) {
   if (act == kActRelu) {
 #pragma unroll
-    for (int j = 0; j < E; ++j) d[j] = z[j] > 0.0f ? d[j] : (z[j] <= 0.0f ? 0.0f : z[j]);
+    for (int j = 0; j < E; ++j) d[j] = z[j] > 0.0f ? d[j] : max_nan(z[j], 0.0f);
   } else if (act == kActGelu) {
 #pragma unroll
     for (int j = 0; j < E; j += 2) {
@@ -338,12 +367,18 @@ __device__ __forceinline__ void slope_lane(int act, const float (&z)[E], float (
       gelu_slope_2(z[j], z[j + 1], s0, s1);
       f2_unpack(f2_mul(f2_pack(d[j], d[j + 1]), f2_pack(s0, s1)), d[j], d[j + 1]);
     }
-  } else if (act == kActSilu || act == kActGeluTanh) {
-    const SlopeForm f = slope_form(act);
+  } else if (act == kActSilu) {
 #pragma unroll
     for (int j = 0; j < E; j += 2) {
       float s0, s1;
-      sigmoid_slope_2(f, z[j], z[j + 1], s0, s1);
+      silu_slope_2(z[j], z[j + 1], s0, s1);
+      f2_unpack(f2_mul(f2_pack(d[j], d[j + 1]), f2_pack(s0, s1)), d[j], d[j + 1]);
+    }
+  } else if (act == kActGeluTanh) {
+#pragma unroll
+    for (int j = 0; j < E; j += 2) {
+      float s0, s1;
+      gelu_tanh_slope_2(z[j], z[j + 1], s0, s1);
       f2_unpack(f2_mul(f2_pack(d[j], d[j + 1]), f2_pack(s0, s1)), d[j], d[j + 1]);
     }
   }
