@@ -450,8 +450,11 @@ tlg_status tlg_mx_dequantize(tlg_mx_format format, int64_t rows, int64_t cols,
  * epilogue as for tlg_gemm_fused, NULL for none: the bias holds N fp16 values
  * (bf16 when C is bf16), the residual has C's type and may be C itself.
  * config: NULL or zero fields choose automatically; block_n, cta_group,
- * stages, raster_group and max_ctas as for tlg_gemm_ex, split_k and k_split 0
- * or 1, overlap_prev is always on.  No workspace.  K == 0 gives C = act(bias)
+ * stages, raster_group and max_ctas as for tlg_gemm_ex, split_k 0 or 1,
+ * overlap_prev is always on.  M <= 32 has a kernel of its own (block_n 16 or
+ * 32: the tokens; cta_group, stages and max_ctas must be 0), where k_split 1,
+ * 2, 4 or 8 CTAs share the K range (at most one per 256 k); elsewhere k_split
+ * is 0 or 1.  No workspace.  K == 0 gives C = act(bias)
  * + residual.  Sizes and errors as tlg_gemm_fused's; lda and ldb are in BYTES
  * (ldq above).  A pipeline wait past its time limit is reported by
  * tlg_device_error().

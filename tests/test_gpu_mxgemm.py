@@ -94,6 +94,45 @@ def test_product_is_exact(tlg, cg, bn, M, N, K):
         assert o.guards_kept()
 
 
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 31, 32])
+@pytest.mark.parametrize("N,K", [(1, 32), (100, 257), (128, 1024), (300, 2000), (1111, 555)])
+def test_few_rows_are_exact(tlg, M, N, K):
+    A, SA, a = operand(M, K, "exact", M + N)
+    B, SB, b = operand(N, K, "exact", K + 1)
+    num_kb = -(-K // 256)
+    for ks in (0, 1, 2, 4, 8):
+        if ks > num_kb:
+            with pytest.raises(tlg.TlgError):
+                tlg.tlg_gemm_mxfp4(A, SA, B, SB, config={"k_split": ks})
+            continue
+        for typ, lead, extra in (("f32", 1, 3), ("f16", 0, 0), ("bf16", 1, 1)):
+            o = Out(M, N, TYPES[typ], lead, extra)
+            tlg.tlg_gemm_mxfp4(A, SA, B, SB, C=o.view, out=typ, config={"k_split": ks})
+            check(o.view, a @ b.T, 0.0, typ)
+            assert o.guards_kept()
+
+
+@pytest.mark.parametrize("M", [1, 5, 16, 32])
+@pytest.mark.parametrize("typ", list(TYPES))
+def test_few_rows_epilogue_is_the_tiles(tlg, M, typ):
+    """Few rows run a kernel of their own; with exact sums its results are those of the tiles, to the bit."""
+    N, K = 700, 1024
+    A, SA, _ = operand(M, K, "exact", M)
+    B, SB, _ = operand(N, K, "exact", 9)
+    SB = (SB.int() - 6).clamp(min=0).to(torch.uint8)
+    bias = torch.randn(N, device="cuda").to(torch.bfloat16 if typ == "bf16" else torch.float16)
+    R = torch.randn(M, N, device="cuda").to(TYPES[typ])
+    for act in ("none", "relu", "gelu", "silu", "gelu_tanh"):
+        want = tlg.tlg_gemm_mxfp4(A, SA, B, SB, bias=bias, activation=act, residual=R, out=typ,
+                                  config={"cta_group": 1, "block_n": 64})
+        got = tlg.tlg_gemm_mxfp4(A, SA, B, SB, bias=bias, activation=act, residual=R, out=typ)
+        assert tlg.tlg_choose_config_mxfp4(M, N, K, typ)["block_n"] in (16, 32)
+        assert torch.equal(got, want), act
+        C = R.clone()
+        tlg.tlg_gemm_mxfp4(A, SA, B, SB, bias=bias, activation=act, residual=C, C=C, out=typ)
+        assert torch.equal(C, want), act
+
+
 @pytest.mark.parametrize("M,N,K", SHAPES + [(2, 4096, 4096), (16, 2048, 8192), (40, 777, 3001)])
 def test_product_automatic_tile_wide_scales(tlg, M, N, K):
     A, SA, a = operand(M, K, "wide", M + 3 * N)

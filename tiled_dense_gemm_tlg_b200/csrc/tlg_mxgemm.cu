@@ -94,6 +94,53 @@ constexpr MxFns fns() {
   return {MxVariant<CG, BN, STAGES, OUT, EPI>::units, MxVariant<CG, BN, STAGES, OUT, EPI>::launch};
 }
 
+// The kernel for few rows of A; `ctas` a cluster of ks.
+template <int BN, int OUT>
+tlg_status launch_tokens(int dev, int clusters, int ks, const MxMaps &m, const MxGemmParams &p, cudaStream_t s) {
+  using Plan = MxTokenPlan<BN>;
+  constexpr auto kernel = mxgemm_tokens_kernel<BN, OUT>;
+  static bool ready[kMaxDevices];
+  static std::mutex mutex;
+  {
+    std::lock_guard<std::mutex> lock(mutex);
+    if (!ready[dev]) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan::kDynamicBytes) !=
+          cudaSuccess) {
+        cudaGetLastError();
+        return TLG_ERR_CUDA;
+      }
+      ready[dev] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters) * static_cast<unsigned>(ks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Plan::kDynamicBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ks);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.sa, m.sb, p, ks) != cudaSuccess) {
+    cudaGetLastError();
+    return TLG_ERR_CUDA;
+  }
+  return TLG_OK;
+}
+
+template <int BN>
+tlg_status launch_tokens_typed(int out, int dev, int clusters, int ks, const MxMaps &m, const MxGemmParams &p,
+                               cudaStream_t s) {
+  if (out == TLG_TYPE_F32) return launch_tokens<BN, kTypeF32>(dev, clusters, ks, m, p, s);
+  if (out == TLG_TYPE_F16) return launch_tokens<BN, kTypeF16>(dev, clusters, ks, m, p, s);
+  return launch_tokens<BN, kTypeBF16>(dev, clusters, ks, m, p, s);
+}
+
 struct MxTile {
   int cta_group, block_n, stages;
   double eff;   // sustained fraction of the MMA peak, relative
@@ -113,25 +160,59 @@ struct MxTile {
 const MxTile kTiles[] = {
     TLG_MX_TILE(1, 64, 6, 0.5),
     TLG_MX_TILE(1, 128, 5, 0.8),
+    TLG_MX_TILE(1, 128, 4, 0.8),
     TLG_MX_TILE(2, 192, 5, 1.0),
     TLG_MX_TILE(2, 256, 5, 1.0),
+    TLG_MX_TILE(2, 256, 4, 1.0),
 };
 
 // --------------------------------------------------------------------------- tile choice
 
 struct MxChoice {
-  const MxTile *tile;
+  const MxTile *tile;  // nullptr: the kernel for few rows of A
   int units;
+  int tokens;          // its columns (tokens), 0 otherwise
   tlg_config cfg;
 };
 
-tlg_status choose(int dev, int sms, int64_t M, int64_t N, int type, bool epi, const tlg_config *req, MxChoice *out) {
+// Columns of the tokens kernel that hold M rows of A, 0 when there are too many.
+int token_columns(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 0; }
+
+// CTAs sharing the K range: doubled while there is an SM for each and a k-block too, or two CTAs
+// to an SM and 16 k-blocks for each (one token, 4096 x 4096 weights: 3.6 us with 4, 4.8 with 2,
+// 4.7 with 8, whose 256 CTAs share SMs; 16384 x 4096: 6.6 with 1, 6.7 with 2; 8192 x 28672:
+// 21.4 with 4, 24.1 with 2).
+int token_split(int64_t N, int num_kb, int sms) {
+  const int64_t tiles = (N + 127) / 128;
+  int ks = 1;
+  while (ks < 8 && ((tiles * ks * 2 <= sms && ks * 2 <= num_kb) ||
+                    (tiles * ks * 2 <= 2 * int64_t(sms) && ks * 2 * 16 <= num_kb)))
+    ks *= 2;
+  return ks;
+}
+
+tlg_status choose(int dev, int sms, int64_t M, int64_t N, int64_t K, int type, bool epi, const tlg_config *req,
+                  MxChoice *out) {
   tlg_config r = {};
   if (req != nullptr) r = *req;
   if (r.raster_group < 0 || r.raster_group > 64 || r.max_ctas < 0 || r.stages < 0 || r.block_n < 0 ||
       r.cta_group < 0 || (r.overlap_prev != 0 && r.overlap_prev != 1) || (r.split_k != 0 && r.split_k != 1) ||
-      (r.k_split != 0 && r.k_split != 1))
+      r.k_split < 0 || r.k_split > 8)
     return TLG_ERR_UNSUPPORTED;
+  const int num_kb = static_cast<int>((K + kMxBK - 1) / kMxBK);
+  out->tokens = 0;
+  // Few rows of A (a request for a cta_group or for tiles asks for the other kernel).
+  if (token_columns(M) != 0 && r.cta_group == 0 && r.stages == 0 && r.max_ctas == 0 &&
+      (r.block_n == 0 || r.block_n == token_columns(M))) {
+    const int ks = r.k_split != 0 ? r.k_split : token_split(N, num_kb, sms);
+    if ((ks & (ks - 1)) != 0 || ks > num_kb) return TLG_ERR_UNSUPPORTED;
+    out->tile = nullptr;
+    out->tokens = token_columns(M);
+    out->units = static_cast<int>((N + 127) / 128);
+    out->cfg = {out->tokens, 4, 1, 1, out->units * ks, 1, 1, ks};
+    return TLG_OK;
+  }
+  if (r.k_split > 1) return TLG_ERR_UNSUPPORTED;
   double best = 0;
   out->tile = nullptr;
   for (const MxTile &t : kTiles) {
@@ -253,7 +334,7 @@ tlg_status tlg_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void *A, int64_
   }
 
   MxChoice c;
-  st = choose(dev, info.sm_count, M, N, out, epi, config, &c);
+  st = choose(dev, info.sm_count, M, N, K, out, epi, config, &c);
   if (st != TLG_OK) return st;
   p.raster_group = c.cfg.raster_group;
   // Boxes (inner x outer): A 128 bytes (256 k) x 128 rows, B 128 bytes x the CTA's rows, scales
@@ -264,16 +345,23 @@ tlg_status tlg_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void *A, int64_
                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t kbytes = static_cast<uint64_t>(row_bytes(TLG_MX_E2M1, K));
   const uint64_t tx = static_cast<uint64_t>(scale_tiles_x(K));
-  const int bn = c.cfg.block_n;
+  // Rows of A and B in a box, and the 128-row scale groups of B a tile meets.
+  const uint32_t a_rows = c.tokens != 0 ? static_cast<uint32_t>(c.tokens) : 128u;
+  const uint32_t b_rows = c.tokens != 0 ? 128u : static_cast<uint32_t>(c.cfg.block_n / c.cfg.cta_group);
+  const uint32_t b_groups = c.tokens == 0 && c.cfg.block_n > 128 ? 2u : 1u;
   MxMaps m;
-  if (!encode_2d(&m.a, u8, A, kbytes, static_cast<uint64_t>(M), static_cast<uint64_t>(lda), 128, 128) ||
-      !encode_2d(&m.b, u8, B, kbytes, static_cast<uint64_t>(N), static_cast<uint64_t>(ldb), 128,
-                 static_cast<uint32_t>(bn / c.cfg.cta_group)) ||
+  if (!encode_2d(&m.a, u8, A, kbytes, static_cast<uint64_t>(M), static_cast<uint64_t>(lda), 128, a_rows) ||
+      !encode_2d(&m.b, u8, B, kbytes, static_cast<uint64_t>(N), static_cast<uint64_t>(ldb), 128, b_rows) ||
       !encode_2d(&m.sa, u32, SA, tx * 128, static_cast<uint64_t>((M + 127) / 128), tx * 512, 256, 1,
                  CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !encode_2d(&m.sb, u32, SB, tx * 128, static_cast<uint64_t>((N + 127) / 128), tx * 512, 256, bn <= 128 ? 1 : 2,
+      !encode_2d(&m.sb, u32, SB, tx * 128, static_cast<uint64_t>((N + 127) / 128), tx * 512, 256, b_groups,
                  CU_TENSOR_MAP_SWIZZLE_NONE))
     return TLG_ERR_CUDA;
+  if (c.tokens != 0) {
+    const int ks = c.cfg.k_split;
+    return c.tokens == 16 ? launch_tokens_typed<16>(out, dev, c.units, ks, m, p, s)
+                          : launch_tokens_typed<32>(out, dev, c.units, ks, m, p, s);
+  }
   if (!p.c_plain && !encode_2d(&m.c, ct, C, static_cast<uint64_t>(N), static_cast<uint64_t>(M),
                                static_cast<uint64_t>(ldc * osz), static_cast<uint32_t>(128 / osz), 32))
     return TLG_ERR_CUDA;
@@ -290,7 +378,8 @@ tlg_status tlg_choose_config_mxfp4(int64_t M, int64_t N, int64_t K, tlg_type out
   if (st != TLG_OK) return st;
   MxChoice c;
   const tlg_config req = *config;
-  st = choose(dev, info.sm_count, std::max<int64_t>(M, 1), std::max<int64_t>(N, 1), out, true, &req, &c);
+  st = choose(dev, info.sm_count, std::max<int64_t>(M, 1), std::max<int64_t>(N, 1), std::max<int64_t>(K, 1), out, true,
+              &req, &c);
   if (st == TLG_OK) *config = c.cfg;
   return st;
 }

@@ -118,7 +118,10 @@ struct MxPlan {
   static constexpr uint32_t kBOffset = STAGES * kABytes;
   static constexpr uint32_t kSfOffset = kBOffset + STAGES * kBBytes;
   static constexpr uint32_t kOutOffset = kSfOffset + STAGES * (kSfaBytes + kSfbBytes);
-  static constexpr uint32_t kBiasOffset = kOutOffset + kMxEpiWarps * kStageOutBytes;
+  // Output boxes of an epilogue warp: two where they fit, so that one is filled while the TMA
+  // unit still reads the other.
+  static constexpr int kBoxes = kOutOffset + kMxEpiWarps * 2 * kStageOutBytes + 2 * BN * 4 + 2048 <= 232448 ? 2 : 1;
+  static constexpr uint32_t kBiasOffset = kOutOffset + kMxEpiWarps * kBoxes * kStageOutBytes;
   static constexpr uint32_t kBarOffset = kBiasOffset + 2 * BN * 4;  // two tiles' bias in fp32
   static constexpr uint32_t kNumBars = 2 * STAGES + 4 + 1;
   static constexpr uint32_t kMiscOffset = kBarOffset + kNumBars * 8;
@@ -408,7 +411,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int ew = warp - 2;
     const int side = ew >> 2;
     constexpr int kPieces = BN / 64;
-    const uint32_t box = s0 + Plan::kOutOffset + static_cast<uint32_t>(ew) * kStageOutBytes;
+    const uint32_t box0 = s0 + Plan::kOutOffset + static_cast<uint32_t>(ew * Plan::kBoxes) * kStageOutBytes;
+    uint32_t boxes_used = 0;
     const uint32_t release_bar0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
     constexpr int kBoxCols = OUT == kTypeF32 ? 32 : 64;
     int acc = 0;
@@ -483,7 +487,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
               mx_store_row<OUT>(p, row, col, w);
               return;
             }
-            if (lane == 0) bulk_wait_group_read<0>();  // this box's previous store has read it
+            const uint32_t box = box0 + boxes_used % Plan::kBoxes * kStageOutBytes;
+            ++boxes_used;
+            if (lane == 0) bulk_wait_group_read<Plan::kBoxes - 1>();  // this box's previous store has read it
             __syncwarp();
             st_box_row(box, lane, w, 0);
             fence_proxy_async_shared();
@@ -533,6 +539,276 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   if (warp == 1) {
     __syncwarp();
     tmem_dealloc<CG>(tmem_base, Plan::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ few rows of A (tokens)
+
+// The same product for M <= BN <= 32 rows of A, where reading B (the weights) once is all the
+// work: the roles are swapped, 128 rows of B being the MMA's M and the rows of A its N, so a
+// single token costs 16 columns of an MMA and not a 128-row tile.  A cluster of KS CTAs (its size)
+// shares the K range of every 128 rows of B, so that few rows of B still keep most SMs
+// loading; each CTA adds the KS fp32 partial sums of its 128 / KS rows in slice order, received
+// through distributed shared memory, and writes them.  Measured back to back in a graph, one
+// token: 4096 x 4096 weights 3.7 us with KS = 4 (6.5 with KS = 1, 6.7 with 128-row tiles),
+// 16384 x 4096 6.7 us with KS = 1 (11 with 128-row tiles; its bytes take 5.5 us).  At 64 rows of
+// A the 128-row tiles win (6.6 against 8.7 us).
+template <int BN>
+struct MxTokenPlan {
+  static constexpr int kStages = 4;
+  static constexpr uint32_t kWBytes = kBM * 128;
+  static constexpr uint32_t kTBytes = BN * 128;
+  static constexpr uint32_t kSfBytes = 4 * kSfTileBytes;  // two scale tiles of each operand
+  static constexpr uint32_t kStageBytes = kWBytes + kTBytes + kSfBytes;
+  static constexpr uint32_t kTOffset = kStages * kWBytes;
+  static constexpr uint32_t kSfOffset = kTOffset + kStages * kTBytes;
+  static constexpr uint32_t kRecvOffset = kSfOffset + kStages * kSfBytes;
+  // Partial sums [slice][row of this CTA][token], fp32; the pad keeps 16-byte accesses of
+  // neighbouring rows in different banks.
+  static constexpr int kRecvRow = BN + 4;
+  static constexpr uint32_t kRecvBytes = kBM * kRecvRow * 4;
+  static constexpr uint32_t kBarOffset = kRecvOffset + kRecvBytes;
+  static constexpr uint32_t kNumBars = 2 * kStages + 2;
+  static constexpr uint32_t kMiscOffset = kBarOffset + kNumBars * 8;
+  static constexpr uint32_t kDynamicBytes = kMiscOffset + 16 + 1024;
+  static constexpr int kSf0 = 32;  // after the accumulator
+  static constexpr uint32_t kTmemCols = 128;
+  static_assert(BN <= kSf0 && kSf0 + 16 * kStages <= kTmemCols, "accumulator and scales must fit");
+  static_assert(kDynamicBytes <= 232448, "shared memory per CTA exceeded");
+};
+
+// The two halves of a cluster barrier (see cluster_sync_all).
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// tmT: the tokens (A), tmW: the weights (B), tmST / tmSW their scales.  The grid is
+// ceil(N / 128) clusters of KS CTAs.
+template <int BN, int OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+    mxgemm_tokens_kernel(const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmW,
+                         const __grid_constant__ CUtensorMap tmST, const __grid_constant__ CUtensorMap tmSW,
+                         const MxGemmParams p, const int ks) {
+  using Plan = MxTokenPlan<BN>;
+  constexpr int ST = Plan::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const uint32_t s0 = smem_u32(smem);
+  auto w_slot = [&](int s) { return s0 + s * Plan::kWBytes; };
+  auto t_slot = [&](int s) { return s0 + Plan::kTOffset + s * Plan::kTBytes; };
+  auto sf_slot = [&](int s) { return s0 + Plan::kSfOffset + s * Plan::kSfBytes; };
+  const uint32_t bar0 = s0 + Plan::kBarOffset;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (ST + s); };
+  const uint32_t done_bar = bar0 + 8u * (2 * ST);
+  const uint32_t drain_bar = bar0 + 8u * (2 * ST + 1);
+  uint32_t *misc = reinterpret_cast<uint32_t *>(smem + Plan::kMiscOffset);
+  volatile uint32_t *abort_flag = misc + 1;
+
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
+  const int slice = ks > 1 ? static_cast<int>(__shfl_sync(0xffffffffu, cluster_ctarank(), 0)) : 0;
+  const int tile = static_cast<int>(blockIdx.x) / ks;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(slice) * p.num_kb / ks);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(slice + 1) * p.num_kb / ks);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(done_bar, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmT);
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmST);
+    tma_prefetch_desc(&tmSW);
+  }
+  if (warp == 1) {
+    tmem_alloc<1>(smem_u32(misc), Plan::kTmemCols);
+    tmem_relinquish<1>();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(misc);
+  if (ks > 1) cluster_arrive();  // this CTA runs: its shared memory may be written
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    uint32_t issued_mask = 0, issued_parity = 0;
+    bool ok = true;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ok = __all_sync(0xffffffffu, mbar_wait_spin(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns, kRoleProducer,
+                                                  &g_device_error, 4096));
+      if (!ok) break;
+      if (elect_one()) {
+        const uint32_t bar = full_bar(stage);
+        mbar_arrive_expect_tx(bar, Plan::kStageBytes);
+        tma_load_2d(w_slot(stage), &tmW, bar, kb * 128, tile * 128);
+        tma_load_2d(sf_slot(stage), &tmSW, bar, kb * 256, tile);
+        tma_load_2d(t_slot(stage), &tmT, bar, kb * 128, 0);
+        tma_load_2d(sf_slot(stage) + 2 * kSfTileBytes, &tmST, bar, kb * 256, 0);
+      }
+      __syncwarp();
+      issued_mask |= 1u << stage;
+      issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+      if (++stage == ST) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    for (int i = 0; i < ST && ok; ++i) {  // no commit-arrive is still on its way
+      ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns, kRoleProducer,
+                                             &g_device_error));
+      if (++stage == ST) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!ok) {
+      for (int s = 0; s < ST; ++s)
+        if (issued_mask & (1u << s))
+          mbar_wait(full_bar(s), (issued_parity >> s) & 1u, nullptr, p.limit_ns, kRoleProducer, &g_device_error);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc[2] = {make_idesc_mxf4(128, BN, 0), make_idesc_mxf4(128, BN, 2)};
+    bool ok = true;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ok = __all_sync(0xffffffffu, mbar_wait_spin(full_bar(stage), phase, abort_flag, p.limit_ns, kRoleMma,
+                                                  &g_device_error, 4096));
+      if (!ok) break;
+      tc_fence_after_sync();
+      if (elect_one()) {
+        const uint32_t sfa = tmem_base + static_cast<uint32_t>(Plan::kSf0 + stage * 16);
+        const uint32_t sfb = sfa + 8;
+        const uint64_t sf_desc = smem_desc_plain(sf_slot(stage));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          tmem_copy_scales<1>(sfa + 4 * h, sf_desc + h * (kSfTileBytes / 16));
+          tmem_copy_scales<1>(sfb + 4 * h, sf_desc + (2 + h) * (kSfTileBytes / 16));
+        }
+        const uint64_t wd = smem_desc_sw128(w_slot(stage), 16, 1024);
+        const uint64_t td = smem_desc_sw128(t_slot(stage), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_mxf4_ss<1>(tmem_base, wd + kk * 2, td + kk * 2, idesc[kk & 1], sfa + 4 * (kk >> 1),
+                         sfb + 4 * (kk >> 1), (kb > kb0 || kk > 0) ? 1u : 0u);
+        mma_commit<1>(empty_bar(stage));
+        if (kb + 1 == kb1) mma_commit<1>(done_bar);
+      }
+      __syncwarp();
+      if (++stage == ST) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!ok) {
+      if (elect_one()) mma_commit_local<1>(drain_bar);
+      __syncwarp();
+      mbar_wait(drain_bar, 0, nullptr, p.limit_ns, kRoleMma, &g_device_error);
+    }
+  }
+
+  // ---------------------------------------------------------------- reduction and epilogue
+  // Warps 2..5 hold the accumulator: lane = row of B, column = token.
+  const int shift = 31 - __clz(kBM / ks);  // log2 of the rows of B this CTA finishes
+  const int rows_per = 1 << shift;
+  const uint32_t recv0 = s0 + Plan::kRecvOffset;
+  const int tid = static_cast<int>(threadIdx.x) - 64;
+  auto bias_of = [&](int col) {
+    return p.bias != nullptr && col < p.N ? load_elem<kBiasType<OUT>>(p.bias, col) : 0.0f;
+  };
+  __syncwarp();
+  if (ks > 1) cluster_wait();  // every CTA of the cluster runs
+  if (warp >= 2) {
+    const uint64_t tile_limit_ns = p.limit_ns + static_cast<uint64_t>(kb1 - kb0) * kWaitPerKBlockNs;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const float bias = ks == 1 ? bias_of(tile * kBM + row) : 0.0f;
+    const bool have =
+        __all_sync(0xffffffffu, mbar_wait(done_bar, 0, abort_flag, tile_limit_ns, kRoleEpilogue, &g_device_error));
+    if (have) {
+      tc_fence_after_sync();
+      uint32_t r[32];
+      tmem_load_32cols(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16), r);
+      if (ks == 1) {
+        // The activation over all tokens at once: its code runs from a cold instruction cache, so
+        // what counts is its length (per token, unrolled: 8.7 us at 16 tokens, 16384 x 4096).
+        const int col = tile * kBM + row;
+        float v[BN];
+#pragma unroll
+        for (int j = 0; j < BN; ++j) v[j] = __uint_as_float(r[j]) + bias;
+        activate_lane<OUT, BN>(p.act, v);
+        if (col < p.N) {
+          if (p.R != nullptr) {
+#pragma unroll
+            for (int j = 0; j < BN; ++j)
+              if (j < p.M) v[j] += load_elem<OUT>(p.R, j * p.ldr + col);
+          }
+#pragma unroll
+          for (int j = 0; j < BN; ++j)
+            if (j < p.M) store_elem<OUT>(p.C, j * p.ldc + col, v[j]);
+        }
+      } else {
+        const uint32_t dst =
+            mapa_shared(recv0, static_cast<uint32_t>(row >> shift)) +
+            static_cast<uint32_t>(((slice << shift) + (row & (rows_per - 1))) * Plan::kRecvRow * 4);
+#pragma unroll
+        for (int j = 0; j < BN; j += 4)
+          if (j < p.M) st_cluster_v4(dst + static_cast<uint32_t>(j * 4), r[j], r[j + 1], r[j + 2], r[j + 3]);
+      }
+    }
+    tc_fence_before_sync();
+  }
+  __syncwarp();
+  if (ks > 1)
+    cluster_sync_all();  // all partial sums are in place
+  else
+    __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc<1>(tmem_base, Plan::kTmemCols);
+  if (ks == 1 || tid < 0 || *abort_flag != 0u) return;
+  // This CTA's rows of B by the tokens: a thread keeps one row and takes every ks-th four tokens.
+  const int col = tile * kBM + (slice << shift) + (tid & (rows_per - 1));
+  if (col >= p.N) return;
+  const float bias = bias_of(col);
+  const uint32_t mine = recv0 + static_cast<uint32_t>((tid & (rows_per - 1)) * Plan::kRecvRow * 4);
+  const uint32_t slice_bytes = static_cast<uint32_t>((Plan::kRecvRow * 4) << shift);
+  for (int t0 = (tid >> shift) * 4; t0 < p.M; t0 += ks * 4) {
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int q = 0; q < ks; ++q) {
+      const uint4 x = ld_shared_v4(mine + static_cast<uint32_t>(q) * slice_bytes + static_cast<uint32_t>(t0 * 4));
+      f2_add_to(v[0], v[1], __uint_as_float(x.x), __uint_as_float(x.y));
+      f2_add_to(v[2], v[3], __uint_as_float(x.z), __uint_as_float(x.w));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] += bias;
+    activate_lane<OUT, 4>(p.act, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t token = t0 + j;
+      if (token < p.M) {
+        if (p.R != nullptr) v[j] += load_elem<OUT>(p.R, token * p.ldr + col);
+        store_elem<OUT>(p.C, token * p.ldc + col, v[j]);
+      }
+    }
   }
 }
 
