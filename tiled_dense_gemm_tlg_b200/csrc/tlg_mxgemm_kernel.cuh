@@ -4,7 +4,7 @@
 // block scaling): each product a * b * 2^(ea + eb) is exact and the sum is kept in fp32.
 //
 // The roles are the fp16 kernel's (tlg_gemm_kernel.cuh): a TMA producer warp, an MMA warp and
-// epilogue warps (eight here) over a ring of operand slots and two TMEM accumulators.  What
+// epilogue warps (sixteen here) over a ring of operand slots and two TMEM accumulators.  What
 // differs:
 //
 //  - A k-block is 256 elements, 128 bytes a row (one 128-byte swizzle row of 4-bit elements),
@@ -17,6 +17,14 @@
 //    bytes, which the producer only requested once the slot's earlier MMAs were done, also
 //    covers overwriting the scales those MMAs read.
 //
+//  - The epilogue of a tile has to fit beside a main loop four times as short, and one warp
+//    alone waits most of the time (for TMEM, shared memory, the special-function unit).  So
+//    sixteen warps, four to a quarter of the rows, take 32 columns each time, little enough
+//    for 96 registers, and load the bias and residual of their next tile's pieces while they
+//    work on this tile's (4096^3 with bias, GELU and residual, back to back: 35.9 us against 39
+//    with eight warps, 64 columns and both read where they are added; 16384 x 4096 x 1024:
+//    91 against 115).  Tried and dropped on the same box: ordinary stores from the box in place
+//    of TMA stores (108 us there), eight columns at a time in a rolled loop (119).
 //  - The 256-column accumulators overlap: TMEM holds two of 256 columns 128 apart and the
 //    scales of five slots.  The epilogue drains the shared 128 columns first and hands them
 //    back; the next tile's MMAs, into the other accumulator, start then.
@@ -103,7 +111,8 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-constexpr int kMxEpiWarps = 8;  // two to a quarter of the tile's rows, taking its 64-column pieces in turn
+constexpr int kMxEpiWarps = 16;  // four to a quarter of the tile's rows, taking its 32-column pieces in turn
+constexpr uint32_t kMxBoxBytes = 32 * 64;  // an epilogue warp's box: 32 rows x 64 bytes
 constexpr int kMxThreads = 32 * (2 + kMxEpiWarps);
 
 template <int CG, int BN, int STAGES>
@@ -118,11 +127,8 @@ struct MxPlan {
   static constexpr uint32_t kBOffset = STAGES * kABytes;
   static constexpr uint32_t kSfOffset = kBOffset + STAGES * kBBytes;
   static constexpr uint32_t kOutOffset = kSfOffset + STAGES * (kSfaBytes + kSfbBytes);
-  // Output boxes of an epilogue warp: two where they fit, so that one is filled while the TMA
-  // unit still reads the other.
-  static constexpr int kBoxes = kOutOffset + kMxEpiWarps * 2 * kStageOutBytes + 2 * BN * 4 + 2048 <= 232448 ? 2 : 1;
-  static constexpr uint32_t kBiasOffset = kOutOffset + kMxEpiWarps * kBoxes * kStageOutBytes;
-  static constexpr uint32_t kBarOffset = kBiasOffset + 2 * BN * 4;  // two tiles' bias in fp32
+  static constexpr uint32_t kBiasOffset = kOutOffset + kMxEpiWarps * kMxBoxBytes;
+  static constexpr uint32_t kBarOffset = kBiasOffset + kMxEpiWarps * 128;  // each warp's 32 columns of bias in fp32
   static constexpr uint32_t kNumBars = 2 * STAGES + 4 + 1;
   static constexpr uint32_t kMiscOffset = kBarOffset + kNumBars * 8;
   static constexpr uint32_t kDynamicBytes = kMiscOffset + 16 + 1024;
@@ -163,54 +169,115 @@ __device__ __forceinline__ void store_elem(void *p, int64_t i, float v) {
 template <int OUT>
 constexpr int kBiasType = OUT == kTypeBF16 ? kTypeBF16 : kTypeF16;
 
-// v[j] += R[row, col0 + j], j < 32 (R may be C: ordinary loads).
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4 &v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// The residual of a warp's 32 rows x 32 columns, loaded ahead (R may be C: ordinary loads, made
+// before the same warp's stores of these elements).  Four lanes load 64 bytes of a row, so
+// that a load instruction covers 8 rows in whole sectors (a row to each lane would cover 32,
+// half a sector each); mx_add_residual hands the rows to their lanes through the warp's output
+// box.  Ragged or unaligned pieces are read where they are added.
 template <int OUT>
-__device__ __forceinline__ void mx_add_residual_32(const MxGemmParams &p, int row, int col0, float (&v)[32]) {
-  if (row >= p.M) return;
-  const int64_t at = static_cast<int64_t>(row) * p.ldr + col0;
-  if (p.r_vec && col0 + 32 <= p.N) {
-    if constexpr (OUT == kTypeF32) {
-      const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p.R) + at);
+struct MxResidual {
+  static constexpr int kHalves = OUT == kTypeF32 ? 2 : 1;  // 64-byte pieces of a row
+  uint4 r[kHalves][4];
+  bool have;
+  float bias;  // of column (lane) of the piece
+};
+
+template <int OUT>
+__device__ __forceinline__ void mx_load_residual(const MxGemmParams &p, int row0, int col0, int lane,
+                                                 MxResidual<OUT> &x) {
+  if (p.bias != nullptr) x.bias = col0 + lane < p.N ? load_elem<kBiasType<OUT>>(p.bias, col0 + lane) : 0.0f;
+  x.have = p.R != nullptr && p.r_vec != 0 && col0 + 32 <= p.N;
+  if (x.have) {
+    const int row = row0 + (lane >> 2);
+    const char *q = static_cast<const char *>(p.R) +
+                    (static_cast<int64_t>(row) * p.ldr + col0) * kTypeBytes<OUT> + (lane & 3) * 16;
+    const int64_t step = 8 * p.ldr * kTypeBytes<OUT>;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const float4 w = q[c];
-        f2_add_to(v[4 * c], v[4 * c + 1], w.x, w.y);
-        f2_add_to(v[4 * c + 2], v[4 * c + 3], w.z, w.w);
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int h = 0; h < MxResidual<OUT>::kHalves; ++h)
+        if (row + 8 * i < p.M) x.r[h][i] = *reinterpret_cast<const uint4 *>(q + i * step + h * 64);
+    }
+  }
+}
+
+// box: the warp's box, read by all its lanes before this.
+template <int OUT>
+__device__ __forceinline__ void mx_add_residual(const MxGemmParams &p, int row, int col0, int lane, uint32_t box,
+                                                const MxResidual<OUT> &x, float (&v)[32]) {
+  if (x.have) {
+#pragma unroll
+    for (int h = 0; h < MxResidual<OUT>::kHalves; ++h) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = (lane >> 2) + 8 * i;
+        st_shared_v4(box + static_cast<uint32_t>(r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) * 16)), x.r[h][i]);
       }
-    } else {
-      const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.R) + at);
+      __syncwarp();
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint4 w = q[c];
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        const uint4 y = ld_shared_v4(box + static_cast<uint32_t>(lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16)));
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float lo, hi;
-          unpack2<OUT>(x[i], lo, hi);
-          f2_add_to(v[c * 8 + 2 * i], v[c * 8 + 2 * i + 1], lo, hi);
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (OUT == kTypeF32) {
+            v[16 * h + 4 * c + k] += __uint_as_float(w[k]);
+          } else if constexpr (OUT == kTypeF16) {
+            add_half2_to(v[8 * c + 2 * k], v[8 * c + 2 * k + 1], w[k]);
+          } else {
+            float lo, hi;
+            unpack2<OUT>(w[k], lo, hi);
+            f2_add_to(v[8 * c + 2 * k], v[8 * c + 2 * k + 1], lo, hi);
+          }
         }
       }
     }
-  } else {
+  } else if (row < p.M) {
+    const int64_t at = static_cast<int64_t>(row) * p.ldr + col0;
 #pragma unroll
     for (int j = 0; j < 32; ++j)
       if (col0 + j < p.N) v[j] += load_elem<OUT>(p.R, at + j);
   }
 }
 
-// Plain predicated stores of one thread's 128-byte row piece (see store_row_tail).
+// Writes one 64-byte row piece of a 32-row box; 16-byte piece c of row r sits at
+// (c ^ (r / 2 % 4)) * 16, so that eight lanes on eight rows, or on two whole rows, meet all banks.
+__device__ __forceinline__ void st_box_row_64(uint32_t box, int r, const uint32_t *w) {
+  const uint32_t row = box + static_cast<uint32_t>(r) * 64u;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + static_cast<uint32_t>((c ^ ((r >> 1) & 3)) * 16)),
+                 "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                 : "memory");
+}
+
+// Writes a warp's box (32 rows x 64 bytes, C's rows row0 .. and columns col0 ..) to a C that TMA
+// cannot store, element by element, neighbouring lanes on neighbouring columns.
 template <int OUT>
-__device__ __forceinline__ void mx_store_row(const MxGemmParams &p, int row, int col0, const uint32_t (&w)[32]) {
-  if (row >= p.M) return;
-  const int64_t at = static_cast<int64_t>(row) * p.ldc + col0;
-  if constexpr (OUT == kTypeF32) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (col0 + j < p.N) static_cast<uint32_t *>(p.C)[at + j] = w[j];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 64; ++j)
-      if (col0 + j < p.N) static_cast<uint16_t *>(p.C)[at + j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+__device__ __forceinline__ void mx_store_box(const MxGemmParams &p, int row0, int col0, int lane, uint32_t box) {
+  constexpr int B = kTypeBytes<OUT>;
+  constexpr int kCols = 64 / B;  // of the box
+  const int cc = lane % kCols;
+#pragma unroll 4
+  for (int r = lane / kCols; r < 32; r += 32 / kCols) {
+    const uint32_t at = box + static_cast<uint32_t>(r * 64 + (((cc * B / 16) ^ ((r >> 1) & 3)) * 16) + cc * B % 16);
+    if (row0 + r < p.M && col0 + cc < p.N) {
+      const int64_t to = static_cast<int64_t>(row0 + r) * p.ldc + col0 + cc;
+      if constexpr (B == 4) {
+        uint32_t y;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(y) : "r"(at) : "memory");
+        static_cast<uint32_t *>(p.C)[to] = y;
+      } else {
+        uint16_t y;
+        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(y) : "r"(at) : "memory");
+        static_cast<uint16_t *>(p.C)[to] = y;
+      }
+    }
   }
 }
 
@@ -405,127 +472,139 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     }
   } else if (warp >= 2) {
     // ---------------------------------------------------------------- epilogue (every CTA)
-    // Warp w drains TMEM lanes 32*(w%4) .. +31, 64 columns at a time, by way of a 4 KB box.  The
-    // two warps of a quarter take its pieces in turn.
+    // Warp w drains TMEM lanes 32*(w%4) .. +31, 32 columns at a time, by way of a 2 KB box.  The
+    // four warps of a quarter take its pieces in turn.
     const int quarter = warp & 3;
     const int ew = warp - 2;
     const int side = ew >> 2;
-    constexpr int kPieces = BN / 64;
-    const uint32_t box0 = s0 + Plan::kOutOffset + static_cast<uint32_t>(ew * Plan::kBoxes) * kStageOutBytes;
-    uint32_t boxes_used = 0;
+    constexpr int kPieces = BN / 32;
+    const uint32_t box = s0 + Plan::kOutOffset + static_cast<uint32_t>(ew) * kMxBoxBytes;
     const uint32_t release_bar0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
-    constexpr int kBoxCols = OUT == kTypeF32 ? 32 : 64;
-    int acc = 0;
-    int bias_buf = 0;
+    constexpr int kBoxCols = 64 / kTypeBytes<OUT>;  // 32 columns of a 16-bit type, 16 of fp32
     uint32_t j = 0;
     const uint64_t tile_limit_ns = p.limit_ns + static_cast<uint64_t>(p.num_kb) * kWaitPerKBlockNs;
-    for (int t = unit; t < tiles; t += num_units, ++j) {
+    // First row of this warp and first column of tile t; the tile column of piece i.
+    int row0 = 0, col_t = 0;
+    auto place = [&](int t) {
       int mb, nb;
       tile_coords(t, num_m, num_n, p.raster_group, mb, nb);
-      const int row0 = mb * kTileM + static_cast<int>(rank) * kBM + quarter * 32;
-      const int row = row0 + lane;
-      const uint32_t sbias = s0 + Plan::kBiasOffset + static_cast<uint32_t>(bias_buf * BN * 4);
-      if (EPI && p.bias != nullptr) {
-        // The tile's bias in fp32, in the buffer of the tile before last (whose readers have
-        // passed the barrier of the last tile).
-        float *sb = reinterpret_cast<float *>(smem + Plan::kBiasOffset) + bias_buf * BN;
-        for (int c = ew * 32 + lane; c < BN; c += 32 * kMxEpiWarps) {
-          const int col = nb * BN + c;
-          sb[c] = col < p.N ? load_elem<kBiasType<OUT>>(p.bias, col) : 0.0f;
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kMxEpiWarps) : "memory");
-        bias_buf ^= 1;
+      row0 = mb * kTileM + static_cast<int>(rank) * kBM + quarter * 32;
+      col_t = nb * BN;
+    };
+    auto piece_col = [&](int i, uint32_t tile) {
+      // Overlapping accumulators: the shared columns (the upper half of accumulator 0, the lower
+      // of accumulator 1) first.
+      return 32 * (Plan::kOverlap && (tile & 1u) == 0 ? (i + 4) % 8 : i);
+    };
+    // The bias and residual of this warp's pieces of a tile are loaded while it works on the tile
+    // before (an fp32 residual, twice the registers, one piece ahead).
+    constexpr int kMine = (kPieces + 3) / 4;
+    constexpr int kSets = OUT == kTypeF32 ? 1 : kMine;
+    MxResidual<OUT> res[kSets];
+    const uint32_t sbias = s0 + Plan::kBiasOffset + static_cast<uint32_t>(ew) * 128u;
+    if (unit < tiles) place(unit);
+    if constexpr (EPI) {
+      if (unit < tiles) {
+#pragma unroll
+        for (int k = 0; k < kSets; ++k)
+          if (side + 4 * k < kPieces) mx_load_residual<OUT>(p, row0, col_t + piece_col(side + 4 * k, 0), lane, res[k]);
       }
-      // On a timeout the warp stops reading tiles but keeps meeting the bias barrier, so no
-      // other epilogue warp waits at it for good.
+    }
+    for (int t = unit; t < tiles; t += num_units, ++j) {
+      // On a timeout the warp stops reading tiles.
       bool ok = *abort_flag == 0u;
       if (ok && !mbar_wait(tfull_bar(j % Plan::kAccBars), (j / Plan::kAccBars) & 1u, abort_flag, tile_limit_ns,
                            kRoleEpilogue, &g_device_error))
         ok = false;
       ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        tc_fence_after_sync();
-        auto release = [&]() {
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (CG == 2)
-              mbar_arrive_cluster(release_bar0 + 8u * (j % Plan::kAccBars));
-            else
-              mbar_arrive(release_bar0 + 8u * (j % Plan::kAccBars));
-          }
-        };
-        if (side >= kPieces) release();
-#pragma unroll 1
-        for (int i = side; i < kPieces; i += 2) {
-          // Overlapping accumulators: the shared columns (the upper half of accumulator 0, the
-          // lower of accumulator 1) first.
-          const int tc = 64 * (Plan::kOverlap && acc == 0 ? (i + 2) % 4 : i);
-          const int col0 = nb * BN + tc;
-          uint32_t ra[32], rb[32];
-          __syncwarp();
-          tmem_load_2x32cols(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                 static_cast<uint32_t>(acc * Plan::kAccStride + tc),
-                             ra, rb);
-          if (Plan::kOverlap ? i < 2 : i + 2 >= kPieces) release();
-          if (row0 >= p.M || col0 >= p.N) continue;
-          float va[32], vb[32];
+      const int tile_row0 = row0, tile_col = col_t;
+      if (t + num_units < tiles) place(t + num_units);  // where the next residual comes from
+      if (!ok) continue;
+      tc_fence_after_sync();
+      auto release = [&]() {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2)
+            mbar_arrive_cluster(release_bar0 + 8u * (j % Plan::kAccBars));
+          else
+            mbar_arrive(release_bar0 + 8u * (j % Plan::kAccBars));
+        }
+      };
+      if (side >= kPieces) release();
+      const int row = tile_row0 + lane;
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            va[c] = __uint_as_float(ra[c]);
-            vb[c] = __uint_as_float(rb[c]);
+      for (int k = 0; k < kMine; ++k) {
+        const int i = side + 4 * k;
+        if (i >= kPieces) break;
+        const int tc = piece_col(i, j);
+        const int col0 = tile_col + tc;
+        const uint32_t acc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                             static_cast<uint32_t>((j & 1u) * Plan::kAccStride + tc);
+        const bool releases = Plan::kOverlap ? i < 4 : i + 4 >= kPieces;
+        const bool inside = tile_row0 < p.M && col0 < p.N;
+        auto box_free = [&]() {  // its last store has read it, and so has every lane
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+        };
+        float v[32];
+        {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_load_32cols(acc, r);
+          if (releases) release();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
+        }
+        if constexpr (EPI) {
+          MxResidual<OUT> &ahead = res[k % kSets];
+          if (inside) {
+            if (p.bias != nullptr) {
+              st_shared_u32(sbias + static_cast<uint32_t>(lane * 4), __float_as_uint(ahead.bias));
+              __syncwarp();
+              add_bias_smem_32(sbias, 0, v);
+            }
+            activate_lane<OUT, 32>(p.act, v);
+            if (p.R != nullptr) {
+              box_free();
+              mx_add_residual<OUT>(p, row, col0, lane, box, ahead, v);
+            }
+            __syncwarp();  // every lane has read the bias
           }
-          auto finish = [&](float(&v)[32], int half) {
-            if constexpr (EPI) {
-              if (p.bias != nullptr) add_bias_smem_32(sbias, tc + 32 * half, v);
-              activate_lane<OUT, 32>(p.act, v);
-              if (p.R != nullptr) mx_add_residual_32<OUT>(p, row, col0 + 32 * half, v);
-            }
-          };
-          auto put = [&](const uint32_t(&w)[32], int col) {
-            if (p.c_plain || (!p.n_aligned && col + kBoxCols > p.N)) {
-              mx_store_row<OUT>(p, row, col, w);
-              return;
-            }
-            const uint32_t box = box0 + boxes_used % Plan::kBoxes * kStageOutBytes;
-            ++boxes_used;
-            if (lane == 0) bulk_wait_group_read<Plan::kBoxes - 1>();  // this box's previous store has read it
+          if (kSets == 1 && kMine > 1 && i + 4 < kPieces)
+            mx_load_residual<OUT>(p, tile_row0, tile_col + piece_col(i + 4, j), lane, ahead);
+          else if (t + num_units < tiles)
+            mx_load_residual<OUT>(p, row0, col_t + piece_col(kSets == 1 ? side : i, j + 1), lane, ahead);
+        }
+        if (!inside) continue;
+#pragma unroll
+        for (int h = 0; h < 32 / kBoxCols; ++h) {
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            if constexpr (OUT == kTypeF32)
+              w[c] = __float_as_uint(v[16 * h + c]);
+            else
+              w[c] = pack2<OUT>(v[2 * c], v[2 * c + 1]);
+          }
+          box_free();
+          st_box_row_64(box, lane, w);
+          const int c0 = col0 + h * kBoxCols;
+          if (p.c_plain || (!p.n_aligned && c0 + kBoxCols > p.N)) {
             __syncwarp();
-            st_box_row(box, lane, w, 0);
+            mx_store_box<OUT>(p, tile_row0, c0, lane, box);
+          } else {
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&tmC, box, col, row0);
+            if (lane == 0 && c0 < p.N) {
+              tma_store_2d(&tmC, box, c0, tile_row0);
               bulk_commit_group();
             }
-          };
-          if constexpr (OUT == kTypeF32) {
-            uint32_t w[32];
-            finish(va, 0);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(va[j]);
-            put(w, col0);
-            if (col0 + 32 < p.N) {
-              finish(vb, 1);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(vb[j]);
-              put(w, col0 + 32);
-            }
-          } else {
-            uint32_t w[32];
-            finish(va, 0);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = pack2<OUT>(va[2 * j], va[2 * j + 1]);
-            finish(vb, 1);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) w[16 + j] = pack2<OUT>(vb[2 * j], vb[2 * j + 1]);
-            put(w, col0);
           }
         }
       }
-      acc ^= 1;
     }
-    if (lane == 0) bulk_wait_group<0>();
+    if (lane == 0) bulk_wait_group<0>();  // every store of this warp has completed
     __syncwarp();
   }
 
