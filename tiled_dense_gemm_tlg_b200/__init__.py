@@ -44,6 +44,11 @@ if not os.path.exists(LIB_PATH):
         "(there is no CPU fallback)")
 
 _lib = ctypes.CDLL(LIB_PATH)
+try:
+    from . import _binding  # marshals tensors for the MX entry points (csrc/tlg_binding.cpp)
+except ImportError as e:
+    raise ImportError("_binding.so is missing or does not load: build it with "
+                      "`python tiled_dense_gemm_tlg_b200/build.py`") from e
 
 TLG_OK, TLG_ERR_INVALID_ARG, TLG_ERR_ALIGNMENT, TLG_ERR_UNSUPPORTED, TLG_ERR_CUDA, TLG_ERR_TIMEOUT = range(6)
 TLG_OUT_F32, TLG_OUT_F16 = 0, 1
@@ -54,10 +59,8 @@ _ACT = {"none": TLG_ACT_NONE, "relu": TLG_ACT_RELU, "gelu": TLG_ACT_GELU, "silu"
         "gelu_tanh": TLG_ACT_GELU_TANH}
 TLG_TYPE_F32, TLG_TYPE_F16, TLG_TYPE_BF16 = 0, 1, 2
 TLG_MX_E2M1, TLG_MX_E4M3 = 0, 1
-_TYPES = {"f32": (TLG_TYPE_F32, torch.float32), "f16": (TLG_TYPE_F16, torch.float16),
-          "bf16": (TLG_TYPE_BF16, torch.bfloat16)}
-_TYPE_OF = {dt: code for code, dt in _TYPES.values()}
-_FORMATS = {"e2m1": (TLG_MX_E2M1, 16), "e4m3": (TLG_MX_E4M3, 32)}  # code, bytes of a block
+_TYPES = {"f32": TLG_TYPE_F32, "f16": TLG_TYPE_F16, "bf16": TLG_TYPE_BF16}
+_FORMATS = {"e2m1": TLG_MX_E2M1, "e4m3": TLG_MX_E4M3}
 
 EXPORTED = ("tlg_gemm_f16f32", "tlg_gemm_f16f16", "tlg_gemm_bias_relu_f16", "tlg_gemm_ex",
             "tlg_gemm_op", "tlg_gemm_fused", "tlg_gemm_ex_noalloc", "tlg_gemm_workspace_size",
@@ -422,64 +425,22 @@ def _activation(activation: str) -> int:
     return _ACT[activation]
 
 
-def _stream_of(stream, device: int) -> int:
-    if stream is not None:
-        return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-    return _raw_stream(device) if device >= 0 else 0
+def _handle(stream):
+    """A stream argument as the binding takes it: a handle, or None for the current stream."""
+    return stream if stream is None else int(getattr(stream, "cuda_stream", stream))
 
 
-def _type_code(t: torch.Tensor, name: str) -> int:
-    code = _TYPE_OF.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be fp32, fp16 or bf16")
-    return code
-
-
-def _same_device(device: int, *tensors):
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError("all tensors must be on one device")
-
-
-def _mx_scale_bytes(rows: int, blocks: int) -> int:
-    return -(-rows // 128) * -(-blocks // 4) * 512
-
-
-def _mx(Q: torch.Tensor, S: torch.Tensor, rows: int, blocks: int, block_bytes: int, name: str = ""):
-    """Checks an MX matrix's two buffers; returns the arguments (Q, ldq, S)."""
-    q, ldq = _mat(Q, f"Q{name}")
-    if Q.dtype != torch.uint8 or Q.shape != (rows, blocks * block_bytes):
-        raise ValueError(f"Q{name} must be a uint8 tensor of shape ({rows}, {blocks * block_bytes})")
-    if S.dtype != torch.uint8 or not S.is_contiguous() or S.numel() < _mx_scale_bytes(rows, blocks):
-        raise ValueError(f"S{name} must be a contiguous uint8 tensor of at least "
-                         f"{_mx_scale_bytes(rows, blocks)} bytes")
-    return q, ldq, S.data_ptr()
-
-
-def _new(rows: int, cols: int, dtype, device):
-    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
-
-
-def _mx_out(Q, S, rows: int, cols: int, block_bytes: int, like: torch.Tensor, device: int):
-    """The MX matrix an operator writes, allocated where not given: (Q, S) and its arguments."""
-    blocks = (cols + 31) // 32
-    if Q is None and S is None:
-        row_bytes = blocks * block_bytes
-        Q = _new(rows, row_bytes, torch.uint8, like.device)
-        S = torch.empty_strided((_mx_scale_bytes(rows, blocks),), (1,), dtype=torch.uint8, device=like.device)
-        return Q, S, Q.data_ptr(), row_bytes, S.data_ptr()
-    if Q is None:
-        Q = _new(rows, blocks * block_bytes, torch.uint8, like.device)
-    if S is None:
-        S = torch.empty(_mx_scale_bytes(rows, blocks), dtype=torch.uint8, device=like.device)
-    _same_device(device, Q, S)
-    return (Q, S) + _mx(Q, S, rows, blocks, block_bytes)
+def _result(r, where: str):
+    """The binding's outputs, or the library's status raised."""
+    if type(r) is int:
+        raise TlgError(r, where)
+    return r
 
 
 def tlg_mx_size(format: str, rows: int, cols: int):
     """(bytes of one row of Q, bytes of S) of a rows x cols MX matrix."""
     q, s = ctypes.c_int64(0), _sz(0)
-    _check(_lib.tlg_mx_size(_format(format)[0], rows, cols, ctypes.byref(q), ctypes.byref(s)), "tlg_mx_size")
+    _check(_lib.tlg_mx_size(_format(format), rows, cols, ctypes.byref(q), ctypes.byref(s)), "tlg_mx_size")
     return int(q.value), int(s.value)
 
 
@@ -487,37 +448,15 @@ def tlg_mx_quantize(X: torch.Tensor, format: str = "e2m1", op: str = "N", Q: tor
                     S: torch.Tensor | None = None, stream=None):
     """(Q, S): X (fp32, fp16 or bf16) in blocks of 32 along its rows; ``op="T"`` quantises X's
     transpose, in blocks down its columns.  ``format``: "e2m1" (4 bits) or "e4m3" (8 bits)."""
-    fmt, block_bytes = _format(format)
-    px, ldx = _mat(X, "X")
-    code = _type_code(X, "X")
-    t = op == "T" or op == "t"
-    cols, rows = X.shape if t else (X.shape[1], X.shape[0])
-    device = X.get_device()
-    Q, S, q, ldq, s = _mx_out(Q, S, rows, cols, block_bytes, X, device)
-    _check(_lib.tlg_mx_quantize(fmt, rows, cols, t, code, px, ldx, q, ldq, s, _stream_of(stream, device)),
-           "tlg_mx_quantize")
-    return Q, S
+    return _result(_binding.mx_quantize(X, _format(format), op == "T" or op == "t", Q, S, _handle(stream)),
+                   "tlg_mx_quantize")
 
 
 def tlg_mx_dequantize(Q: torch.Tensor, S: torch.Tensor, cols: int, format: str = "e2m1", out: str = "f16",
                       X: torch.Tensor | None = None, stream=None):
     """The values of an MX matrix with ``cols`` columns, as "f32", "f16" or "bf16"."""
-    fmt, block_bytes = _format(format)
-    code, dtype = _out_type(out)
-    rows = Q.shape[0]
-    device = Q.get_device()
-    q, ldq, s = _mx(Q, S, rows, (cols + 31) // 32, block_bytes)
-    if X is None:
-        X = _new(rows, cols, dtype, Q.device)
-        px, ldx = X.data_ptr(), cols
-    else:
-        if X.dtype != dtype or X.shape != (rows, cols):
-            raise ValueError(f"X must be {dtype} of shape ({rows}, {cols})")
-        px, ldx = _mat(X, "X")
-    _same_device(device, X, S)
-    _check(_lib.tlg_mx_dequantize(fmt, rows, cols, q, ldq, s, code, px, ldx, _stream_of(stream, device)),
-           "tlg_mx_dequantize")
-    return X
+    return _result(_binding.mx_dequantize(Q, S, cols, _format(format), _out_type(out), X, _handle(stream)),
+                   "tlg_mx_dequantize")
 
 
 def tlg_gemm_mxfp4(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch.Tensor,
@@ -527,73 +466,28 @@ def tlg_gemm_mxfp4(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch
     """C = act(A.B^T + bias[col]) + residual[row, col]: A (M x K) and B (N x K) are 4-bit MX matrices
     (``tlg_mx_quantize(..., format="e2m1")``), C is "f32", "f16" or "bf16".  The bias is fp16, or
     bf16 for a bf16 C; the residual has C's type and may be ``C`` itself."""
-    M, kb = A.shape
-    N, kb2 = B.shape
-    if kb2 != kb or kb % 16:
-        raise ValueError(f"A and B must hold whole blocks of one K: {tuple(A.shape)} and {tuple(B.shape)} bytes")
-    code, dtype = _out_type(out)
-    device = A.get_device()
-    pa, lda, psa = _mx(A, SA, M, kb // 16, 16, "A")
-    pb, ldb, psb = _mx(B, SB, N, kb // 16, 16, "B")
-    if C is None:
-        C = _new(M, N, dtype, A.device)
-        pc, ldc = C.data_ptr(), N
-    else:
-        if C.dtype != dtype or C.shape != (M, N):
-            raise ValueError(f"C must be {dtype} of shape ({M}, {N})")
-        pc, ldc = _mat(C, "C")
-    epi = None
-    if bias is not None or residual is not None or activation != "none":
-        epi = tlg_fused_epilogue(None, _activation(activation), None, 0)
-        if bias is not None:
-            bdt = torch.bfloat16 if out == "bf16" else torch.float16
-            if bias.dtype != bdt or bias.shape != (N,) or (N > 1 and bias.stride(0) != 1):
-                raise ValueError(f"bias must be a contiguous {bdt} vector of length {N}")
-            epi.bias = bias.data_ptr()
-        if residual is not None:
-            if residual.dtype != dtype or residual.shape != (M, N):
-                raise ValueError(f"residual must be {dtype} of shape ({M}, {N})")
-            epi.residual, epi.ldr = _mat(residual, "residual")
-        epi = ctypes.byref(epi)
-    _same_device(device, SA, B, SB, C, bias, residual)
-    cfg = ctypes.byref(tlg_config(**{k: int(v) for k, v in config.items()})) if config is not None else None
-    _check(_lib.tlg_gemm_mxfp4(M, N, kb * 2, pa, lda, psa, pb, ldb, psb, epi, pc, ldc, code, cfg,
-                               _stream_of(stream, device)), "tlg_gemm_mxfp4")
-    return C
+    cfg = tlg_config(**{k: int(v) for k, v in config.items()}) if config is not None else None
+    return _result(_binding.gemm_mxfp4(A, SA, B, SB, bias, _activation(activation), residual, C, _out_type(out),
+                                       ctypes.addressof(cfg) if cfg is not None else 0, _handle(stream)),
+                   "tlg_gemm_mxfp4")
 
 
 def tlg_choose_config_mxfp4(M: int, N: int, K: int, out: str = "f16", request: dict | None = None) -> dict:
     """The configuration tlg_gemm_mxfp4 would run for this shape (request fields of 0 = automatic)."""
     cfg = tlg_config(**{k: int(v) for k, v in (request or {}).items()})
-    _check(_lib.tlg_choose_config_mxfp4(M, N, K, _out_type(out)[0], ctypes.byref(cfg)), "tlg_choose_config_mxfp4")
+    _check(_lib.tlg_choose_config_mxfp4(M, N, K, _out_type(out), ctypes.byref(cfg)), "tlg_choose_config_mxfp4")
     return cfg.as_dict()
 
 
 def tlg_act_forward_mx(Z: torch.Tensor, activation: str, Y: torch.Tensor | None = None,
                        Q: torch.Tensor | None = None, S: torch.Tensor | None = None, stream=None):
     """(Y, Q, S): Y = act(Z) in Z's type (``Y`` may be ``Z`` itself), and Z saved in 8 bits (E4M3)."""
-    act = _activation(activation)
-    pz, ldz = _mat(Z, "Z")
-    code = _type_code(Z, "Z")
-    rows, cols = Z.shape
-    device = Z.get_device()
-    if Y is None:
-        Y = _new(rows, cols, Z.dtype, Z.device)
-        py, ldy = Y.data_ptr(), cols
-    else:
-        if Y.dtype != Z.dtype or Y.shape != Z.shape:
-            raise ValueError(f"Y must be {Z.dtype} of shape ({rows}, {cols})")
-        py, ldy = _mat(Y, "Y")
-        _same_device(device, Y)
-    Q, S, q, ldq, s = _mx_out(Q, S, rows, cols, 32, Z, device)
-    _check(_lib.tlg_act_forward_mx(rows, cols, act, code, pz, ldz, py, ldy, q, ldq, s, _stream_of(stream, device)),
-           "tlg_act_forward_mx")
-    return Y, Q, S
+    return _result(_binding.act_forward_mx(Z, _activation(activation), Y, Q, S, _handle(stream)), "tlg_act_forward_mx")
 
 
 def tlg_act_backward_mx_workspace_size(rows: int, cols: int, type: str = "f16") -> int:
     n = _sz(0)
-    _check(_lib.tlg_act_backward_mx_workspace_size(rows, cols, _out_type(type)[0], ctypes.byref(n)),
+    _check(_lib.tlg_act_backward_mx_workspace_size(rows, cols, _out_type(type), ctypes.byref(n)),
            "tlg_act_backward_mx_workspace_size")
     return int(n.value)
 
@@ -604,38 +498,8 @@ def tlg_act_backward_mx(dY: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, acti
     """(dZ, dbias): dZ = dY * act'(Z) in dY's type (``dZ`` may be ``dY`` itself), Z read from its 8-bit
     checkpoint, and the fp32 column sums of dZ (None with ``bias_grad=False``).  ``workspace``: a
     device buffer of tlg_act_backward_mx_workspace_size bytes; allocated here when not given."""
-    act = _activation(activation)
-    py, ldy = _mat(dY, "dY")
-    code = _type_code(dY, "dY")
-    rows, cols = dY.shape
-    device = dY.get_device()
-    q, ldq, s = _mx(Q, S, rows, (cols + 31) // 32, 32)
-    if dZ is None:
-        dZ = _new(rows, cols, dY.dtype, dY.device)
-        pz, ldz = dZ.data_ptr(), cols
-    else:
-        if dZ.dtype != dY.dtype or dZ.shape != dY.shape:
-            raise ValueError(f"dZ must be {dY.dtype} of shape ({rows}, {cols})")
-        pz, ldz = _mat(dZ, "dZ")
-    pb, ws_ptr, ws_bytes = None, None, 0
-    if bias_grad or dbias is not None:
-        if dbias is None:
-            dbias = torch.empty_strided((cols,), (1,), dtype=torch.float32, device=dY.device)
-        elif dbias.dtype != torch.float32 or dbias.shape != (cols,) or not dbias.is_contiguous():
-            raise ValueError(f"dbias must be a contiguous fp32 vector of length {cols}")
-        pb = dbias.data_ptr()
-        if workspace is None:
-            n = _sz(0)
-            _check(_lib.tlg_act_backward_mx_workspace_size(rows, cols, code, ctypes.byref(n)),
-                   "tlg_act_backward_mx_workspace_size")
-            if n.value:
-                workspace = torch.empty_strided((n.value,), (1,), dtype=torch.uint8, device=dY.device)
-        if workspace is not None:
-            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _same_device(device, Q, S, dZ, dbias, workspace)
-    _check(_lib.tlg_act_backward_mx(rows, cols, act, code, py, ldy, q, ldq, s, pz, ldz, pb, ws_ptr, ws_bytes,
-                                    _stream_of(stream, device)), "tlg_act_backward_mx")
-    return dZ, dbias
+    return _result(_binding.act_backward_mx(dY, Q, S, _activation(activation), dZ, dbias, bool(bias_grad), workspace,
+                                            _handle(stream)), "tlg_act_backward_mx")
 
 
 def raw_library():

@@ -1,4 +1,4 @@
-"""Build libtlg.so in-tree with nvcc for sm_100a (B200).
+"""Build libtlg.so in-tree with nvcc for sm_100a (B200), and the Python binding's native part.
 
     python tiled_dense_gemm_tlg_b200/build.py [--force]
 
@@ -7,7 +7,8 @@
 The library is plain CUDA C++ behind the C interface in include/tlg.h; it does
 not link against torch.  The CUDA runtime is linked statically and the one
 driver call it needs (tensor-map encoding) is looked up at run time, so the
-library builds on a machine without a GPU or driver.
+library builds on a machine without a GPU or driver.  _binding.so (tlg_binding.cpp, g++)
+marshals torch tensors into calls of the library; it alone links against torch.
 """
 
 from __future__ import annotations
@@ -23,6 +24,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtlg.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "tlg_binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-O2", "--expt-relaxed-constexpr",
@@ -52,6 +55,36 @@ def needs_build() -> bool:
     return any(os.path.getmtime(f) > t for f in inputs())
 
 
+def binding_needs_build() -> bool:
+    if not os.path.exists(BINDING):
+        return True
+    t = os.path.getmtime(BINDING)
+    return any(os.path.getmtime(f) > t for f in (BINDING_SRC, os.path.join(INCLUDE, "tlg.h"), os.path.abspath(__file__)))
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile tlg_binding.cpp against the running interpreter's torch; links the libtlg.so beside it."""
+    if not (force or binding_needs_build()):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    incs = [INCLUDE, *include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(a for i in incs for a in ("-isystem", i)), "-o", tmp, BINDING_SRC, "-L", PKG, "-ltlg", "-L", torch_lib,
+           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + (res.stdout + res.stderr)[-20000:])
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def _compile(src: str, obj: str):
     cmd = [nvcc(), *ARCH, *FLAGS, "-I", INCLUDE, "-I", CSRC, "-Xcompiler", "-fPIC", "-c", "-o", obj, src]
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -59,8 +92,10 @@ def _compile(src: str, obj: str):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every .cu (one translation unit per operand layout, in parallel) and link libtlg.so."""
+    """Compile every .cu (one translation unit per operand layout, in parallel), link libtlg.so, and
+    build the binding's native part beside it."""
     if not (force or needs_build()):
+        build_binding()
         return LIB
     import concurrent.futures
 
@@ -92,6 +127,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         sys.stderr.write("\n".join(log_lines))
     os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
 
 
