@@ -182,27 +182,33 @@ __device__ __forceinline__ void issue_load_mx(const uint8_t *q, const uint8_t *s
   }
 }
 
-// The row kernels: a CTA owns a stripe of U * 32 * E columns (U pieces of 32 * E) and the rows
-// [blockIdx.y * rows_per, +rows_per); its warps take the rows in turn.  Of one row a warp loads
-// all U pieces before it works on the first (16 * U bytes a lane in flight); with the columns
-// fixed, each row costs a few pointer steps, and the pieces of a row are constant distances
-// apart in every matrix.  (An item-at-a-time walk over rows and pieces spent 13 instructions an
-// element on quantising, most of them on addresses.)
+// The row kernels: a warp owns a stripe of U * 32 * E columns (U pieces of 32 * E) and some of the
+// rows [blockIdx.y * rows_per, +rows_per) of its CTA.  Of one row it loads all U pieces before it
+// works on the first (16 * U bytes a lane in flight); with the columns fixed, each row costs a
+// few pointer steps, and the pieces of a row are constant distances apart in every matrix.  (An
+// item-at-a-time walk over rows and pieces spent 13 instructions an element on quantising, most
+// of them on addresses.)  2^across of a CTA's warps lie side by side, the others take the next
+// rows.
 template <int T, int U>
 struct Stripe {
   static constexpr int E = kLaneElems<T>;
   static constexpr int kPiece = 32 * E;              // columns of a piece
   static constexpr int kPieceScales = kPiece / kMxBlock / 4 * 512;  // bytes between two pieces' scales
   uint32_t c0;    // first column
-  int left;       // columns from c0 on
+  int left;       // columns from c0 on, 0 for a warp past the last one
   int block;      // this lane's block in piece 0
-  uint32_t r0, r1;
-  __device__ __forceinline__ Stripe(uint32_t rows, uint32_t cols, uint32_t rows_per, int lane) {
-    c0 = blockIdx.x * (kPiece * U);
-    left = static_cast<int>(min(cols - c0, uint32_t(kPiece * U)));
+  uint32_t r, step, r1;  // this warp's rows: r, r + step, ... below r1
+  __device__ __forceinline__ Stripe(uint32_t rows, uint32_t cols, uint32_t rows_per, int across, int lane, int warp) {
+    const int side = warp & ((1 << across) - 1);
+    const uint32_t at = ((blockIdx.x << across) + static_cast<uint32_t>(side)) * (kPiece * U);
+    const uint32_t r0 = blockIdx.y * rows_per;
+    const bool in = at < cols;
+    c0 = in ? at : 0;
+    left = in ? static_cast<int>(min(cols - c0, uint32_t(kPiece * U))) : 0;
     block = static_cast<int>(c0 / kMxBlock) + lane * E / kMxBlock;
-    r0 = blockIdx.y * rows_per;
-    r1 = min(rows, r0 + rows_per);
+    r1 = in ? min(rows, r0 + rows_per) : 0;
+    r = r0 + (warp >> across);
+    step = kRowWarps >> across;
   }
   // Bytes of this lane's elements in a row of an ordinary matrix / of an MX matrix.
   __device__ __forceinline__ int64_t at(int lane, bool vec) const {
@@ -224,7 +230,7 @@ __device__ __forceinline__ int64_t scale_row(uint32_t row, int64_t tile_row_byte
 template <int T, int FMT, bool ACT, bool VEC, int U>
 __global__ void __launch_bounds__(kRowThreads, 4)
     quantize_rows_kernel(const RowMat x, const MxMat o, const RowMat y, int act, uint32_t rows,
-                         uint32_t cols, uint32_t rows_per) {
+                         uint32_t cols, uint32_t rows_per, int across) {
   using St = Stripe<T, U>;
   constexpr int E = St::E, B = kTypeBytes<T>;
   constexpr int kLanesPerBlock = kMxBlock / E;
@@ -233,16 +239,16 @@ __global__ void __launch_bounds__(kRowThreads, 4)
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t *st = stage[VEC ? 0 : warp];
-  const St s(rows, cols, rows_per, lane);
+  const St s(rows, cols, rows_per, across, lane, warp);
   const int64_t tile_row = o.tiles_x * 512;
-  const char *src = static_cast<const char *>(x.p) + static_cast<int64_t>(s.r0 + warp) * x.ld * B + s.at(0, false);
-  char *dst = static_cast<char *>(const_cast<void *>(y.p)) + static_cast<int64_t>(s.r0 + warp) * y.ld * B + s.at(0, false);
-  uint8_t *oq = const_cast<uint8_t *>(o.q) + static_cast<int64_t>(s.r0 + warp) * o.ldq + s.template q_at<FMT>(lane);
+  const char *src = static_cast<const char *>(x.p) + static_cast<int64_t>(s.r) * x.ld * B + s.at(0, false);
+  char *dst = static_cast<char *>(const_cast<void *>(y.p)) + static_cast<int64_t>(s.r) * y.ld * B + s.at(0, false);
+  uint8_t *oq = const_cast<uint8_t *>(o.q) + static_cast<int64_t>(s.r) * o.ldq + s.template q_at<FMT>(lane);
   uint8_t *os = const_cast<uint8_t *>(o.s) + scale_offset(0, s.block, o.tiles_x);
   // Whole stripes (all but the last) need no column checks.
   auto run = [&](auto full) {
     constexpr bool kFull = decltype(full)::value;
-    for (uint32_t r = s.r0 + warp; r < s.r1; r += kRowWarps) {
+    for (uint32_t r = s.r; r < s.r1; r += s.step) {
       uint32_t w[U][4];
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -272,9 +278,9 @@ __global__ void __launch_bounds__(kRowThreads, 4)
           }
         }
       }
-      src += kRowWarps * x.ld * B;
-      oq += kRowWarps * o.ldq;
-      if constexpr (ACT) dst += kRowWarps * y.ld * B;
+      src += s.step * x.ld * B;
+      oq += s.step * o.ldq;
+      if constexpr (ACT) dst += s.step * y.ld * B;
     }
   };
   if (s.left == St::kPiece * U)
@@ -285,7 +291,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 
 template <int T, int FMT, bool VEC, int U>
 __global__ void __launch_bounds__(kRowThreads, 4)
-    dequantize_rows_kernel(const MxMat in, const RowMat x, uint32_t rows, uint32_t cols, uint32_t rows_per) {
+    dequantize_rows_kernel(const MxMat in, const RowMat x, uint32_t rows, uint32_t cols, uint32_t rows_per, int across) {
   using St = Stripe<T, U>;
   constexpr int E = St::E, B = kTypeBytes<T>;
   __shared__ __align__(16) uint32_t stage[VEC ? 1 : kRowWarps][128];
@@ -293,15 +299,15 @@ __global__ void __launch_bounds__(kRowThreads, 4)
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t *st = stage[VEC ? 0 : warp];
-  const St s(rows, cols, rows_per, lane);
+  const St s(rows, cols, rows_per, across, lane, warp);
   const int64_t tile_row = in.tiles_x * 512;
-  char *dst = static_cast<char *>(const_cast<void *>(x.p)) + static_cast<int64_t>(s.r0 + warp) * x.ld * B + s.at(0, false);
-  const uint8_t *iq = in.q + static_cast<int64_t>(s.r0 + warp) * in.ldq + s.template q_at<FMT>(lane);
+  char *dst = static_cast<char *>(const_cast<void *>(x.p)) + static_cast<int64_t>(s.r) * x.ld * B + s.at(0, false);
+  const uint8_t *iq = in.q + static_cast<int64_t>(s.r) * in.ldq + s.template q_at<FMT>(lane);
   const uint8_t *is = in.s + scale_offset(0, s.block, in.tiles_x);
   // Whole stripes (all but the last) need no column checks.
   auto run = [&](auto full) {
     constexpr bool kFull = decltype(full)::value;
-    for (uint32_t r = s.r0 + warp; r < s.r1; r += kRowWarps) {
+    for (uint32_t r = s.r; r < s.r1; r += s.step) {
       MxLane<FMT, E> q[U];
       const int64_t sr = scale_row(r, tile_row);
 #pragma unroll
@@ -318,8 +324,8 @@ __global__ void __launch_bounds__(kRowThreads, 4)
           store_lane<T, VEC, kFull>(dst + u * (St::kPiece * B), s.left - u * St::kPiece, lane, st, w);
         }
       }
-      dst += kRowWarps * x.ld * B;
-      iq += kRowWarps * in.ldq;
+      dst += s.step * x.ld * B;
+      iq += s.step * in.ldq;
     }
   };
   if (s.left == St::kPiece * U)
@@ -452,7 +458,7 @@ constexpr int kAhead = 2;
 template <int T, bool SUM, bool VEC, int U>
 __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
     act_backward_kernel(const RowMat dy, const MxMat z, const RowMat dz, int act, uint32_t rows,
-                        uint32_t cols, uint32_t rows_per, float *part) {
+                        uint32_t cols, uint32_t rows_per, int across, float *part) {
   using St = Stripe<T, U>;
   constexpr int E = St::E, B = kTypeBytes<T>;
   constexpr int kQ = kQBytes<kE4M3, E>;
@@ -470,11 +476,11 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const St s(rows, cols, rows_per, lane);
+  const St s(rows, cols, rows_per, across, lane, warp);
   const int64_t tile_row = z.tiles_x * 512;
-  const char *src = static_cast<const char *>(dy.p) + static_cast<int64_t>(s.r0 + warp) * dy.ld * B + s.at(0, false);
-  char *dst = static_cast<char *>(const_cast<void *>(dz.p)) + static_cast<int64_t>(s.r0 + warp) * dz.ld * B + s.at(0, false);
-  const uint8_t *zq = z.q + static_cast<int64_t>(s.r0 + warp) * z.ldq + s.template q_at<kE4M3>(lane);
+  const char *src = static_cast<const char *>(dy.p) + static_cast<int64_t>(s.r) * dy.ld * B + s.at(0, false);
+  char *dst = static_cast<char *>(const_cast<void *>(dz.p)) + static_cast<int64_t>(s.r) * dz.ld * B + s.at(0, false);
+  const uint8_t *zq = z.q + static_cast<int64_t>(s.r) * z.ldq + s.template q_at<kE4M3>(lane);
   float acc[U][E];
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
       const uint8_t *zs = z.s + scale_offset(0, s.block, z.tiles_x);
       const char *fsrc = src + lane * 16;  // of the row to fetch next
       const uint8_t *fq = zq - lane * kQ + lane * 16;
-      uint32_t fr = s.r0 + warp;
+      uint32_t fr = s.r;
       auto fetch = [&](int slot) {
         if (fr < s.r1) {
 #pragma unroll
@@ -507,9 +513,9 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
           if (lane * 16 < U * 32 * kQ) copy_async_16(&a.q[slot][warp][lane * 16], fq);
         }
         copy_async_commit();
-        fr += kRowWarps;
-        fsrc += kRowWarps * dy.ld * B;
-        fq += kRowWarps * z.ldq;
+        fr += s.step;
+        fsrc += s.step * dy.ld * B;
+        fq += s.step * z.ldq;
       };
       uint32_t bytes[U];
       auto fetch_scales = [&](uint32_t r) {
@@ -521,15 +527,15 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
       int slot = 0;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) fetch(i);
-      fetch_scales(s.r0 + warp);
-      for (uint32_t r = s.r0 + warp; r < s.r1; r += kRowWarps) {
+      fetch_scales(s.r);
+      for (uint32_t r = s.r; r < s.r1; r += s.step) {
         copy_async_wait<kAhead - 1>();
         __syncwarp();  // every lane's copies of this row have landed, and the row before is read
         fetch(slot == 0 ? kAhead : slot - 1);  // into the slot of the row before
         uint32_t now[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) now[u] = bytes[u];
-        fetch_scales(r + kRowWarps);
+        fetch_scales(r + s.step);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const uint4 x = a.dy[slot][u][tid];
@@ -539,7 +545,7 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
           work(u, w, q, now[u]);
           store_lane<T, true, true>(dst + u * (St::kPiece * B), kCols, lane, nullptr, w);
         }
-        dst += kRowWarps * dz.ld * B;
+        dst += s.step * dz.ld * B;
         slot = slot == kAhead ? 0 : slot + 1;
       }
       copy_async_wait<0>();
@@ -547,7 +553,7 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
   } else {
     uint32_t *st = VEC ? nullptr : sh.stage[VEC ? 0 : warp];
     const uint8_t *zs = z.s + scale_offset(0, s.block, z.tiles_x);
-    for (uint32_t r = s.r0 + warp; r < s.r1; r += kRowWarps) {
+    for (uint32_t r = s.r; r < s.r1; r += s.step) {
       uint32_t w[U][4];
       MxLane<kE4M3, E> q[U];
       const int64_t sr = scale_row(r, tile_row);
@@ -566,9 +572,9 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
           store_lane<T, VEC, false>(dst + u * (St::kPiece * B), s.left - u * St::kPiece, lane, st, w[u]);
         }
       }
-      src += kRowWarps * dy.ld * B;
-      dst += kRowWarps * dz.ld * B;
-      zq += kRowWarps * z.ldq;
+      src += s.step * dy.ld * B;
+      dst += s.step * dz.ld * B;
+      zq += s.step * z.ldq;
     }
   }
   if constexpr (SUM) __syncthreads();  // every warp is done with its part of the shared memory
@@ -580,11 +586,13 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
         *reinterpret_cast<float4 *>(&sh.sums[warp][u * St::kPiece + lane * E + j]) =
             make_float4(acc[u][j], acc[u][j + 1], acc[u][j + 2], acc[u][j + 3]);
     __syncthreads();
-    for (int c = threadIdx.x; c < s.left; c += kRowThreads) {
-      float t = sh.sums[0][c];
-#pragma unroll
-      for (int i = 1; i < kRowWarps; ++i) t += sh.sums[i][c];
-      part[static_cast<int64_t>(blockIdx.y) * cols + (s.c0 + c)] = t;
+    const int span = kCols << across;  // the CTA's columns
+    const uint32_t first = blockIdx.x * static_cast<uint32_t>(span);
+    for (int c = threadIdx.x; c < span && first + c < cols; c += kRowThreads) {
+      const int side = c / kCols;
+      float t = sh.sums[side][c % kCols];
+      for (int i = side + (1 << across); i < kRowWarps; i += 1 << across) t += sh.sums[i][c % kCols];
+      part[static_cast<int64_t>(blockIdx.y) * cols + (first + c)] = t;
     }
   }
 }
@@ -665,37 +673,44 @@ tlg_status with_format(int format, F f) {
 // device all the same, one in small calls.
 constexpr int kWide = 4, kWideBackward = 2;
 
-// A row kernel's grid: column stripes x row splits, about `per_sm` CTAs an SM, each warp with a
-// few rows.
+// log2 of the warps of a CTA side by side.  Two in the backward kernel: half the row splits, and
+// so half the partial sums (8192 x 16384 bf16, SiLU: 129 us, 142 with one, 134 with eight); the
+// others do not care.
+constexpr int kAcross = 0, kAcrossBackward = 1;
+
+// A row kernel's grid: column stripes x row splits, about `per_sm` CTAs an SM.
 struct RowGrid {
-  int u;
+  int u, across;
   dim3 grid;
   uint32_t rows_per;
 };
 
-RowGrid row_grid(int64_t rows, int64_t cols, int type, bool vec, int wide, int sms, int per_sm) {
+RowGrid row_grid(int64_t rows, int64_t cols, int type, bool vec, int wide, int most_across, int least_rows, int sms,
+                 int per_sm) {
   const int64_t piece = 32 * 16 / type_bytes(type);
-  const int64_t row_groups = (rows + kRowWarps - 1) / kRowWarps;  // a row to each warp of a CTA
   RowGrid g;
   if (!vec && type != TLG_TYPE_F32) wide = 1;  // element loads: eight a piece are enough in flight
-  g.u = row_groups * ((cols + piece * wide - 1) / (piece * wide)) >= 2 * int64_t(sms) ? wide : 1;
+  const int64_t items = (rows + kRowWarps - 1) / kRowWarps * ((cols + piece * wide - 1) / (piece * wide));
+  g.u = items >= 2 * int64_t(sms) ? wide : 1;
   const int64_t stripes = (cols + piece * g.u - 1) / (piece * g.u);
-  int64_t splits = std::max<int64_t>(1, std::min<int64_t>({(int64_t(sms) * per_sm + stripes - 1) / stripes, row_groups, 65535}));
-  g.rows_per = static_cast<uint32_t>((row_groups + splits - 1) / splits * kRowWarps);
-  splits = (rows + g.rows_per - 1) / g.rows_per;
-  g.grid = dim3(static_cast<unsigned>(stripes), static_cast<unsigned>(splits));
+  // as many warps side by side as leave at most a tenth of them without columns
+  g.across = most_across;
+  while (g.across > 0 && ((stripes + (int64_t(1) << g.across) - 1) >> g.across << g.across) * 10 > stripes * 11)
+    --g.across;
+  const int64_t step = kRowWarps >> g.across;
+  const int64_t ctas_x = (stripes + (int64_t(1) << g.across) - 1) >> g.across;
+  const int64_t row_groups = (rows + step - 1) / step;  // a row to each warp of a CTA
+  const int64_t splits = std::max<int64_t>(
+      1, std::min<int64_t>({(int64_t(sms) * per_sm + ctas_x - 1) / ctas_x, (row_groups + least_rows - 1) / least_rows, 65535}));
+  g.rows_per = static_cast<uint32_t>((row_groups + splits - 1) / splits * step);
+  g.grid = dim3(static_cast<unsigned>(ctas_x), static_cast<unsigned>((rows + g.rows_per - 1) / g.rows_per));
   return g;
 }
 
 // The same for the backward kernel, whose splits each leave a partial column sum: at least two
-// rows to a warp.
+// rows to a warp.  It does not depend on the matrices' alignment, so the workspace does not.
 RowGrid backward_grid(int64_t rows, int64_t cols, int type, int sms) {
-  RowGrid g = row_grid(rows, cols, type, true, kWideBackward, sms, 4);
-  if (g.rows_per < 2 * kRowWarps) {
-    g.rows_per = 2 * kRowWarps;
-    g.grid.y = static_cast<unsigned>((rows + g.rows_per - 1) / g.rows_per);
-  }
-  return g;
+  return row_grid(rows, cols, type, true, kWideBackward, kAcrossBackward, 2, sms, 4);
 }
 
 template <typename F>
@@ -749,11 +764,11 @@ tlg_status tlg_mx_quantize(tlg_mx_format format, int64_t rows, int64_t cols, tlg
                       kT == kTypeF32 ? 512 : 256, s, X, ldx, pair, o, rows, cols, tiles_r, tiles);
       }
       const bool vec = vec_rows(X, ldx, type);
-      const RowGrid g = row_grid(rows, cols, type, vec, kWide, info.sm_count, 4);
+      const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, 4);
       return with_flag(vec, [&](auto V) {
         return with_width(g.u, [&](auto U) {
           return launch(quantize_rows_kernel<kT, kF, false, decltype(V)::value, decltype(U)::value>, g.grid,
-                        kRowThreads, s, RowMat{X, ldx}, o, RowMat{}, 0, rows, cols, g.rows_per);
+                        kRowThreads, s, RowMat{X, ldx}, o, RowMat{}, 0, rows, cols, g.rows_per, g.across);
         });
       });
     });
@@ -776,14 +791,14 @@ tlg_status tlg_mx_dequantize(tlg_mx_format format, int64_t rows, int64_t cols, c
   if (st != TLG_OK) return st;
   const MxMat in = mx_mat(Q, ldq, S, cols);
   const bool vec = vec_rows(X, ldx, type);
-  const RowGrid g = row_grid(rows, cols, type, vec, kWide, info.sm_count, 4);
+  const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, 4);
   return with_type(type, [&](auto T) {
     return with_format(format, [&](auto F) {
       return with_flag(vec, [&](auto V) {
         return with_width(g.u, [&](auto U) {
           return launch(
               dequantize_rows_kernel<decltype(T)::value, decltype(F)::value, decltype(V)::value, decltype(U)::value>,
-              g.grid, kRowThreads, static_cast<cudaStream_t>(stream), in, RowMat{X, ldx}, rows, cols, g.rows_per);
+              g.grid, kRowThreads, static_cast<cudaStream_t>(stream), in, RowMat{X, ldx}, rows, cols, g.rows_per, g.across);
         });
       });
     });
@@ -809,13 +824,13 @@ tlg_status tlg_act_forward_mx(int64_t rows, int64_t cols, tlg_activation activat
   if (st != TLG_OK) return st;
   const MxMat o = mx_mat(Q, ldq, S, cols);
   const bool vec = vec_rows(Z, ldz, type) && vec_rows(Y, ldy, type);
-  const RowGrid g = row_grid(rows, cols, type, vec, kWide, info.sm_count, 4);
+  const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, 4);
   return with_type(type, [&](auto T) {
     return with_flag(vec, [&](auto V) {
       return with_width(g.u, [&](auto U) {
         return launch(quantize_rows_kernel<decltype(T)::value, kE4M3, true, decltype(V)::value, decltype(U)::value>,
                       g.grid, kRowThreads, static_cast<cudaStream_t>(stream), RowMat{Z, ldz}, o, RowMat{Y, ldy},
-                      static_cast<int>(activation), rows, cols, g.rows_per);
+                      static_cast<int>(activation), rows, cols, g.rows_per, g.across);
       });
     });
   });
@@ -895,7 +910,7 @@ tlg_status tlg_act_backward_mx(int64_t rows, int64_t cols, tlg_activation activa
         auto run = [&](auto U) {
           return launch(act_backward_kernel<kT, decltype(SUM)::value, decltype(V)::value, decltype(U)::value>, g.grid,
                         kRowThreads, s, RowMat{dY, lddy}, z, RowMat{dZ, lddz}, static_cast<int>(activation), rows,
-                        cols, g.rows_per, part);
+                        cols, g.rows_per, g.across, part);
         };
         return g.u == 1 ? run(std::integral_constant<int, 1>()) : run(std::integral_constant<int, kWideBackward>());
       });

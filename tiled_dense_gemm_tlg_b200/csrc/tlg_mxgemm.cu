@@ -248,7 +248,9 @@ tlg_status choose(int dev, int sms, int64_t M, int64_t N, int64_t K, int type, b
   c.block_n = out->tile->block_n;
   c.stages = out->tile->stages;
   c.cta_group = out->tile->cta_group;
-  c.raster_group = r.raster_group != 0 ? r.raster_group : 8;
+  // Tile rows walked together: 32 for the 256 wide tile (8192^3 under the power cap: 220 us against
+  // 226 with 8; 87 MB of DRAM reads against 150), 8 for the others, which do not care.
+  c.raster_group = r.raster_group != 0 ? r.raster_group : (c.block_n == 256 ? 32 : 8);
   c.max_ctas = out->units * c.cta_group;
   c.split_k = 1;
   c.overlap_prev = 1;
