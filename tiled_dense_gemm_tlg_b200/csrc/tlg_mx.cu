@@ -228,12 +228,16 @@ __device__ __forceinline__ int64_t scale_row(uint32_t row, int64_t tile_row_byte
 // Quantises X row by row; with ACT also writes Y = act(X).  The lanes of a block (4 of 16-bit
 // elements, 8 of fp32) agree on its largest magnitude by shuffles.
 template <int T, int FMT, bool ACT, bool VEC, int U>
-__global__ void __launch_bounds__(kRowThreads, 4)
+__global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
     quantize_rows_kernel(const RowMat x, const MxMat o, const RowMat y, int act, uint32_t rows,
                          uint32_t cols, uint32_t rows_per, int across) {
   using St = Stripe<T, U>;
   constexpr int E = St::E, B = kTypeBytes<T>;
   constexpr int kLanesPerBlock = kMxBlock / E;
+  // Rows read element by element are loaded a row ahead, over the shared-memory round trip of the
+  // row before (4000 x 3001 fp32 to 4 bits: 12.4 us, 13.6 without); with whole 16-byte loads the
+  // registers are better spent on a fourth CTA (8192 x 16384 bf16: 53.6 us against 60).
+  constexpr bool kAheadOne = !VEC;
   __shared__ __align__(16) uint32_t stage[VEC ? 1 : kRowWarps][128];
   grid_dependency_wait();
   grid_launch_dependents();
@@ -248,11 +252,23 @@ __global__ void __launch_bounds__(kRowThreads, 4)
   // Whole stripes (all but the last) need no column checks.
   auto run = [&](auto full) {
     constexpr bool kFull = decltype(full)::value;
+    uint32_t next[U][4];  // the row to work on next
+    auto issue = [&]() {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (kFull || u * St::kPiece < s.left)
+          issue_load<T, VEC, kFull>(src + u * (St::kPiece * B), s.left - u * St::kPiece, lane, next[u]);
+      src += s.step * x.ld * B;
+    };
+    if (kAheadOne && s.r < s.r1) issue();
     for (uint32_t r = s.r; r < s.r1; r += s.step) {
+      if (!kAheadOne) issue();
       uint32_t w[U][4];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (kFull || u * St::kPiece < s.left) issue_load<T, VEC, kFull>(src + u * (St::kPiece * B), s.left - u * St::kPiece, lane, w[u]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[u][j] = next[u][j];
+      if (kAheadOne && r + s.step < s.r1) issue();
       const int64_t sr = scale_row(r, tile_row);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -278,7 +294,6 @@ __global__ void __launch_bounds__(kRowThreads, 4)
           }
         }
       }
-      src += s.step * x.ld * B;
       oq += s.step * o.ldq;
       if constexpr (ACT) dst += s.step * y.ld * B;
     }
@@ -597,10 +612,14 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
   }
 }
 
-// dbias[c] = the sum over `parts` partial sums: a warp takes every eighth one of 32 columns, and
-// the eight sums are added in order.
-__global__ void __launch_bounds__(kRowThreads) column_sum_kernel(const float *part, int parts, int64_t cols, float *dbias) {
-  __shared__ float sums[kRowWarps][32];
+// dbias[c] = the sum over `parts` partial sums: each of a CTA's W warps takes every W-th one of 32
+// columns, and their sums are added in order.  W = 32 where a narrow matrix has hundreds of
+// row splits and a warp's chain of loads takes the time (16384 x 1000 fp16, 592 splits, the whole
+// backward call: 24.7 us, 30.5 with 8), else 8, which find room beside the kernel before sooner
+// (2000 x 5000: 18.3 us, 20.3 with 32).
+template <int W>
+__global__ void __launch_bounds__(32 * W) column_sum_kernel(const float *part, int parts, int64_t cols, float *dbias) {
+  __shared__ float sums[W][32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -608,13 +627,13 @@ __global__ void __launch_bounds__(kRowThreads) column_sum_kernel(const float *pa
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 8
-    for (int i = warp; i < parts; i += kRowWarps) s += part[i * cols + c];
+    for (int i = warp; i < parts; i += W) s += part[i * cols + c];
   }
   sums[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < cols) {
 #pragma unroll
-    for (int i = 1; i < kRowWarps; ++i) s += sums[i][lane];
+    for (int i = 1; i < W; ++i) s += sums[i][lane];
     dbias[c] = s;
   }
 }
@@ -700,9 +719,21 @@ RowGrid row_grid(int64_t rows, int64_t cols, int type, bool vec, int wide, int m
   const int64_t step = kRowWarps >> g.across;
   const int64_t ctas_x = (stripes + (int64_t(1) << g.across) - 1) >> g.across;
   const int64_t row_groups = (rows + step - 1) / step;  // a row to each warp of a CTA
-  const int64_t splits = std::max<int64_t>(
-      1, std::min<int64_t>({(int64_t(sms) * per_sm + ctas_x - 1) / ctas_x, (row_groups + least_rows - 1) / least_rows, 65535}));
-  g.rows_per = static_cast<uint32_t>((row_groups + splits - 1) / splits * step);
+  // Row groups a CTA takes: few enough for per_sm CTAs an SM, and from there on what leaves the
+  // busiest SM the fewest (4000 x 3001 fp32 back from 4 bits: 13.8 us with 432 CTAs of seven
+  // groups, 16.6 with 504 of six, of which some SMs get four and most three).
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(int64_t(sms) * per_sm / ctas_x, 65535));
+  const int64_t fewest = std::max<int64_t>({1, (row_groups + most - 1) / most, std::min<int64_t>(least_rows, row_groups)});
+  int64_t take = fewest, best = INT64_MAX;
+  for (int64_t c = fewest; c <= 2 * fewest && c < fewest + 16; ++c) {
+    const int64_t ctas = ctas_x * ((row_groups + c - 1) / c);
+    const int64_t busiest = (ctas + sms - 1) / sms * c;
+    if (busiest < best) {
+      best = busiest;
+      take = c;
+    }
+  }
+  g.rows_per = static_cast<uint32_t>(take * step);
   g.grid = dim3(static_cast<unsigned>(ctas_x), static_cast<unsigned>((rows + g.rows_per - 1) / g.rows_per));
   return g;
 }
@@ -764,7 +795,7 @@ tlg_status tlg_mx_quantize(tlg_mx_format format, int64_t rows, int64_t cols, tlg
                       kT == kTypeF32 ? 512 : 256, s, X, ldx, pair, o, rows, cols, tiles_r, tiles);
       }
       const bool vec = vec_rows(X, ldx, type);
-      const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, 4);
+      const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, vec ? 4 : 3);
       return with_flag(vec, [&](auto V) {
         return with_width(g.u, [&](auto U) {
           return launch(quantize_rows_kernel<kT, kF, false, decltype(V)::value, decltype(U)::value>, g.grid,
@@ -791,7 +822,7 @@ tlg_status tlg_mx_dequantize(tlg_mx_format format, int64_t rows, int64_t cols, c
   if (st != TLG_OK) return st;
   const MxMat in = mx_mat(Q, ldq, S, cols);
   const bool vec = vec_rows(X, ldx, type);
-  const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, 4);
+  const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, vec ? 4 : 3);
   return with_type(type, [&](auto T) {
     return with_format(format, [&](auto F) {
       return with_flag(vec, [&](auto V) {
@@ -824,7 +855,7 @@ tlg_status tlg_act_forward_mx(int64_t rows, int64_t cols, tlg_activation activat
   if (st != TLG_OK) return st;
   const MxMat o = mx_mat(Q, ldq, S, cols);
   const bool vec = vec_rows(Z, ldz, type) && vec_rows(Y, ldy, type);
-  const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, 4);
+  const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, vec ? 4 : 3);
   return with_type(type, [&](auto T) {
     return with_flag(vec, [&](auto V) {
       return with_width(g.u, [&](auto U) {
@@ -917,7 +948,9 @@ tlg_status tlg_act_backward_mx(int64_t rows, int64_t cols, tlg_activation activa
     });
   });
   if (st != TLG_OK || part == dbias) return st;
-  return launch(column_sum_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), kRowThreads, s, part, splits, cols, dbias);
+  const dim3 sum_grid(static_cast<unsigned>((cols + 31) / 32));
+  return splits > 128 ? launch(column_sum_kernel<32>, sum_grid, 1024, s, part, splits, cols, dbias)
+                      : launch(column_sum_kernel<8>, sum_grid, 256, s, part, splits, cols, dbias);
 }
 
 }  // extern "C"
