@@ -260,6 +260,68 @@ def test_streams_and_graphs(tlg):
     assert torch.equal(captured[0], eager[0]) and torch.equal(captured[1], eager[1])
 
 
+def test_given_stream(tlg):
+    """Outputs and the workspace of a call on a given stream belong to that stream."""
+    z = torch.randn((300, 700), device="cuda").half()
+    dy = torch.randn((300, 700), device="cuda").half()
+    want = tlg.tlg_act_backward_mx(dy, *tlg.tlg_act_forward_mx(z, "silu")[1:], "silu")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        Y, Q, S = tlg.tlg_act_forward_mx(z, "silu", stream=side)
+        got = tlg.tlg_act_backward_mx(dy, Q, S, "silu", stream=side.cuda_stream)
+        assert torch.cuda.current_stream() != side
+        side.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_one_row_of_any_stride(tlg):
+    x = torch.randn((3, 4095), device="cuda").half()
+    codes, scale = mx.quantize(x[1:2].double().cpu().numpy(), "e4m3")
+    wide = torch.zeros((1, 5000), device="cuda").half()
+    wide[:, :4095] = x[1]
+    for row in (x[1:2], wide[:, :4095], wide[:, :4095].as_strided((1, 4095), (3, 1))):
+        Q, S = tlg.tlg_mx_quantize(row, format="e4m3")
+        check_mx(Q, S, codes, scale, "e4m3")
+        Y, Q, S = tlg.tlg_act_forward_mx(row, "relu")
+        check_mx(Q, S, codes, scale, "e4m3")
+        assert torch.equal(Y, row.clamp(min=0))
+
+
+def test_calls_on_two_streams_at_once(tlg):
+    """Calls that overlap in time, each with a workspace of its own."""
+    rng = np.random.default_rng(1)
+    Q, S, _ = saved(rng.standard_normal((4096, 2048)))
+    dys = [torch.randn((4096, 2048), device="cuda") for _ in range(2)]
+    want = [tlg.tlg_act_backward_mx(dy, Q, S, "gelu") for dy in dys]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(4):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(tlg.tlg_act_backward_mx(dys[i], Q, S, "gelu"))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for dz, db in got[i]:
+            assert torch.equal(dz, want[i][0]) and torch.equal(db, want[i][1])
+
+
+def test_workspace_is_checked(tlg):
+    dy = torch.ones((3000, 700), device="cuda")
+    Q, S, _ = saved(np.zeros((3000, 700)))
+    need = tlg.tlg_act_backward_mx_workspace_size(3000, 700, "f32")
+    with pytest.raises(tlg.TlgError):
+        tlg.tlg_act_backward_mx(dy, Q, S, "gelu", workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")  # its contents do not matter
+    dz, db = tlg.tlg_act_backward_mx(dy, Q, S, "gelu", workspace=ws)
+    # GELU'(0) = 1/2, computed with an error below 1e-6 (the polynomial's constant is 0.5 - 6e-8); the
+    # sum of 3000 of them adds that error 3000 times and rounds at most 3000 times, each time by at
+    # most 2^-24 of a partial sum no larger than 1500
+    assert ((dz - 0.5).abs() <= 1e-6).all() and (ws[need:] == 0xFF).all()
+    assert ((db - 1500).abs() <= 3000 * (1e-6 + 2.0 ** -24 * 1500)).all()
+
+
 def test_large_row_offsets(tlg):
     # a row stride whose offsets pass 2^31 elements and 2^32 bytes
     ld = (1 << 31) // 4 + 64

@@ -201,6 +201,11 @@ def test_empty_k_and_empty_output(tlg):
     assert lib.tlg_gemm_mxfp4(5, 70, 0, None, 0, None, None, 0, None, ctypes.byref(epi), C.data_ptr(), 70, 1, None,
                               st) == 0
     assert torch.equal(C, (bias.float().clamp(min=0) + R.float()).half())
+    empty = [torch.empty((n, 0), dtype=torch.uint8, device="cuda") for n in (5, 70)]
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    for typ, b in (("f16", bias), ("f32", bias), ("bf16", bias.bfloat16())):
+        got = tlg.tlg_gemm_mxfp4(empty[0], none, empty[1], none, bias=b, activation="relu", out=typ)
+        assert torch.equal(got, b.float().clamp(min=0).to(TYPES[typ]).expand(5, 70))
     A, SA, _ = operand(4, 64, "exact", 0)
     assert tlg.tlg_gemm_mxfp4(A[:0], SA, A, SA).shape == (0, 4)
 
@@ -254,6 +259,33 @@ def test_a_layer_forward_and_backward_in_four_bits(tlg):
     exact_dw = (d * mx.slope("gelu", Z.double().cpu().numpy())).T @ X.double().cpu().numpy()
     rel = np.linalg.norm(dW.double().cpu().numpy() - exact_dw) / np.linalg.norm(exact_dw)
     assert rel < 0.25  # two E2M1 operands, each element off by at most 1/4 of itself or 1/8 of its block's top
+
+
+def test_single_rows_of_any_stride(tlg):
+    A, SA, a = operand(1, 500, "exact", 3)
+    B, SB, b = operand(1, 500, "exact", 4)
+    wide = [torch.zeros((1, 400), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    wide[0][:, :256], wide[1][:, :256] = A, B
+    views = [w[:, :256].as_strided((1, 256), (7, 1)) for w in wide]
+    for cfg in (None, {"cta_group": 1, "block_n": 64}):
+        C = tlg.tlg_gemm_mxfp4(views[0], SA, views[1], SB, out="f32", config=cfg)
+        assert np.array_equal(C.cpu().numpy(), a @ b.T)
+
+
+@pytest.mark.parametrize("M,N,K", [(20, 300, 1500), (700, 500, 1024)])
+def test_two_calls_at_once(tlg, M, N, K):
+    A, SA, a = operand(M, K, "exact", 1)
+    B, SB, b = operand(N, K, "exact", 2)
+    want = torch.from_numpy(a @ b.T).cuda()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(tlg.tlg_gemm_mxfp4(A, SA, B, SB, out="f32"))
+    torch.cuda.synchronize()
+    assert all(torch.equal(c.double(), want) for c in got)
 
 
 def test_streams_and_graphs(tlg):

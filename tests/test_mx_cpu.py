@@ -124,6 +124,7 @@ def test_quantize_refusals(tlg):
     assert call(Q=A + 16) == bad and call(S=A + 64) == bad  # an output over the input
     assert call(S=2 * A + 32) == bad  # scales over elements
     assert call(rows=2 ** 30, ldx=2 ** 36) == unsup
+    assert call(ldq=40) == align and call(rows=1, ldq=40) != align  # a single row's stride does not matter
     assert call(rows=0, X=None, Q=None, S=None) == tlg.TLG_OK
     assert call(cols=0, X=None, Q=None, S=None) == tlg.TLG_OK
 

@@ -640,7 +640,10 @@ __global__ void __launch_bounds__(32 * W) column_sum_kernel(const float *part, i
 
 // ------------------------------------------------------------------ host side
 
-bool vec_rows(const void *p, int64_t ld, int type) { return aligned16(p) && (ld * type_bytes(type)) % 16 == 0; }
+// Whether every row starts on 16 bytes (of a single row, the stride does not matter).
+bool vec_rows(const void *p, int64_t rows, int64_t ld, int type) {
+  return aligned16(p) && (rows == 1 || (ld * type_bytes(type)) % 16 == 0);
+}
 
 MxMat mx_mat(const void *Q, int64_t ldq, const void *S, int64_t cols) {
   return {static_cast<const uint8_t *>(Q), ldq, static_cast<const uint8_t *>(S), scale_tiles_x(cols),
@@ -794,7 +797,7 @@ tlg_status tlg_mx_quantize(tlg_mx_format format, int64_t rows, int64_t cols, tlg
         return launch(quantize_cols_kernel<kT, kF>, dim3(static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 30))),
                       kT == kTypeF32 ? 512 : 256, s, X, ldx, pair, o, rows, cols, tiles_r, tiles);
       }
-      const bool vec = vec_rows(X, ldx, type);
+      const bool vec = vec_rows(X, rows, ldx, type);
       const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, vec ? 4 : 3);
       return with_flag(vec, [&](auto V) {
         return with_width(g.u, [&](auto U) {
@@ -821,7 +824,7 @@ tlg_status tlg_mx_dequantize(tlg_mx_format format, int64_t rows, int64_t cols, c
   st = device_ready({X, Q, S}, &info);
   if (st != TLG_OK) return st;
   const MxMat in = mx_mat(Q, ldq, S, cols);
-  const bool vec = vec_rows(X, ldx, type);
+  const bool vec = vec_rows(X, rows, ldx, type);
   const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, vec ? 4 : 3);
   return with_type(type, [&](auto T) {
     return with_format(format, [&](auto F) {
@@ -854,7 +857,7 @@ tlg_status tlg_act_forward_mx(int64_t rows, int64_t cols, tlg_activation activat
   st = device_ready({Z, Y, Q, S}, &info);
   if (st != TLG_OK) return st;
   const MxMat o = mx_mat(Q, ldq, S, cols);
-  const bool vec = vec_rows(Z, ldz, type) && vec_rows(Y, ldy, type);
+  const bool vec = vec_rows(Z, rows, ldz, type) && vec_rows(Y, rows, ldy, type);
   const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, vec ? 4 : 3);
   return with_type(type, [&](auto T) {
     return with_flag(vec, [&](auto V) {
@@ -937,7 +940,7 @@ tlg_status tlg_act_backward_mx(int64_t rows, int64_t cols, tlg_activation activa
   st = with_type(type, [&](auto T) {
     constexpr int kT = decltype(T)::value;
     return with_flag(dbias != nullptr, [&](auto SUM) {
-      return with_flag(vec_rows(dY, lddy, type) && vec_rows(dZ, lddz, type), [&](auto V) {
+      return with_flag(vec_rows(dY, rows, lddy, type) && vec_rows(dZ, rows, lddz, type), [&](auto V) {
         auto run = [&](auto U) {
           return launch(act_backward_kernel<kT, decltype(SUM)::value, decltype(V)::value, decltype(U)::value>, g.grid,
                         kRowThreads, s, RowMat{dY, lddy}, z, RowMat{dZ, lddz}, static_cast<int>(activation), rows,

@@ -36,7 +36,7 @@ inline tlg_status check_matrix(const void *p, int64_t rows, int64_t cols, int64_
 // The elements and scales of a rows x cols MX matrix.
 inline tlg_status check_mx(int f, int64_t rows, int64_t cols, const void *Q, int64_t ldq, const void *S, Range *q, Range *s) {
   if (Q == nullptr || S == nullptr || ldq < row_bytes(f, cols)) return TLG_ERR_INVALID_ARG;
-  if (!aligned16(Q) || !aligned16(S) || ldq % 16 != 0) return TLG_ERR_ALIGNMENT;
+  if (!aligned16(Q) || !aligned16(S) || (rows > 1 && ldq % 16 != 0)) return TLG_ERR_ALIGNMENT;
   if (ldq > kMaxLd || (rows > 1 && rows - 1 > (int64_t(1) << 60) / ldq)) return TLG_ERR_UNSUPPORTED;
   extent(Q, rows, row_bytes(f, cols), ldq, 1, &q->lo, &q->hi);
   s->lo = reinterpret_cast<uintptr_t>(S);

@@ -353,6 +353,8 @@ tlg_status tlg_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void *A, int64_
   // two tiles (256 words) x the 128-row groups a tile meets, C 64 bytes x 32 rows.
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
   const uint64_t kbytes = static_cast<uint64_t>(row_bytes(TLG_MX_E2M1, K));
+  if (M == 1) lda = static_cast<int64_t>(kbytes);  // the stride of a single row may be anything
+  if (N == 1) ldb = static_cast<int64_t>(kbytes);
   const uint64_t tx = static_cast<uint64_t>(scale_tiles_x(K));
   // Rows of A and B in a box, and the 128-row scale groups of B a tile meets.
   const uint32_t a_rows = c.tokens != 0 ? static_cast<uint32_t>(c.tokens) : 128u;
