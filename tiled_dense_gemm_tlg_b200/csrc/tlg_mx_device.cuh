@@ -85,32 +85,40 @@ __device__ __forceinline__ void from_floats(const float (&v)[E], uint32_t (&w)[4
   }
 }
 
-// The larger of two packed pairs of unsigned 16-bit values, each half by itself.
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+// The larger of m and the magnitudes of w's two elements, each half by itself; a NaN stays.
+template <int T>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) {
   uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  if constexpr (T == kTypeF16)
+    asm("{\n\t.reg .b32 t;\n\tabs.f16x2 t, %2;\n\tmax.NaN.f16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+  else
+    asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %2;\n\tmax.NaN.bf16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(m), "r"(w));
   return r;
 }
 
-// Bits of the largest magnitude, as fp32, among the elements in w.  Magnitudes are compared
-// as integers, which orders them like their values and puts Inf and then NaN above every
-// finite one, so a non-finite element shows in the result.
+// Bits of a 16-bit magnitude as fp32: NaN and infinity stay the largest.
+template <int T>
+__device__ __forceinline__ uint32_t magnitude_bits(uint32_t half) {
+  if constexpr (T == kTypeF16)
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(half))));
+  else
+    return half << 16;
+}
+
+// Bits of the largest magnitude, as fp32, among the elements in w.  As integers they order like
+// the values, with infinity and then NaN above every finite one, so a non-finite element shows
+// in the result.
 template <int T, int N>
 __device__ __forceinline__ uint32_t amax_bits(const uint32_t (&w)[N]) {
+  uint32_t m = 0;
   if constexpr (T == kTypeF32) {
-    uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < N; ++j) m = max(m, w[j] & 0x7fffffffu);
     return m;
   } else {
-    uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < N; ++j) m = max_u16x2(m, w[j] & 0x7fff7fffu);
-    m = max(m & 0xffffu, m >> 16);
-    if constexpr (T == kTypeF16)
-      return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
-    else
-      return m << 16;
+    for (int j = 0; j < N; ++j) m = max_abs2<T>(m, w[j]);
+    return magnitude_bits<T>(max(m & 0xffffu, m >> 16));
   }
 }
 
