@@ -724,17 +724,21 @@ RowGrid row_grid(int64_t rows, int64_t cols, int type, bool vec, int wide, int m
   const int64_t step = kRowWarps >> g.across;
   const int64_t ctas_x = (stripes + (int64_t(1) << g.across) - 1) >> g.across;
   const int64_t row_groups = (rows + step - 1) / step;  // a row to each warp of a CTA
-  // Row groups a CTA takes: few enough for per_sm CTAs an SM, and from there on what leaves the
-  // busiest SM the fewest (4000 x 3001 fp32 back from 4 bits: 13.8 us with 432 CTAs of seven
-  // groups, 16.6 with 504 of six, of which some SMs get four and most three).
+  // Row groups a CTA takes: few enough for per_sm CTAs an SM, and from there on what is done first:
+  // the busiest SM's k CTAs take k times as long as one with all the SM's bandwidth, and fewer of
+  // them hide less of each other's latency (the 1.5 / k, which ranks 4000 x 3001 fp32 back from
+  // 4 bits, 13.8 us with 432 CTAs of seven groups and 16.6 with 504 of six, and 4096 x 4096 bf16 to
+  // 4 bits, better with 512 of four than with 296 of seven).
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(int64_t(sms) * per_sm / ctas_x, 65535));
   const int64_t fewest = std::max<int64_t>({1, (row_groups + most - 1) / most, std::min<int64_t>(least_rows, row_groups)});
-  int64_t take = fewest, best = INT64_MAX;
+  int64_t take = fewest;
+  double best = 0;
   for (int64_t c = fewest; c <= 2 * fewest && c < fewest + 16; ++c) {
     const int64_t ctas = ctas_x * ((row_groups + c - 1) / c);
-    const int64_t busiest = (ctas + sms - 1) / sms * c;
-    if (busiest < best) {
-      best = busiest;
+    const double k = static_cast<double>((ctas + sms - 1) / sms);
+    const double cost = static_cast<double>(c) * (k + 1.5);
+    if (best == 0 || cost < best) {
+      best = cost;
       take = c;
     }
   }
@@ -744,9 +748,16 @@ RowGrid row_grid(int64_t rows, int64_t cols, int type, bool vec, int wide, int m
 }
 
 // The same for the backward kernel, whose splits each leave a partial column sum: at least two
-// rows to a warp.  It does not depend on the matrices' alignment, so the workspace does not.
-RowGrid backward_grid(int64_t rows, int64_t cols, int type, int sms) {
-  return row_grid(rows, cols, type, true, kWideBackward, kAcrossBackward, 2, sms, 4);
+// rows to a warp, and as many CTAs an SM as its registers allow.
+RowGrid backward_grid(int64_t rows, int64_t cols, int type, bool vec, int sms) {
+  return row_grid(rows, cols, type, true, kWideBackward, kAcrossBackward, 2, sms, vec ? 4 : 3);
+}
+
+// Workspace bytes of its partial sums; the caller does not know which matrices will be aligned.
+size_t backward_workspace(int64_t rows, int64_t cols, int type, int sms) {
+  const unsigned splits = std::max(backward_grid(rows, cols, type, true, sms).grid.y,
+                                   backward_grid(rows, cols, type, false, sms).grid.y);
+  return splits > 1 ? static_cast<size_t>(splits) * static_cast<size_t>(cols) * 4 : 0;
 }
 
 template <typename F>
@@ -882,8 +893,7 @@ tlg_status tlg_act_backward_mx_workspace_size(int64_t rows, int64_t cols, tlg_ty
   DeviceInfo info;
   const tlg_status ds = current_device(&dev, &info);
   if (ds != TLG_OK) return ds;
-  const unsigned splits = backward_grid(rows, cols, type, info.sm_count).grid.y;
-  *bytes = splits > 1 ? static_cast<size_t>(splits) * static_cast<size_t>(cols) * 4 : 0;
+  *bytes = backward_workspace(rows, cols, type, info.sm_count);
   return TLG_OK;
 }
 
@@ -930,11 +940,12 @@ tlg_status tlg_act_backward_mx(int64_t rows, int64_t cols, tlg_activation activa
   if (dbias != nullptr && workspace != nullptr && meets(rb, rw)) return TLG_ERR_INVALID_ARG;
   st = device_ready({dY, Q, S, dZ, dbias, workspace}, &info);
   if (st != TLG_OK) return st;
-  const RowGrid g = backward_grid(rows, cols, type, info.sm_count);
+  const bool vec = vec_rows(dY, rows, lddy, type) && vec_rows(dZ, rows, lddz, type);
+  const RowGrid g = backward_grid(rows, cols, type, vec, info.sm_count);
   const int splits = static_cast<int>(g.grid.y);
   float *part = dbias;
   if (dbias != nullptr && splits > 1) {
-    if (workspace == nullptr || workspace_bytes < static_cast<size_t>(splits) * static_cast<size_t>(cols) * 4)
+    if (workspace == nullptr || workspace_bytes < backward_workspace(rows, cols, type, info.sm_count))
       return TLG_ERR_INVALID_ARG;
     part = static_cast<float *>(workspace);
   }
@@ -942,7 +953,7 @@ tlg_status tlg_act_backward_mx(int64_t rows, int64_t cols, tlg_activation activa
   st = with_type(type, [&](auto T) {
     constexpr int kT = decltype(T)::value;
     return with_flag(dbias != nullptr, [&](auto SUM) {
-      return with_flag(vec_rows(dY, rows, lddy, type) && vec_rows(dZ, rows, lddz, type), [&](auto V) {
+      return with_flag(vec, [&](auto V) {
         auto run = [&](auto U) {
           return launch(act_backward_kernel<kT, decltype(SUM)::value, decltype(V)::value, decltype(U)::value>, g.grid,
                         kRowThreads, s, RowMat{dY, lddy}, z, RowMat{dZ, lddz}, static_cast<int>(activation), rows,
