@@ -228,3 +228,12 @@ def test_binding_refusals(tlg):
         tlg.tlg_act_backward_mx(X, Q, S, "gelu")  # e4m3 rows of 40 columns are 64 bytes
     with pytest.raises(tlg.TlgError):  # no CPU fallback
         tlg.tlg_mx_quantize(X, Q=Q, S=S)
+
+
+def test_workspace_must_be_contiguous(tlg):
+    """A broadcast tensor has more elements than bytes behind it."""
+    X = torch.zeros((4, 40), dtype=torch.float16)
+    Q, S = torch.zeros((4, 64), dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
+    for workspace in (torch.zeros(1).expand(1 << 20), torch.zeros(1 << 12)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            tlg.tlg_act_backward_mx(X, Q, S, "gelu", workspace=workspace)

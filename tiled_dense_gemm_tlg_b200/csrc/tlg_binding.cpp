@@ -302,6 +302,7 @@ PyObject *act_backward_mx(PyObject *, PyObject *const *a, Py_ssize_t n) {
       }
       if (const at::Tensor *given = maybe(a[7], "workspace")) {
         same_device(dy, given);
+        if (!given->is_contiguous()) raise(PyExc_ValueError, "%s must be contiguous", "workspace");
         ws = *given;
         ws_bytes = ws.nbytes();
       } else {
