@@ -15,6 +15,8 @@
  * bias and a ReLU before the fp16 store ("domestic-GPU TileLang adoption",
  * xdnf.cn/news/333523, section 4.2); tlg_gemm_fused generalises it to a bias,
  * an activation (ReLU or GELU) and a residual connection (same page, 4.1).
+ * Beside it stand operators over 4-bit and 8-bit microscaled matrices (their
+ * section below).
  *
  * Conventions shared by every entry point below:
  *

@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 // shares the K range of every 128 rows of B, so that few rows of B still keep most SMs
 // loading; each CTA adds the KS fp32 partial sums of its 128 / KS rows in slice order, received
 // through distributed shared memory, and writes them.  Measured back to back in a graph, one
-// token: 4096 x 4096 weights 3.7 us with KS = 4 (6.5 with KS = 1, 6.7 with 128-row tiles),
+// token: 4096 x 4096 weights 3.6 us with KS = 4 (6.4 with KS = 1, 7.0 with 128-row tiles),
 // 16384 x 4096 6.7 us with KS = 1 (11 with 128-row tiles; its bytes take 5.5 us).  At 64 rows of
 // A the 128-row tiles win (6.6 against 8.7 us).
 template <int BN>
