@@ -20,11 +20,13 @@
 //  - The epilogue of a tile has to fit beside a main loop four times as short, and one warp
 //    alone waits most of the time (for TMEM, shared memory, the special-function unit).  So
 //    sixteen warps, four to a quarter of the rows, take 32 columns each time, little enough
-//    for 96 registers, and load the bias and residual of their next tile's pieces while they
-//    work on this tile's (4096^3 with bias, GELU and residual, back to back: 35.9 us against 39
-//    with eight warps, 64 columns and both read where they are added; 16384 x 4096 x 1024:
-//    91 against 115).  Tried and dropped on the same box: ordinary stores from the box in place
-//    of TMA stores (108 us there), eight columns at a time in a rolled loop (119).
+//    for 96 registers, and load the bias and residual of their next piece while they work on
+//    this one.  With bias, GELU and residual, back to back: 4096^3 32 us, 16384 x 4096 x 1024
+//    76; with eight warps, 64 columns and both read where they are added it was 3 and 24 us
+//    more, with all pieces of a tile unrolled and loaded a tile ahead 1.5 and 14 more (code
+//    that did not stay in the instruction cache).  Tried and dropped: ordinary stores from the
+//    box in place of TMA stores, eight columns at a time in a rolled loop (17 and 28 us more at
+//    16384 x 4096 x 1024).
 //  - The 256-column accumulators overlap: TMEM holds two of 256 columns 128 apart and the
 //    scales of five slots.  The epilogue drains the shared 128 columns first and hands them
 //    back; the next tile's MMAs, into the other accumulator, start then.
@@ -169,6 +171,15 @@ __device__ __forceinline__ void store_elem(void *p, int64_t i, float v) {
 template <int OUT>
 constexpr int kBiasType = OUT == kTypeBF16 ? kTypeBF16 : kTypeF16;
 
+// A bias element as loaded; converted where it is used, so that the load is not waited for before.
+template <int OUT>
+__device__ __forceinline__ float bias_value(uint16_t bits) {
+  if constexpr (OUT == kTypeBF16)
+    return __uint_as_float(static_cast<uint32_t>(bits) << 16);
+  else
+    return __half2float(__ushort_as_half(bits));
+}
+
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4 &v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -183,13 +194,13 @@ struct MxResidual {
   static constexpr int kHalves = OUT == kTypeF32 ? 2 : 1;  // 64-byte pieces of a row
   uint4 r[kHalves][4];
   bool have;
-  float bias;  // of column (lane) of the piece
+  uint16_t bias;  // of column (lane) of the piece
 };
 
 template <int OUT>
 __device__ __forceinline__ void mx_load_residual(const MxGemmParams &p, int row0, int col0, int lane,
                                                  MxResidual<OUT> &x) {
-  if (p.bias != nullptr) x.bias = col0 + lane < p.N ? load_elem<kBiasType<OUT>>(p.bias, col0 + lane) : 0.0f;
+  if (p.bias != nullptr) x.bias = col0 + lane < p.N ? static_cast<const uint16_t *>(p.bias)[col0 + lane] : uint16_t(0);
   x.have = p.R != nullptr && p.r_vec != 0 && col0 + 32 <= p.N;
   if (x.have) {
     const int row = row0 + (lane >> 2);
@@ -279,6 +290,14 @@ __device__ __forceinline__ void mx_store_box(const MxGemmParams &p, int row0, in
       }
     }
   }
+}
+
+// Tells the pair's MMA warp that this warp has read its TMEM columns (tcgen05.wait::ld, then
+// tcgen05.fence::before_thread_sync, come before it).  Nothing in memory is handed over, so the
+// arrival is relaxed: a release at cluster scope waits for the warp's earlier memory traffic, up
+// to 3000 cycles a tile under load (16384 x 4096 x 1024 with 256 x 192 tiles).
+__device__ __forceinline__ void mbar_arrive_drained(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 template <int CG, int BN, int STAGES, int OUT, bool EPI>
@@ -473,11 +492,14 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   } else if (warp >= 2) {
     // ---------------------------------------------------------------- epilogue (every CTA)
     // Warp w drains TMEM lanes 32*(w%4) .. +31, 32 columns at a time, by way of a 2 KB box.  The
-    // four warps of a quarter take its pieces in turn.
+    // four warps of a quarter take its pieces in turn; where there are two or six pieces, the pair
+    // of warps with a piece more changes from tile to tile.
     const int quarter = warp & 3;
     const int ew = warp - 2;
     const int side = ew >> 2;
     constexpr int kPieces = BN / 32;
+    static_assert(kPieces % 2 == 0, "pieces go to pairs of warps");
+    auto first_piece = [&](uint32_t tile) { return kPieces % 4 != 0 && (tile & 1u) != 0 ? side ^ 2 : side; };
     const uint32_t box = s0 + Plan::kOutOffset + static_cast<uint32_t>(ew) * kMxBoxBytes;
     const uint32_t release_bar0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
     constexpr int kBoxCols = 64 / kTypeBytes<OUT>;  // 32 columns of a 16-bit type, 16 of fp32
@@ -496,20 +518,11 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       // of accumulator 1) first.
       return 32 * (Plan::kOverlap && (tile & 1u) == 0 ? (i + 4) % 8 : i);
     };
-    // The bias and residual of this warp's pieces of a tile are loaded while it works on the tile
-    // before (an fp32 residual, twice the registers, one piece ahead).
-    constexpr int kMine = (kPieces + 3) / 4;
-    constexpr int kSets = OUT == kTypeF32 ? 1 : kMine;
-    MxResidual<OUT> res[kSets];
+    // The bias and residual of this warp's next piece are loaded while it works on this one.
+    MxResidual<OUT> ahead;
     const uint32_t sbias = s0 + Plan::kBiasOffset + static_cast<uint32_t>(ew) * 128u;
     if (unit < tiles) place(unit);
-    if constexpr (EPI) {
-      if (unit < tiles) {
-#pragma unroll
-        for (int k = 0; k < kSets; ++k)
-          if (side + 4 * k < kPieces) mx_load_residual<OUT>(p, row0, col_t + piece_col(side + 4 * k, 0), lane, res[k]);
-      }
-    }
+    if (EPI && unit < tiles && side < kPieces) mx_load_residual<OUT>(p, row0, col_t + piece_col(side, 0), lane, ahead);
     for (int t = unit; t < tiles; t += num_units, ++j) {
       // On a timeout the warp stops reading tiles.
       bool ok = *abort_flag == 0u;
@@ -526,17 +539,25 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         __syncwarp();
         if (lane == 0) {
           if constexpr (CG == 2)
-            mbar_arrive_cluster(release_bar0 + 8u * (j % Plan::kAccBars));
+            mbar_arrive_drained(release_bar0 + 8u * (j % Plan::kAccBars));
           else
             mbar_arrive(release_bar0 + 8u * (j % Plan::kAccBars));
         }
       };
-      if (side >= kPieces) release();
+      const int first = first_piece(j), next = first_piece(j + 1);
+      auto load_ahead = [&](int i) {  // for the piece after piece i of this tile
+        const bool here = i + 4 < kPieces;
+        if (EPI && (here || (t + num_units < tiles && next < kPieces)))
+          mx_load_residual<OUT>(p, here ? tile_row0 : row0,
+                                here ? tile_col + piece_col(i + 4, j) : col_t + piece_col(next, j + 1), lane, ahead);
+      };
+      if (first >= kPieces) {
+        release();
+        load_ahead(kPieces);
+      }
       const int row = tile_row0 + lane;
-#pragma unroll
-      for (int k = 0; k < kMine; ++k) {
-        const int i = side + 4 * k;
-        if (i >= kPieces) break;
+#pragma unroll 1
+      for (int i = first; i < kPieces; i += 4) {
         const int tc = piece_col(i, j);
         const int col0 = tile_col + tc;
         const uint32_t acc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
@@ -557,10 +578,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
         }
         if constexpr (EPI) {
-          MxResidual<OUT> &ahead = res[k % kSets];
           if (inside) {
             if (p.bias != nullptr) {
-              st_shared_u32(sbias + static_cast<uint32_t>(lane * 4), __float_as_uint(ahead.bias));
+              st_shared_u32(sbias + static_cast<uint32_t>(lane * 4), __float_as_uint(bias_value<OUT>(ahead.bias)));
               __syncwarp();
               add_bias_smem_32(sbias, 0, v);
             }
@@ -571,10 +591,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             }
             __syncwarp();  // every lane has read the bias
           }
-          if (kSets == 1 && kMine > 1 && i + 4 < kPieces)
-            mx_load_residual<OUT>(p, tile_row0, tile_col + piece_col(i + 4, j), lane, ahead);
-          else if (t + num_units < tiles)
-            mx_load_residual<OUT>(p, row0, col_t + piece_col(kSets == 1 ? side : i, j + 1), lane, ahead);
+          load_ahead(i);
         }
         if (!inside) continue;
 #pragma unroll
