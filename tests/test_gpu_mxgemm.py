@@ -176,6 +176,25 @@ def test_fused_epilogue(tlg, act, typ, cg, bn):
             assert o.guards_kept()
 
 
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("cg,bn", TILES)
+@pytest.mark.parametrize("N,lead,extra", [(330, 0, 0), (330, 2, 0), (330, 1, 1), (336, 0, 0), (331, 0, 5), (335, 8, 1),
+                                          (47, 2, 3)])
+def test_residuals_of_any_alignment(tlg, typ, cg, bn, N, lead, extra):
+    """Base and rows aligned to 16, 4 or 2 bytes, and ends inside 16 and 4 bytes; C has another layout,
+    and then the residual's.  Inputs are small multiples of 1/64, so the only rounding is the last."""
+    M, K = 270, 96
+    A, SA, a = operand(M, K, "exact", N)
+    B, SB, b = operand(N, K, "exact", lead + 1)
+    R = torch.from_numpy(np.random.default_rng(extra).integers(-64, 65, (M, N)) / 64).to(TYPES[typ])
+    r = Out(M, N, TYPES[typ], lead, extra, R)
+    want = a @ b.T + R.double().numpy()
+    for o in (Out(M, N, TYPES[typ], 8, 8), r):
+        tlg.tlg_gemm_mxfp4(A, SA, B, SB, residual=r.view, C=o.view, out=typ, config={"cta_group": cg, "block_n": bn})
+        check(o.view, want, 0.0, typ)
+        assert o.guards_kept()
+
+
 def test_nan_scale_reaches_its_row_and_column_only(tlg):
     M, N, K = 150, 210, 300
     for cg, bn in TILES + [(0, 0)]:

@@ -165,13 +165,13 @@ struct MxTile {
 
 // Tiles the library is built with: 128 * cta_group rows by block_n columns.  The costs are
 // fitted to 4096^3 (16 k-blocks a tile) and 16384 x 4096 x 1024 (4), fp16 C, back to back: plain
-// 37.6 / 27.3 / 29.5 us and 47 / 47 / 46 us with the 128, 192 and 256 wide tiles, with the full
-// epilogue 41 / 36 / 36 and 79 / 104 / 91.
+// 37.5 / 27.4 / 27.4 us and 47 / 40 / 38 us with the 128, 192 and 256 wide tiles, with the full
+// epilogue 41 / 33 / 32 and 75 / 75 / 76.
 const MxTile kTiles[] = {
     TLG_MX_TILE(1, 64, 6, {0.273, {0.4, 0.8}, {1.3, 2.0}}),
-    TLG_MX_TILE(1, 128, 5, {0.305, {0.5, 1.2}, {1.65, 2.8}}),
-    TLG_MX_TILE(2, 192, 5, {0.313, {0.6, 2.6}, {2.35, 5.2}}),
-    TLG_MX_TILE(2, 256, 5, {0.385, {1.2, 3.5}, {3.2, 6.5}}),
+    TLG_MX_TILE(1, 128, 5, {0.305, {0.5, 1.0}, {1.65, 2.7}}),
+    TLG_MX_TILE(2, 192, 5, {0.313, {0.5, 1.7}, {2.0, 4.0}}),
+    TLG_MX_TILE(2, 256, 5, {0.385, {0.7, 1.9}, {2.7, 5.35}}),
 };
 
 // --------------------------------------------------------------------------- tile choice
@@ -329,6 +329,7 @@ tlg_status tlg_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void *A, int64_
   p.R = e.residual;
   p.ldr = e.ldr;
   p.r_vec = (e.residual != nullptr && aligned16(e.residual) && (e.ldr * osz) % 16 == 0) ? 1 : 0;
+  p.r_words = (reinterpret_cast<uintptr_t>(e.residual) % 4 == 0 && (e.ldr * osz) % 4 == 0) ? 1 : 0;
   if (K == 0) {
     const int64_t total = M * N;
     const int blocks = static_cast<int>(std::min<int64_t>((total + 255) / 256, 4096));
@@ -376,9 +377,9 @@ tlg_status tlg_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void *A, int64_
   const CUtensorMapDataType ct = out == TLG_TYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                  : out == TLG_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if (!p.c_plain && !encode_2d(&m.c, ct, C, static_cast<uint64_t>(N), static_cast<uint64_t>(M),
-                               static_cast<uint64_t>(ldc * osz), static_cast<uint32_t>(64 / osz), 32,
-                               CU_TENSOR_MAP_SWIZZLE_64B))
+  auto stride = [&](int64_t ld) { return static_cast<uint64_t>(M == 1 ? (N * osz + 15) / 16 * 16 : ld * osz); };
+  if (!p.c_plain && !encode_2d(&m.c, ct, C, static_cast<uint64_t>(N), static_cast<uint64_t>(M), stride(ldc),
+                               static_cast<uint32_t>(64 / osz), 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return TLG_ERR_CUDA;
   return c.tile->fns[out][epi].launch(c.units, m, p, s);
 }

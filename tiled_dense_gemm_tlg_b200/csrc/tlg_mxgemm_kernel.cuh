@@ -20,13 +20,12 @@
 //  - The epilogue of a tile has to fit beside a main loop four times as short, and one warp
 //    alone waits most of the time (for TMEM, shared memory, the special-function unit).  So
 //    sixteen warps, four to a quarter of the rows, take 32 columns each time, little enough
-//    for 96 registers, and load the bias and residual of their next piece while they work on
-//    this one.  With bias, GELU and residual, back to back: 4096^3 32 us, 16384 x 4096 x 1024
-//    76; with eight warps, 64 columns and both read where they are added it was 3 and 24 us
-//    more, with all pieces of a tile unrolled and loaded a tile ahead 1.5 and 14 more (code
-//    that did not stay in the instruction cache).  Tried and dropped: ordinary stores from the
-//    box in place of TMA stores, eight columns at a time in a rolled loop (17 and 28 us more at
-//    16384 x 4096 x 1024).
+//    for 96 registers, and copy the residual of a piece to shared memory while they compute its
+//    activation.  With bias, GELU and residual, back to back: 4096^3 32 us, 16384 x 4096 x 1024
+//    74; with eight warps, 64 columns and the residual read where it is added it was 3 and 24 us
+//    more, with all pieces of a tile unrolled 1.5 and 14 more (code that did not stay in the
+//    instruction cache).  Tried and dropped: ordinary stores from the box in place of TMA
+//    stores, eight columns at a time in a rolled loop (17 and 28 us more at 16384 x 4096 x 1024).
 //  - The 256-column accumulators overlap: TMEM holds two of 256 columns 128 apart and the
 //    scales of five slots.  The epilogue drains the shared 128 columns first and hands them
 //    back; the next tile's MMAs, into the other accumulator, start then.
@@ -104,6 +103,7 @@ struct MxGemmParams {
   const void *R;     // residual in C's type, or nullptr; may be C itself (same ldc)
   int64_t ldr;
   int r_vec;         // R's base and row stride are 16-byte aligned
+  int r_words;       // and 4-byte aligned
 };
 
 // True in one lane of a converged warp.
@@ -180,89 +180,91 @@ __device__ __forceinline__ float bias_value(uint16_t bits) {
     return __half2float(__ushort_as_half(bits));
 }
 
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4 &v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+// The residual of a warp's 32 rows goes through its output box, 64 bytes of a row at a time, copied
+// there asynchronously while bias and activation are computed.  Tried and dropped: loaded to
+// registers a piece ahead (tcgen05.wait::ld waits for ordinary loads in flight too, and the
+// registers spill: fp32 C at 16384 x 4096 x 1024 156 us against 141), the tile's residual
+// prefetched to L2 by the producer (4096^3 from DRAM with bias and GELU: 39.3 us against 38.2).
+// R may be C: the warp reads these elements before it stores them.
+//
+// Byte `byte` of row r of a box: 16-byte piece c of a row sits at (c ^ (r / 2 % 4)) * 16, so that
+// eight lanes on eight rows, or on two whole rows, meet all banks.
+__device__ __forceinline__ uint32_t box_at(uint32_t box, int r, int byte) {
+  return box + static_cast<uint32_t>(r * 64 + (((byte / 16) ^ ((r >> 1) & 3)) * 16) + byte % 16);
 }
 
-// The residual of a warp's 32 rows x 32 columns, loaded ahead (R may be C: ordinary loads, made
-// before the same warp's stores of these elements).  Four lanes load 64 bytes of a row, so
-// that a load instruction covers 8 rows in whole sectors (a row to each lane would cover 32,
-// half a sector each); mx_add_residual hands the rows to their lanes through the warp's output
-// box.  Ragged or unaligned pieces are read where they are added.
-template <int OUT>
-struct MxResidual {
-  static constexpr int kHalves = OUT == kTypeF32 ? 2 : 1;  // 64-byte pieces of a row
-  uint4 r[kHalves][4];
-  bool have;
-  uint16_t bias;  // of column (lane) of the piece
-};
+// Starts the copy in pieces of BYTES, neighbouring lanes on neighbouring pieces; zeros beyond R.
+template <int OUT, int BYTES>
+__device__ __forceinline__ void mx_copy_box(const MxGemmParams &p, int row0, int col0, int lane, uint32_t box) {
+  constexpr int kLanes = 64 / BYTES;  // to a row
+  const int byte = lane % kLanes * BYTES;
+  const int left = max(0, min(BYTES, (p.N - col0) * kTypeBytes<OUT> - byte));
+  const char *q = static_cast<const char *>(p.R) + (static_cast<int64_t>(row0) * p.ldr + col0) * kTypeBytes<OUT> + byte;
+#pragma unroll 4
+  for (int r = lane / kLanes; r < 32; r += 32 / kLanes) {
+    const int size = row0 + r < p.M ? left : 0;
+    const void *from = size > 0 ? q + r * p.ldr * kTypeBytes<OUT> : p.R;
+    if constexpr (BYTES == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(box_at(box, r, byte)), "l"(from), "r"(size)
+                   : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(box_at(box, r, byte)), "l"(from), "r"(size)
+                   : "memory");
+  }
+}
 
+// box: read by all lanes before this.
 template <int OUT>
-__device__ __forceinline__ void mx_load_residual(const MxGemmParams &p, int row0, int col0, int lane,
-                                                 MxResidual<OUT> &x) {
-  if (p.bias != nullptr) x.bias = col0 + lane < p.N ? static_cast<const uint16_t *>(p.bias)[col0 + lane] : uint16_t(0);
-  x.have = p.R != nullptr && p.r_vec != 0 && col0 + 32 <= p.N;
-  if (x.have) {
-    const int row = row0 + (lane >> 2);
-    const char *q = static_cast<const char *>(p.R) +
-                    (static_cast<int64_t>(row) * p.ldr + col0) * kTypeBytes<OUT> + (lane & 3) * 16;
-    const int64_t step = 8 * p.ldr * kTypeBytes<OUT>;
+__device__ __forceinline__ void mx_fetch_residual(const MxGemmParams &p, int row0, int col0, int lane, uint32_t box) {
+  if (p.r_vec) {
+    mx_copy_box<OUT, 16>(p, row0, col0, lane, box);
+  } else if (kTypeBytes<OUT> == 4 || p.r_words) {
+    mx_copy_box<OUT, 4>(p, row0, col0, lane, box);
+  } else {  // 16-bit elements at odd places: too small for an asynchronous copy
+    constexpr int kBatch = 4;
+    const bool in = col0 + lane < p.N;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += kBatch) {
+      const uint16_t *q = static_cast<const uint16_t *>(p.R) + static_cast<int64_t>(row0 + r0) * p.ldr + col0 + lane;
+      uint16_t y[kBatch];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kBatch; ++i) y[i] = in && row0 + r0 + i < p.M ? q[i * p.ldr] : uint16_t(0);
 #pragma unroll
-      for (int h = 0; h < MxResidual<OUT>::kHalves; ++h)
-        if (row + 8 * i < p.M) x.r[h][i] = *reinterpret_cast<const uint4 *>(q + i * step + h * 64);
+      for (int i = 0; i < kBatch; ++i)
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(box_at(box, r0 + i, lane * 2)), "h"(y[i]) : "memory");
     }
   }
 }
 
-// box: the warp's box, read by all its lanes before this.
+// Adds what mx_fetch_residual brought to the piece's columns [16 h, ..) (fp32) or to all 32.
 template <int OUT>
-__device__ __forceinline__ void mx_add_residual(const MxGemmParams &p, int row, int col0, int lane, uint32_t box,
-                                                const MxResidual<OUT> &x, float (&v)[32]) {
-  if (x.have) {
+__device__ __forceinline__ void mx_add_residual(int h, int lane, uint32_t box, float (&v)[32]) {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
 #pragma unroll
-    for (int h = 0; h < MxResidual<OUT>::kHalves; ++h) {
-      __syncwarp();
+  for (int c = 0; c < 4; ++c) {
+    const uint4 y = ld_shared_v4(box_at(box, lane, c * 16));
+    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = (lane >> 2) + 8 * i;
-        st_shared_v4(box + static_cast<uint32_t>(r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) * 16)), x.r[h][i]);
-      }
-      __syncwarp();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint4 y = ld_shared_v4(box + static_cast<uint32_t>(lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16)));
-        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (OUT == kTypeF32) {
-            v[16 * h + 4 * c + k] += __uint_as_float(w[k]);
-          } else if constexpr (OUT == kTypeF16) {
-            add_half2_to(v[8 * c + 2 * k], v[8 * c + 2 * k + 1], w[k]);
-          } else {
-            float lo, hi;
-            unpack2<OUT>(w[k], lo, hi);
-            f2_add_to(v[8 * c + 2 * k], v[8 * c + 2 * k + 1], lo, hi);
-          }
-        }
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (OUT == kTypeF32) {
+        v[16 * h + 4 * c + k] += __uint_as_float(w[k]);
+      } else if constexpr (OUT == kTypeF16) {
+        add_half2_to(v[8 * c + 2 * k], v[8 * c + 2 * k + 1], w[k]);
+      } else {
+        float lo, hi;
+        unpack2<OUT>(w[k], lo, hi);
+        f2_add_to(v[8 * c + 2 * k], v[8 * c + 2 * k + 1], lo, hi);
       }
     }
-  } else if (row < p.M) {
-    const int64_t at = static_cast<int64_t>(row) * p.ldr + col0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (col0 + j < p.N) v[j] += load_elem<OUT>(p.R, at + j);
   }
 }
 
-// Writes one 64-byte row piece of a 32-row box; 16-byte piece c of row r sits at
-// (c ^ (r / 2 % 4)) * 16, so that eight lanes on eight rows, or on two whole rows, meet all banks.
+// Writes one 64-byte row piece of a 32-row box.
 __device__ __forceinline__ void st_box_row_64(uint32_t box, int r, const uint32_t *w) {
-  const uint32_t row = box + static_cast<uint32_t>(r) * 64u;
 #pragma unroll
   for (int c = 0; c < 4; ++c)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + static_cast<uint32_t>((c ^ ((r >> 1) & 3)) * 16)),
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box_at(box, r, c * 16)),
                  "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
                  : "memory");
 }
@@ -276,7 +278,7 @@ __device__ __forceinline__ void mx_store_box(const MxGemmParams &p, int row0, in
   const int cc = lane % kCols;
 #pragma unroll 4
   for (int r = lane / kCols; r < 32; r += 32 / kCols) {
-    const uint32_t at = box + static_cast<uint32_t>(r * 64 + (((cc * B / 16) ^ ((r >> 1) & 3)) * 16) + cc * B % 16);
+    const uint32_t at = box_at(box, r, cc * B);
     if (row0 + r < p.M && col0 + cc < p.N) {
       const int64_t to = static_cast<int64_t>(row0 + r) * p.ldc + col0 + cc;
       if constexpr (B == 4) {
@@ -518,11 +520,14 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       // of accumulator 1) first.
       return 32 * (Plan::kOverlap && (tile & 1u) == 0 ? (i + 4) % 8 : i);
     };
-    // The bias and residual of this warp's next piece are loaded while it works on this one.
-    MxResidual<OUT> ahead;
+    // The bias of this warp's next piece is loaded while it works on this one.
+    uint16_t ahead = 0;
+    auto load_bias = [&](int col) {
+      if (p.bias != nullptr && col + lane < p.N) ahead = static_cast<const uint16_t *>(p.bias)[col + lane];
+    };
     const uint32_t sbias = s0 + Plan::kBiasOffset + static_cast<uint32_t>(ew) * 128u;
     if (unit < tiles) place(unit);
-    if (EPI && unit < tiles && side < kPieces) mx_load_residual<OUT>(p, row0, col_t + piece_col(side, 0), lane, ahead);
+    if (EPI && unit < tiles && side < kPieces) load_bias(col_t + piece_col(side, 0));
     for (int t = unit; t < tiles; t += num_units, ++j) {
       // On a timeout the warp stops reading tiles.
       bool ok = *abort_flag == 0u;
@@ -531,7 +536,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         ok = false;
       ok = __all_sync(0xffffffffu, ok);
       const int tile_row0 = row0, tile_col = col_t;
-      if (t + num_units < tiles) place(t + num_units);  // where the next residual comes from
+      if (t + num_units < tiles) place(t + num_units);  // where the next bias comes from
       if (!ok) continue;
       tc_fence_after_sync();
       auto release = [&]() {
@@ -548,14 +553,12 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       auto load_ahead = [&](int i) {  // for the piece after piece i of this tile
         const bool here = i + 4 < kPieces;
         if (EPI && (here || (t + num_units < tiles && next < kPieces)))
-          mx_load_residual<OUT>(p, here ? tile_row0 : row0,
-                                here ? tile_col + piece_col(i + 4, j) : col_t + piece_col(next, j + 1), lane, ahead);
+          load_bias(here ? tile_col + piece_col(i + 4, j) : col_t + piece_col(next, j + 1));
       };
       if (first >= kPieces) {
         release();
         load_ahead(kPieces);
       }
-      const int row = tile_row0 + lane;
 #pragma unroll 1
       for (int i = first; i < kPieces; i += 4) {
         const int tc = piece_col(i, j);
@@ -579,15 +582,23 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
         if constexpr (EPI) {
           if (inside) {
+            if (p.R != nullptr) {
+              box_free();
+              mx_fetch_residual<OUT>(p, tile_row0, col0, lane, box);
+            }
             if (p.bias != nullptr) {
-              st_shared_u32(sbias + static_cast<uint32_t>(lane * 4), __float_as_uint(bias_value<OUT>(ahead.bias)));
+              st_shared_u32(sbias + static_cast<uint32_t>(lane * 4), __float_as_uint(bias_value<OUT>(ahead)));
               __syncwarp();
               add_bias_smem_32(sbias, 0, v);
             }
             activate_lane<OUT, 32>(p.act, v);
             if (p.R != nullptr) {
-              box_free();
-              mx_add_residual<OUT>(p, row, col0, lane, box, ahead, v);
+              mx_add_residual<OUT>(0, lane, box, v);
+              if constexpr (OUT == kTypeF32) {
+                __syncwarp();
+                mx_fetch_residual<OUT>(p, tile_row0, col0 + 16, lane, box);
+                mx_add_residual<OUT>(1, lane, box, v);
+              }
             }
             __syncwarp();  // every lane has read the bias
           }
