@@ -39,55 +39,77 @@ struct RowMat {
   int64_t ld;
 };
 
-// Elements [c0, c0 + 32 E) of a row, E to a lane; zeros from column `cols` on.  Without VEC they
-// are read element by element, neighbouring lanes on neighbouring elements (lane l: elements l,
-// l + 32, ...); finish_load rearranges them.
-// FULL: the whole piece lies before `cols`.
+// Elements [c0, c0 + 32 E) of a row, E to a lane; zeros from column `cols` on.  Without VEC,
+// neighbouring lanes read neighbouring words (lane l: words l, l + 32, ...); finish_load rearranges
+// them.  A row of 16-bit elements may start in the middle of a word: word k then holds elements
+// 2k - 1 and 2k, and word 0 the piece's last and first one, which are read one by one.  (8000 x 8191
+// bf16 to 4 bits: 51 us; all elements one by one 74.)
+// FULL: the whole piece lies before `cols`.  first: the first element, where it is apart.
+template <int T, bool VEC>
+__device__ __forceinline__ bool starts_inside_word(const char *base) {
+  return !VEC && kTypeBytes<T> == 2 && (reinterpret_cast<uintptr_t>(base) & 2) != 0;
+}
+
+// Elements of a lane's word j of such a piece, and whether they are apart in memory.
+struct WordElems {
+  int lo, hi;
+  bool apart;
+  __device__ __forceinline__ WordElems(int j, int lane, bool inside) {
+    const int k = j * 32 + lane;
+    apart = inside && k == 0;
+    lo = apart ? 255 : 2 * k - (inside ? 1 : 0);
+    hi = 2 * k + (inside ? 0 : 1);
+  }
+};
+
 template <int T, bool VEC, bool FULL>
-__device__ __forceinline__ void issue_load(const char *base, int left, int lane, uint32_t (&w)[4]) {
+__device__ __forceinline__ void issue_load(const char *base, int left, int lane, uint32_t (&w)[4], uint32_t &first) {
   constexpr int E = kLaneElems<T>;
   if (VEC && (FULL || (lane + 1) * E <= left)) {
     const uint4 a = *reinterpret_cast<const uint4 *>(base + lane * 16);
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    return;
-  }
-  const int first = VEC ? lane * E : lane;
-  constexpr int step = VEC ? 1 : 32;
-  if constexpr (T == kTypeF32) {
+  } else if constexpr (T == kTypeF32) {
+    const int at = VEC ? lane * E : lane;
+    constexpr int step = VEC ? 1 : 32;
     const uint32_t *q = reinterpret_cast<const uint32_t *>(base);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = FULL || first + j * step < left ? q[first + j * step] : 0u;
+    for (int j = 0; j < 4; ++j) w[j] = FULL || at + j * step < left ? q[at + j * step] : 0u;
   } else {
     const unsigned short *q = reinterpret_cast<const unsigned short *>(base);
+    const bool inside = starts_inside_word<T, VEC>(base);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int c = first + 2 * j * step;
-      const uint32_t lo = FULL || c < left ? q[c] : 0u;
-      const uint32_t hi = FULL || c + step < left ? q[c + step] : 0u;
-      w[j] = lo | (hi << 16);
+      WordElems e(j, lane, inside);
+      if constexpr (VEC) e.lo = lane * E + 2 * j, e.hi = e.lo + 1;
+      // Nothing here waits for a load: a word's two halves are joined in finish_load.
+      w[j] = 0;
+      if (!e.apart && (FULL || e.hi < left))
+        w[j] = *reinterpret_cast<const uint32_t *>(q + e.lo);
+      else if (FULL || e.lo < left)
+        w[j] = q[e.lo];
     }
+    if (!VEC) first = inside && lane == 0 ? q[0] : 0;
   }
 }
 
-// `stage`: 512 bytes of shared memory per warp.
+// `stage`: 512 bytes of shared memory per warp; `inside`: starts_inside_word of the row.
 template <int T, bool VEC>
-__device__ __forceinline__ void finish_load(int lane, uint32_t *stage, uint32_t (&w)[4]) {
+__device__ __forceinline__ void finish_load(int lane, bool inside, uint32_t first, uint32_t *stage, uint32_t (&w)[4]) {
   if constexpr (!VEC) {
+    if (kTypeBytes<T> == 2) w[0] |= first << 16;
     __syncwarp();
-    if constexpr (T == kTypeF32) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) stage[j * 32 + lane] = w[j];
-    } else {
-      unsigned short *h = reinterpret_cast<unsigned short *>(stage);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[2 * j * 32 + lane] = static_cast<unsigned short>(w[j]);
-        h[(2 * j + 1) * 32 + lane] = static_cast<unsigned short>(w[j] >> 16);
-      }
-    }
+    for (int j = 0; j < 4; ++j) stage[j * 32 + lane] = w[j];
     __syncwarp();
     const uint4 a = reinterpret_cast<const uint4 *>(stage)[lane];
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    if (kTypeBytes<T> == 2 && inside) {
+      const uint32_t n = __shfl_sync(0xffffffffu, w[0], (lane + 1) & 31);
+      w[0] = __funnelshift_r(w[0], w[1], 16);
+      w[1] = __funnelshift_r(w[1], w[2], 16);
+      w[2] = __funnelshift_r(w[2], w[3], 16);
+      w[3] = __funnelshift_r(w[3], n, 16);
+    }
   }
 }
 
@@ -100,32 +122,41 @@ __device__ __forceinline__ void store_lane(char *base, int left, int lane, uint3
     return;
   }
   uint32_t x[4] = {w[0], w[1], w[2], w[3]};
+  const bool inside = starts_inside_word<T, VEC>(base);
   if constexpr (!VEC) {
+    if (kTypeBytes<T> == 2 && inside) {
+      const uint32_t n = __shfl_sync(0xffffffffu, w[3], (lane + 31) & 31);
+      x[0] = __funnelshift_r(n, w[0], 16);
+      x[1] = __funnelshift_r(w[0], w[1], 16);
+      x[2] = __funnelshift_r(w[1], w[2], 16);
+      x[3] = __funnelshift_r(w[2], w[3], 16);
+    }
     __syncwarp();
-    reinterpret_cast<uint4 *>(stage)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4 *>(stage)[lane] = make_uint4(x[0], x[1], x[2], x[3]);
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (T == kTypeF32) {
-        x[j] = stage[j * 32 + lane];
-      } else {
-        const unsigned short *h = reinterpret_cast<const unsigned short *>(stage);
-        x[j] = h[2 * j * 32 + lane] | (static_cast<uint32_t>(h[(2 * j + 1) * 32 + lane]) << 16);
-      }
-    }
+    for (int j = 0; j < 4; ++j) x[j] = stage[j * 32 + lane];
   }
-  const int first = VEC ? lane * E : lane;
-  constexpr int step = VEC ? 1 : 32;
   if constexpr (T == kTypeF32) {
+    const int at = VEC ? lane * E : lane;
+    constexpr int step = VEC ? 1 : 32;
     uint32_t *q = reinterpret_cast<uint32_t *>(base);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (FULL || first + j * step < left) q[first + j * step] = x[j];
+      if (FULL || at + j * step < left) q[at + j * step] = x[j];
   } else {
     unsigned short *q = reinterpret_cast<unsigned short *>(base);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (FULL || first + j * step < left) q[first + j * step] = static_cast<unsigned short>(x[j / 2] >> (16 * (j & 1)));
+    for (int j = 0; j < 4; ++j) {
+      WordElems e(j, lane, inside);
+      if constexpr (VEC) e.lo = lane * E + 2 * j, e.hi = e.lo + 1;
+      if (!e.apart && (FULL || e.hi < left)) {
+        *reinterpret_cast<uint32_t *>(q + e.lo) = x[j];
+      } else {
+        if (FULL || e.lo < left) q[e.lo] = static_cast<unsigned short>(x[j]);
+        if (FULL || e.hi < left) q[e.hi] = static_cast<unsigned short>(x[j] >> 16);
+      }
+    }
   }
 }
 
@@ -225,10 +256,15 @@ __device__ __forceinline__ int64_t scale_row(uint32_t row, int64_t tile_row_byte
   return (row >> 7) * tile_row_bytes + ((row & 31) * 16 + ((row >> 5) & 3) * 4);
 }
 
+// CTAs an SM.  Rows that are not aligned wait for shared memory as well as for their loads: 16-bit ones
+// do best with five (8000 x 8191 bf16 to 4 bits 51 us, 66 with three), fp32 ones, whose registers
+// would spill, with three (4000 x 8191: 37 us, 51 with five).
+constexpr int quantize_ctas(int type, bool vec) { return vec ? 4 : type == kTypeF32 ? 3 : 5; }
+
 // Quantises X row by row; with ACT also writes Y = act(X).  The lanes of a block (4 of 16-bit
 // elements, 8 of fp32) agree on its largest magnitude by shuffles.
 template <int T, int FMT, bool ACT, bool VEC, int U>
-__global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
+__global__ void __launch_bounds__(kRowThreads, quantize_ctas(T, VEC))
     quantize_rows_kernel(const RowMat x, const MxMat o, const RowMat y, int act, uint32_t rows,
                          uint32_t cols, uint32_t rows_per, int across) {
   using St = Stripe<T, U>;
@@ -252,29 +288,34 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
   // Whole stripes (all but the last) need no column checks.
   auto run = [&](auto full) {
     constexpr bool kFull = decltype(full)::value;
-    uint32_t next[U][4];  // the row to work on next
+    uint32_t next[U][4], first_next[U] = {};  // the row to work on next
+    bool inside_next = false;
     auto issue = [&]() {
+      inside_next = starts_inside_word<T, VEC>(src);
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (kFull || u * St::kPiece < s.left)
-          issue_load<T, VEC, kFull>(src + u * (St::kPiece * B), s.left - u * St::kPiece, lane, next[u]);
+          issue_load<T, VEC, kFull>(src + u * (St::kPiece * B), s.left - u * St::kPiece, lane, next[u], first_next[u]);
       src += s.step * x.ld * B;
     };
     if (kAheadOne && s.r < s.r1) issue();
     for (uint32_t r = s.r; r < s.r1; r += s.step) {
       if (!kAheadOne) issue();
-      uint32_t w[U][4];
+      uint32_t w[U][4], first[U];
+      const bool inside = inside_next;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u) {
+        first[u] = first_next[u];
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[u][j] = next[u][j];
+      }
       if (kAheadOne && r + s.step < s.r1) issue();
       const int64_t sr = scale_row(r, tile_row);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (kFull || u * St::kPiece < s.left) {
           float v[E];
-          finish_load<T, VEC>(lane, st, w[u]);
+          finish_load<T, VEC>(lane, inside, first[u], st, w[u]);
           to_floats<T, E>(w[u], v);
           uint32_t m = amax_bits<T, 4>(w[u]);
 #pragma unroll
@@ -571,7 +612,7 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
     uint32_t *st = VEC ? nullptr : sh.stage[VEC ? 0 : warp];
     const uint8_t *zs = z.s + scale_offset(0, s.block, z.tiles_x);
     for (uint32_t r = s.r; r < s.r1; r += s.step) {
-      uint32_t w[U][4];
+      uint32_t w[U][4], first[U] = {};
       MxLane<kE4M3, E> q[U];
       const int64_t sr = scale_row(r, tile_row);
 #pragma unroll
@@ -579,12 +620,12 @@ __global__ void __launch_bounds__(kRowThreads, VEC ? 4 : 3)
         issue_load_mx<kE4M3, E>(zq + u * (32 * kQ), zs + sr + u * St::kPieceScales,
                                 s.block + u * (St::kPiece / kMxBlock) < z.blocks, q[u]);
         if (u * St::kPiece < s.left)
-          issue_load<T, VEC, false>(src + u * (St::kPiece * B), s.left - u * St::kPiece, lane, w[u]);
+          issue_load<T, VEC, false>(src + u * (St::kPiece * B), s.left - u * St::kPiece, lane, w[u], first[u]);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (u * St::kPiece < s.left) {
-          finish_load<T, VEC>(lane, st, w[u]);
+          finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(src), first[u], st, w[u]);
           work(u, w[u], q[u].q, q[u].byte);
           store_lane<T, VEC, false>(dst + u * (St::kPiece * B), s.left - u * St::kPiece, lane, st, w[u]);
         }
@@ -709,11 +750,9 @@ struct RowGrid {
   uint32_t rows_per;
 };
 
-RowGrid row_grid(int64_t rows, int64_t cols, int type, bool vec, int wide, int most_across, int least_rows, int sms,
-                 int per_sm) {
+RowGrid row_grid(int64_t rows, int64_t cols, int type, int wide, int most_across, int least_rows, int sms, int per_sm) {
   const int64_t piece = 32 * 16 / type_bytes(type);
   RowGrid g;
-  if (!vec && type != TLG_TYPE_F32) wide = 1;  // element loads: eight a piece are enough in flight
   const int64_t items = (rows + kRowWarps - 1) / kRowWarps * ((cols + piece * wide - 1) / (piece * wide));
   g.u = items >= 2 * int64_t(sms) ? wide : 1;
   const int64_t stripes = (cols + piece * g.u - 1) / (piece * g.u);
@@ -750,7 +789,13 @@ RowGrid row_grid(int64_t rows, int64_t cols, int type, bool vec, int wide, int m
 // The same for the backward kernel, whose splits each leave a partial column sum: at least two
 // rows to a warp, and as many CTAs an SM as its registers allow.
 RowGrid backward_grid(int64_t rows, int64_t cols, int type, bool vec, int sms) {
-  return row_grid(rows, cols, type, true, kWideBackward, kAcrossBackward, 2, sms, vec ? 4 : 3);
+  return row_grid(rows, cols, type, kWideBackward, kAcrossBackward, 2, sms, vec ? 4 : 3);
+}
+
+// And for quantising: 16-bit rows that are not aligned fill the SM with more CTAs of one piece instead
+// (8000 x 8191 bf16 with SiLU: 94 us, 103 with four pieces and three CTAs).
+RowGrid quantize_grid(int64_t rows, int64_t cols, int type, bool vec, int sms) {
+  return row_grid(rows, cols, type, vec || type == TLG_TYPE_F32 ? kWide : 1, kAcross, 1, sms, quantize_ctas(type, vec));
 }
 
 // Workspace bytes of its partial sums; the caller does not know which matrices will be aligned.
@@ -811,7 +856,7 @@ tlg_status tlg_mx_quantize(tlg_mx_format format, int64_t rows, int64_t cols, tlg
                       kT == kTypeF32 ? 512 : 256, s, X, ldx, pairs, o, rows, cols, tiles_r, tiles);
       }
       const bool vec = vec_rows(X, rows, ldx, type);
-      const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, vec ? 4 : 3);
+      const RowGrid g = quantize_grid(rows, cols, type, vec, info.sm_count);
       return with_flag(vec, [&](auto V) {
         return with_width(g.u, [&](auto U) {
           return launch(quantize_rows_kernel<kT, kF, false, decltype(V)::value, decltype(U)::value>, g.grid,
@@ -838,7 +883,7 @@ tlg_status tlg_mx_dequantize(tlg_mx_format format, int64_t rows, int64_t cols, c
   if (st != TLG_OK) return st;
   const MxMat in = mx_mat(Q, ldq, S, cols);
   const bool vec = vec_rows(X, rows, ldx, type);
-  const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, vec ? 4 : 3);
+  const RowGrid g = row_grid(rows, cols, type, kWide, kAcross, 1, info.sm_count, 4);
   return with_type(type, [&](auto T) {
     return with_format(format, [&](auto F) {
       return with_flag(vec, [&](auto V) {
@@ -871,7 +916,7 @@ tlg_status tlg_act_forward_mx(int64_t rows, int64_t cols, tlg_activation activat
   if (st != TLG_OK) return st;
   const MxMat o = mx_mat(Q, ldq, S, cols);
   const bool vec = vec_rows(Z, rows, ldz, type) && vec_rows(Y, rows, ldy, type);
-  const RowGrid g = row_grid(rows, cols, type, vec, kWide, kAcross, 1, info.sm_count, vec ? 4 : 3);
+  const RowGrid g = quantize_grid(rows, cols, type, vec, info.sm_count);
   return with_type(type, [&](auto T) {
     return with_flag(vec, [&](auto V) {
       return with_width(g.u, [&](auto U) {
