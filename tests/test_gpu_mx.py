@@ -288,6 +288,34 @@ def test_one_row_of_any_stride(tlg):
         assert torch.equal(Y, row.clamp(min=0))
 
 
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("cols", [1, 2, 31, 129, 255, 256, 257, 511, 513, 1023, 1025, 2049])
+@pytest.mark.parametrize("lead,odd", [(0, 0), (1, 0), (0, 1), (1, 1)])
+def test_any_alignment_gives_the_aligned_bits(tlg, typ, cols, lead, odd):
+    """Rows that start at any element, and whose neighbours share their words, against the same
+    values in 16-byte aligned rows: every element is computed alone, so the bits are the same."""
+    rows = 2401 if cols == 1025 else 133  # the many fill the device, and warps take several pieces
+    extra = (odd - cols) % 2  # rows an odd or an even number of elements apart, as close as that allows
+    x, dy = values(rows, cols, TYPES[typ], cols), values(rows, cols, TYPES[typ], cols + 1)
+    flat = [Strided(t, 0, -cols % 8) for t in (x, dy)]
+    X, dY = Strided(x, lead, extra), Strided(dy, lead, extra)
+    for fmt in ("e2m1", "e4m3"):
+        want, got = (tlg.tlg_mx_quantize(t.view, format=fmt) for t in (flat[0], X))
+        assert torch.equal(want[0], got[0])
+        index = torch.from_numpy(mx.scale_index(rows, -(-want[0].shape[1] // (16 if fmt == "e2m1" else 32) // 4) * 4)).cuda()
+        assert torch.equal(want[1][index], got[1][index])
+        o = [Strided(torch.zeros_like(x), *at) for at in ((0, -cols % 8), (lead, extra))]
+        for t in o:
+            tlg.tlg_mx_dequantize(*want, cols, format=fmt, out=typ, X=t.view)
+        assert torch.equal(bits(o[0].view), bits(o[1].view)) and o[1].guards_kept()
+    y, q, s = tlg.tlg_act_forward_mx(flat[0].view, "silu")
+    tlg.tlg_act_forward_mx(X.view, "silu", Y=X.view)  # in place
+    assert torch.equal(bits(X.view), bits(y)) and X.guards_kept()
+    dz, _ = tlg.tlg_act_backward_mx(flat[1].view, q, s, "silu", bias_grad=False)
+    tlg.tlg_act_backward_mx(dY.view, q, s, "silu", dZ=dY.view)
+    assert torch.equal(bits(dY.view), bits(dz)) and dY.guards_kept()
+
+
 def test_calls_on_two_streams_at_once(tlg):
     """Calls that overlap in time, each with a workspace of its own."""
     rng = np.random.default_rng(1)
