@@ -198,7 +198,9 @@ template <int OUT, int BYTES>
 __device__ __forceinline__ void mx_copy_box(const MxGemmParams &p, int row0, int col0, int lane, uint32_t box) {
   constexpr int kLanes = 64 / BYTES;  // to a row
   const int byte = lane % kLanes * BYTES;
-  const int left = max(0, min(BYTES, (p.N - col0) * kTypeBytes<OUT> - byte));
+  // Counted in elements first: a row of R may hold more than 2^31 bytes.
+  const int cols = min(p.N - col0, 64 / kTypeBytes<OUT>);
+  const int left = max(0, min(BYTES, cols * kTypeBytes<OUT> - byte));
   const char *q = static_cast<const char *>(p.R) + (static_cast<int64_t>(row0) * p.ldr + col0) * kTypeBytes<OUT> + byte;
 #pragma unroll 4
   for (int r = lane / kLanes; r < 32; r += 32 / kLanes) {
