@@ -1,0 +1,40 @@
+"""The activations' derivatives in tlg_act_backward_mx at the ends of their range: saved values that
+decode to infinity."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+ACTS = ["none", "relu", "gelu", "silu", "gelu_tanh"]
+
+
+@pytest.fixture(scope="module")
+def tlg():
+    import tiled_dense_gemm_tlg_b200 as t
+    return t
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("typ", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cols", [64, 300, 2048])
+def test_largest_inputs(tlg, act, typ, cols):
+    """The type's largest value is saved as 2^128, which fp32 reads back as infinity; the derivative
+    there is 1, and on the negative side 0 (1 for the identity)."""
+    rows = 40
+    z = torch.zeros((rows, cols), dtype=typ)
+    z[1::2, 0::3] = torch.finfo(typ).max
+    z[1::2, 1::3] = -torch.finfo(typ).max
+    Y, Q, S = tlg.tlg_act_forward_mx(z.cuda(), act)
+    assert torch.isinf(tlg.tlg_mx_dequantize(Q, S, cols, format="e4m3", out="f32")).any()
+    dy = torch.randint(-8, 9, (rows, cols), generator=torch.Generator().manual_seed(cols)).to(typ)
+    dz, db = tlg.tlg_act_backward_mx(dy.cuda(), Q, S, act)
+    zf = z.double()
+    at_zero = {"none": 1.0, "relu": 0.0}.get(act, 0.5)
+    slope = torch.where(zf > 0, 1.0, torch.where(zf < 0, 1.0 if act == "none" else 0.0, at_zero))
+    want = dy.double() * slope
+    # |dY| <= 8 times the derivative's error, and a rounding of 4 or less
+    bound = 8e-6 + 4 * torch.finfo(typ).eps / 2
+    assert ((dz.double().cpu() - want).abs() <= bound).all()
+    # sums of multiples of 1/2, each term within 8e-6
+    assert ((db.double().cpu() - want.sum(dim=0)).abs() <= rows * 8e-6 + rows * 2.0 ** -24 * 8 * rows).all()

@@ -333,10 +333,11 @@ __device__ __forceinline__ void gelu_slope_2(float x0, float x1, float &s0, floa
 
 // The derivative of x sigmoid(u): s + x s (1 - s) u'(x), with s = 1 / (1 + t), 1 - s = t s,
 // t = 2^(-u log2 e).  x is held to where the derivative is 0 or 1 to fp32's last place and t
-// still finite, so no product is 0 times infinity; a NaN stays.
-//   SiLU: u = x.  Only negative x needs holding (above, t underflows to 0 and x t s to 0).
+// still finite, so no product is 0 times infinity (a saved value may read back as infinity: the
+// largest fp32 and bf16 values round up to 2^128 in 8 bits); a NaN stays.
+//   SiLU: u = x; |x| held to 80.
 __device__ __forceinline__ void silu_slope_2(float x0, float x1, float &s0, float &s1) {
-  const uint64_t x = f2_pack(max_nan(x0, -80.0f), max_nan(x1, -80.0f));
+  const uint64_t x = f2_pack(clamp_nan(x0, 80.0f), clamp_nan(x1, 80.0f));
   float z0, z1;
   f2_unpack(f2_mul(x, f2_splat(-1.4426950408889634f)), z0, z1);
   const uint64_t t = f2_pack(ex2_approx(z0), ex2_approx(z1));
