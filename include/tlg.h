@@ -488,8 +488,9 @@ tlg_status tlg_act_forward_mx(int64_t rows, int64_t cols, tlg_activation activat
  * values of the E4M3 MX matrix (Q, S), and, when dbias is not NULL, dbias[c] =
  * the sum over the rows of dZ[., c] (cols fp32 values), summed in fp32 before
  * dZ is rounded, in an order that does not depend on timing.  dZ may be dY
- * itself.  act' is computed in fp32 with an error below 1e-6; ReLU's is 0 at
- * 0, and a NaN in Z makes dZ NaN.
+ * itself.  act' is computed in fp32 with an error below 1e-6, and GELU's on
+ * [-12, -2], where it is small, within 2e-5 of its value; ReLU's is 0 at 0,
+ * and a NaN in Z makes dZ NaN.
  * workspace: tlg_act_backward_mx_workspace_size() bytes of device memory,
  * 256-byte aligned, needed when dbias is not NULL (TLG_ERR_INVALID_ARG when too
  * small; the size may be 0).  Its contents on entry do not matter; calls that

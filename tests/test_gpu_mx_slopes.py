@@ -1,8 +1,11 @@
 """The activations' derivatives in tlg_act_backward_mx at the ends of their range: saved values that
-decode to infinity."""
+decode to infinity, and the negative side of GELU where the derivative is small."""
 
+import numpy as np
 import pytest
 import torch
+
+from oracle import mx
 
 pytestmark = pytest.mark.gpu
 
@@ -13,6 +16,11 @@ ACTS = ["none", "relu", "gelu", "silu", "gelu_tanh"]
 def tlg():
     import tiled_dense_gemm_tlg_b200 as t
     return t
+
+
+def saved(z):
+    codes, scale = mx.quantize(z, "e4m3")
+    return torch.from_numpy(mx.pack(codes, "e4m3")).cuda(), torch.from_numpy(mx.tile_scales(scale, 255)).cuda()
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -38,3 +46,19 @@ def test_largest_inputs(tlg, act, typ, cols):
     assert ((dz.double().cpu() - want).abs() <= bound).all()
     # sums of multiples of 1/2, each term within 8e-6
     assert ((db.double().cpu() - want.sum(dim=0)).abs() <= rows * 8e-6 + rows * 2.0 ** -24 * 8 * rows).all()
+
+
+def test_gelu_slope_keeps_relative_accuracy(tlg):
+    """Saved values of three mantissa bits come back exactly.  The derivative's fit is within 1e-5
+    of it, relatively, on [-12, -2] (checked on the CPU with its roundings); the hardware's exp2 and
+    reciprocal add at most 2^-22 each."""
+    v = np.array([-2, -2.5, -3, -3.5, -4, -4.5, -5, -5.5, -6, -6.5, -7, -8, -9, -10, -12])
+    Q, S = saved(np.repeat(v[:, None], 96, axis=1))
+    dy = torch.full((len(v), 96), 1024.0, device="cuda")
+    dz = tlg.tlg_act_backward_mx(dy, Q, S, "gelu")[0].double().cpu().numpy() / 1024
+    want = mx.slope("gelu", v)[:, None]
+    assert (np.abs(dz / want - 1) < 2e-5).all(), np.abs(dz / want - 1).max(axis=1)
+    v = np.array([-14, -100, -1e30])  # further out it is 0 to fp32's smallest numbers
+    Q, S = saved(np.repeat(v[:, None], 96, axis=1))
+    dz = tlg.tlg_act_backward_mx(dy[:3], Q, S, "gelu")[0]
+    assert (dz.abs() < 1e-37).all()

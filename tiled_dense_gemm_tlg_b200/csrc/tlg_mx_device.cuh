@@ -301,34 +301,39 @@ __device__ __forceinline__ float clamp_nan(float x, float limit) {
   return r;
 }
 
-// GELU'(x) = Phi(x) + x phi(x) = 1/2 + sign(x) (1/2 - T(a)), a = min(|x|, 6),
-// T(a) = Phi(-a) - a phi(a) = exp(-a^2 / 2) P(a), P a degree-10 polynomial
-// (fit_gelu_slope.py beside this file prints it): error below 2e-7, one exp2.
+// GELU'(x) = Phi(x) + x phi(x): with a = |x| and T(a) = Phi(-a) - a phi(a) it is T(a) below 0 and
+// 1 - T(a) above.  T(a) = exp(-a^2 / 2) (E(t) - a / sqrt(2 pi)), E a degree-6 polynomial in
+// t = 1 / (1 + 0.38 a) (fit_gelu_slope.py beside this file prints it).  Its error is below 2e-7, and
+// below 0, where T is taken as it is, at most 1e-5 of T from -2 on: a gradient that is scaled up, or
+// a difference 1/2 - (1/2 - T), would show more.  a is held to 14, where the exponential is 0 (an
+// infinite a would give 0 times infinity); a NaN stays.
 __device__ __forceinline__ constexpr float gelu_slope_coef(int k) {  // lowest degree first
-  constexpr float c[11] = {0.49999994f,     -0.797878802f,   0.249916792f,    -0.132513806f,
-                           0.0611548908f,   -0.024313936f,   0.00793939456f,  -0.00197462924f,
-                           0.000339738879f, -3.52078423e-05f, 1.63169318e-06f};
+  constexpr float c[7] = {0.000803342089f, 0.139656156f, 0.221370354f, -0.081764549f,
+                          0.440671146f, -0.27447772f, 0.0537412576f};
   return c[k];
 }
 
 __device__ __forceinline__ void gelu_slope_2(float x0, float x1, float &s0, float &s1) {
   auto mag = [](float x) {
     float r;
-    asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %1;\n\tmin.NaN.f32 %0, t, %2;\n\t}" : "=f"(r) : "f"(x), "f"(6.0f));
+    asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %1;\n\tmin.NaN.f32 %0, t, %2;\n\t}" : "=f"(r) : "f"(x), "f"(14.0f));
     return r;
   };
   const uint64_t a = f2_pack(mag(x0), mag(x1));
-  float u0, u1;
+  float u0, u1, d0, d1;
   f2_unpack(f2_mul(f2_mul(a, f2_splat(-0.72134752044448170f)), a), u0, u1);  // -a^2/2 log2(e)
-  uint64_t p = f2_splat(gelu_slope_coef(10));
+  f2_unpack(f2_fma(a, f2_splat(0.38f), f2_splat(1.0f)), d0, d1);
+  const uint64_t t = f2_pack(rcp_approx(d0), rcp_approx(d1));
+  uint64_t p = f2_splat(gelu_slope_coef(6));
 #pragma unroll
-  for (int k = 9; k >= 0; --k) p = f2_fma(p, a, f2_splat(gelu_slope_coef(k)));
-  const uint64_t t = f2_mul(p, f2_pack(ex2_approx(u0), ex2_approx(u1)));
-  float h0, h1;
-  f2_unpack(f2_fma(t, f2_splat(-1.0f), f2_splat(0.5f)), h0, h1);
-  h0 = __uint_as_float(__float_as_uint(h0) ^ (__float_as_uint(x0) & 0x80000000u));
-  h1 = __uint_as_float(__float_as_uint(h1) ^ (__float_as_uint(x1) & 0x80000000u));
-  f2_unpack(f2_add(f2_pack(h0, h1), f2_splat(0.5f)), s0, s1);
+  for (int k = 5; k >= 0; --k) p = f2_fma(p, t, f2_splat(gelu_slope_coef(k)));
+  p = f2_fma(a, f2_splat(-0.39894228040143268f), p);  // -1 / sqrt(2 pi)
+  const uint64_t s = f2_mul(p, f2_pack(ex2_approx(u0), ex2_approx(u1)));
+  float t0, t1, r0, r1;
+  f2_unpack(s, t0, t1);
+  f2_unpack(f2_fma(s, f2_splat(-1.0f), f2_splat(1.0f)), r0, r1);
+  s0 = x0 < 0.0f ? t0 : r0;
+  s1 = x1 < 0.0f ? t1 : r1;
 }
 
 // The derivative of x sigmoid(u): s + x s (1 - s) u'(x), with s = 1 / (1 + t), 1 - s = t s,
