@@ -453,8 +453,9 @@ tlg_status tlg_mx_dequantize(tlg_mx_format format, int64_t rows, int64_t cols,
  * (bf16 when C is bf16), the residual has C's type and may be C itself.
  * config: NULL or zero fields choose automatically; block_n, cta_group,
  * stages, raster_group and max_ctas as for tlg_gemm_ex, split_k 0 or 1,
- * overlap_prev is always on.  M <= 32 has a kernel of its own (block_n 16 or
- * 32: the tokens; cta_group, stages and max_ctas must be 0), where k_split 1,
+ * overlap_prev is always on.  M <= 32 has a kernel of its own (block_n 16 up
+ * to 16 rows, else 32; it runs when cta_group, stages and max_ctas are 0, or
+ * when block_n names it and they are 0 or what it runs with), where k_split 1,
  * 2, 4 or 8 CTAs share the K range (at most one per 256 k); elsewhere k_split
  * is 0 or 1.  No workspace.  K == 0 gives C = act(bias)
  * + residual.  Sizes and errors as tlg_gemm_fused's; lda and ldb are in BYTES
@@ -468,9 +469,20 @@ tlg_status tlg_gemm_mxfp4(int64_t M, int64_t N, int64_t K,
                           void *C, int64_t ldc, tlg_type out,
                           const tlg_config *config, void *stream);
 
-/* tlg_choose_config for tlg_gemm_mxfp4. */
+/*
+ * The configuration tlg_gemm_mxfp4 runs for this shape and type of C, as
+ * tlg_choose_config: the request in *config (zero fields: automatic) is
+ * replaced by the answer, which passed back as a request gives itself.  The
+ * choice depends on whether there is an epilogue: the first function answers
+ * for the plain product (epilogue NULL, or none of its parts), the second for
+ * a call with `epilogue` (only which parts are set matters; its pointers are
+ * not followed).
+ */
 tlg_status tlg_choose_config_mxfp4(int64_t M, int64_t N, int64_t K, tlg_type out,
                                    tlg_config *config);
+tlg_status tlg_choose_config_mxfp4_fused(int64_t M, int64_t N, int64_t K,
+                                         const tlg_fused_epilogue *epilogue,
+                                         tlg_type out, tlg_config *config);
 
 /*
  * Y = act(Z), and Z saved for the backward pass as an E4M3 MX matrix, in one

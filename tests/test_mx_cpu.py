@@ -237,3 +237,13 @@ def test_workspace_must_be_contiguous(tlg):
     for workspace in (torch.zeros(1).expand(1 << 20), torch.zeros(1 << 12)[::2]):
         with pytest.raises(ValueError, match="workspace"):
             tlg.tlg_act_backward_mx(X, Q, S, "gelu", workspace=workspace)
+
+
+def test_choose_config_refusals(tlg):
+    lib, bad = tlg.raw_library(), tlg.TLG_ERR_INVALID_ARG
+    cfg, E = tlg.tlg_config(), tlg.tlg_fused_epilogue
+    assert lib.tlg_choose_config_mxfp4_fused(8, 8, 8, None, 1, None) == bad
+    assert lib.tlg_choose_config_mxfp4_fused(8, -8, 8, None, 1, ctypes.byref(cfg)) == bad
+    assert lib.tlg_choose_config_mxfp4_fused(8, 8, 8, ctypes.byref(E(None, 9, None, 0)), 1, ctypes.byref(cfg)) == bad
+    with pytest.raises(ValueError):
+        tlg.tlg_choose_config_mxfp4_fused(8, 8, 8, activation="swish")

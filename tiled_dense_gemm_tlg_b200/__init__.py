@@ -115,7 +115,9 @@ _lib.tlg_act_backward_mx_workspace_size.argtypes = [_i64, _i64, _i32, ctypes.POI
 _lib.tlg_gemm_mxfp4.argtypes = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, ctypes.POINTER(tlg_fused_epilogue),
                                 _p, _i64, _i32, ctypes.POINTER(tlg_config), _p]
 _lib.tlg_choose_config_mxfp4.argtypes = [_i64, _i64, _i64, _i32, ctypes.POINTER(tlg_config)]
-for _name in ("tlg_gemm_mxfp4", "tlg_choose_config_mxfp4", "tlg_mx_size", "tlg_mx_quantize", "tlg_mx_dequantize", "tlg_act_forward_mx", "tlg_act_backward_mx",
+_lib.tlg_choose_config_mxfp4_fused.argtypes = [_i64, _i64, _i64, ctypes.POINTER(tlg_fused_epilogue), _i32,
+                                               ctypes.POINTER(tlg_config)]
+for _name in ("tlg_gemm_mxfp4", "tlg_choose_config_mxfp4", "tlg_choose_config_mxfp4_fused", "tlg_mx_size", "tlg_mx_quantize", "tlg_mx_dequantize", "tlg_act_forward_mx", "tlg_act_backward_mx",
               "tlg_act_backward_mx_workspace_size", "tlg_gemm_f16f32", "tlg_gemm_f16f16", "tlg_gemm_bias_relu_f16", "tlg_gemm_ex",
               "tlg_gemm_op", "tlg_gemm_fused", "tlg_gemm_ex_noalloc", "tlg_gemm_workspace_size", "tlg_gemm_workspace_size_op", "tlg_choose_config", "tlg_device_error", "tlg_selftest_timeout"):
     getattr(_lib, _name).restype = _i32
@@ -473,9 +475,22 @@ def tlg_gemm_mxfp4(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch
 
 
 def tlg_choose_config_mxfp4(M: int, N: int, K: int, out: str = "f16", request: dict | None = None) -> dict:
-    """The configuration tlg_gemm_mxfp4 would run for this shape (request fields of 0 = automatic)."""
+    """The configuration tlg_gemm_mxfp4 runs for this shape without an epilogue (request fields of 0 =
+    automatic); the choice with one may differ, see ``tlg_choose_config_mxfp4_fused``."""
     cfg = tlg_config(**{k: int(v) for k, v in (request or {}).items()})
     _check(_lib.tlg_choose_config_mxfp4(M, N, K, _out_type(out), ctypes.byref(cfg)), "tlg_choose_config_mxfp4")
+    return cfg.as_dict()
+
+
+def tlg_choose_config_mxfp4_fused(M: int, N: int, K: int, bias: bool = False, activation: str = "none",
+                                  residual: bool = False, out: str = "f16", request: dict | None = None) -> dict:
+    """The configuration tlg_gemm_mxfp4 runs for this shape with such an epilogue: ``bias`` and
+    ``residual`` say whether the call has them."""
+    cfg = tlg_config(**{k: int(v) for k, v in (request or {}).items()})
+    # set or not is all that matters of the pointers
+    epi = tlg_fused_epilogue(1 if bias else None, _activation(activation), 1 if residual else None, 0)
+    _check(_lib.tlg_choose_config_mxfp4_fused(M, N, K, ctypes.byref(epi), _out_type(out), ctypes.byref(cfg)),
+           "tlg_choose_config_mxfp4_fused")
     return cfg.as_dict()
 
 

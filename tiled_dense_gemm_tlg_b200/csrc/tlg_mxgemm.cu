@@ -209,15 +209,18 @@ tlg_status choose(int dev, int sms, int64_t M, int64_t N, int64_t K, int type, b
     return TLG_ERR_UNSUPPORTED;
   const int num_kb = static_cast<int>((K + kMxBK - 1) / kMxBK);
   out->tokens = 0;
-  // Few rows of A (a request for a cta_group or for tiles asks for the other kernel).
-  if (token_columns(M) != 0 && r.cta_group == 0 && r.stages == 0 && r.max_ctas == 0 &&
-      (r.block_n == 0 || r.block_n == token_columns(M))) {
+  // Few rows of A.  A request for a cta_group, stages or max_ctas alone asks for tiles; beside the
+  // kernel's block_n they have to be what it runs with, as in its own answer.
+  const bool named = r.block_n != 0 && r.block_n == token_columns(M);
+  if (named ? r.cta_group <= 1 && (r.stages == 0 || r.stages == MxTokenPlan<16>::kStages)
+            : token_columns(M) != 0 && r.block_n == 0 && r.cta_group == 0 && r.stages == 0 && r.max_ctas == 0) {
     const int ks = r.k_split != 0 ? r.k_split : token_split(N, num_kb, sms);
     if ((ks & (ks - 1)) != 0 || ks > num_kb) return TLG_ERR_UNSUPPORTED;
     out->tile = nullptr;
     out->tokens = token_columns(M);
     out->units = static_cast<int>((N + 127) / 128);
-    out->cfg = {out->tokens, 4, 1, 1, out->units * ks, 1, 1, ks};
+    if (r.max_ctas != 0 && r.max_ctas < out->units * ks) return TLG_ERR_UNSUPPORTED;
+    out->cfg = {out->tokens, MxTokenPlan<16>::kStages, 1, 1, out->units * ks, 1, 1, ks};
     return TLG_OK;
   }
   if (r.k_split > 1) return TLG_ERR_UNSUPPORTED;
@@ -256,6 +259,11 @@ tlg_status choose(int dev, int sms, int64_t M, int64_t N, int64_t K, int type, b
   c.overlap_prev = 1;
   c.k_split = 1;
   return TLG_OK;
+}
+
+// Whether the epilogue is more than the plain product's.
+bool has_work(const tlg_fused_epilogue *e) {
+  return e != nullptr && (e->bias != nullptr || e->activation != TLG_ACT_NONE || e->residual != nullptr);
 }
 
 tlg_status check_sizes(int64_t M, int64_t N, int64_t K, int out) {
@@ -314,7 +322,7 @@ tlg_status tlg_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void *A, int64_
     if (q != nullptr && !device_accessible(q, dev)) return TLG_ERR_INVALID_ARG;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool epi = e.bias != nullptr || e.activation != TLG_ACT_NONE || e.residual != nullptr;
+  const bool epi = has_work(&e);
   MxGemmParams p = {};
   p.C = C;
   p.ldc = ldc;
@@ -384,20 +392,26 @@ tlg_status tlg_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void *A, int64_
   return c.tile->fns[out][epi].launch(c.units, m, p, s);
 }
 
-tlg_status tlg_choose_config_mxfp4(int64_t M, int64_t N, int64_t K, tlg_type out, tlg_config *config) {
+tlg_status tlg_choose_config_mxfp4_fused(int64_t M, int64_t N, int64_t K, const tlg_fused_epilogue *epilogue,
+                                         tlg_type out, tlg_config *config) {
   if (config == nullptr) return TLG_ERR_INVALID_ARG;
   tlg_status st = check_sizes(M, N, K, out);
   if (st != TLG_OK) return st;
+  if (epilogue != nullptr && !valid_activation(epilogue->activation)) return TLG_ERR_INVALID_ARG;
   int dev = 0;
   DeviceInfo info;
   st = current_device(&dev, &info);
   if (st != TLG_OK) return st;
   MxChoice c;
   const tlg_config req = *config;
-  st = choose(dev, info.sm_count, std::max<int64_t>(M, 1), std::max<int64_t>(N, 1), std::max<int64_t>(K, 1), out, true,
-              &req, &c);
+  st = choose(dev, info.sm_count, std::max<int64_t>(M, 1), std::max<int64_t>(N, 1), std::max<int64_t>(K, 1), out,
+              has_work(epilogue), &req, &c);
   if (st == TLG_OK) *config = c.cfg;
   return st;
+}
+
+tlg_status tlg_choose_config_mxfp4(int64_t M, int64_t N, int64_t K, tlg_type out, tlg_config *config) {
+  return tlg_choose_config_mxfp4_fused(M, N, K, nullptr, out, config);
 }
 
 }  // extern "C"
