@@ -501,8 +501,9 @@ tlg_status tlg_act_forward_mx(int64_t rows, int64_t cols, tlg_activation activat
  * the sum over the rows of dZ[., c] (cols fp32 values), summed in fp32 before
  * dZ is rounded, in an order that does not depend on timing.  dZ may be dY
  * itself.  act' is computed in fp32 with an error below 1e-6, and GELU's on
- * [-12, -2], where it is small, within 2e-5 of its value; ReLU's is 0 at 0,
- * and a NaN in Z makes dZ NaN.
+ * [-12, -2], where it is small, within 2e-5 of its value.  ReLU's is 0 at 0,
+ * and where it is 0 dZ is 0 whatever dY holds.  A NaN in Z makes dZ NaN, except
+ * with TLG_ACT_NONE, whose derivative is 1 for every Z: dZ = dY.
  * workspace: tlg_act_backward_mx_workspace_size() bytes of device memory,
  * 256-byte aligned, needed when dbias is not NULL (TLG_ERR_INVALID_ARG when too
  * small; the size may be 0).  Its contents on entry do not matter; calls that

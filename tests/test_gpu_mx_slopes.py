@@ -1,5 +1,5 @@
 """The activations' derivatives in tlg_act_backward_mx at the ends of their range: saved values that
-decode to infinity, and the negative side of GELU where the derivative is small."""
+decode to infinity, the negative side of GELU where the derivative is small, and the identity."""
 
 import numpy as np
 import pytest
@@ -62,3 +62,14 @@ def test_gelu_slope_keeps_relative_accuracy(tlg):
     Q, S = saved(np.repeat(v[:, None], 96, axis=1))
     dz = tlg.tlg_act_backward_mx(dy[:3], Q, S, "gelu")[0]
     assert (dz.abs() < 1e-37).all()
+
+
+@pytest.mark.parametrize("typ", [torch.float32, torch.float16, torch.bfloat16])
+def test_identity_passes_the_gradient(tlg, typ):
+    """The identity's derivative is 1 whatever Z holds, a NaN block included."""
+    z = np.random.default_rng(0).standard_normal((33, 200))
+    z[5, 40] = np.nan
+    Q, S = saved(z)
+    dy = torch.randn((33, 200), device="cuda").to(typ)
+    dz, _ = tlg.tlg_act_backward_mx(dy, Q, S, "none")
+    assert torch.equal(dz, dy)

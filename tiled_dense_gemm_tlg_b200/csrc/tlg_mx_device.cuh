@@ -368,7 +368,7 @@ __device__ __forceinline__ void gelu_tanh_slope_2(float x0, float x1, float &s0,
 }
 
 // d[j] *= act'(z[j]).  ReLU's derivative at 0 is 0, and d is dropped there whatever it is (an
-// infinite d included); a NaN z makes d NaN for every activation.
+// infinite d included); a NaN z makes d NaN for every activation but the identity, which leaves d.
 template <int E>
 __device__ __forceinline__ void slope_lane(int act, const float (&z)[E], float (&d)[E]) {
   if (act == kActRelu) {
