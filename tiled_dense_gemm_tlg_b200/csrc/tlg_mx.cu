@@ -794,8 +794,10 @@ RowGrid backward_grid(int64_t rows, int64_t cols, int type, bool vec, int sms) {
 
 // And for quantising: 16-bit rows that are not aligned fill the SM with more CTAs of one piece instead
 // (8000 x 8191 bf16 with SiLU: 94 us, 103 with four pieces and three CTAs).
+constexpr int quantize_width(int type, bool vec) { return vec || type == kTypeF32 ? kWide : 1; }
+
 RowGrid quantize_grid(int64_t rows, int64_t cols, int type, bool vec, int sms) {
-  return row_grid(rows, cols, type, vec || type == TLG_TYPE_F32 ? kWide : 1, kAcross, 1, sms, quantize_ctas(type, vec));
+  return row_grid(rows, cols, type, quantize_width(type, vec), kAcross, 1, sms, quantize_ctas(type, vec));
 }
 
 // Workspace bytes of its partial sums; the caller does not know which matrices will be aligned.
@@ -805,9 +807,13 @@ size_t backward_workspace(int64_t rows, int64_t cols, int type, int sms) {
   return splits > 1 ? static_cast<size_t>(splits) * static_cast<size_t>(cols) * 4 : 0;
 }
 
-template <typename F>
+// Calls f with the pieces a warp takes, 1 or WIDE.
+template <int WIDE, typename F>
 tlg_status with_width(int u, F f) {
-  return u == 1 ? f(std::integral_constant<int, 1>()) : f(std::integral_constant<int, kWide>());
+  if constexpr (WIDE > 1) {
+    if (u != 1) return f(std::integral_constant<int, WIDE>());
+  }
+  return f(std::integral_constant<int, 1>());
 }
 
 }  // namespace
@@ -858,7 +864,7 @@ tlg_status tlg_mx_quantize(tlg_mx_format format, int64_t rows, int64_t cols, tlg
       const bool vec = vec_rows(X, rows, ldx, type);
       const RowGrid g = quantize_grid(rows, cols, type, vec, info.sm_count);
       return with_flag(vec, [&](auto V) {
-        return with_width(g.u, [&](auto U) {
+        return with_width<quantize_width(kT, decltype(V)::value)>(g.u, [&](auto U) {
           return launch(quantize_rows_kernel<kT, kF, false, decltype(V)::value, decltype(U)::value>, g.grid,
                         kRowThreads, s, RowMat{X, ldx}, o, RowMat{}, 0, rows, cols, g.rows_per, g.across);
         });
@@ -887,7 +893,7 @@ tlg_status tlg_mx_dequantize(tlg_mx_format format, int64_t rows, int64_t cols, c
   return with_type(type, [&](auto T) {
     return with_format(format, [&](auto F) {
       return with_flag(vec, [&](auto V) {
-        return with_width(g.u, [&](auto U) {
+        return with_width<kWide>(g.u, [&](auto U) {
           return launch(
               dequantize_rows_kernel<decltype(T)::value, decltype(F)::value, decltype(V)::value, decltype(U)::value>,
               g.grid, kRowThreads, static_cast<cudaStream_t>(stream), in, RowMat{X, ldx}, rows, cols, g.rows_per, g.across);
@@ -919,7 +925,7 @@ tlg_status tlg_act_forward_mx(int64_t rows, int64_t cols, tlg_activation activat
   const RowGrid g = quantize_grid(rows, cols, type, vec, info.sm_count);
   return with_type(type, [&](auto T) {
     return with_flag(vec, [&](auto V) {
-      return with_width(g.u, [&](auto U) {
+      return with_width<quantize_width(decltype(T)::value, decltype(V)::value)>(g.u, [&](auto U) {
         return launch(quantize_rows_kernel<decltype(T)::value, kE4M3, true, decltype(V)::value, decltype(U)::value>,
                       g.grid, kRowThreads, static_cast<cudaStream_t>(stream), RowMat{Z, ldz}, o, RowMat{Y, ldy},
                       static_cast<int>(activation), rows, cols, g.rows_per, g.across);
@@ -999,12 +1005,11 @@ tlg_status tlg_act_backward_mx(int64_t rows, int64_t cols, tlg_activation activa
     constexpr int kT = decltype(T)::value;
     return with_flag(dbias != nullptr, [&](auto SUM) {
       return with_flag(vec, [&](auto V) {
-        auto run = [&](auto U) {
+        return with_width<kWideBackward>(g.u, [&](auto U) {
           return launch(act_backward_kernel<kT, decltype(SUM)::value, decltype(V)::value, decltype(U)::value>, g.grid,
                         kRowThreads, s, RowMat{dY, lddy}, z, RowMat{dZ, lddz}, static_cast<int>(activation), rows,
                         cols, g.rows_per, g.across, part);
-        };
-        return g.u == 1 ? run(std::integral_constant<int, 1>()) : run(std::integral_constant<int, kWideBackward>());
+        });
       });
     });
   });

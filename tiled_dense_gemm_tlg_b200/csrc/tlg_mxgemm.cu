@@ -94,7 +94,7 @@ constexpr MxFns fns() {
   return {MxVariant<CG, BN, STAGES, OUT, EPI>::units, MxVariant<CG, BN, STAGES, OUT, EPI>::launch};
 }
 
-// The kernel for few rows of A; `ctas` a cluster of ks.
+// The kernel for few rows of A: `clusters` clusters of ks CTAs.
 template <int BN, int OUT>
 tlg_status launch_tokens(int dev, int clusters, int ks, const MxMaps &m, const MxGemmParams &p, cudaStream_t s) {
   using Plan = MxTokenPlan<BN>;

@@ -693,10 +693,6 @@ __device__ __forceinline__ void cluster_arrive() {
 
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
 // tmT: the tokens (A), tmW: the weights (B), tmST / tmSW their scales.  The grid is
 // ceil(N / 128) clusters of KS CTAs.
 template <int BN, int OUT>
