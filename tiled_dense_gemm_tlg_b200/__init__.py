@@ -5,7 +5,8 @@ Argument marshalling only: every step of the GEMM runs in the CUDA kernels of
 device memory and the current stream.  There is no CPU fallback: importing
 this package fails when the library has not been built, and a call with CPU
 tensors is rejected by the library (TLG_ERR_INVALID_ARG) rather than returning
-an empty result.
+an empty result.  The microscaled entry points also need ``_binding.so``, built
+against torch's headers; without it they raise ImportError.
 
 Functions (same names as the C entry points):
 
@@ -46,9 +47,18 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 try:
     from . import _binding  # marshals tensors for the MX entry points (csrc/tlg_binding.cpp)
-except ImportError as e:
-    raise ImportError("_binding.so is missing or does not load: build it with "
-                      "`python tiled_dense_gemm_tlg_b200/build.py`") from e
+except ImportError as _e:
+    class _NoBinding:
+        """Raises what is wrong with _binding.so at the first call that needs it; the others go without."""
+
+        def __init__(self, cause: ImportError):
+            self._cause = cause
+
+        def __getattr__(self, name):
+            raise ImportError("_binding.so is missing or does not load: build it with "
+                              "`python tiled_dense_gemm_tlg_b200/build.py`") from self._cause
+
+    _binding = _NoBinding(_e)
 
 TLG_OK, TLG_ERR_INVALID_ARG, TLG_ERR_ALIGNMENT, TLG_ERR_UNSUPPORTED, TLG_ERR_CUDA, TLG_ERR_TIMEOUT = range(6)
 TLG_OUT_F32, TLG_OUT_F16 = 0, 1

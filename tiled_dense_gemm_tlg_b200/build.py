@@ -55,11 +55,21 @@ def needs_build() -> bool:
     return any(os.path.getmtime(f) > t for f in inputs())
 
 
+def binding_built_for() -> str:
+    """What _binding.so depends on beside its sources; it carries this text as its docstring."""
+    from importlib import metadata
+
+    return f"Built for torch {metadata.version('torch')}, Python {sys.version.split()[0]} ({sys.implementation.cache_tag})."
+
+
 def binding_needs_build() -> bool:
     if not os.path.exists(BINDING):
         return True
     t = os.path.getmtime(BINDING)
-    return any(os.path.getmtime(f) > t for f in (BINDING_SRC, os.path.join(INCLUDE, "tlg.h"), os.path.abspath(__file__)))
+    if any(os.path.getmtime(f) > t for f in (BINDING_SRC, os.path.join(INCLUDE, "tlg.h"), os.path.abspath(__file__))):
+        return True
+    with open(BINDING, "rb") as f:
+        return binding_built_for().encode() not in f.read()
 
 
 def build_binding(force: bool = False) -> str:
@@ -76,11 +86,13 @@ def build_binding(force: bool = False) -> str:
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f'-DTLG_BUILT_FOR="{binding_built_for()}"',
            *(a for i in incs for a in ("-isystem", i)), "-o", tmp, BINDING_SRC, "-L", PKG, "-ltlg", "-L", torch_lib,
            "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError("g++ failed:\n" + (res.stdout + res.stderr)[-20000:])
+        raise RuntimeError("g++ failed on the binding of the microscaled entry points (libtlg.so is built):\n"
+                           + (res.stdout + res.stderr)[-20000:])
     os.replace(tmp, BINDING)
     return BINDING
 

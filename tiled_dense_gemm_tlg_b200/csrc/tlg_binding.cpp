@@ -325,7 +325,8 @@ PyObject *act_backward_mx(PyObject *, PyObject *const *a, Py_ssize_t n) {
 #define TLG_METHOD(NAME) {#NAME, reinterpret_cast<PyCFunction>(NAME), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {TLG_METHOD(mx_quantize),     TLG_METHOD(mx_dequantize),   TLG_METHOD(gemm_mxfp4),
                           TLG_METHOD(act_forward_mx), TLG_METHOD(act_backward_mx), {nullptr, nullptr, 0, nullptr}};
-PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods};
+// The docstring says which torch and Python this was compiled for; the build looks for it.
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", TLG_BUILT_FOR, -1, kMethods};
 
 }  // namespace
 
