@@ -247,3 +247,9 @@ def test_choose_config_refusals(tlg):
     assert lib.tlg_choose_config_mxfp4_fused(8, 8, 8, ctypes.byref(E(None, 9, None, 0)), 1, ctypes.byref(cfg)) == bad
     with pytest.raises(ValueError):
         tlg.tlg_choose_config_mxfp4_fused(8, 8, 8, activation="swish")
+
+
+@pytest.mark.parametrize("op", ["transpose", "", "TN", None, 1])
+def test_quantize_refuses_other_ops(tlg, op):
+    with pytest.raises(ValueError, match="op"):
+        tlg.tlg_mx_quantize(torch.zeros((4, 40), dtype=torch.float16), op=op)

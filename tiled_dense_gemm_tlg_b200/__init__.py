@@ -460,7 +460,9 @@ def tlg_mx_quantize(X: torch.Tensor, format: str = "e2m1", op: str = "N", Q: tor
                     S: torch.Tensor | None = None, stream=None):
     """(Q, S): X (fp32, fp16 or bf16) in blocks of 32 along its rows; ``op="T"`` quantises X's
     transpose, in blocks down its columns.  ``format``: "e2m1" (4 bits) or "e4m3" (8 bits)."""
-    return _result(_binding.mx_quantize(X, _format(format), op == "T" or op == "t", Q, S, _handle(stream)),
+    if op not in ("N", "n", "T", "t"):
+        raise ValueError("op must be N or T")
+    return _result(_binding.mx_quantize(X, _format(format), op in "Tt", Q, S, _handle(stream)),
                    "tlg_mx_quantize")
 
 
