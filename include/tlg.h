@@ -405,11 +405,12 @@ tlg_status tlg_gemm_workspace_size_op(int64_t M, int64_t N, int64_t K,
  * is written, TLG_OK (tlg_act_backward_mx still writes dbias = 0 for rows of
  * 0).  Other matrices need only element alignment; those whose base and row
  * stride are multiples of 16 bytes are accessed 16 bytes at a time.  Inputs
- * must not overlap outputs except where an entry point says so, and every
- * buffer is device memory of the current device.  These calls launch as
- * programmatic dependents of the kernel before them in the stream: only their
- * launch overlaps it; they touch memory after it has completed.  All may be
- * captured into CUDA graphs.
+ * must not overlap outputs except where an entry point says so, which is judged
+ * by the bytes from a buffer's first element to its last (so two column ranges
+ * of one matrix overlap), and every buffer is device memory of the current
+ * device.  These calls launch as programmatic dependents of the kernel before
+ * them in the stream: only their launch overlaps it; they touch memory after
+ * it has completed.  All may be captured into CUDA graphs.
  */
 
 /* Element types of ordinary matrices (f32 and f16 as in tlg_out). */

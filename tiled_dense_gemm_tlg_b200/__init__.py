@@ -21,8 +21,8 @@ Functions (same names as the C entry points):
 * ``tlg_gemm_mxfp4(A, SA, B, SB, ...)``    C = act(A.B^T + bias) + residual over 4-bit operands
 * ``tlg_act_forward_mx(Z, activation)``, ``tlg_act_backward_mx(dY, Q, S, activation)``
   an activation whose input is saved in 8 bits, and its backward pass
-* ``tlg_choose_config``, ``tlg_device_error``, ``tlg_selftest_timeout``,
-  ``tlg_status_string``, ``tlg_version``
+* ``tlg_choose_config``, ``tlg_choose_config_mxfp4``, ``tlg_choose_config_mxfp4_fused``,
+  ``tlg_device_error``, ``tlg_selftest_timeout``, ``tlg_status_string``, ``tlg_version``
 
 A and B are 2-D fp16 tensors with unit stride along their last dimension
 (row-major); their row strides become lda / ldb.  An MX matrix is a pair of uint8
@@ -75,7 +75,10 @@ _FORMATS = {"e2m1": TLG_MX_E2M1, "e4m3": TLG_MX_E4M3}
 EXPORTED = ("tlg_gemm_f16f32", "tlg_gemm_f16f16", "tlg_gemm_bias_relu_f16", "tlg_gemm_ex",
             "tlg_gemm_op", "tlg_gemm_fused", "tlg_gemm_ex_noalloc", "tlg_gemm_workspace_size",
             "tlg_gemm_workspace_size_op", "tlg_choose_config", "tlg_device_error",
-            "tlg_selftest_timeout", "tlg_status_string", "tlg_version")
+            "tlg_selftest_timeout", "tlg_status_string", "tlg_version",
+            "tlg_mx_size", "tlg_mx_quantize", "tlg_mx_dequantize", "tlg_gemm_mxfp4", "tlg_choose_config_mxfp4",
+            "tlg_choose_config_mxfp4_fused", "tlg_act_forward_mx", "tlg_act_backward_mx",
+            "tlg_act_backward_mx_workspace_size")
 
 
 class tlg_config(ctypes.Structure):

@@ -166,7 +166,8 @@ struct MxTile {
 // Tiles the library is built with: 128 * cta_group rows by block_n columns.  The costs are
 // fitted to 4096^3 (16 k-blocks a tile) and 16384 x 4096 x 1024 (4), fp16 C, back to back: plain
 // 37.5 / 27.4 / 27.4 us and 47 / 40 / 38 us with the 128, 192 and 256 wide tiles, with the full
-// epilogue 41 / 33 / 32 and 75 / 75 / 76.
+// epilogue 41 / 33 / 32 and 75 / 75 / 76.  They serve every type of C; with fp32, which stores twice the
+// bytes, they are not fitted.
 const MxTile kTiles[] = {
     TLG_MX_TILE(1, 64, 6, {0.273, {0.4, 0.8}, {1.3, 2.0}}),
     TLG_MX_TILE(1, 128, 5, {0.305, {0.5, 1.0}, {1.65, 2.7}}),
