@@ -52,3 +52,15 @@ def test_the_build_notices_another_torch(build, monkeypatch):
     from importlib import metadata
     monkeypatch.setattr(metadata, "version", lambda name: "1.0")
     assert build.binding_needs_build()
+
+
+def test_a_torch_that_is_no_installed_package(build, monkeypatch):
+    from importlib import metadata
+
+    import torch
+
+    def missing(name):
+        raise metadata.PackageNotFoundError(name)
+
+    monkeypatch.setattr(metadata, "version", missing)
+    assert f"torch {torch.__version__}," in build.binding_built_for()

@@ -59,7 +59,13 @@ def binding_built_for() -> str:
     """What _binding.so depends on beside its sources; it carries this text as its docstring."""
     from importlib import metadata
 
-    return f"Built for torch {metadata.version('torch')}, Python {sys.version.split()[0]} ({sys.implementation.cache_tag})."
+    try:
+        version = metadata.version("torch")
+    except metadata.PackageNotFoundError:  # a torch that was not installed as a package
+        import torch
+
+        version = torch.__version__
+    return f"Built for torch {version}, Python {sys.version.split()[0]} ({sys.implementation.cache_tag})."
 
 
 def binding_needs_build() -> bool:
