@@ -69,3 +69,27 @@ def test_forward(tlg, typ, rows, cols):
         Y, Q, S = tlg.tlg_act_forward_mx(z.cuda(), act)
         check_mx(Q, S, codes, scale, "e4m3")
         assert (np.abs(Y.double().cpu().numpy() - want) <= y_bound(act, typ, want, z.double().numpy())).all()
+
+
+@pytest.mark.parametrize("odd", [0, 1])
+def test_row_offsets_past_32_bits(tlg, odd):
+    """Every matrix in rows so far apart that the last ones lie past 2^31 elements and 2^32 bytes."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB of free device memory")
+    rows, cols = 5, 300
+    ld = (1 << 31) // 4 + 64 + odd
+    far = lambda dtype, ld, cols: torch.empty((rows * ld,), dtype=dtype, device="cuda").view(rows, ld)[:, :cols]
+    x, y = far(torch.float16, ld, cols), far(torch.float16, ld, cols)
+    q = far(torch.uint8, (1 << 30) + 64, 320)
+    z = torch.randn((rows, cols), device="cuda").half()
+    x.copy_(z)
+    Y, Q, S = tlg.tlg_act_forward_mx(z, "gelu")
+    S.zero_(), tlg.tlg_act_forward_mx(z, "gelu", Q=Q, S=S)
+    s = torch.zeros_like(S)
+    tlg.tlg_act_forward_mx(x, "gelu", Y=y, Q=q, S=s)
+    assert torch.equal(y, Y) and torch.equal(q, Q) and torch.equal(s, S)
+    tlg.tlg_mx_dequantize(q, s, cols, format="e4m3", out="f16", X=y)
+    assert torch.equal(y, tlg.tlg_mx_dequantize(Q, S, cols, format="e4m3", out="f16"))
+    want, db = tlg.tlg_act_backward_mx(z, Q, S, "gelu")
+    got, db2 = tlg.tlg_act_backward_mx(x, q, s, "gelu", dZ=y)
+    assert torch.equal(y, want) and torch.equal(db, db2)
