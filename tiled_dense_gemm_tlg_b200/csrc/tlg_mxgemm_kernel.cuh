@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 // through distributed shared memory, and writes them.  Measured back to back in a graph, one
 // token: 4096 x 4096 weights 3.6 us with KS = 4 (6.4 with KS = 1, 7.0 with 128-row tiles),
 // 16384 x 4096 6.7 us with KS = 1 (11 with 128-row tiles; its bytes take 5.5 us).  At 64 rows of
-// A the 128-row tiles win (6.6 against 8.7 us).
+// A and 16384 x 4096 weights, tiles enough for every SM, the 128-row tiles win (6.6 against 8.7 us).
 template <int BN>
 struct MxTokenPlan {
   static constexpr int kStages = 4;
