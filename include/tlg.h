@@ -15,8 +15,8 @@
  * bias and a ReLU before the fp16 store ("domestic-GPU TileLang adoption",
  * xdnf.cn/news/333523, section 4.2); tlg_gemm_fused generalises it to a bias,
  * an activation (ReLU or GELU) and a residual connection (same page, 4.1).
- * Beside it stand operators over 4-bit and 8-bit microscaled matrices (their
- * section below).
+ * Beside it stand operators over 4-bit and 8-bit microscaled matrices, and
+ * those of a feed-forward block around its products (their sections below).
  *
  * Conventions shared by every entry point below:
  *
@@ -519,6 +519,54 @@ tlg_status tlg_act_backward_mx(int64_t rows, int64_t cols, tlg_activation activa
 /* Workspace bytes of tlg_act_backward_mx with a dbias, for the current device. */
 tlg_status tlg_act_backward_mx_workspace_size(int64_t rows, int64_t cols, tlg_type type,
                                               size_t *bytes);
+
+/* ---------------------------------------------------------------- around the linear layers
+ *
+ * Operators of a feed-forward block beside its linear layers: products grouped by expert with their
+ * gradients, the root-mean-square norm with the residual's addition and its backward pass, and
+ * products of a few rows with integer 4-bit weights.  (These entry points have no counterpart on the
+ * pages; they exist for users who train and serve whole blocks with the products above.)  Pointers,
+ * ownership, streams, graphs and errors are as for the microscaled operators: matrices need element
+ * alignment only, those with a base and row stride that are multiples of 16 bytes are accessed faster,
+ * inputs must not overlap outputs except where an entry point says so, and calls launch as programmatic
+ * dependents of the kernel before them.
+ */
+
+/*
+ * Products grouped by expert.  The rows of A and C are sorted by group: those of group g are
+ * offsets[g] <= r < offsets[g + 1], and
+ *
+ *   C[r] = act(A[r] . op(B_g))     A: rows x K, C: rows x N
+ *
+ * with B_g the matrix at B + g * stride_b elements, K x N (TLG_OP_N, ldb >= N) or N x K (TLG_OP_T,
+ * ldb >= K), as tlg_gemm_op.  stride_b may be 0: every group has the same B.  type is the type of A and
+ * B (TLG_TYPE_F16 or TLG_TYPE_BF16), out that of C: the same, or TLG_TYPE_F32.  Sums are fp32, rounded
+ * once after the activation, whose accuracy is tlg_gemm_fused's.
+ *
+ * offsets: groups + 1 int32 values in device memory, read by the kernel (0 <= groups <= 1024).  They
+ * must not decrease; values outside [0, rows] are held to it, and a group that ends before it begins
+ * has no rows.  Rows of C before offsets[0] and from offsets[groups] on are left as they were.  K == 0
+ * gives C = act(0) in the groups' rows.  The input gradient is the same call: dA_g = dC_g . op(B_g)^T
+ * takes dC for A and the other op.  A pipeline wait past its time limit is reported by
+ * tlg_device_error().
+ */
+tlg_status tlg_gemm_grouped(int64_t rows, int64_t N, int64_t K, int32_t groups, const int32_t *offsets,
+                            tlg_type type, const void *A, int64_t lda,
+                            tlg_op op_b, const void *B, int64_t ldb, int64_t stride_b,
+                            tlg_activation activation,
+                            void *C, int64_t ldc, tlg_type out, void *stream);
+
+/*
+ * Its weight gradient: dB_g = A_g^T . dC_g (K x N) or, for TLG_OP_T, its transpose (N x K), in the
+ * layout of B: lddb and stride_db (not 0 for more than one group; the matrices must not overlap) in
+ * elements.  dC has A's type; out is that type or TLG_TYPE_F32.  A group without rows gets dB_g = 0, and
+ * every dB_g is overwritten.  Sums run over a group's rows in order, in fp32, rounded once; what other
+ * rows hold (NaN, infinities) does not matter.
+ */
+tlg_status tlg_gemm_grouped_dw(int64_t rows, int64_t N, int64_t K, int32_t groups, const int32_t *offsets,
+                               tlg_type type, const void *A, int64_t lda, const void *dC, int64_t lddc,
+                               tlg_op op_b, void *dB, int64_t lddb, int64_t stride_db,
+                               tlg_type out, void *stream);
 
 /*
  * Resolve a configuration for this shape.  On input *config (never NULL)

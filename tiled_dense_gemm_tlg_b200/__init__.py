@@ -78,7 +78,7 @@ EXPORTED = ("tlg_gemm_f16f32", "tlg_gemm_f16f16", "tlg_gemm_bias_relu_f16", "tlg
             "tlg_selftest_timeout", "tlg_status_string", "tlg_version",
             "tlg_mx_size", "tlg_mx_quantize", "tlg_mx_dequantize", "tlg_gemm_mxfp4", "tlg_choose_config_mxfp4",
             "tlg_choose_config_mxfp4_fused", "tlg_act_forward_mx", "tlg_act_backward_mx",
-            "tlg_act_backward_mx_workspace_size")
+            "tlg_act_backward_mx_workspace_size", "tlg_gemm_grouped", "tlg_gemm_grouped_dw")
 
 
 class tlg_config(ctypes.Structure):
@@ -130,7 +130,9 @@ _lib.tlg_gemm_mxfp4.argtypes = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, ct
 _lib.tlg_choose_config_mxfp4.argtypes = [_i64, _i64, _i64, _i32, ctypes.POINTER(tlg_config)]
 _lib.tlg_choose_config_mxfp4_fused.argtypes = [_i64, _i64, _i64, ctypes.POINTER(tlg_fused_epilogue), _i32,
                                                ctypes.POINTER(tlg_config)]
-for _name in ("tlg_gemm_mxfp4", "tlg_choose_config_mxfp4", "tlg_choose_config_mxfp4_fused", "tlg_mx_size", "tlg_mx_quantize", "tlg_mx_dequantize", "tlg_act_forward_mx", "tlg_act_backward_mx",
+_lib.tlg_gemm_grouped.argtypes = [_i64, _i64, _i64, _i32, _p, _i32, _p, _i64, _i32, _p, _i64, _i64, _i32, _p, _i64, _i32, _p]
+_lib.tlg_gemm_grouped_dw.argtypes = [_i64, _i64, _i64, _i32, _p, _i32, _p, _i64, _p, _i64, _i32, _p, _i64, _i64, _i32, _p]
+for _name in ("tlg_gemm_grouped", "tlg_gemm_grouped_dw", "tlg_gemm_mxfp4", "tlg_choose_config_mxfp4", "tlg_choose_config_mxfp4_fused", "tlg_mx_size", "tlg_mx_quantize", "tlg_mx_dequantize", "tlg_act_forward_mx", "tlg_act_backward_mx",
               "tlg_act_backward_mx_workspace_size", "tlg_gemm_f16f32", "tlg_gemm_f16f16", "tlg_gemm_bias_relu_f16", "tlg_gemm_ex",
               "tlg_gemm_op", "tlg_gemm_fused", "tlg_gemm_ex_noalloc", "tlg_gemm_workspace_size", "tlg_gemm_workspace_size_op", "tlg_choose_config", "tlg_device_error", "tlg_selftest_timeout"):
     getattr(_lib, _name).restype = _i32
@@ -530,6 +532,39 @@ def tlg_act_backward_mx(dY: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, acti
     device buffer of tlg_act_backward_mx_workspace_size bytes; allocated here when not given."""
     return _result(_binding.act_backward_mx(dY, Q, S, _activation(activation), dZ, dbias, bool(bias_grad), workspace,
                                             _handle(stream)), "tlg_act_backward_mx")
+
+
+# ------------------------------------------------------------------ around the linear layers
+
+
+def _op(op: str, name: str) -> bool:
+    if op not in ("N", "n", "T", "t"):
+        raise ValueError(f"{name} must be N or T")
+    return op in "Tt"
+
+
+def _out_or_same(out) -> int:
+    return -1 if out is None else _out_type(out)
+
+
+def tlg_gemm_grouped(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, op_b: str = "N",
+                     activation: str = "none", C: torch.Tensor | None = None, out: str | None = None, stream=None):
+    """C[r] = act(A[r].op(B[g])) for the rows offsets[g] <= r < offsets[g + 1] of group g.
+
+    A (fp16 or bf16) holds the groups' rows one after the other, B a matrix for each group (groups x K x N, or
+    groups x N x K with ``op_b="T"``), ``offsets`` groups + 1 int32 values on the device.  ``out``: A's type (None)
+    or "f32".  Rows outside the groups are not written (undefined in a C allocated here).  The input gradient is
+    ``tlg_gemm_grouped(dC, B, offsets, op_b=<the other>)``."""
+    return _result(_binding.gemm_grouped(A, B, offsets, _op(op_b, "op_b"), _activation(activation), C,
+                                         _out_or_same(out), _handle(stream)), "tlg_gemm_grouped")
+
+
+def tlg_gemm_grouped_dw(A: torch.Tensor, dC: torch.Tensor, offsets: torch.Tensor, op_b: str = "N",
+                        dB: torch.Tensor | None = None, out: str | None = None, stream=None):
+    """The weight gradient of ``tlg_gemm_grouped`` (without its activation): dB[g] = A_g^T.dC_g, groups x K x N, or
+    groups x N x K with ``op_b="T"``; 0 for a group without rows.  ``out``: A's type (None) or "f32"."""
+    return _result(_binding.gemm_grouped_dw(A, dC, offsets, _op(op_b, "op_b"), dB, _out_or_same(out),
+                                            _handle(stream)), "tlg_gemm_grouped_dw")
 
 
 def raw_library():

@@ -1,4 +1,4 @@
-// Native argument marshalling for the microscaled (MX) entry points: checks the tensors,
+// Native argument marshalling for the microscaled (MX) entry points and those around the linear layers: checks the tensors,
 // allocates outputs that were not given with torch's allocator, and calls libtlg.  Nothing is
 // computed here.  A small call is bound by its host side: from Python, with ctypes, the checks
 // and allocations cost 9 to 17 us a call, several times the kernels' time.
@@ -14,6 +14,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <cstdint>
 #include <exception>
 #include <optional>
 
@@ -322,9 +324,90 @@ PyObject *act_backward_mx(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// A stack of row-major matrices, `stride` elements apart.
+struct Stack {
+  Mat m;
+  int64_t stride;
+};
+
+Stack stack(const at::Tensor &t, const char *name) {
+  if (t.dim() != 3) raise(PyExc_ValueError, "%s must be a 3-D tensor", name);
+  const int64_t rows = t.size(1), cols = t.size(2), ld = t.stride(1);
+  if (cols > 1 && t.stride(2) != 1)
+    raise(PyExc_ValueError, "%s must be row-major (unit stride along its last dimension)", name);
+  if (rows > 1 && ld < cols) raise(PyExc_ValueError, "%s has overlapping rows", name);
+  return {{t.data_ptr(), ld > cols ? ld : cols}, t.size(0) > 1 ? t.stride(0) : 0};
+}
+
+// The groups' offsets and their number.
+int32_t groups_of(const at::Tensor &o) {
+  if (o.scalar_type() != at::kInt || o.dim() != 1 || o.size(0) < 1 || !o.is_contiguous())
+    raise(PyExc_ValueError, "offsets must be a contiguous int32 vector with an element more than there are groups%s", "");
+  return static_cast<int32_t>(std::min<int64_t>(o.size(0) - 1, INT32_MAX));
+}
+
+// (A, B, offsets, transposed, activation, C, type, stream); type -1: A's
+PyObject *gemm_grouped(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject * {
+    const at::Tensor &ta = tensor(a[0], "A"), &tb = tensor(a[1], "B"), &to = tensor(a[2], "offsets");
+    const Stream stream(a[7], ta);
+    const Mat ma = mat(ta, "A");
+    const Stack b = stack(tb, "B");
+    const tlg_type type = type_of(ta, "A");
+    const int32_t groups = groups_of(to);
+    const bool t = integer(a[3]) != 0;
+    const int64_t rows = ta.size(0), K = ta.size(1), N = tb.size(t ? 1 : 2), out = integer(a[6]);
+    if (tb.scalar_type() != ta.scalar_type()) raise(PyExc_TypeError, "A and B must have one type%s", "");
+    if (tb.size(0) != groups || tb.size(t ? 2 : 1) != K)
+      raise(PyExc_ValueError, "B must hold a matrix for each group, with A's columns as its inner dimension%s", "");
+    same_device(ta, &tb);
+    same_device(ta, &to);
+    const at::Tensor c = out_matrix(a[5], "C", rows, N, scalar_type(out < 0 ? type : out), ta);
+    const Mat mc = mat(c, "C");
+    const tlg_status st = tlg_gemm_grouped(
+        rows, N, K, groups, static_cast<const int32_t *>(to.data_ptr()), type, ma.p, ma.ld, t ? TLG_OP_T : TLG_OP_N,
+        b.m.p, b.m.ld, b.stride, static_cast<tlg_activation>(integer(a[4])), mc.p, mc.ld,
+        static_cast<tlg_type>(out < 0 ? type : out), stream);
+    return st != TLG_OK ? PyLong_FromLong(st) : wrap(c);
+  });
+}
+
+// (A, dC, offsets, transposed, dB, type, stream); type -1: A's
+PyObject *gemm_grouped_dw(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 7, [&]() -> PyObject * {
+    const at::Tensor &ta = tensor(a[0], "A"), &td = tensor(a[1], "dC"), &to = tensor(a[2], "offsets");
+    const Stream stream(a[6], ta);
+    const Mat ma = mat(ta, "A"), md = mat(td, "dC");
+    const tlg_type type = type_of(ta, "A");
+    const int32_t groups = groups_of(to);
+    const bool t = integer(a[3]) != 0;
+    const int64_t rows = ta.size(0), K = ta.size(1), N = td.size(1), out = integer(a[5]) < 0 ? type : integer(a[5]);
+    if (td.scalar_type() != ta.scalar_type()) raise(PyExc_TypeError, "A and dC must have one type%s", "");
+    if (td.size(0) != rows) raise(PyExc_ValueError, "A and dC must have the same rows%s", "");
+    same_device(ta, &td);
+    same_device(ta, &to);
+    at::Tensor db;
+    if (const at::Tensor *given = maybe(a[4], "dB")) {
+      same_device(ta, given);
+      if (given->scalar_type() != scalar_type(out) || given->dim() != 3 || given->size(0) != groups ||
+          given->size(1) != (t ? N : K) || given->size(2) != (t ? K : N))
+        raise(PyExc_ValueError, "dB must be of the output type and hold a matrix in B's layout for each group%s", "");
+      db = *given;
+    } else {
+      db = empty({groups, t ? N : K, t ? K : N}, scalar_type(out), ta.device());
+    }
+    const Stack b = stack(db, "dB");
+    const tlg_status st = tlg_gemm_grouped_dw(
+        rows, N, K, groups, static_cast<const int32_t *>(to.data_ptr()), type, ma.p, ma.ld, md.p, md.ld,
+        t ? TLG_OP_T : TLG_OP_N, b.m.p, b.m.ld, b.stride, static_cast<tlg_type>(out), stream);
+    return st != TLG_OK ? PyLong_FromLong(st) : wrap(db);
+  });
+}
+
 #define TLG_METHOD(NAME) {#NAME, reinterpret_cast<PyCFunction>(NAME), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {TLG_METHOD(mx_quantize),     TLG_METHOD(mx_dequantize),   TLG_METHOD(gemm_mxfp4),
-                          TLG_METHOD(act_forward_mx), TLG_METHOD(act_backward_mx), {nullptr, nullptr, 0, nullptr}};
+                          TLG_METHOD(act_forward_mx), TLG_METHOD(act_backward_mx),
+                          TLG_METHOD(gemm_grouped),    TLG_METHOD(gemm_grouped_dw), {nullptr, nullptr, 0, nullptr}};
 // The docstring says which torch and Python this was compiled for; the build looks for it.
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", TLG_BUILT_FOR, -1, kMethods};
 

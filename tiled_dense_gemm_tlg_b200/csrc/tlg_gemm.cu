@@ -91,6 +91,19 @@ bool encode_2d(CUtensorMap *tm, CUtensorMapDataType dtype, const void *base, uin
   return r == CUDA_SUCCESS;
 }
 
+bool encode_3d(CUtensorMap *tm, CUtensorMapDataType dtype, const void *base, uint64_t inner,
+               uint64_t mid, uint64_t outer, uint64_t row_bytes, uint64_t matrix_bytes,
+               uint32_t box_inner, uint32_t box_mid) {
+  const cuuint64_t dims[3] = {inner, mid, outer};
+  const cuuint64_t strides[2] = {row_bytes, matrix_bytes};
+  const cuuint32_t box[3] = {box_inner, box_mid, 1};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  const CUresult r = g_encode(tm, dtype, 3, const_cast<void *>(base), dims, strides, box, estride,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace tlg
 
 namespace {
@@ -1161,7 +1174,8 @@ tlg_status tlg_device_error(int clear, uint32_t *code_out) {
   // Every translation unit's kernels report into that unit's own word.
   tlg_status (*const readers[])(bool, uint32_t *) = {tlg::error_word_host, tlg::error_word_nn,
                                                      tlg::error_word_nt, tlg::error_word_tn,
-                                                     tlg::error_word_tt, tlg::error_word_mxgemm};
+                                                     tlg::error_word_tt, tlg::error_word_mxgemm,
+                                                     tlg::error_word_grouped};
   uint32_t v = 0;
   for (auto read : readers) {
     uint32_t w = 0;

@@ -1,0 +1,590 @@
+// Products grouped by expert for sm_100a: the rows of A belong to groups of ragged size, each with a
+// matrix B_g of its own, and the gradients of such products.
+//
+//   forward:  C[r] = act(A[r] . op(B_g)) for offsets[g] <= r < offsets[g + 1]
+//   gradient: dB_g = A_g^T . dC_g, the rows of the group being the summed index
+//
+// The roles of the two operands are swapped against the plain GEMM: the weights are the MMA's M (128
+// rows a CTA, TMEM lanes), the tokens its N (TMEM columns).  The tensor core takes any multiple of
+// 16 columns, chosen per tile by the instruction descriptor, so a group of 5 rows costs 16 columns of
+// an MMA and not a 128-row tile, and the same kernel serves one token and a training batch.  A
+// TMEM lane is a column of C, so that a warp's 32 lanes write consecutive elements and the ragged end of
+// a group is a bound on the columns of TMEM: rows behind a group's last are never written.
+// In the gradient the lanes are the contiguous index of dB, its other index the MMA's N.
+//
+// Sizes of the groups live on the device.  Every CTA turns them into a table of tiles in shared
+// memory (two warp scans), and the persistent work units (a CTA, or a CTA pair) walk the list of all
+// tiles with the stride of their number.
+//
+//   warp 0      TMA producer: a ring of slots of one k-block (64 elements) of both operands
+//   warp 1      MMA issuer (the pair's leader), owner of the TMEM allocation
+//   warp 2      gradient only: clears what a group's last k-block holds of the next group's rows (TMA
+//               fills with zeros only past the end of the whole matrix; a product with 0 would keep
+//               a NaN) in both operands before the MMAs read them
+//   warps 4-11  epilogue: two to a quarter of the lanes, taking its 32-column pieces in turn
+//   warps 12-15 plain-load builds only: loads for operands that TMA cannot describe
+#pragma once
+
+#include "tlg_mxgemm_kernel.cuh"
+
+namespace tlg {
+
+constexpr int kGroupedN = 0, kGroupedT = 1, kGroupedDw = 2;  // B stored K x N, N x K; the gradient of B
+constexpr int kGroupedMax = 1024;  // groups
+constexpr int kGroupedEpiWarp = 4, kGroupedEpiWarps = 8;
+constexpr int kGroupedLoader = kGroupedEpiWarp + kGroupedEpiWarps;
+constexpr int kGroupedThreads = 32 * kGroupedLoader;
+constexpr int kGroupedThreadsLsu = kGroupedThreads + 32 * kLoaderWarps;
+
+struct GroupedParams {
+  const int32_t *offsets;  // groups + 1
+  int groups;
+  int rows;      // of A (and dC)
+  int lanes;     // the contiguous extent of C or dB
+  int inner;     // forward: K; gradient: the other extent of dB
+  void *C;       // or dB
+  int64_t ldc;
+  int64_t stride_c;  // gradient: between groups
+  int raster;    // lane tiles walked together
+  int act;
+  int shared_w;  // every group has the same B
+  uint64_t limit_ns;
+  // plain loads: the M and N operands as stored
+  const uint16_t *W, *X;
+  int64_t ldw, ldx, stride_w;
+};
+
+template <int CG, int BN, int STAGES>
+struct GroupedPlan {
+  static constexpr uint32_t kWBytes = kBM * 128;
+  static constexpr uint32_t kXBytes = BN / CG * 128;
+  static constexpr uint32_t kXOffset = STAGES * kWBytes;
+  static constexpr uint32_t kBarOffset = kXOffset + STAGES * kXBytes;
+  // full, empty and tail of every slot; accumulator full and empty twice; drain
+  static constexpr uint32_t kNumBars = 3 * STAGES + 4 + 1;
+  static constexpr uint32_t kMiscOffset = kBarOffset + kNumBars * 8;
+  static constexpr uint32_t kStartOffset = kMiscOffset + 16;                      // first tile of each group
+  static constexpr uint32_t kBeginOffset = kStartOffset + (kGroupedMax + 1) * 4;  // first row
+  static constexpr uint32_t kSizeOffset = kBeginOffset + kGroupedMax * 4;         // rows
+  static constexpr uint32_t kSumOffset = kSizeOffset + kGroupedMax * 4;           // tiles of 32 groups
+  static constexpr uint32_t kDynamicBytes = kSumOffset + kGroupedMax / 32 * 4 + 1024;
+  static constexpr uint32_t kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
+  static_assert(kXBytes % 1024 == 0 && BN / CG % 32 == 0 && kTmemCols <= 512, "operand tiles and accumulators");
+  static_assert(kDynamicBytes <= 232448, "shared memory per CTA exceeded");
+};
+
+// What a tile computes: TMEM lanes [lane0, +128 CG) by `cols` columns.
+struct GroupedTile {
+  int g;
+  int lane0;
+  int col0;  // forward: row of A (and C) of column 0; gradient: row of dB_g
+  int cols;  // columns to write
+  int n;     // columns of the MMA
+  int k0;    // gradient: the group's first row
+  int k;     // elements summed
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Tiles of a group: lane tiles by column tiles.  Forward: the group's rows, in as many pieces of at
+// most BN as it takes, of even size (260 rows: 160 and 100, not 256 and 4).
+template <int KIND, int BN>
+__device__ __forceinline__ int grouped_col_tiles(const GroupedParams &p, int size) {
+  return ceil_div(KIND == kGroupedDw ? p.inner : size, BN);
+}
+
+// Tile t of the list; g0: a group not behind the tile's (the search starts there, 32 at a time).  All
+// lanes of the warp.
+template <int KIND, int CG, int BN>
+__device__ __forceinline__ GroupedTile grouped_tile(const GroupedParams &p, const int *start, const int *begin,
+                                                    const int *size, int t, int &g0, int lane) {
+  uint32_t past;
+  while (true) {
+    const int i = g0 + lane;
+    past = __ballot_sync(0xffffffffu, i >= p.groups || start[i + 1] > t);
+    if (past != 0) break;
+    g0 += 32;
+  }
+  GroupedTile r;
+  r.g = g0 += __ffs(past) - 1;
+  const int m = size[r.g];
+  const int col_tiles = grouped_col_tiles<KIND, BN>(p, m), lane_tiles = ceil_div(p.lanes, kBM * CG);
+  // Bands of `raster` lane tiles, each walked over all column tiles: the units at work share both
+  // operands in L2.
+  int l = t - start[r.g];
+  const int band = l / (p.raster * col_tiles);
+  l -= band * p.raster * col_tiles;
+  const int wide = min(p.raster, lane_tiles - band * p.raster);
+  const int ct = l / wide;
+  r.lane0 = (band * p.raster + l - ct * wide) * kBM * CG;
+  if constexpr (KIND == kGroupedDw) {
+    r.col0 = ct * BN;
+    r.cols = min(BN, p.inner - r.col0);
+    r.n = ceil_div(r.cols, 64 * CG) * 64 * CG;
+    r.k0 = begin[r.g];
+    r.k = m;
+  } else {
+    const int per = ceil_div(ceil_div(m, col_tiles), 16 * CG) * 16 * CG;
+    r.col0 = begin[r.g] + ct * per;
+    r.cols = min(per, m - ct * per);
+    r.n = ceil_div(r.cols, 16 * CG) * 16 * CG;
+    r.k0 = 0;
+    r.k = p.inner;
+  }
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *tm, uint32_t bar_cluster, int32_t x,
+                                                 int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Instruction descriptor as make_idesc_f16, for fp16 or bf16 operands (format 1) and without its N.
+template <int TYPE>
+__device__ __forceinline__ constexpr uint32_t grouped_idesc(int m, bool a_mn, bool b_mn) {
+  return make_idesc_f16(m, 0, a_mn, b_mn) | (TYPE == kTypeBF16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+// Fills one operand tile of a slot with plain loads: `count` (a multiple of 4) M or N indices by 64 k,
+// zeros past the limits.  K-major: a warp takes a row of 64 k at a time; MN-major: a k's row, 64 at a time.
+template <bool MN>
+__device__ __forceinline__ void grouped_fill(uint32_t dst, const uint16_t *base, int64_t ld, int count, int mn_left,
+                                             int k_left, int warp, int lane) {
+  constexpr int kBatch = 8;
+  const int items = MN ? ceil_div(count, 64) * 64 : count;  // rows of 64 elements, 2 to a lane
+  const int inner = lane * 2;
+  for (int i0 = warp; i0 < items; i0 += kLoaderWarps * kBatch) {
+    uint32_t w[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * kLoaderWarps;
+      const int k = MN ? i & 63 : inner, mn = MN ? (i >> 6) * 64 + inner : i;
+      const bool lo = i < items && mn < mn_left && k < k_left;
+      const bool hi = i < items && (MN ? mn + 1 < mn_left && k < k_left : mn < mn_left && k + 1 < k_left);
+      const uint16_t *q = base + (lo ? (MN ? k * ld + mn : mn * ld + k) : 0);
+      w[b] = ld_u16_pred(q, lo) | ld_u16_pred(q + (hi ? 1 : 0), hi) << 16;
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * kLoaderWarps;
+      const int k = MN ? i & 63 : inner, mn = MN ? (i >> 6) * 64 + inner : i;
+      if (i < items) st_shared_u32(dst + (MN ? mnmajor_offset(mn, k) : kmajor_offset(mn, k)), w[b]);
+    }
+  }
+}
+
+template <int KIND, int CG, int BN, int STAGES, int TYPE, int OUT, bool LSU>
+__global__ void __launch_bounds__(LSU ? kGroupedThreadsLsu : kGroupedThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const __grid_constant__ CUtensorMap tmX128, const GroupedParams p) {
+  using Plan = GroupedPlan<CG, BN, STAGES>;
+  constexpr bool kDw = KIND == kGroupedDw;
+  constexpr bool kWmn = KIND != kGroupedT, kXmn = kDw;  // MN-major operands
+  static_assert(!LSU || CG == 1, "the plain-load path is built for one-CTA tiles");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const uint32_t s0 = smem_u32(smem);
+  auto w_slot = [&](int s) { return s0 + s * Plan::kWBytes; };
+  auto x_slot = [&](int s) { return s0 + Plan::kXOffset + s * Plan::kXBytes; };
+  const uint32_t bar0 = s0 + Plan::kBarOffset;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tail_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (3 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (3 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 4);
+  uint32_t *misc = reinterpret_cast<uint32_t *>(smem + Plan::kMiscOffset);
+  volatile uint32_t *abort_flag = misc + 1;
+  int *start = reinterpret_cast<int *>(smem + Plan::kStartOffset);
+  int *begin = reinterpret_cast<int *>(smem + Plan::kBeginOffset);
+  int *size = reinterpret_cast<int *>(smem + Plan::kSizeOffset);
+  int *sums = reinterpret_cast<int *>(smem + Plan::kSumOffset);
+
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = (CG == 2) ? __shfl_sync(0xffffffffu, cluster_ctarank(), 0) : 0u;
+  const bool leader = rank == 0;
+  const int unit = CG == 2 ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int num_units = CG == 2 ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      // The gradient's tail is announced by each CTA's tail warp, so its other slots take as many arrivals.
+      mbar_init(full_bar(s), LSU ? kLoaderWarps : kDw ? CG : 1);
+      mbar_init(empty_bar(s), 1);
+      mbar_init(tail_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), kGroupedEpiWarps * CG);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+    if constexpr (!LSU) {
+      tma_prefetch_desc(&tmW);
+      tma_prefetch_desc(&tmX);
+      if (!kDw) tma_prefetch_desc(&tmX128);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc<CG>(smem_u32(misc), Plan::kTmemCols);
+    tmem_relinquish<CG>();
+  }
+  grid_dependency_wait();  // global memory is touched only after this
+  grid_launch_dependents();
+
+  // The table of tiles.  Offsets are held to [0, rows], and a group that ends before it begins has no
+  // rows, so that no offsets lead outside the matrices.
+  const int lane_tiles = ceil_div(p.lanes, kBM * CG);
+  const int blocks = ceil_div(p.groups, 32), num_warps = static_cast<int>(blockDim.x >> 5);
+  for (int b = warp; b < blocks; b += num_warps) {
+    const int g = b * 32 + lane;
+    int tiles = 0;
+    if (g < p.groups) {
+      const int lo = min(max(p.offsets[g], 0), p.rows), hi = min(max(p.offsets[g + 1], 0), p.rows);
+      begin[g] = lo;
+      size[g] = max(hi - lo, 0);
+      tiles = grouped_col_tiles<KIND, BN>(p, max(hi - lo, 0)) * lane_tiles;
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, tiles, d);
+      if (lane >= d) tiles += v;
+    }
+    if (g < p.groups) start[g + 1] = tiles;  // of this block of 32
+    if (lane == 31) sums[b] = tiles;
+  }
+  __syncthreads();
+  {
+    int before = lane < blocks ? sums[lane] : 0;
+    const int own = before;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, before, d);
+      if (lane >= d) before += v;
+    }
+    before -= own;  // tiles of the blocks before block `lane`
+    for (int b = warp; b < blocks; b += num_warps) {
+      const int add = __shfl_sync(0xffffffffu, before, b);
+      if (b * 32 + lane < p.groups) start[b * 32 + lane + 1] += add;
+    }
+    if (threadIdx.x == 0) start[0] = 0;
+  }
+  tc_fence_before_sync();
+  __syncwarp();
+  if constexpr (CG == 2)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(misc);
+  const int tiles = start[p.groups];
+  int g0 = 0;
+  auto tile_at = [&](int t) { return grouped_tile<KIND, CG, BN>(p, start, begin, size, t, g0, lane); };
+
+  if (!LSU && warp == 0) {
+    // ---------------------------------------------------------------- producer (every CTA)
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t issued_mask = 0, issued_parity = 0;
+    uint32_t tail_mask = 0, tail_parity = 0;  // tails issued, and the parity of each slot's next one
+    bool ok = true;
+    for (int t = unit; t < tiles && ok; t += num_units) {
+      const GroupedTile w = tile_at(t);
+      const int num_kb = ceil_div(w.k, kBK);
+      const int lane0 = w.lane0 + static_cast<int>(rank) * kBM;
+      const int nh = w.n / CG;  // columns of the MMA held by this CTA
+      const int x0 = w.col0 + static_cast<int>(rank) * nh;
+      const int boxes = ceil_div(nh, kDw ? 64 : 32);
+      const uint32_t bytes = Plan::kWBytes + static_cast<uint32_t>(boxes) * (kDw ? 8192u : 4096u);
+      for (int kb = 0; kb < num_kb; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait_spin(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns,
+                                                    kRoleProducer, &g_device_error, 4096));
+        if (!ok) break;
+        const bool tail = kDw && (kb + 1) * kBK > w.k;
+        if (elect_one()) {
+          uint32_t bar;
+          if (tail) {  // each CTA's tail warp hands its part over
+            bar = tail_bar(stage);
+            mbar_arrive_expect_tx(bar, bytes);
+          } else if constexpr (CG == 1) {
+            bar = full_bar(stage);
+            mbar_arrive_expect_tx(bar, bytes);
+          } else {
+            if (leader) {
+              mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
+              if (kDw) mbar_arrive(full_bar(stage));
+            }
+            bar = mapa_shared(full_bar(stage), 0);
+          }
+          auto load = [&](uint32_t dst, const CUtensorMap *tm, int32_t x, int32_t y) {
+            if (CG == 1 || tail)
+              tma_load_2d(dst, tm, bar, x, y);
+            else
+              tma_load_2d_pair(dst, tm, bar, x, y);
+          };
+          const int k = kb * kBK;
+          if constexpr (kDw) {
+            load(w_slot(stage), &tmW, lane0, w.k0 + k);
+            load(w_slot(stage) + 8192, &tmW, lane0 + 64, w.k0 + k);
+            for (int c = 0; c < boxes; ++c) load(x_slot(stage) + c * 8192, &tmX, x0 + c * 64, w.k0 + k);
+          } else {
+            auto load3 = [&](uint32_t dst, int32_t x, int32_t y) {
+              const int32_t z = p.shared_w ? 0 : w.g;
+              if constexpr (CG == 1)
+                tma_load_3d(dst, &tmW, bar, x, y, z);
+              else
+                tma_load_3d_pair(dst, &tmW, bar, x, y, z);
+            };
+            if constexpr (KIND == kGroupedT) {
+              load3(w_slot(stage), k, lane0);
+            } else {
+              load3(w_slot(stage), lane0, k);
+              load3(w_slot(stage) + 8192, lane0 + 64, k);
+            }
+            if (nh % 128 == 0) {
+              for (int c = 0; c < nh / 128; ++c) load(x_slot(stage) + c * 16384, &tmX128, k, x0 + c * 128);
+            } else {
+              for (int c = 0; c < boxes; ++c) load(x_slot(stage) + c * 4096, &tmX, k, x0 + c * 32);
+            }
+          }
+        }
+        __syncwarp();
+        if (tail) {
+          issued_mask &= ~(1u << stage);
+          tail_mask |= 1u << stage;
+          tail_parity ^= 1u << stage;
+        } else {
+          issued_mask |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    for (int i = 0; i < STAGES && ok; ++i) {  // no commit-arrive is still on its way
+      ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns, kRoleProducer,
+                                             &g_device_error));
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!ok) {
+      // Let the copies already issued land before shared memory goes away.
+      for (int s = 0; s < STAGES; ++s) {
+        if (leader && (issued_mask & (1u << s)) != 0)
+          mbar_wait(full_bar(s), (issued_parity >> s) & 1u, nullptr, p.limit_ns, kRoleProducer, &g_device_error);
+        if ((tail_mask & (1u << s)) != 0)
+          mbar_wait(tail_bar(s), ((tail_parity >> s) & 1u) ^ 1u, nullptr, p.limit_ns, kRoleProducer, &g_device_error);
+      }
+    }
+  } else if (LSU && warp >= kGroupedLoader) {
+    // ---------------------------------------------------------------- plain loads
+    const int lw = warp - kGroupedLoader;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = unit; t < tiles && ok; t += num_units) {
+      const GroupedTile w = tile_at(t);
+      const int num_kb = ceil_div(w.k, kBK);
+      const uint16_t *wp, *xp;
+      if constexpr (kDw) {
+        wp = p.W + static_cast<int64_t>(w.k0) * p.ldw + w.lane0;
+        xp = p.X + static_cast<int64_t>(w.k0) * p.ldx + w.col0;
+      } else {
+        wp = p.W + w.g * p.stride_w + (KIND == kGroupedT ? static_cast<int64_t>(w.lane0) * p.ldw : w.lane0);
+        xp = p.X + static_cast<int64_t>(w.col0) * p.ldx;
+      }
+      for (int kb = 0; kb < num_kb; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait_spin(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns,
+                                                    kRoleProducer, &g_device_error, 4096));
+        if (!ok) break;
+        const int64_t k = static_cast<int64_t>(kb) * kBK;
+        const int k_left = w.k - kb * kBK;
+        grouped_fill<kWmn>(w_slot(stage), wp + (kWmn ? k * p.ldw : k), p.ldw, kBM, p.lanes - w.lane0, k_left, lw, lane);
+        grouped_fill<kXmn>(x_slot(stage), xp + (kXmn ? k * p.ldx : k), p.ldx, w.n, w.cols, k_left, lw, lane);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full_bar(stage));
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    for (int i = 0; i < STAGES && ok; ++i) {
+      ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns, kRoleProducer,
+                                             &g_device_error));
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  } else if (warp == 1 && leader) {
+    // ---------------------------------------------------------------- MMA issuer (leader CTA)
+    constexpr uint32_t idesc0 = grouped_idesc<TYPE>(kBM * CG, kWmn, kXmn);
+    constexpr uint32_t kWStep = kWmn ? 16 * 128 / 16 : 32 / 16;  // 16 k, in 16-byte units
+    constexpr uint32_t kXStep = kXmn ? 16 * 128 / 16 : 32 / 16;
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t j = 0;  // tiles done
+    bool ok = true;
+    for (int t = unit; t < tiles && ok; t += num_units, ++j) {
+      const GroupedTile w = tile_at(t);
+      const int num_kb = ceil_div(w.k, kBK);
+      const uint32_t idesc = idesc0 | (static_cast<uint32_t>(w.n >> 3) << 17);
+      ok = __all_sync(0xffffffffu, mbar_wait(tempty_bar(j & 1u), ((j >> 1) & 1u) ^ 1u, abort_flag, p.limit_ns,
+                                             kRoleMma, &g_device_error));
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint32_t d_tmem = tmem_base + (j & 1u) * BN;
+      for (int kb = 0; kb < num_kb; ++kb) {
+        const bool tail = kDw && (kb + 1) * kBK > w.k;
+        // the tail's last writes come from the pair's other CTA, so they are acquired at cluster scope
+        const bool got = CG == 2 && tail
+                             ? mbar_wait_cluster(full_bar(stage), phase, abort_flag, p.limit_ns, kRoleMma, &g_device_error)
+                             : mbar_wait_spin(full_bar(stage), phase, abort_flag, p.limit_ns, kRoleMma, &g_device_error, 4096);
+        ok = __all_sync(0xffffffffu, got);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (elect_one()) {
+          const uint64_t wd = smem_desc_sw128(w_slot(stage), kWmn ? 8192 : 16, 1024);
+          const uint64_t xd = smem_desc_sw128(x_slot(stage), kXmn ? 8192 : 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            mma_f16_ss<CG>(d_tmem, wd + kk * kWStep, xd + kk * kXStep, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          mma_commit<CG>(empty_bar(stage));
+        }
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) mma_commit<CG>(tfull_bar(j & 1u));
+      __syncwarp();
+    }
+    if (!ok) {
+      if (elect_one()) mma_commit_local<CG>(drain_bar);
+      __syncwarp();
+      mbar_wait(drain_bar, 0, nullptr, p.limit_ns, kRoleMma, &g_device_error);
+    }
+  } else if (!LSU && kDw && warp == 2) {
+    // ---------------------------------------------------------------- the groups' last k-blocks (every CTA)
+    int stage = 0;
+    uint32_t parity = 0;  // of each slot's next tail
+    bool ok = true;
+    for (int t = unit; t < tiles; t += num_units) {
+      const GroupedTile w = tile_at(t);
+      const int num_kb = ceil_div(w.k, kBK), valid = w.k % kBK;
+      const int last = (stage + num_kb + STAGES - 1) % STAGES;
+      stage = (stage + num_kb) % STAGES;
+      if (valid == 0) continue;
+      const uint64_t limit = p.limit_ns + static_cast<uint64_t>(num_kb) * kWaitPerKBlockNs;
+      ok = __all_sync(0xffffffffu, mbar_wait(tail_bar(last), (parity >> last) & 1u, abort_flag, limit,
+                                                   kRoleProducer, &g_device_error));
+      if (!ok) break;
+      parity ^= 1u << last;
+      // rows [valid, 64) of each 64-element block are consecutive bytes
+      const int x_blocks = w.n / CG / 64;
+      for (int b = 0; b < 2 + x_blocks; ++b) {
+        const uint32_t at = b < 2 ? w_slot(last) + b * 8192 : x_slot(last) + (b - 2) * 8192;
+        for (int i = valid * 128 + lane * 16; i < 8192; i += 512)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + i), "r"(0u) : "memory");
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2)
+          mbar_arrive_cluster(mapa_shared(full_bar(last), 0));
+        else
+          mbar_arrive(full_bar(last));
+      }
+    }
+  } else if (warp >= kGroupedEpiWarp && warp < kGroupedLoader) {
+    // ---------------------------------------------------------------- epilogue (every CTA)
+    const int quarter = warp & 3;
+    const int side = (warp - kGroupedEpiWarp) >> 2;
+    const uint32_t release_bar0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
+    uint32_t j = 0;
+    for (int t = unit; t < tiles; t += num_units, ++j) {
+      const GroupedTile w = tile_at(t);
+      const uint64_t limit = p.limit_ns + static_cast<uint64_t>(ceil_div(w.k, kBK)) * kWaitPerKBlockNs;
+      bool ok = *abort_flag == 0u;
+      if (ok && !mbar_wait(tfull_bar(j & 1u), (j >> 1) & 1u, abort_flag, limit, kRoleEpilogue, &g_device_error))
+        ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) continue;
+      tc_fence_after_sync();
+      auto release = [&]() {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2)
+            mbar_arrive_drained(release_bar0 + 8u * (j & 1u));
+          else
+            mbar_arrive(release_bar0 + 8u * (j & 1u));
+        }
+      };
+      const int at = w.lane0 + static_cast<int>(rank) * kBM + quarter * 32 + lane;  // column of C or dB
+      const int pieces = ceil_div(w.cols, 32);
+      if (side >= pieces) release();
+#pragma unroll 1
+      for (int i = side; i < pieces; i += 2) {
+        float v[32];
+        {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_load_32cols(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (j & 1u) * BN +
+                               static_cast<uint32_t>(i * 32),
+                           r);
+          if (i + 2 >= pieces) release();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = w.k > 0 ? __uint_as_float(r[c]) : 0.0f;  // the empty sum
+        }
+        if constexpr (!kDw) activate_lane<OUT, 32>(p.act, v);
+        if (at < p.lanes) {
+          const int left = w.cols - i * 32;
+          int64_t to = static_cast<int64_t>(w.col0 + i * 32) * p.ldc + at;
+          if constexpr (kDw) to += w.g * p.stride_c;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c < left) store_elem<OUT>(p.C, to + c * p.ldc, v[c]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncwarp();
+  if constexpr (CG == 2)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc<CG>(tmem_base, Plan::kTmemCols);
+  }
+}
+
+}  // namespace tlg

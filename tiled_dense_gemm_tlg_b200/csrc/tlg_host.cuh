@@ -44,4 +44,9 @@ bool encode_2d(CUtensorMap *tm, CUtensorMapDataType dtype, const void *base, uin
                uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
+// The same for `outer` such matrices, matrix_bytes apart; a box lies in one of them.
+bool encode_3d(CUtensorMap *tm, CUtensorMapDataType dtype, const void *base, uint64_t inner,
+               uint64_t mid, uint64_t outer, uint64_t row_bytes, uint64_t matrix_bytes,
+               uint32_t box_inner, uint32_t box_mid);
+
 }  // namespace tlg
