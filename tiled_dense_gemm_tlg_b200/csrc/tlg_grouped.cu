@@ -31,7 +31,7 @@ struct GroupedVariant {
   static void fill(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int ctas, cudaStream_t s) {
     *cfg = {};
     cfg->gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg->blockDim = dim3(LSU ? kGroupedThreadsLsu : kGroupedThreads);
+    cfg->blockDim = dim3(GroupedRoles<OUT, LSU>::kThreads);
     cfg->dynamicSmemBytes = Plan::kDynamicBytes;
     cfg->stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

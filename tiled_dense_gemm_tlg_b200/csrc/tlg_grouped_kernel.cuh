@@ -21,8 +21,13 @@
 //   warp 2      gradient only: clears what a group's last k-block holds of the next group's rows (TMA
 //               fills with zeros only past the end of the whole matrix; a product with 0 would keep
 //               a NaN) in both operands before the MMAs read them
-//   warps 4-11  epilogue: two to a quarter of the lanes, taking its 32-column pieces in turn
-//   warps 12-15 plain-load builds only: loads for operands that TMA cannot describe
+//   warps 4-    epilogue: two (fp32: four) to a quarter of the lanes, taking its 32-column pieces in turn
+//   the last 4  plain-load builds only: loads for operands that TMA cannot describe
+//
+// The tensor core's adder truncates: over a long sum the accumulator falls short by about 2e-8 of its
+// size per MMA (1.2e-6 at K = 1000, 2e-5 at 16384), more than an fp32 result should lose.  Builds
+// with an fp32 output therefore sum at most kGroupedSpan k-blocks in TMEM, and the epilogue warps add
+// those partial sums, rounding to nearest, in registers.  For a 16-bit output it is far below the rounding.
 #pragma once
 
 #include "tlg_mxgemm_kernel.cuh"
@@ -31,10 +36,16 @@ namespace tlg {
 
 constexpr int kGroupedN = 0, kGroupedT = 1, kGroupedDw = 2;  // B stored K x N, N x K; the gradient of B
 constexpr int kGroupedMax = 1024;  // groups
-constexpr int kGroupedEpiWarp = 4, kGroupedEpiWarps = 8;
-constexpr int kGroupedLoader = kGroupedEpiWarp + kGroupedEpiWarps;
-constexpr int kGroupedThreads = 32 * kGroupedLoader;
-constexpr int kGroupedThreadsLsu = kGroupedThreads + 32 * kLoaderWarps;
+constexpr int kGroupedEpiWarp = 4;
+constexpr int kGroupedSpan = 8;    // k-blocks summed in TMEM for an fp32 output
+
+// Warps by the type of the output: fp32 sums of 64 columns to a thread leave no room for 128.
+template <int OUT, bool LSU>
+struct GroupedRoles {
+  static constexpr int kEpiWarps = OUT == kTypeF32 ? 16 : 8;
+  static constexpr int kLoader = kGroupedEpiWarp + kEpiWarps;
+  static constexpr int kThreads = 32 * (kLoader + (LSU ? kLoaderWarps : 0));
+};
 
 struct GroupedParams {
   const int32_t *offsets;  // groups + 1
@@ -187,10 +198,12 @@ __device__ __forceinline__ void grouped_fill(uint32_t dst, const uint16_t *base,
 }
 
 template <int KIND, int CG, int BN, int STAGES, int TYPE, int OUT, bool LSU>
-__global__ void __launch_bounds__(LSU ? kGroupedThreadsLsu : kGroupedThreads, 1)
+__global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const __grid_constant__ CUtensorMap tmX128, const GroupedParams p) {
   using Plan = GroupedPlan<CG, BN, STAGES>;
+  using Roles = GroupedRoles<OUT, LSU>;
+  constexpr bool kSpans = OUT == kTypeF32;
   constexpr bool kDw = KIND == kGroupedDw;
   constexpr bool kWmn = KIND != kGroupedT, kXmn = kDw;  // MN-major operands
   static_assert(!LSU || CG == 1, "the plain-load path is built for one-CTA tiles");
@@ -230,7 +243,7 @@ __global__ void __launch_bounds__(LSU ? kGroupedThreadsLsu : kGroupedThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), kGroupedEpiWarps * CG);
+      mbar_init(tempty_bar(a), Roles::kEpiWarps * CG);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0u;
@@ -396,9 +409,9 @@ __global__ void __launch_bounds__(LSU ? kGroupedThreadsLsu : kGroupedThreads, 1)
           mbar_wait(tail_bar(s), ((tail_parity >> s) & 1u) ^ 1u, nullptr, p.limit_ns, kRoleProducer, &g_device_error);
       }
     }
-  } else if (LSU && warp >= kGroupedLoader) {
+  } else if (LSU && warp >= Roles::kLoader) {
     // ---------------------------------------------------------------- plain loads
-    const int lw = warp - kGroupedLoader;
+    const int lw = warp - Roles::kLoader;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -445,18 +458,33 @@ __global__ void __launch_bounds__(LSU ? kGroupedThreadsLsu : kGroupedThreads, 1)
     constexpr uint32_t kXStep = kXmn ? 16 * 128 / 16 : 32 / 16;
     int stage = 0;
     uint32_t phase = 0;
-    uint32_t j = 0;  // tiles done
+    uint32_t j = 0;  // accumulators handed over
     bool ok = true;
-    for (int t = unit; t < tiles && ok; t += num_units, ++j) {
+    for (int t = unit; t < tiles && ok; t += num_units) {
       const GroupedTile w = tile_at(t);
       const int num_kb = ceil_div(w.k, kBK);
       const uint32_t idesc = idesc0 | (static_cast<uint32_t>(w.n >> 3) << 17);
-      ok = __all_sync(0xffffffffu, mbar_wait(tempty_bar(j & 1u), ((j >> 1) & 1u) ^ 1u, abort_flag, p.limit_ns,
-                                             kRoleMma, &g_device_error));
+      int first = 0;  // k-block of this accumulator
+      auto take = [&]() {
+        ok = __all_sync(0xffffffffu, mbar_wait(tempty_bar(j & 1u), ((j >> 1) & 1u) ^ 1u, abort_flag, p.limit_ns,
+                                               kRoleMma, &g_device_error));
+        tc_fence_after_sync();
+      };
+      auto hand_over = [&]() {
+        if (elect_one()) mma_commit<CG>(tfull_bar(j & 1u));
+        __syncwarp();
+        ++j;
+      };
+      take();
       if (!ok) break;
-      tc_fence_after_sync();
-      const uint32_t d_tmem = tmem_base + (j & 1u) * BN;
       for (int kb = 0; kb < num_kb; ++kb) {
+        if (kSpans && kb - first == kGroupedSpan) {
+          hand_over();
+          first = kb;
+          take();
+          if (!ok) break;
+        }
+        const uint32_t d_tmem = tmem_base + (j & 1u) * BN;
         const bool tail = kDw && (kb + 1) * kBK > w.k;
         // the tail's last writes come from the pair's other CTA, so they are acquired at cluster scope
         const bool got = CG == 2 && tail
@@ -470,7 +498,7 @@ __global__ void __launch_bounds__(LSU ? kGroupedThreadsLsu : kGroupedThreads, 1)
           const uint64_t xd = smem_desc_sw128(x_slot(stage), kXmn ? 8192 : 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
-            mma_f16_ss<CG>(d_tmem, wd + kk * kWStep, xd + kk * kXStep, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+            mma_f16_ss<CG>(d_tmem, wd + kk * kWStep, xd + kk * kXStep, idesc, (kb > first || kk > 0) ? 1u : 0u);
           mma_commit<CG>(empty_bar(stage));
         }
         __syncwarp();
@@ -480,8 +508,7 @@ __global__ void __launch_bounds__(LSU ? kGroupedThreadsLsu : kGroupedThreads, 1)
         }
       }
       if (!ok) break;
-      if (elect_one()) mma_commit<CG>(tfull_bar(j & 1u));
-      __syncwarp();
+      hand_over();
     }
     if (!ok) {
       if (elect_one()) mma_commit_local<CG>(drain_bar);
@@ -520,47 +547,45 @@ __global__ void __launch_bounds__(LSU ? kGroupedThreadsLsu : kGroupedThreads, 1)
           mbar_arrive(full_bar(last));
       }
     }
-  } else if (warp >= kGroupedEpiWarp && warp < kGroupedLoader) {
+  } else if (warp >= kGroupedEpiWarp && warp < Roles::kLoader) {
     // ---------------------------------------------------------------- epilogue (every CTA)
     const int quarter = warp & 3;
     const int side = (warp - kGroupedEpiWarp) >> 2;
+    constexpr int kSides = Roles::kEpiWarps / 4;
+    constexpr int kMine = (BN / 32 + kSides - 1) / kSides;  // pieces of a warp
     const uint32_t release_bar0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
     uint32_t j = 0;
-    for (int t = unit; t < tiles; t += num_units, ++j) {
-      const GroupedTile w = tile_at(t);
-      const uint64_t limit = p.limit_ns + static_cast<uint64_t>(ceil_div(w.k, kBK)) * kWaitPerKBlockNs;
-      bool ok = *abort_flag == 0u;
+    bool ok = true;
+    auto wait_full = [&](uint64_t limit) {
+      ok = ok && *abort_flag == 0u;
       if (ok && !mbar_wait(tfull_bar(j & 1u), (j >> 1) & 1u, abort_flag, limit, kRoleEpilogue, &g_device_error))
         ok = false;
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) continue;
       tc_fence_after_sync();
-      auto release = [&]() {
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 2)
-            mbar_arrive_drained(release_bar0 + 8u * (j & 1u));
-          else
-            mbar_arrive(release_bar0 + 8u * (j & 1u));
-        }
-      };
+    };
+    auto release = [&]() {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2)
+          mbar_arrive_drained(release_bar0 + 8u * (j & 1u));
+        else
+          mbar_arrive(release_bar0 + 8u * (j & 1u));
+      }
+    };
+    auto load_piece = [&](int i, uint32_t(&r)[32]) {
+      __syncwarp();
+      tmem_load_32cols(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (j & 1u) * BN +
+                           static_cast<uint32_t>(i * 32),
+                       r);
+    };
+    for (int t = unit; t < tiles && ok; t += num_units) {
+      const GroupedTile w = tile_at(t);
+      const int num_kb = ceil_div(w.k, kBK);
+      const uint64_t limit = p.limit_ns + static_cast<uint64_t>(num_kb) * kWaitPerKBlockNs;
       const int at = w.lane0 + static_cast<int>(rank) * kBM + quarter * 32 + lane;  // column of C or dB
       const int pieces = ceil_div(w.cols, 32);
-      if (side >= pieces) release();
-#pragma unroll 1
-      for (int i = side; i < pieces; i += 2) {
-        float v[32];
-        {
-          uint32_t r[32];
-          __syncwarp();
-          tmem_load_32cols(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (j & 1u) * BN +
-                               static_cast<uint32_t>(i * 32),
-                           r);
-          if (i + 2 >= pieces) release();
-#pragma unroll
-          for (int c = 0; c < 32; ++c) v[c] = w.k > 0 ? __uint_as_float(r[c]) : 0.0f;  // the empty sum
-        }
+      auto store_piece = [&](int i, float(&v)[32]) {
         if constexpr (!kDw) activate_lane<OUT, 32>(p.act, v);
         if (at < p.lanes) {
           const int left = w.cols - i * 32;
@@ -570,6 +595,51 @@ __global__ void __launch_bounds__(LSU ? kGroupedThreadsLsu : kGroupedThreads, 1)
           for (int c = 0; c < 32; ++c)
             if (c < left) store_elem<OUT>(p.C, to + c * p.ldc, v[c]);
         }
+      };
+      if constexpr (kSpans) {
+        float sum[kMine][32];
+#pragma unroll
+        for (int m = 0; m < kMine; ++m)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) sum[m][c] = 0.0f;  // the empty sum
+        int kb = 0;
+        do {
+          wait_full(limit);
+          if (!ok) break;
+#pragma unroll
+          for (int m = 0; m < kMine; ++m) {
+            const int i = side + m * kSides;
+            if (i < pieces && num_kb > 0) {
+              uint32_t r[32];
+              load_piece(i, r);
+#pragma unroll
+              for (int c = 0; c < 32; c += 2)
+                f2_add_to(sum[m][c], sum[m][c + 1], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+            }
+          }
+          release();
+          ++j;
+          kb += kGroupedSpan;
+        } while (kb < num_kb);
+        if (!ok) break;
+#pragma unroll
+        for (int m = 0; m < kMine; ++m)
+          if (side + m * kSides < pieces) store_piece(side + m * kSides, sum[m]);
+      } else {
+        wait_full(limit);
+        if (!ok) break;
+        if (side >= pieces) release();
+#pragma unroll 1
+        for (int i = side; i < pieces; i += kSides) {
+          uint32_t r[32];
+          load_piece(i, r);
+          if (i + kSides >= pieces) release();
+          float v[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = w.k > 0 ? __uint_as_float(r[c]) : 0.0f;  // the empty sum
+          store_piece(i, v);
+        }
+        ++j;
       }
     }
   }
