@@ -569,6 +569,77 @@ tlg_status tlg_gemm_grouped_dw(int64_t rows, int64_t N, int64_t K, int32_t group
                                tlg_type out, void *stream);
 
 /*
+ * The root-mean-square norm of every row, with the residual's addition in front of it:
+ *
+ *   H = X + R,   rstd[r] = 1 / sqrt(mean of H[r]^2 + eps),   Y = H * rstd * weight
+ *
+ * X, R, H and Y are rows x cols matrices of one type (any tlg_type), weight a vector of cols elements of
+ * that type, rstd rows fp32 values.  R may be NULL (H = X); H and rstd may be NULL where they are not
+ * needed.  H and Y may each be X or R itself (same base and row stride).  Computed in fp32 from the
+ * unrounded H and rounded once; the sum of a row does not depend on timing.  eps >= 0 and finite.
+ * cols <= 16384 (TLG_ERR_UNSUPPORTED beyond).
+ */
+tlg_status tlg_rmsnorm_forward(int64_t rows, int64_t cols, tlg_type type,
+                               const void *X, int64_t ldx, const void *R, int64_t ldr,
+                               const void *weight, float eps, void *H, int64_t ldh,
+                               void *Y, int64_t ldy, float *rstd, void *stream);
+
+/*
+ * The same with Y written as an MX matrix, quantised from the fp32 values as tlg_mx_quantize does:
+ * TLG_MX_E2M1 for the A operand of tlg_gemm_mxfp4, TLG_MX_E4M3 in 8 bits.  A row that holds a NaN or an
+ * infinity reads back as NaN.
+ */
+tlg_status tlg_rmsnorm_forward_mx(int64_t rows, int64_t cols, tlg_type type,
+                                  const void *X, int64_t ldx, const void *R, int64_t ldr,
+                                  const void *weight, float eps, void *H, int64_t ldh,
+                                  tlg_mx_format format, void *Q, int64_t ldq, void *S,
+                                  float *rstd, void *stream);
+
+/*
+ * Its backward pass, from the H and rstd of the forward pass: with x = H * rstd and g = dY * weight,
+ *
+ *   dX = rstd * (g - x * mean over the row of (g * x)) + dH,   dweight[c] = sum over the rows of dY * x
+ *
+ * dX is the gradient of X and of R alike.  dH, what arrives on the residual stream behind the norm, may
+ * be NULL, and so may dweight (cols fp32 values).  dX may be dY or dH itself (same base and row stride).
+ * Sums are fp32, in an order that does not depend on timing.  rows of 0: dweight = 0.  cols <= 16384.
+ * workspace: tlg_rmsnorm_backward_workspace_size() bytes of device memory, 256-byte aligned, needed when
+ * dweight is not NULL (TLG_ERR_INVALID_ARG when too small; the size may be 0).  Its contents on entry do
+ * not matter; calls that overlap in time must not share one.
+ */
+tlg_status tlg_rmsnorm_backward(int64_t rows, int64_t cols, tlg_type type,
+                                const void *dY, int64_t lddy, const void *H, int64_t ldh,
+                                const void *weight, const float *rstd, const void *dH, int64_t lddh,
+                                void *dX, int64_t lddx, float *dweight,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of tlg_rmsnorm_backward with a dweight, for the current device. */
+tlg_status tlg_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols, tlg_type type, size_t *bytes);
+
+/*
+ * A product of few rows (tokens) with integer 4-bit weights that have a scale for each group of k:
+ *
+ *   C = act(X . W^T + bias) + residual,   W[n, k] = (q[n, k] - z[n, k / group]) * s[n, k / group]
+ *
+ *  - X is M x K of type TLG_TYPE_F16 or TLG_TYPE_BF16; C is M x N of that type or TLG_TYPE_F32.
+ *  - Q holds q (0 .. 15), row-major with a row stride of ldq BYTES, two elements to a byte, 2i in the low
+ *    half of byte i.  A row holds ceil(K / 32) * 16 bytes, whose elements past K do not matter.  Q must be
+ *    16-byte aligned and ldq a multiple of 16.
+ *  - S holds s, N x ceil(K / group) contiguous values of X's type, Z the zero points z, as many bytes of
+ *    0 .. 15 (their low four bits count), or NULL for z = 8 everywhere.
+ *  - group is a power of two from 32 on.
+ *
+ * Products and sums are fp32 and no weight is rounded: a group's sum of (q - z) * X is multiplied by its
+ * scale.  epilogue as for tlg_gemm_fused, NULL for none: the bias holds N elements of X's type, the residual
+ * has C's type and may be C itself.  M may be any: rows of X are taken 16 at a time, which read the
+ * weights again each time, so the call is made for the few rows of a decoding step.  K == 0 gives C =
+ * act(bias) + residual.  No workspace.
+ */
+tlg_status tlg_gemv_q4(int64_t M, int64_t N, int64_t K, tlg_type type, const void *X, int64_t ldx,
+                       const void *Q, int64_t ldq, const void *S, const uint8_t *Z, int64_t group,
+                       const tlg_fused_epilogue *epilogue, void *C, int64_t ldc, tlg_type out, void *stream);
+
+/*
  * Resolve a configuration for this shape.  On input *config (never NULL)
  * holds the requested fields, zero meaning "choose for me" (all zero: the
  * automatic choice); on output it holds the configuration tlg_gemm_ex would

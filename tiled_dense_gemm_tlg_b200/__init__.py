@@ -21,6 +21,11 @@ Functions (same names as the C entry points):
 * ``tlg_gemm_mxfp4(A, SA, B, SB, ...)``    C = act(A.B^T + bias) + residual over 4-bit operands
 * ``tlg_act_forward_mx(Z, activation)``, ``tlg_act_backward_mx(dY, Q, S, activation)``
   an activation whose input is saved in 8 bits, and its backward pass
+* ``tlg_gemm_grouped(A, B, offsets, ...)``, ``tlg_gemm_grouped_dw(A, dC, offsets, ...)``  products grouped by
+  expert, fp16 or bf16, and their weight gradient
+* ``tlg_rmsnorm_forward(X, weight, ...)``, ``tlg_rmsnorm_forward_mx(...)``, ``tlg_rmsnorm_backward(...)``  the
+  root-mean-square norm with the residual's addition, its output also in 8 or 4 bits
+* ``tlg_gemv_q4(X, Q, S, Z, ...)``         products of a few rows with integer 4-bit weights and group scales
 * ``tlg_choose_config``, ``tlg_choose_config_mxfp4``, ``tlg_choose_config_mxfp4_fused``,
   ``tlg_device_error``, ``tlg_selftest_timeout``, ``tlg_status_string``, ``tlg_version``
 
@@ -78,7 +83,9 @@ EXPORTED = ("tlg_gemm_f16f32", "tlg_gemm_f16f16", "tlg_gemm_bias_relu_f16", "tlg
             "tlg_selftest_timeout", "tlg_status_string", "tlg_version",
             "tlg_mx_size", "tlg_mx_quantize", "tlg_mx_dequantize", "tlg_gemm_mxfp4", "tlg_choose_config_mxfp4",
             "tlg_choose_config_mxfp4_fused", "tlg_act_forward_mx", "tlg_act_backward_mx",
-            "tlg_act_backward_mx_workspace_size", "tlg_gemm_grouped", "tlg_gemm_grouped_dw")
+            "tlg_act_backward_mx_workspace_size", "tlg_gemm_grouped", "tlg_gemm_grouped_dw",
+            "tlg_rmsnorm_forward", "tlg_rmsnorm_forward_mx", "tlg_rmsnorm_backward",
+            "tlg_rmsnorm_backward_workspace_size", "tlg_gemv_q4")
 
 
 class tlg_config(ctypes.Structure):
@@ -132,7 +139,15 @@ _lib.tlg_choose_config_mxfp4_fused.argtypes = [_i64, _i64, _i64, ctypes.POINTER(
                                                ctypes.POINTER(tlg_config)]
 _lib.tlg_gemm_grouped.argtypes = [_i64, _i64, _i64, _i32, _p, _i32, _p, _i64, _i32, _p, _i64, _i64, _i32, _p, _i64, _i32, _p]
 _lib.tlg_gemm_grouped_dw.argtypes = [_i64, _i64, _i64, _i32, _p, _i32, _p, _i64, _p, _i64, _i32, _p, _i64, _i64, _i32, _p]
-for _name in ("tlg_gemm_grouped", "tlg_gemm_grouped_dw", "tlg_gemm_mxfp4", "tlg_choose_config_mxfp4", "tlg_choose_config_mxfp4_fused", "tlg_mx_size", "tlg_mx_quantize", "tlg_mx_dequantize", "tlg_act_forward_mx", "tlg_act_backward_mx",
+_f32 = ctypes.c_float
+_lib.tlg_rmsnorm_forward.argtypes = [_i64, _i64, _i32, _p, _i64, _p, _i64, _p, _f32, _p, _i64, _p, _i64, _p, _p]
+_lib.tlg_rmsnorm_forward_mx.argtypes = [_i64, _i64, _i32, _p, _i64, _p, _i64, _p, _f32, _p, _i64, _i32, _p, _i64, _p, _p, _p]
+_lib.tlg_rmsnorm_backward.argtypes = [_i64, _i64, _i32, _p, _i64, _p, _i64, _p, _p, _p, _i64, _p, _i64, _p, _p, _sz, _p]
+_lib.tlg_rmsnorm_backward_workspace_size.argtypes = [_i64, _i64, _i32, ctypes.POINTER(_sz)]
+_lib.tlg_gemv_q4.argtypes = [_i64, _i64, _i64, _i32, _p, _i64, _p, _i64, _p, _p, _i64, ctypes.POINTER(tlg_fused_epilogue),
+                             _p, _i64, _i32, _p]
+for _name in ("tlg_rmsnorm_forward", "tlg_rmsnorm_forward_mx", "tlg_rmsnorm_backward",
+              "tlg_rmsnorm_backward_workspace_size", "tlg_gemv_q4", "tlg_gemm_grouped", "tlg_gemm_grouped_dw", "tlg_gemm_mxfp4", "tlg_choose_config_mxfp4", "tlg_choose_config_mxfp4_fused", "tlg_mx_size", "tlg_mx_quantize", "tlg_mx_dequantize", "tlg_act_forward_mx", "tlg_act_backward_mx",
               "tlg_act_backward_mx_workspace_size", "tlg_gemm_f16f32", "tlg_gemm_f16f16", "tlg_gemm_bias_relu_f16", "tlg_gemm_ex",
               "tlg_gemm_op", "tlg_gemm_fused", "tlg_gemm_ex_noalloc", "tlg_gemm_workspace_size", "tlg_gemm_workspace_size_op", "tlg_choose_config", "tlg_device_error", "tlg_selftest_timeout"):
     getattr(_lib, _name).restype = _i32
@@ -565,6 +580,58 @@ def tlg_gemm_grouped_dw(A: torch.Tensor, dC: torch.Tensor, offsets: torch.Tensor
     groups x N x K with ``op_b="T"``; 0 for a group without rows.  ``out``: A's type (None) or "f32"."""
     return _result(_binding.gemm_grouped_dw(A, dC, offsets, _op(op_b, "op_b"), dB, _out_or_same(out),
                                             _handle(stream)), "tlg_gemm_grouped_dw")
+
+
+def tlg_rmsnorm_forward(X: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                        eps: float = 1e-6, Y: torch.Tensor | None = None, H: torch.Tensor | None = None,
+                        rstd: torch.Tensor | None = None, stream=None):
+    """(Y, H, rstd): H = X + residual, rstd = 1 / sqrt(mean(H^2) + eps) of each row in fp32, Y = H * rstd * weight.
+    Without a residual H is X itself (a given ``H`` gets a copy).  All matrices and ``weight`` have X's type (fp32,
+    fp16 or bf16); ``H`` and ``Y`` may be ``X`` or ``residual`` themselves.  At most 16384 columns."""
+    return _result(_binding.rmsnorm_forward(X, weight, residual, eps, H, Y, -1, None, None, rstd, _handle(stream)),
+                   "tlg_rmsnorm_forward")
+
+
+def tlg_rmsnorm_forward_mx(X: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                           eps: float = 1e-6, format: str = "e4m3", H: torch.Tensor | None = None,
+                           Q: torch.Tensor | None = None, S: torch.Tensor | None = None,
+                           rstd: torch.Tensor | None = None, stream=None):
+    """(Q, S, H, rstd): ``tlg_rmsnorm_forward`` with Y as an MX matrix, "e4m3" (8 bits) or "e2m1" (4 bits, the
+    operand of ``tlg_gemm_mxfp4``)."""
+    return _result(_binding.rmsnorm_forward(X, weight, residual, eps, H, None, _format(format), Q, S, rstd,
+                                            _handle(stream)), "tlg_rmsnorm_forward_mx")
+
+
+def tlg_rmsnorm_backward_workspace_size(rows: int, cols: int, type: str = "f16") -> int:
+    n = _sz(0)
+    _check(_lib.tlg_rmsnorm_backward_workspace_size(rows, cols, _out_type(type), ctypes.byref(n)),
+           "tlg_rmsnorm_backward_workspace_size")
+    return int(n.value)
+
+
+def tlg_rmsnorm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                         dH: torch.Tensor | None = None, dX: torch.Tensor | None = None,
+                         dweight: torch.Tensor | None = None, weight_grad: bool = True,
+                         workspace: torch.Tensor | None = None, stream=None):
+    """(dX, dweight): the gradient of X and of the residual alike, with ``dH``, what arrives on the residual
+    stream behind the norm, added to it (``dX`` may be ``dY`` or ``dH`` itself), and the fp32 gradient of the weight
+    (None with ``weight_grad=False``).  ``workspace``: a device buffer of tlg_rmsnorm_backward_workspace_size bytes;
+    allocated here when not given."""
+    return _result(_binding.rmsnorm_backward(dY, H, weight, rstd, dH, dX, dweight, bool(weight_grad), workspace,
+                                             _handle(stream)), "tlg_rmsnorm_backward")
+
+
+def tlg_gemv_q4(X: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, Z: torch.Tensor | None = None, group: int = 128,
+                bias: torch.Tensor | None = None, activation: str = "none", residual: torch.Tensor | None = None,
+                C: torch.Tensor | None = None, out: str | None = None, stream=None):
+    """C = act(X.W^T + bias) + residual for a few rows X (fp16 or bf16) and 4-bit weights
+    W[n, k] = (q[n, k] - Z[n, k // group]) * S[n, k // group].
+
+    ``Q``: N x 16 ceil(K / 32) bytes, element 2i of a row in the low half of byte i, 2i + 1 in the high half.
+    ``S``: N x ceil(K / group) of X's type; ``Z``: as many uint8 zero points, None for 8.  ``group``: a power of
+    two from 32 on.  The bias has X's type, the residual C's; ``out``: X's type (None) or "f32"."""
+    return _result(_binding.gemv_q4(X, Q, S, Z, group, bias, _activation(activation), residual, C, _out_or_same(out),
+                                    _handle(stream)), "tlg_gemv_q4")
 
 
 def raw_library():

@@ -404,10 +404,183 @@ PyObject *gemm_grouped_dw(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// A contiguous vector of n elements of a type.
+void *vector(const at::Tensor &t, const char *name, int64_t n, at::ScalarType type) {
+  if (t.scalar_type() != type || t.dim() != 1 || t.size(0) != n || !t.is_contiguous()) {
+    PyErr_Format(PyExc_ValueError, "%s must be a contiguous %s vector of %lld elements", name, c10::toString(type),
+                 static_cast<long long>(n));
+    throw Raised();
+  }
+  return t.data_ptr();
+}
+
+double real(PyObject *o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised();
+  return v;
+}
+
+// (X, weight, residual, eps, H, Y, format or -1, Q, S, rstd, stream) -> (Y, H, rstd) or (Q, S, H, rstd)
+PyObject *rmsnorm_forward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject * {
+    const at::Tensor &x = tensor(a[0], "X"), &w = tensor(a[1], "weight");
+    const Stream stream(a[10], x);
+    const Mat mx_ = mat(x, "X");
+    const tlg_type type = type_of(x, "X");
+    const int64_t rows = x.size(0), cols = x.size(1), format = integer(a[6]);
+    const float eps = static_cast<float>(real(a[3]));
+    same_device(x, &w);
+    void *pw = vector(w, "weight", cols, x.scalar_type());
+    const at::Tensor *r = maybe(a[2], "residual");
+    Mat mr = {nullptr, 0}, mh = {nullptr, 0};
+    at::Tensor h = x;
+    if (r != nullptr || a[4] != Py_None) {
+      h = out_matrix(a[4], "H", rows, cols, x.scalar_type(), x);
+      mh = mat(h, "H");
+    }
+    if (r != nullptr) {
+      same_device(x, r);
+      if (r->scalar_type() != x.scalar_type() || !is_shape(*r, rows, cols))
+        raise(PyExc_ValueError, "residual must have X's type and shape%s", "");
+      mr = mat(*r, "residual");
+    }
+    at::Tensor rstd;
+    if (const at::Tensor *given = maybe(a[9], "rstd")) {
+      same_device(x, given);
+      vector(*given, "rstd", rows, at::kFloat);
+      rstd = *given;
+    } else {
+      rstd = empty({rows}, at::kFloat, x.device());
+    }
+    float *ps = static_cast<float *>(rstd.data_ptr());
+    if (format < 0) {
+      const at::Tensor y = out_matrix(a[5], "Y", rows, cols, x.scalar_type(), x);
+      const Mat my = mat(y, "Y");
+      const tlg_status st = tlg_rmsnorm_forward(rows, cols, type, mx_.p, mx_.ld, mr.p, mr.ld, pw, eps, mh.p, mh.ld, my.p,
+                                                my.ld, ps, stream);
+      return st != TLG_OK ? PyLong_FromLong(st) : tuple_of(wrap(y), wrap(h), wrap(rstd));
+    }
+    const Mx o = mx_out(a[7], a[8], rows, cols, format, x);
+    const tlg_status st =
+        tlg_rmsnorm_forward_mx(rows, cols, type, mx_.p, mx_.ld, mr.p, mr.ld, pw, eps, mh.p, mh.ld,
+                               static_cast<tlg_mx_format>(format), o.m.p, o.m.ld, o.s.data_ptr(), ps, stream);
+    if (st != TLG_OK) return PyLong_FromLong(st);
+    PyObject *t = PyTuple_New(4);
+    PyTuple_SET_ITEM(t, 0, wrap(o.q));
+    PyTuple_SET_ITEM(t, 1, wrap(o.s));
+    PyTuple_SET_ITEM(t, 2, wrap(h));
+    PyTuple_SET_ITEM(t, 3, wrap(rstd));
+    return t;
+  });
+}
+
+// (dY, H, weight, rstd, dH, dX, dweight, whether to sum, workspace, stream)
+PyObject *rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject * {
+    const at::Tensor &dy = tensor(a[0], "dY"), &h = tensor(a[1], "H"), &w = tensor(a[2], "weight"),
+                     &rstd = tensor(a[3], "rstd");
+    const Stream stream(a[9], dy);
+    const Mat my = mat(dy, "dY");
+    const tlg_type type = type_of(dy, "dY");
+    const int64_t rows = dy.size(0), cols = dy.size(1);
+    for (const at::Tensor *t : {&h, &w, &rstd}) same_device(dy, t);
+    if (h.scalar_type() != dy.scalar_type() || !is_shape(h, rows, cols))
+      raise(PyExc_ValueError, "H must have dY's type and shape%s", "");
+    const Mat mh = mat(h, "H");
+    void *pw = vector(w, "weight", cols, dy.scalar_type());
+    const float *ps = static_cast<const float *>(vector(rstd, "rstd", rows, at::kFloat));
+    Mat md = {nullptr, 0};
+    if (const at::Tensor *d = maybe(a[4], "dH")) {
+      same_device(dy, d);
+      if (d->scalar_type() != dy.scalar_type() || !is_shape(*d, rows, cols))
+        raise(PyExc_ValueError, "dH must have dY's type and shape%s", "");
+      md = mat(*d, "dH");
+    }
+    const at::Tensor dx = out_matrix(a[5], "dX", rows, cols, dy.scalar_type(), dy);
+    const Mat mx_ = mat(dx, "dX");
+    at::Tensor dw, ws;
+    size_t ws_bytes = 0;
+    if (a[6] != Py_None || integer(a[7]) != 0) {
+      if (const at::Tensor *given = maybe(a[6], "dweight")) {
+        same_device(dy, given);
+        vector(*given, "dweight", cols, at::kFloat);
+        dw = *given;
+      } else {
+        dw = empty({cols}, at::kFloat, dy.device());
+      }
+      if (const at::Tensor *given = maybe(a[8], "workspace")) {
+        same_device(dy, given);
+        if (!given->is_contiguous()) raise(PyExc_ValueError, "%s must be contiguous", "workspace");
+        ws = *given;
+        ws_bytes = ws.nbytes();
+      } else {
+        const tlg_status st = tlg_rmsnorm_backward_workspace_size(rows, cols, type, &ws_bytes);
+        if (st != TLG_OK) return PyLong_FromLong(st);
+        if (ws_bytes != 0) ws = empty({static_cast<int64_t>(ws_bytes)}, at::kByte, dy.device());
+      }
+    }
+    const tlg_status st = tlg_rmsnorm_backward(
+        rows, cols, type, my.p, my.ld, mh.p, mh.ld, pw, ps, md.p, md.ld, mx_.p, mx_.ld,
+        dw.defined() ? static_cast<float *>(dw.data_ptr()) : nullptr, ws.defined() ? ws.data_ptr() : nullptr, ws_bytes,
+        stream);
+    if (st != TLG_OK) return PyLong_FromLong(st);
+    PyObject *none = Py_None;
+    if (!dw.defined()) Py_INCREF(none);
+    return tuple_of(wrap(dx), dw.defined() ? wrap(dw) : none);
+  });
+}
+
+// (X, Q, S, Z, group, bias, activation, residual, C, type, stream); type -1: X's
+PyObject *gemv_q4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject * {
+    const at::Tensor &x = tensor(a[0], "X"), &q = tensor(a[1], "Q"), &s = tensor(a[2], "S");
+    const Stream stream(a[10], x);
+    const Mat mx_ = mat(x, "X"), mq = mat(q, "Q");
+    const tlg_type type = type_of(x, "X");
+    const int64_t M = x.size(0), K = x.size(1), N = q.size(0), group = integer(a[4]);
+    const int64_t out = integer(a[9]) < 0 ? type : integer(a[9]);
+    if (group < 1) raise(PyExc_ValueError, "group must be positive%s", "");
+    const int64_t groups = K / group + (K % group != 0);
+    if (q.scalar_type() != at::kByte || q.size(1) != blocks_of(K) * 16)
+      raise(PyExc_ValueError, "Q must be a uint8 matrix of 16 bytes for every 32 columns of X%s", "");
+    if (s.scalar_type() != x.scalar_type() || !is_shape(s, N, groups) || !s.is_contiguous())
+      raise(PyExc_ValueError, "S must be contiguous, of X's type, with a scale for each row of Q and group%s", "");
+    same_device(x, &q);
+    same_device(x, &s);
+    const uint8_t *pz = nullptr;
+    if (const at::Tensor *z = maybe(a[3], "Z")) {
+      same_device(x, z);
+      if (z->scalar_type() != at::kByte || !is_shape(*z, N, groups) || !z->is_contiguous())
+        raise(PyExc_ValueError, "Z must be contiguous, uint8, with S's shape%s", "");
+      pz = static_cast<const uint8_t *>(z->data_ptr());
+    }
+    const at::Tensor c = out_matrix(a[8], "C", M, N, scalar_type(out), x);
+    const Mat mc = mat(c, "C");
+    tlg_fused_epilogue e = {nullptr, static_cast<int32_t>(integer(a[6])), nullptr, 0};
+    if (const at::Tensor *bias = maybe(a[5], "bias")) {
+      same_device(x, bias);
+      e.bias = vector(*bias, "bias", N, x.scalar_type());
+    }
+    if (const at::Tensor *r = maybe(a[7], "residual")) {
+      same_device(x, r);
+      if (r->scalar_type() != scalar_type(out) || !is_shape(*r, M, N))
+        raise(PyExc_ValueError, "residual must have C's type and shape%s", "");
+      const Mat mr = mat(*r, "residual");
+      e.residual = mr.p;
+      e.ldr = mr.ld;
+    }
+    const tlg_status st = tlg_gemv_q4(M, N, K, type, mx_.p, mx_.ld, mq.p, mq.ld, s.data_ptr(), pz, group, &e, mc.p, mc.ld,
+                                      static_cast<tlg_type>(out), stream);
+    return st != TLG_OK ? PyLong_FromLong(st) : wrap(c);
+  });
+}
+
 #define TLG_METHOD(NAME) {#NAME, reinterpret_cast<PyCFunction>(NAME), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {TLG_METHOD(mx_quantize),     TLG_METHOD(mx_dequantize),   TLG_METHOD(gemm_mxfp4),
                           TLG_METHOD(act_forward_mx), TLG_METHOD(act_backward_mx),
-                          TLG_METHOD(gemm_grouped),    TLG_METHOD(gemm_grouped_dw), {nullptr, nullptr, 0, nullptr}};
+                          TLG_METHOD(gemm_grouped),    TLG_METHOD(gemm_grouped_dw),
+                          TLG_METHOD(rmsnorm_forward), TLG_METHOD(rmsnorm_backward), TLG_METHOD(gemv_q4),
+                          {nullptr, nullptr, 0, nullptr}};
 // The docstring says which torch and Python this was compiled for; the build looks for it.
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", TLG_BUILT_FOR, -1, kMethods};
 

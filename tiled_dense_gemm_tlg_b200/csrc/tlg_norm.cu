@@ -1,0 +1,529 @@
+// The root-mean-square norm with the residual's addition, its output in the inputs' type or as a
+// microscaled (MX) matrix, and its backward pass.
+//
+//   forward:  h = x + r,  s = 1 / sqrt(mean(h^2) + eps),  y = h s w
+//   backward: with x^ = h s and g = dy w,  dx = s (g - x^ mean(g x^)) + dh,  dw = sum over rows of dy x^
+//
+// Both are bound by HBM traffic: a row is read once, held in registers while its sum is taken, and
+// written once.  `nw` warps share a row; each has up to U pieces of 32 lanes x 16 bytes, nw pieces apart.
+// CTAs are persistent and load their next row before they wait for the sum of this one, so that the
+// reduction's latency (two barriers, shuffles) runs under the next row's loads; the weights stay in
+// registers.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "tlg.h"
+#include "tlg_rows.cuh"
+
+namespace tlg {
+namespace {
+
+constexpr int64_t kNormMaxCols = 16384;
+
+// How a row is spread: warps of a CTA, warps to a row (a CTA of more takes several rows at a time),
+// pieces to a warp.
+struct NormShape {
+  int u, warps, nw;
+};
+
+NormShape norm_shape(int64_t cols, int type) {
+  const int64_t piece = 32 * 16 / type_bytes(type);
+  const int pieces = static_cast<int>((cols + piece - 1) / piece);
+  if (pieces <= 8) {
+    int nw = 1;
+    while (nw < pieces) nw *= 2;
+    return {1, 8, nw};
+  }
+  if (pieces <= 16) return {2, 8, 8};
+  if (pieces <= 32) return {2, 16, 16};
+  return {pieces <= 64 ? 4 : 8, 16, 16};
+}
+
+// Rows are loaded a row ahead where the registers hold two.
+template <int U>
+constexpr bool kNormAhead = U <= 2;
+
+// A lane's part of one row of up to U pieces, as loaded.
+template <int U>
+struct RowPart {
+  uint32_t w[U][4], first[U];
+};
+
+template <int T, bool VEC, int U>
+__device__ __forceinline__ void load_row(const RowMat &m, int64_t row, int c0, int step, int cols, int lane,
+                                         RowPart<U> &part) {
+  const char *base = static_cast<const char *>(m.p) + (row * m.ld + c0) * kTypeBytes<T>;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part.w[u][j] = 0;
+    part.first[u] = 0;
+    const int left = cols - c0 - u * step;
+    if (left > 0)
+      issue_load<T, VEC, false>(base + static_cast<int64_t>(u) * step * kTypeBytes<T>, left, lane, part.w[u], part.first[u]);
+  }
+}
+
+// Piece u's values, zeros past the last column; `base`: the piece's first byte in memory.
+template <int T, bool VEC, int U, int E>
+__device__ __forceinline__ void row_values(RowPart<U> &part, int u, const char *base, int lane, uint32_t *stage,
+                                           float (&v)[E]) {
+  finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(base), part.first[u], stage, part.w[u]);
+  to_floats<T, E>(part.w[u], v);
+}
+
+template <int T, bool VEC, int U>
+__device__ __forceinline__ const char *piece_at(const RowMat &m, int64_t row, int c0, int u, int step) {
+  return static_cast<const char *>(m.p) + (row * m.ld + c0 + static_cast<int64_t>(u) * step) * kTypeBytes<T>;
+}
+
+// The sum of x over the nw warps of a row, in every lane of them.  part: an entry for each warp; the same
+// entries are written again only behind the next call's barrier.
+__device__ __forceinline__ float row_sum(float x, int warp, int lane, int nw, float *part) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+  if (nw == 1) return x;
+  if (lane == 0) part[warp] = x;
+  __syncthreads();
+  x = lane < nw ? part[(warp & ~(nw - 1)) + lane] : 0.0f;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
+}
+
+struct NormArgs {
+  RowMat x, r, h, y;  // r.p, h.p: may be nullptr
+  MxMat q;
+  const void *w;
+  float *rstd;        // may be nullptr
+  float eps;
+  int64_t rows;
+  int cols, nw;
+};
+
+// FMT: kE2M1 or kE4M3 for an MX matrix, -1 for Y in the inputs' type.
+template <int T, bool VEC, int U, int WARPS, int FMT>
+__global__ void __launch_bounds__(32 * WARPS) norm_forward_kernel(const NormArgs a) {
+  constexpr int E = kLaneElems<T>, B = kTypeBytes<T>;
+  __shared__ __align__(16) uint32_t stage_all[VEC ? 1 : WARPS][128];
+  __shared__ float sums[2][WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t *stage = stage_all[VEC ? 0 : warp];
+  const int at_once = WARPS / a.nw;  // rows of a CTA
+  const int c0 = (warp & (a.nw - 1)) * 32 * E, step = a.nw * 32 * E;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  int64_t row = static_cast<int64_t>(blockIdx.x) * at_once + warp / a.nw;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * at_once;
+  const int64_t rounds = (a.rows - static_cast<int64_t>(blockIdx.x) * at_once + row_step - 1) / row_step;
+  RowPart<U> nx, nr, wp;
+  const RowMat wm = {a.w, 0};
+  load_row<T, VEC, U>(wm, 0, c0, step, a.cols, lane, wp);
+  auto fetch = [&](int64_t r) {
+    if (r < a.rows) {
+      load_row<T, VEC, U>(a.x, r, c0, step, a.cols, lane, nx);
+      if (a.r.p != nullptr) load_row<T, VEC, U>(a.r, r, c0, step, a.cols, lane, nr);
+    }
+  };
+  if (kNormAhead<U>) fetch(row);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(piece_at<T, VEC, U>(wm, 0, c0, u, step)), wp.first[u], stage, wp.w[u]);
+  for (int64_t i = 0; i < rounds; ++i, row += row_step) {
+    const bool in = row < a.rows;
+    if (!kNormAhead<U>) fetch(row);
+    float v[U][E];
+    float sum = 0.0f;
+    if (in) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        row_values<T, VEC, U, E>(nx, u, piece_at<T, VEC, U>(a.x, row, c0, u, step), lane, stage, v[u]);
+        if (a.r.p != nullptr) {
+          float b[E];
+          row_values<T, VEC, U, E>(nr, u, piece_at<T, VEC, U>(a.r, row, c0, u, step), lane, stage, b);
+#pragma unroll
+          for (int j = 0; j < E; j += 2) f2_add_to(v[u][j], v[u][j + 1], b[j], b[j + 1]);
+        }
+      }
+    }
+    if (kNormAhead<U>) fetch(row + row_step);
+    if (in) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) sum = fmaf(v[u][j], v[u][j], sum);
+        const int left = a.cols - c0 - u * step;
+        if (a.h.p != nullptr && left > 0) {
+          uint32_t o[4];
+          from_floats<T, E>(v[u], o);
+          store_lane<T, VEC, false>(const_cast<char *>(piece_at<T, VEC, U>(a.h, row, c0, u, step)), left, lane, stage, o);
+        }
+      }
+    }
+    sum = row_sum(sum, warp, lane, a.nw, sums[i & 1]);
+    if (!in) continue;
+    const float s = __frsqrt_rn(sum / static_cast<float>(a.cols) + a.eps);
+    if (a.rstd != nullptr && c0 == 0 && lane == 0) a.rstd[row] = s;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int left = a.cols - c0 - u * step;
+      if (left <= 0) continue;
+      float w[E], y[E];
+      to_floats<T, E>(wp.w[u], w);
+#pragma unroll
+      for (int j = 0; j < E; ++j) y[j] = v[u][j] * s * w[j];
+      if constexpr (FMT < 0) {
+        uint32_t o[4];
+        from_floats<T, E>(y, o);
+        store_lane<T, VEC, false>(const_cast<char *>(piece_at<T, VEC, U>(a.y, row, c0, u, step)), left, lane, stage, o);
+      } else {
+        constexpr int kFmt = FMT < 0 ? 0 : FMT;
+        constexpr int kLanesPerBlock = kMxBlock / E;
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          if (lane * E + j >= left) y[j] = 0.0f;  // also where the row's factor is not finite
+          m = max(m, __float_as_uint(y[j]) & 0x7fffffffu);
+        }
+#pragma unroll
+        for (int d = 1; d < kLanesPerBlock; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const uint32_t byte = scale_byte<kFmt>(m);
+        uint32_t q[kQWords<kFmt, E>];
+        encode<kFmt, E>(y, inverse_scale(byte), q);
+        const int first = c0 + u * step;
+        const int block = first / kMxBlock + lane * E / kMxBlock;
+        if (block < a.q.blocks)
+          store_q<kFmt, E>(const_cast<uint8_t *>(a.q.q) + row * a.q.ldq + (first / E + lane) * kQBytes<kFmt, E>, q);
+        if (lane % kLanesPerBlock == 0 && (block >> 2) < a.q.tiles_x)
+          const_cast<uint8_t *>(a.q.s)[scale_offset(row, block, a.q.tiles_x)] = static_cast<uint8_t>(byte);
+      }
+    }
+  }
+}
+
+struct NormBackArgs {
+  RowMat dy, h, dh, dx;  // dh.p: may be nullptr
+  const void *w;
+  const float *rstd;
+  float *part;           // a row of partial sums for each CTA, or dweight itself; may be nullptr
+  int64_t rows;
+  int cols, nw;
+};
+
+// The sums for dw stay in registers, row after row in order; CTAs leave their sums in `part`, which
+// column_sum_kernel adds in order, so the result does not depend on timing.
+template <int T, bool VEC, int U, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) norm_backward_kernel(const NormBackArgs a) {
+  constexpr int E = kLaneElems<T>;
+  __shared__ __align__(16) uint32_t stage_all[VEC ? 1 : WARPS][128];
+  __shared__ float sums[2][WARPS];
+  __shared__ __align__(16) float columns[U == 1 ? WARPS : 1][U == 1 ? 32 * E : 4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t *stage = stage_all[VEC ? 0 : warp];
+  const int at_once = WARPS / a.nw;
+  const int c0 = (warp & (a.nw - 1)) * 32 * E, step = a.nw * 32 * E;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  int64_t row = static_cast<int64_t>(blockIdx.x) * at_once + warp / a.nw;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * at_once;
+  const int64_t rounds = (a.rows - static_cast<int64_t>(blockIdx.x) * at_once + row_step - 1) / row_step;
+  RowPart<U> ny, nh, nd, wp;
+  float ns = 0.0f;
+  const RowMat wm = {a.w, 0};
+  load_row<T, VEC, U>(wm, 0, c0, step, a.cols, lane, wp);
+  auto fetch = [&](int64_t r) {
+    if (r < a.rows) {
+      load_row<T, VEC, U>(a.dy, r, c0, step, a.cols, lane, ny);
+      load_row<T, VEC, U>(a.h, r, c0, step, a.cols, lane, nh);
+      if (a.dh.p != nullptr) load_row<T, VEC, U>(a.dh, r, c0, step, a.cols, lane, nd);
+      ns = a.rstd[r];
+    }
+  };
+  if (kNormAhead<U>) fetch(row);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(piece_at<T, VEC, U>(wm, 0, c0, u, step)), wp.first[u], stage, wp.w[u]);
+  float acc[U][E];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int j = 0; j < E; ++j) acc[u][j] = 0.0f;
+  for (int64_t i = 0; i < rounds; ++i, row += row_step) {
+    const bool in = row < a.rows;
+    if (!kNormAhead<U>) fetch(row);
+    const float s = ns;
+    float dot = 0.0f;
+    RowPart<U> y = ny, h = nh, d = nd;
+    if (in) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float vy[E], vh[E], w[E];
+        row_values<T, VEC, U, E>(y, u, piece_at<T, VEC, U>(a.dy, row, c0, u, step), lane, stage, vy);
+        row_values<T, VEC, U, E>(h, u, piece_at<T, VEC, U>(a.h, row, c0, u, step), lane, stage, vh);
+        to_floats<T, E>(wp.w[u], w);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const float t = vy[j] * (vh[j] * s);
+          acc[u][j] += t;
+          dot = fmaf(t, w[j], dot);
+        }
+        if (a.dh.p != nullptr)
+          finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(piece_at<T, VEC, U>(a.dh, row, c0, u, step)), d.first[u], stage, d.w[u]);
+      }
+    }
+    if (kNormAhead<U>) fetch(row + row_step);
+    dot = row_sum(dot, warp, lane, a.nw, sums[i & 1]) / static_cast<float>(a.cols);
+    if (!in) continue;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int left = a.cols - c0 - u * step;
+      if (left <= 0) continue;
+      float vy[E], vh[E], w[E];
+      to_floats<T, E>(y.w[u], vy);
+      to_floats<T, E>(h.w[u], vh);
+      to_floats<T, E>(wp.w[u], w);
+#pragma unroll
+      for (int j = 0; j < E; ++j) vy[j] = s * fmaf(-dot, vh[j] * s, vy[j] * w[j]);
+      if (a.dh.p != nullptr) {
+        to_floats<T, E>(d.w[u], vh);
+#pragma unroll
+        for (int j = 0; j < E; ++j) vy[j] += vh[j];
+      }
+      uint32_t o[4];
+      from_floats<T, E>(vy, o);
+      store_lane<T, VEC, false>(const_cast<char *>(piece_at<T, VEC, U>(a.dx, row, c0, u, step)), left, lane, stage, o);
+    }
+  }
+  if (a.part == nullptr) return;
+  float *part = a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
+  if constexpr (U == 1) {  // the rows taken at once
+#pragma unroll
+    for (int j = 0; j < E; ++j) columns[warp][lane * E + j] = acc[0][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += 32 * WARPS) {
+      float t = 0.0f;
+      for (int g = 0; g < at_once; ++g) t += columns[g * a.nw + c / (32 * E)][c % (32 * E)];
+      part[c] = t;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int c = c0 + u * step + lane * E + j;
+        if (c < a.cols) part[c] = acc[u][j];
+      }
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+// Calls f with the pieces and warps of norm_shape.
+template <int T, typename F>
+tlg_status with_shape(const NormShape &n, F f) {
+  using W8 = std::integral_constant<int, 8>;
+  using W16 = std::integral_constant<int, 16>;
+  if (n.u == 1) return f(std::integral_constant<int, 1>(), W8());
+  if (n.u == 2) return n.warps == 8 ? f(std::integral_constant<int, 2>(), W8()) : f(std::integral_constant<int, 2>(), W16());
+  if constexpr (T == kTypeF32) {
+    if (n.u == 8) return f(std::integral_constant<int, 8>(), W16());
+  }
+  return f(std::integral_constant<int, 4>(), W16());
+}
+
+unsigned norm_grid(const NormShape &n, int64_t rows, int sms, int per_sm) {
+  const int64_t at_once = n.warps / n.nw;
+  return static_cast<unsigned>(std::min<int64_t>((rows + at_once - 1) / at_once, int64_t(sms) * per_sm));
+}
+
+// CTAs of the backward kernel, each of which leaves a row of partial sums.
+unsigned backward_ctas(int64_t rows, int64_t cols, int type, int sms) {
+  const NormShape n = norm_shape(cols, type);
+  return norm_grid(n, rows, sms, n.warps == 8 ? 3 : 1);
+}
+
+tlg_status check_norm(int64_t rows, int64_t cols, int type) {
+  if (!valid_type(type)) return TLG_ERR_INVALID_ARG;
+  const tlg_status st = check_extents(rows, cols);
+  if (st != TLG_OK) return st;
+  return cols > kNormMaxCols ? TLG_ERR_UNSUPPORTED : TLG_OK;
+}
+
+// Whether a matrix, if it is there, may be accessed 16 bytes at a time.
+bool vec_or_none(const void *p, int64_t rows, int64_t ld, int type) {
+  return p == nullptr || vec_rows(p, rows, ld, type);
+}
+
+tlg_status check_vector(const void *p, int64_t n, int64_t esz, Range *r) {
+  if (p == nullptr) return TLG_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(esz) != 0) return TLG_ERR_ALIGNMENT;
+  r->lo = reinterpret_cast<uintptr_t>(p);
+  r->hi = r->lo + static_cast<uintptr_t>(n * esz);
+  return TLG_OK;
+}
+
+// The forward pass; format < 0: Y, else Q and S.
+tlg_status norm_forward(int64_t rows, int64_t cols, int type, const void *X, int64_t ldx, const void *R, int64_t ldr,
+                        const void *weight, float eps, void *H, int64_t ldh, void *Y, int64_t ldy, int format, void *Q,
+                        int64_t ldq, void *S, float *rstd, void *stream) {
+  tlg_status st = check_norm(rows, cols, type);
+  if (st != TLG_OK) return st;
+  if (!(eps >= 0.0f) || std::isinf(eps) || (format >= 0 && !valid_format(format))) return TLG_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return TLG_OK;
+  const int64_t esz = type_bytes(type);
+  Range in[3] = {}, out[4] = {};  // X, R, weight; H, Y or Q, S, rstd
+  st = check_matrix(X, rows, cols, ldx, esz, &in[0]);
+  if (st == TLG_OK && R != nullptr) st = check_matrix(R, rows, cols, ldr, esz, &in[1]);
+  if (st == TLG_OK) st = check_vector(weight, cols, esz, &in[2]);
+  if (st == TLG_OK && H != nullptr) st = check_matrix(H, rows, cols, ldh, esz, &out[0]);
+  if (st == TLG_OK) {
+    st = format < 0 ? check_matrix(Y, rows, cols, ldy, esz, &out[1]) : check_mx(format, rows, cols, Q, ldq, S, &out[1], &out[2]);
+  }
+  if (st == TLG_OK && rstd != nullptr) st = check_vector(rstd, rows, 4, &out[3]);
+  if (st != TLG_OK) return st;
+  // H and Y may be X or R themselves: an element is read by the lane that writes it, before it does.
+  auto same = [&](const void *o, int64_t ldo, int i) {
+    return i == 0 ? o == X && ldo == ldx : i == 1 && o == R && ldo == ldr;
+  };
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 3; ++i)
+      if (meets(out[o], in[i]) && !(o == 0 && same(H, ldh, i)) && !(o == 1 && format < 0 && same(Y, ldy, i)))
+        return TLG_ERR_INVALID_ARG;
+    for (int k = 0; k < o; ++k)
+      if (meets(out[o], out[k])) return TLG_ERR_INVALID_ARG;
+  }
+  DeviceInfo info;
+  st = device_ready({X, R, weight, H, Y, Q, S, rstd}, &info);
+  if (st != TLG_OK) return st;
+  const NormShape n = norm_shape(cols, type);
+  NormArgs a = {{X, ldx}, {R, ldr}, {H, ldh}, {Y, ldy}, format < 0 ? MxMat{} : mx_mat(Q, ldq, S, cols), weight, rstd, eps, rows,
+                static_cast<int>(cols), n.nw};
+  const bool vec = aligned16(weight) && vec_rows(X, rows, ldx, type) && vec_or_none(R, rows, ldr, type) &&
+                   vec_or_none(H, rows, ldh, type) && vec_or_none(Y, rows, ldy, type);
+  const unsigned grid = norm_grid(n, rows, info.sm_count, n.warps == 8 ? 4 : 2);
+  return with_type(type, [&](auto T) {
+    constexpr int kT = decltype(T)::value;
+    return with_flag(vec, [&](auto V) {
+      return with_shape<kT>(n, [&](auto U, auto W) {
+        constexpr int kU = decltype(U)::value, kW = decltype(W)::value;
+        constexpr bool kV = decltype(V)::value;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        if (format < 0) return launch(norm_forward_kernel<kT, kV, kU, kW, -1>, dim3(grid), 32 * kW, s, a);
+        if (format == TLG_MX_E2M1) return launch(norm_forward_kernel<kT, kV, kU, kW, kE2M1>, dim3(grid), 32 * kW, s, a);
+        return launch(norm_forward_kernel<kT, kV, kU, kW, kE4M3>, dim3(grid), 32 * kW, s, a);
+      });
+    });
+  });
+}
+
+}  // namespace
+}  // namespace tlg
+
+using namespace tlg;
+
+extern "C" {
+
+tlg_status tlg_rmsnorm_forward(int64_t rows, int64_t cols, tlg_type type, const void *X, int64_t ldx, const void *R,
+                               int64_t ldr, const void *weight, float eps, void *H, int64_t ldh, void *Y, int64_t ldy,
+                               float *rstd, void *stream) {
+  return norm_forward(rows, cols, type, X, ldx, R, ldr, weight, eps, H, ldh, Y, ldy, -1, nullptr, 0, nullptr, rstd, stream);
+}
+
+tlg_status tlg_rmsnorm_forward_mx(int64_t rows, int64_t cols, tlg_type type, const void *X, int64_t ldx, const void *R,
+                                  int64_t ldr, const void *weight, float eps, void *H, int64_t ldh,
+                                  tlg_mx_format format, void *Q, int64_t ldq, void *S, float *rstd, void *stream) {
+  if (!valid_format(format)) return TLG_ERR_INVALID_ARG;
+  return norm_forward(rows, cols, type, X, ldx, R, ldr, weight, eps, H, ldh, nullptr, 0, format, Q, ldq, S, rstd, stream);
+}
+
+tlg_status tlg_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols, tlg_type type, size_t *bytes) {
+  if (bytes == nullptr) return TLG_ERR_INVALID_ARG;
+  *bytes = 0;
+  const tlg_status st = check_norm(rows, cols, type);
+  if (st != TLG_OK || rows == 0 || cols == 0) return st;
+  int dev = 0;
+  DeviceInfo info;
+  const tlg_status ds = current_device(&dev, &info);
+  if (ds != TLG_OK) return ds;
+  const unsigned ctas = backward_ctas(rows, cols, type, info.sm_count);
+  *bytes = ctas > 1 ? static_cast<size_t>(ctas) * static_cast<size_t>(cols) * 4 : 0;
+  return TLG_OK;
+}
+
+tlg_status tlg_rmsnorm_backward(int64_t rows, int64_t cols, tlg_type type, const void *dY, int64_t lddy, const void *H,
+                                int64_t ldh, const void *weight, const float *rstd, const void *dH, int64_t lddh,
+                                void *dX, int64_t lddx, float *dweight, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+  tlg_status st = check_norm(rows, cols, type);
+  if (st != TLG_OK || cols == 0) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  DeviceInfo info;
+  Range rw = {}, rk = {};
+  if (dweight != nullptr) {
+    st = check_vector(dweight, cols, 4, &rw);
+    if (st != TLG_OK) return st;
+  }
+  if (workspace != nullptr) {
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return TLG_ERR_ALIGNMENT;
+    rk.lo = reinterpret_cast<uintptr_t>(workspace);
+    rk.hi = rk.lo + workspace_bytes;
+  }
+  if (rows == 0) {  // the sum over no rows
+    if (dweight == nullptr) return TLG_OK;
+    st = device_ready({dweight}, &info);
+    if (st != TLG_OK) return st;
+    if (cudaMemsetAsync(dweight, 0, static_cast<size_t>(cols) * 4, s) != cudaSuccess) {
+      cudaGetLastError();
+      return TLG_ERR_CUDA;
+    }
+    return TLG_OK;
+  }
+  const int64_t esz = type_bytes(type);
+  Range ry, rh, rwt, rr, rd = {}, rx;
+  st = check_matrix(dY, rows, cols, lddy, esz, &ry);
+  if (st == TLG_OK) st = check_matrix(H, rows, cols, ldh, esz, &rh);
+  if (st == TLG_OK) st = check_vector(weight, cols, esz, &rwt);
+  if (st == TLG_OK) st = check_vector(rstd, rows, 4, &rr);
+  if (st == TLG_OK && dH != nullptr) st = check_matrix(dH, rows, cols, lddh, esz, &rd);
+  if (st == TLG_OK) st = check_matrix(dX, rows, cols, lddx, esz, &rx);
+  if (st != TLG_OK) return st;
+  if (meets(rx, ry) && !(dX == dY && lddx == lddy)) return TLG_ERR_INVALID_ARG;
+  if (dH != nullptr && meets(rx, rd) && !(dX == dH && lddx == lddh)) return TLG_ERR_INVALID_ARG;
+  if (meets(rx, rh) || meets(rx, rwt) || meets(rx, rr)) return TLG_ERR_INVALID_ARG;
+  for (const Range &r : {ry, rh, rwt, rr, rd, rx})
+    if (meets(rw, r) || meets(rk, r)) return TLG_ERR_INVALID_ARG;
+  if (meets(rw, rk)) return TLG_ERR_INVALID_ARG;
+  st = device_ready({dY, H, weight, rstd, dH, dX, dweight, workspace}, &info);
+  if (st != TLG_OK) return st;
+  const unsigned ctas = backward_ctas(rows, cols, type, info.sm_count);
+  float *part = dweight;
+  if (dweight != nullptr && ctas > 1) {
+    if (workspace == nullptr || workspace_bytes < static_cast<size_t>(ctas) * static_cast<size_t>(cols) * 4)
+      return TLG_ERR_INVALID_ARG;
+    part = static_cast<float *>(workspace);
+  }
+  const NormShape n = norm_shape(cols, type);
+  const NormBackArgs a = {{dY, lddy}, {H, ldh}, {dH, lddh}, {dX, lddx}, weight, rstd, part, rows, static_cast<int>(cols), n.nw};
+  const bool vec = aligned16(weight) && vec_rows(dY, rows, lddy, type) && vec_rows(H, rows, ldh, type) &&
+                   vec_or_none(dH, rows, lddh, type) && vec_rows(dX, rows, lddx, type);
+  st = with_type(type, [&](auto T) {
+    constexpr int kT = decltype(T)::value;
+    return with_flag(vec, [&](auto V) {
+      return with_shape<kT>(n, [&](auto U, auto W) {
+        constexpr int kU = decltype(U)::value, kW = decltype(W)::value;
+        return launch(norm_backward_kernel<kT, decltype(V)::value, kU, kW>, dim3(ctas), 32 * kW, s, a);
+      });
+    });
+  });
+  if (st != TLG_OK || part == dweight) return st;
+  const dim3 sum_grid(static_cast<unsigned>((cols + 31) / 32));
+  return ctas > 128 ? launch(column_sum_kernel<32>, sum_grid, 1024, s, part, static_cast<int>(ctas), cols, dweight)
+                    : launch(column_sum_kernel<8>, sum_grid, 256, s, part, static_cast<int>(ctas), cols, dweight);
+}
+
+}  // extern "C"
