@@ -90,49 +90,57 @@ __device__ __forceinline__ void q4_copy(uint32_t dst, const void *src, int size)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
 
-// Slots of a warp's ring, as many as fit beside each other.
-template <int NT, int R>
-constexpr int kQ4Stages = NT == 1 ? (R == 1 ? 8 : 5) : (R == 2 ? 4 : 3);
+// Slots of a ring.
+template <int NT, int WK>
+constexpr int kQ4Stages = WK == kQ4Warps ? 8 : NT == 1 ? 6 : 5;
 
-// Bytes of a warp's slot: W's 16 R rows of 64 bytes, X's tokens of 256.
-__host__ __device__ constexpr int q4_slot(int r, int tokens) { return r * 1024 + tokens * 256; }
+// Bytes of a slot: a unit of WR * 16 R rows of W, 64 bytes of each, and of X's tokens, 256 of each.
+__host__ __device__ constexpr int q4_slot(int rows, int tokens) { return rows * 64 + tokens * 256; }
 // Row stride of the scales in shared memory, in words; odd, so that eight rows lie in different banks.
 __host__ __device__ constexpr int q4_scale_ld(int groups) { return (groups < kQ4Panel ? groups : kQ4Panel) | 1; }
 
-// NT: blocks of 8 tokens; R: blocks of 16 rows of W; GC: blocks of 32 k that have one scale in a unit (1, 2, 4).
-template <int T, int NT, int R, int GC>
+// NT: blocks of 8 tokens; R: blocks of 16 rows of W to a warp; WK: warps that share K, each group of
+// WR = 8 / WK warps with a ring of its own, in which X is shared; GC: blocks of 32 k that have one scale in a
+// unit (1, 2, 4).
+template <int T, int NT, int R, int WK, int GC>
 __global__ void __launch_bounds__(32 * kQ4Warps) gemv_q4_kernel(const Q4Params p) {
-  constexpr int ST = kQ4Stages<NT, R>;
+  constexpr int ST = kQ4Stages<NT, WK>;
+  constexpr int WR = kQ4Warps / WK;
+  constexpr int kRows = WR * 16 * R;  // of a CTA
   constexpr uint32_t kMagic = T == kTypeF16 ? 0x64006400u : 0x43004300u;
   extern __shared__ __align__(16) uint8_t q4_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wr = warp % WR, wk = warp / WR;
   const int g = lane >> 2, t = lane & 3;
   const int tile = static_cast<int>(blockIdx.x) / p.token_blocks;
   const int token0 = (static_cast<int>(blockIdx.x) - tile * p.token_blocks) * (8 * NT);
   const int tokens = min(p.M - token0, 8 * NT);
-  const int n0 = tile * (16 * R);
-  const int slot_bytes = q4_slot(R, tokens);
-  const uint32_t ring = smem_u32(q4_smem) + static_cast<uint32_t>(warp * ST * slot_bytes);
+  const int n0 = tile * kRows;
+  const int slot_bytes = q4_slot(kRows, tokens);
+  const uint32_t ring = smem_u32(q4_smem) + static_cast<uint32_t>(wk * ST * slot_bytes);
   const int scale_ld = q4_scale_ld(p.groups);
   // a word for each row and group: the scale's bits low, the zero point high
-  uint32_t *scales = reinterpret_cast<uint32_t *>(q4_smem + kQ4Warps * ST * slot_bytes);
+  uint32_t *scales = reinterpret_cast<uint32_t *>(q4_smem + WK * ST * slot_bytes);
   grid_dependency_wait();
   grid_launch_dependents();
 
   const int blocks = (p.K + 31) / 32;  // of a row of W
+  // this lane's part of a unit of W: block t of rows g, g + 8, ..
+  const int row0 = n0 + wr * 16 * R + g;
+  const uint8_t *w_from = p.Q + row0 * p.ldq + t * 16;
   auto issue = [&](int unit, int slot) {
-    const uint32_t w = ring + static_cast<uint32_t>(slot * slot_bytes), x = w + R * 1024;
+    const uint32_t w = ring + static_cast<uint32_t>(slot * slot_bytes + wr * 1024 * R), x = ring + static_cast<uint32_t>(slot * slot_bytes + kRows * 64);
     const int k0 = unit * kQ4Unit;
-    // W: a lane's 16 bytes are block c of row r, at (c ^ r / 2 % 4) of the row's four places
+    // W: block c of row r at (c ^ r / 2 % 4) of the row's four places
 #pragma unroll
     for (int i = 0; i < 2 * R; ++i) {
-      const int r = i * 8 + g, c = t, b = unit * 4 + c;
-      const bool in = n0 + r < p.N && b < blocks;
-      q4_copy(w + static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) * 16)),
-              in ? p.Q + (n0 + r) * p.ldq + static_cast<int64_t>(b) * 16 : p.Q, in ? 16 : 0);
+      const int r = i * 8 + g;
+      const bool in = row0 + i * 8 < p.N && unit * 4 + t < blocks;
+      q4_copy(w + static_cast<uint32_t>(r * 64 + ((t ^ ((r >> 1) & 3)) * 16)),
+              in ? w_from + i * 8 * p.ldq + static_cast<int64_t>(unit) * 64 : p.Q, in ? 16 : 0);
     }
     // X: 8 elements of token m at (q ^ 4 (m % 2)) of its 16 places
-    for (int i = lane; i < tokens * 16; i += 32) {
+    for (int i = wr * 32 + lane; i < tokens * 16; i += WR * 32) {
       const int m = i >> 4, q = i & 15, k = k0 + q * 8;
       const uint32_t to = x + static_cast<uint32_t>(m * 256 + ((q ^ ((m & 1) << 2)) * 16));
       const uint16_t *from = p.X + (token0 + m) * p.ldx + k;
@@ -166,28 +174,41 @@ __global__ void __launch_bounds__(32 * kQ4Warps) gemv_q4_kernel(const Q4Params p
     if (u0 > 0) __syncthreads();  // the last panel's scales are read
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s) {
-      const int u = u0 + warp + s * kQ4Warps;
+      const int u = u0 + wk + s * WK;
       if (u < u1) issue(u, s);
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    // scales and zero points of the panel: 0 past the last row or group
+    // scales and zero points of the panel, 0 past the last row: a warp takes 2 WR R rows, all loads of 32
+    // groups in flight at once
     const int held = min(p.groups - first_group, kQ4Panel);
-    for (int i = threadIdx.x; i < 16 * R * held; i += 32 * kQ4Warps) {
-      const int r = i / held, j = i - r * held;
-      const bool in = n0 + r < p.N;
-      const int64_t at = static_cast<int64_t>(n0 + r) * p.groups + first_group + j;
-      const uint32_t z = in && p.Z != nullptr ? p.Z[at] & 15u : 8u;
-      scales[r * scale_ld + j] = (in ? p.S[at] : 0u) | z << 16;
+    for (int j = lane; j < held; j += 32) {
+      constexpr int kMine = kRows / kQ4Warps;
+      uint32_t v[kMine], z[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int n = n0 + warp * kMine + i;
+        const int64_t at = static_cast<int64_t>(n) * p.groups + first_group + j;
+        v[i] = n < p.N ? p.S[at] : 0u;
+        z[i] = n < p.N && p.Z != nullptr ? p.Z[at] : 8u;
+      }
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) scales[(warp * kMine + i) * scale_ld + j] = v[i] | (z[i] & 15u) << 16;
     }
     __syncthreads();
     int slot = 0;
-    for (int u = u0 + warp; u < u1; u += kQ4Warps) {
+    for (int first = u0; first < u1; first += WK) {  // the warps that share a ring go through it together
+      const int u = first + wk;
       asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
-      __syncwarp();  // every lane's copies have landed, and the slot before is read
-      const int ahead = u + (ST - 1) * kQ4Warps;
+      // every copy into this slot has landed, and the slot before is read
+      if constexpr (WR > 1)
+        __syncthreads();
+      else
+        __syncwarp();
+      const int ahead = u + (ST - 1) * WK;
       if (ahead < u1) issue(ahead, slot == 0 ? ST - 1 : slot - 1);
       asm volatile("cp.async.commit_group;" ::: "memory");
-      const uint32_t w = ring + static_cast<uint32_t>(slot * slot_bytes), x = w + R * 1024;
+      if (u >= u1) break;
+      const uint32_t w = ring + static_cast<uint32_t>(slot * slot_bytes + wr * 1024 * R), x = ring + static_cast<uint32_t>(slot * slot_bytes + kRows * 64);
       float acc[R][NT][4];
       uint32_t zero[R][2];
       float scale[R][2];
@@ -195,7 +216,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps) gemv_q4_kernel(const Q4Params p
       for (int c = 0; c < 4; ++c) {
         if (c % GC == 0) {
           const int j = static_cast<int>((static_cast<int64_t>(u) * kQ4Unit + c * 32) >> p.group_log2) - first_group;
-          const uint32_t *s = scales + min(j, held - 1);  // blocks past K have no group; their X is 0
+          const uint32_t *s = scales + wr * 16 * R * scale_ld + min(j, held - 1);  // blocks past K have no group; their X is 0
 #pragma unroll
           for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -254,7 +275,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps) gemv_q4_kernel(const Q4Params p
     __syncwarp();
   }
 
-  // The warps' sums, added in warp order: [warp][token][row], in the rings' place.
+  // The sums of the warps that share K, added in order: [wk][token][row], in the rings' place.
   __syncthreads();
   float *sums = reinterpret_cast<float *>(q4_smem);
 #pragma unroll
@@ -263,16 +284,16 @@ __global__ void __launch_bounds__(32 * kQ4Warps) gemv_q4_kernel(const Q4Params p
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int m = n * 8 + t * 2 + (j & 1), row = r * 16 + g + (j >> 1) * 8;
-        if (m < tokens) sums[(warp * tokens + m) * (16 * R) + row] = total[r][n][j];
+        const int m = n * 8 + t * 2 + (j & 1), row = wr * 16 * R + r * 16 + g + (j >> 1) * 8;
+        if (m < tokens) sums[(wk * tokens + m) * kRows + row] = total[r][n][j];
       }
   __syncthreads();
-  for (int i = threadIdx.x; i < tokens * 16 * R; i += 32 * kQ4Warps) {
-    const int m = i / (16 * R), row = i - m * (16 * R), n = n0 + row;
+  for (int i = threadIdx.x; i < tokens * kRows; i += 32 * kQ4Warps) {
+    const int m = i / kRows, row = i - m * kRows, n = n0 + row;
     if (n >= p.N) continue;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kQ4Warps; ++w) v += sums[(w * tokens + m) * (16 * R) + row];
+    for (int w = 0; w < WK; ++w) v += sums[(w * tokens + m) * kRows + row];
     if (p.bias != nullptr) v += load_elem<T>(p.bias, n);
     const int64_t token = token0 + m;
     if (p.out_f32) {
@@ -289,12 +310,13 @@ __global__ void __launch_bounds__(32 * kQ4Warps) gemv_q4_kernel(const Q4Params p
 
 // ------------------------------------------------------------------ host side
 
-template <int T, int NT, int R, int GC>
+template <int T, int NT, int R, int WK, int GC>
 tlg_status launch_q4(int dev, Q4Params p, cudaStream_t s) {
-  constexpr auto kernel = gemv_q4_kernel<T, NT, R, GC>;
-  constexpr int kMost = kQ4Warps * kQ4Stages<NT, R> * q4_slot(R, 8 * NT) + 16 * R * q4_scale_ld(kQ4Panel) * 4;
+  constexpr auto kernel = gemv_q4_kernel<T, NT, R, WK, GC>;
+  constexpr int kRows = kQ4Warps / WK * 16 * R, kStages = kQ4Stages<NT, WK>;
+  constexpr int kMost = WK * kStages * q4_slot(kRows, 8 * NT) + kRows * q4_scale_ld(kQ4Panel) * 4;
   static_assert(kMost <= 232448, "shared memory per CTA exceeded");
-  static_assert(kQ4Stages<NT, R> * q4_slot(R, 1) >= 16 * R * 4, "a warp's sums of a token fit its ring");
+  static_assert(kStages * q4_slot(kRows, 1) >= kRows * 4, "a slice's sums of a token fit its ring");
   static bool ready[kMaxDevices];
   static std::mutex mutex;
   {
@@ -309,13 +331,12 @@ tlg_status launch_q4(int dev, Q4Params p, cudaStream_t s) {
   }
   const int tokens = std::min(p.M, 8 * NT);
   p.token_blocks = (p.M + 8 * NT - 1) / (8 * NT);
-  const int64_t tiles = (p.N + 16 * R - 1) / (16 * R);
+  const int64_t tiles = (p.N + kRows - 1) / kRows;
   if (tiles * p.token_blocks > kMaxExtent) return TLG_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.token_blocks));
   cfg.blockDim = dim3(32 * kQ4Warps);
-  cfg.dynamicSmemBytes = kQ4Warps * kQ4Stages<NT, R> * q4_slot(R, tokens) +
-                         16 * R * q4_scale_ld(p.groups) * 4;
+  cfg.dynamicSmemBytes = WK * kStages * q4_slot(kRows, tokens) + kRows * q4_scale_ld(p.groups) * 4;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -329,18 +350,18 @@ tlg_status launch_q4(int dev, Q4Params p, cudaStream_t s) {
   return TLG_OK;
 }
 
-template <int T, int NT, int R>
+template <int T, int NT, int R, int WK>
 tlg_status launch_q4_group(int dev, const Q4Params &p, cudaStream_t s) {
-  if (p.group_log2 == 5) return launch_q4<T, NT, R, 1>(dev, p, s);
-  if (p.group_log2 == 6) return launch_q4<T, NT, R, 2>(dev, p, s);
-  return launch_q4<T, NT, R, 4>(dev, p, s);
+  if (p.group_log2 == 5) return launch_q4<T, NT, R, WK, 1>(dev, p, s);
+  if (p.group_log2 == 6) return launch_q4<T, NT, R, WK, 2>(dev, p, s);
+  return launch_q4<T, NT, R, WK, 4>(dev, p, s);
 }
 
 template <int T>
-tlg_status launch_q4_shape(int dev, int sms, const Q4Params &p, cudaStream_t s) {
-  if (p.M > 8) return p.N >= 64 * sms ? launch_q4_group<T, 2, 4>(dev, p, s) : launch_q4_group<T, 2, 2>(dev, p, s);
-  if (p.M > 2 && p.N >= 32 * sms) return launch_q4_group<T, 1, 2>(dev, p, s);
-  return launch_q4_group<T, 1, 1>(dev, p, s);
+tlg_status launch_q4_shape(int dev, const Q4Params &p, cudaStream_t s) {
+  if (p.M > 8) return launch_q4_group<T, 2, 1, 2>(dev, p, s);
+  if (p.M > 2) return launch_q4_group<T, 1, 1, 2>(dev, p, s);
+  return launch_q4_group<T, 1, 1, 8>(dev, p, s);
 }
 
 }  // namespace
@@ -415,8 +436,8 @@ tlg_status tlg_gemv_q4(int64_t M, int64_t N, int64_t K, tlg_type type, const voi
   p.R = e.residual;
   p.ldr = e.ldr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return type == TLG_TYPE_F16 ? launch_q4_shape<kTypeF16>(dev, info.sm_count, p, s)
-                              : launch_q4_shape<kTypeBF16>(dev, info.sm_count, p, s);
+  return type == TLG_TYPE_F16 ? launch_q4_shape<kTypeF16>(dev, p, s)
+                              : launch_q4_shape<kTypeBF16>(dev, p, s);
 }
 
 }  // extern "C"
