@@ -3,9 +3,9 @@
 //   C = act(X . W^T + bias) + residual,  W[n, k] = (q[n, k] - z[n, k / group]) s[n, k / group]
 //
 // Reading the weights (half a byte each) is all the work there is for one token, so the kernel is built
-// around a stream of weights: a CTA takes 16 R rows of W, its eight warps share K in units of 128, and
-// each warp copies its units (64 bytes of a row) asynchronously into a ring of its own, without any
-// barrier between warps until their sums are added at the end.
+// around a stream of weights: a CTA takes a block of W's rows, its eight warps share K in units of 256
+// or 128, and TMA brings their units (128 or 64 bytes of a row, and the tokens' elements) into a ring of each
+// group of warps, without any barrier across the CTA until the groups' sums are added at the end.
 //
 // The products run on the tensor core (mma.sync m16n8k16, W's rows as its M, tokens as its N): eight
 // tokens at a time cost what one does, and the CUDA cores, which convert 4 bits to 16, have no time for
@@ -29,13 +29,14 @@
 #include "tlg.h"
 #include "tlg_mxgemm_kernel.cuh"
 #include "tlg_rows.cuh"
+#include "tlg_variants.cuh"
 
 namespace tlg {
 namespace {
 
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s per pipeline wait
 constexpr int kQ4Warps = 8;
-constexpr int kQ4Unit = 128;     // k of a unit
-constexpr int kQ4Panel = 128;    // groups whose scales are held in shared memory at a time
+constexpr int kQ4Panel = 64;     // groups whose scales are held in shared memory at a time
 
 struct Q4Params {
   const uint8_t *Q;
@@ -56,6 +57,13 @@ struct Q4Params {
   const void *R;     // C's type
   int64_t ldr;
 };
+
+// (v & mask) | magic in one instruction: both constants in registers.
+__device__ __forceinline__ uint32_t q4_place(uint32_t v, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(magic));
+  return r;
+}
 
 template <int T>
 __device__ __forceinline__ uint32_t q4_sub(uint32_t a, uint32_t b) {
@@ -85,154 +93,203 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   return v;
 }
 
-// Copies 16 bytes to shared memory asynchronously, only the first `size` of them read, zeros behind.
-__device__ __forceinline__ void q4_copy(uint32_t dst, const void *src, int size) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
-}
+// Shared memory of a CTA: WK rings of ST slots, each a unit of kRows rows of W and of 8 NT tokens (boxes of 64
+// elements), the panel's scales, and the barriers.  NT == 0: a single token, which all columns of the
+// products share.
+template <int NT, int R, int WK>
+struct Q4Plan {
+  static constexpr int kWR = kQ4Warps / WK;  // warps that share a ring
+  static constexpr int kRows = kWR * 16 * R;
+  static constexpr int kTokens = NT == 0 ? 1 : 8 * NT;
+  static constexpr int kBlocks = NT == 2 ? 4 : 8;  // of 32 k in a unit
+  static constexpr int kUnit = kBlocks * 32;
+  static constexpr int kStages = NT == 0 && R == 1 ? 4 : NT == 2 && WK == 4 ? 3 : 2;
+  static constexpr uint32_t kWRow = kBlocks * 16;
+  static constexpr uint32_t kWBytes = kRows * kWRow;
+  static constexpr uint32_t kXBox = NT * 1024;
+  static constexpr uint32_t kXBytes = NT == 0 ? kUnit * 2 : kBlocks / 2 * kXBox;
+  static constexpr uint32_t kXOffset = WK * kStages * kWBytes;
+  static constexpr uint32_t kScaleOffset = kXOffset + WK * kStages * kXBytes;
+  // Row stride of the scales, in words; odd, so that eight rows lie in different banks.
+  static constexpr uint32_t kScaleLd = kQ4Panel + 1;
+  static constexpr uint32_t kBarOffset = kScaleOffset + (kRows * kScaleLd * 4 + 7) / 8 * 8;
+  static constexpr uint32_t kDynamicBytes = kBarOffset + WK * kStages * 16 + 16;
+  static_assert(kWBytes % 1024 == 0 && (NT == 0 || kXBytes % 1024 == 0), "swizzled boxes are 1024-byte aligned");
+  static_assert(2 * (kDynamicBytes + 1024) <= 233472, "two CTAs to an SM");
+  static_assert(kXOffset >= WK * kRows * kTokens * 4, "the rings' sums fit them");
+};
 
-// Slots of a ring.
-template <int NT, int WK>
-constexpr int kQ4Stages = WK == kQ4Warps ? 8 : NT == 1 ? 6 : 5;
-
-// Bytes of a slot: a unit of WR * 16 R rows of W, 64 bytes of each, and of X's tokens, 256 of each.
-__host__ __device__ constexpr int q4_slot(int rows, int tokens) { return rows * 64 + tokens * 256; }
-// Row stride of the scales in shared memory, in words; odd, so that eight rows lie in different banks.
-__host__ __device__ constexpr int q4_scale_ld(int groups) { return (groups < kQ4Panel ? groups : kQ4Panel) | 1; }
-
-// NT: blocks of 8 tokens; R: blocks of 16 rows of W to a warp; WK: warps that share K, each group of
-// WR = 8 / WK warps with a ring of its own, in which X is shared; GC: blocks of 32 k that have one scale in a
-// unit (1, 2, 4).
+// NT: blocks of 8 tokens, 0 for one token; R: blocks of 16 rows of W to a warp; WK: groups of warps that
+// share K, each of kWR warps with a ring of its own; GC: blocks of 32 k that have one scale (1, 2, 4).
 template <int T, int NT, int R, int WK, int GC>
-__global__ void __launch_bounds__(32 * kQ4Warps) gemv_q4_kernel(const Q4Params p) {
-  constexpr int ST = kQ4Stages<NT, WK>;
-  constexpr int WR = kQ4Warps / WK;
-  constexpr int kRows = WR * 16 * R;  // of a CTA
+__global__ void __launch_bounds__(32 * kQ4Warps, 2)
+    gemv_q4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Q4Params p) {
+  using Plan = Q4Plan<NT, R, WK>;
+  constexpr int ST = Plan::kStages, WR = Plan::kWR, kRows = Plan::kRows, kUnit = Plan::kUnit;
+  constexpr int NC = NT == 0 ? 1 : NT;  // blocks of 8 columns
   constexpr uint32_t kMagic = T == kTypeF16 ? 0x64006400u : 0x43004300u;
-  extern __shared__ __align__(16) uint8_t q4_smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  extern __shared__ __align__(1024) uint8_t q4_smem[];
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int wr = warp % WR, wk = warp / WR;
   const int g = lane >> 2, t = lane & 3;
   const int tile = static_cast<int>(blockIdx.x) / p.token_blocks;
-  const int token0 = (static_cast<int>(blockIdx.x) - tile * p.token_blocks) * (8 * NT);
-  const int tokens = min(p.M - token0, 8 * NT);
+  const int token0 = (static_cast<int>(blockIdx.x) - tile * p.token_blocks) * Plan::kTokens;
+  const int tokens = min(p.M - token0, Plan::kTokens);
   const int n0 = tile * kRows;
-  const int slot_bytes = q4_slot(kRows, tokens);
-  const uint32_t ring = smem_u32(q4_smem) + static_cast<uint32_t>(wk * ST * slot_bytes);
-  const int scale_ld = q4_scale_ld(p.groups);
+  const uint32_t s0 = smem_u32(q4_smem);
+  auto w_slot = [&](int s) { return s0 + static_cast<uint32_t>(wk * ST + s) * Plan::kWBytes; };
+  auto x_slot = [&](int s) { return s0 + Plan::kXOffset + static_cast<uint32_t>(wk * ST + s) * Plan::kXBytes; };
+  auto full_bar = [&](int s) { return s0 + Plan::kBarOffset + static_cast<uint32_t>((wk * ST + s) * 16); };
+  auto empty_bar = [&](int s) { return full_bar(s) + 8u; };
   // a word for each row and group: the scale's bits low, the zero point high
-  uint32_t *scales = reinterpret_cast<uint32_t *>(q4_smem + WK * ST * slot_bytes);
+  uint32_t *scales = reinterpret_cast<uint32_t *>(q4_smem + Plan::kScaleOffset);
+  volatile uint32_t *abort_flag = reinterpret_cast<uint32_t *>(q4_smem + Plan::kDynamicBytes - 16);
+
+  if (lane == 0 && wr == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), WR);
+    }
+    if (warp == 0) *abort_flag = 0u;
+    fence_mbar_init();
+    if (p.K > 0) tma_prefetch_desc(&tmW);
+    if (p.K > 0 && p.x_vec) tma_prefetch_desc(&tmX);
+  }
+  __syncthreads();
   grid_dependency_wait();
   grid_launch_dependents();
 
-  const int blocks = (p.K + 31) / 32;  // of a row of W
-  // this lane's part of a unit of W: block t of rows g, g + 8, ..
-  const int row0 = n0 + wr * 16 * R + g;
-  const uint8_t *w_from = p.Q + row0 * p.ldq + t * 16;
-  auto issue = [&](int unit, int slot) {
-    const uint32_t w = ring + static_cast<uint32_t>(slot * slot_bytes + wr * 1024 * R), x = ring + static_cast<uint32_t>(slot * slot_bytes + kRows * 64);
-    const int k0 = unit * kQ4Unit;
-    // W: block c of row r at (c ^ r / 2 % 4) of the row's four places
-#pragma unroll
-    for (int i = 0; i < 2 * R; ++i) {
-      const int r = i * 8 + g;
-      const bool in = row0 + i * 8 < p.N && unit * 4 + t < blocks;
-      q4_copy(w + static_cast<uint32_t>(r * 64 + ((t ^ ((r >> 1) & 3)) * 16)),
-              in ? w_from + i * 8 * p.ldq + static_cast<int64_t>(unit) * 64 : p.Q, in ? 16 : 0);
-    }
-    // X: 8 elements of token m at (q ^ 4 (m % 2)) of its 16 places
-    for (int i = wr * 32 + lane; i < tokens * 16; i += WR * 32) {
-      const int m = i >> 4, q = i & 15, k = k0 + q * 8;
-      const uint32_t to = x + static_cast<uint32_t>(m * 256 + ((q ^ ((m & 1) << 2)) * 16));
-      const uint16_t *from = p.X + (token0 + m) * p.ldx + k;
-      const int left = min(max(p.K - k, 0), 8);
-      if (p.x_vec) {
-        q4_copy(to, left > 0 ? from : p.X, left * 2);
+  const int units = (p.K + kUnit - 1) / kUnit;
+  const int mine = units > wk ? (units - wk + WK - 1) / WK : 0;  // units wk, wk + WK, ..
+  // One lane of the group asks for its i-th unit; TMA fills with zeros what lies outside the matrices.
+  auto issue = [&](int i, int slot) {
+    const int k = (wk + i * WK) * kUnit;
+    const uint32_t bar = full_bar(slot);
+    mbar_arrive_expect_tx(bar, Plan::kWBytes + (p.x_vec ? Plan::kXBytes : 0u));
+    tma_load_2d(w_slot(slot), &tmW, bar, k / 2, n0);
+    if (p.x_vec) {
+      if constexpr (NT == 0) {
+        tma_load_2d(x_slot(slot), &tmX, bar, k, token0);
       } else {
-        uint32_t v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v[j] = ld_u16_pred(from + 2 * j, 2 * j < left) | ld_u16_pred(from + 2 * j + 1, 2 * j + 1 < left) << 16;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                     : "memory");
+        for (int b = 0; b < Plan::kBlocks / 2; ++b)
+          tma_load_2d(x_slot(slot) + b * Plan::kXBox, &tmX, bar, k + b * 64, token0);
       }
     }
   };
+  const bool issuer = wr == 0 && lane == 0;
+  if (issuer) {
+    for (int i = 0; i < min(ST, mine); ++i) issue(i, i);
+  }
+  // Without TMA (X at odd places): the group's lanes write the unit's X as TMA would have.
+  auto fill_x = [&](int i, int slot) {
+    constexpr int kPieces = kUnit / 8;  // of 16 bytes, of a token
+    const uint32_t x = x_slot(slot);
+    const int k0 = (wk + i * WK) * kUnit;
+#pragma unroll 2
+    for (int e = wr * 32 + lane; e < Plan::kTokens * kPieces; e += WR * 32) {
+      const int m = e / kPieces, q = e % kPieces, k = k0 + q * 8;
+      const uint16_t *from = p.X + static_cast<int64_t>(token0 + m) * p.ldx + k;
+      const int left = m < tokens ? min(max(p.K - k, 0), 8) : 0;
+      uint32_t v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = ld_u16_pred(from + 2 * j, 2 * j < left) | ld_u16_pred(from + 2 * j + 1, 2 * j + 1 < left) << 16;
+      const uint32_t to = NT == 0 ? x + q * 16
+                                  : x + (q >> 3) * Plan::kXBox + static_cast<uint32_t>(m * 128 + (((q & 7) ^ (m & 7)) * 16));
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                   : "memory");
+    }
+  };
+  auto group_sync = [&]() {
+    if constexpr (WR == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + wk), "n"(WR * 32) : "memory");
+  };
 
-  float total[R][NT][4];
+  // What a lane reads of a slot: word t of block c of W's rows g, g + 8, .., and 8 elements of block c of a
+  // token; the block's place is an exclusive-or of address bits (the boxes' swizzle).  Column g of the
+  // products is token 4 (g % 2) + g / 2: the two tokens of a quarter-warp then lie in different banks.
+  const int col_token = 4 * (g & 1) + (g >> 1);
+  const uint32_t w_at = static_cast<uint32_t>((wr * 16 * R + g) * Plan::kWRow + (Plan::kBlocks == 8 ? g : (g >> 1) & 3) * 16 + t * 4);
+  const uint32_t x_at = NT == 0 ? t * 16 : static_cast<uint32_t>(col_token * 128 + (t ^ col_token) * 16);
+
+  float total[R][NC][4];
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NC; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) total[r][n][j] = 0.0f;
 
-  const int units = (p.K + kQ4Unit - 1) / kQ4Unit;
-  const int panel_units = max(1, static_cast<int>(std::min<int64_t>(int64_t(kQ4Panel) << p.group_log2, int64_t(1) << 30) / kQ4Unit));
+  const int panel_units = max(1, static_cast<int>(std::min<int64_t>(int64_t(kQ4Panel) << p.group_log2, int64_t(1) << 30) / kUnit));
+  // opaque, so that they stay in registers
+  uint32_t mask = 0x000f000fu, magic = kMagic;
+  asm volatile("" : "+r"(mask), "+r"(magic));
+  bool ok = true;
+  int slot = 0, i = 0;
+  uint32_t phase = 0;
   for (int u0 = 0; u0 < units; u0 += panel_units) {
     const int u1 = min(units, u0 + panel_units);
-    const int first_group = static_cast<int>((static_cast<int64_t>(u0) * kQ4Unit) >> p.group_log2);
+    const int first_group = static_cast<int>((static_cast<int64_t>(u0) * kUnit) >> p.group_log2);
     if (u0 > 0) __syncthreads();  // the last panel's scales are read
-#pragma unroll
-    for (int s = 0; s < ST - 1; ++s) {
-      const int u = u0 + wk + s * WK;
-      if (u < u1) issue(u, s);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    // scales and zero points of the panel, 0 past the last row: a warp takes 2 WR R rows, all loads of 32
-    // groups in flight at once
+    // scales and zero points of the panel, 0 past the last row: a warp takes an eighth of the rows, all
+    // loads of 32 groups in flight at once
     const int held = min(p.groups - first_group, kQ4Panel);
     for (int j = lane; j < held; j += 32) {
       constexpr int kMine = kRows / kQ4Warps;
       uint32_t v[kMine], z[kMine];
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int n = n0 + warp * kMine + i;
+      for (int r = 0; r < kMine; ++r) {
+        const int n = n0 + warp * kMine + r;
         const int64_t at = static_cast<int64_t>(n) * p.groups + first_group + j;
-        v[i] = n < p.N ? p.S[at] : 0u;
-        z[i] = n < p.N && p.Z != nullptr ? p.Z[at] : 8u;
+        v[r] = n < p.N ? p.S[at] : 0u;
+        z[r] = n < p.N && p.Z != nullptr ? p.Z[at] : 8u;
       }
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) scales[(warp * kMine + i) * scale_ld + j] = v[i] | (z[i] & 15u) << 16;
+      for (int r = 0; r < kMine; ++r) scales[(warp * kMine + r) * Plan::kScaleLd + j] = v[r] | (z[r] & 15u) << 16;
     }
     __syncthreads();
-    int slot = 0;
-    for (int first = u0; first < u1; first += WK) {  // the warps that share a ring go through it together
-      const int u = first + wk;
-      asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
-      // every copy into this slot has landed, and the slot before is read
-      if constexpr (WR > 1)
-        __syncthreads();
-      else
-        __syncwarp();
-      const int ahead = u + (ST - 1) * WK;
-      if (ahead < u1) issue(ahead, slot == 0 ? ST - 1 : slot - 1);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (u >= u1) break;
-      const uint32_t w = ring + static_cast<uint32_t>(slot * slot_bytes + wr * 1024 * R), x = ring + static_cast<uint32_t>(slot * slot_bytes + kRows * 64);
-      float acc[R][NT][4];
+    for (; ok && wk + i * WK < u1; ++i) {
+      const int u = wk + i * WK;
+      // Refills the slot of the unit before this one, which the group has had time to leave.
+      if (issuer && i > 0 && i - 1 + ST < mine) {
+        const int last = slot == 0 ? ST - 1 : slot - 1;
+        const uint32_t last_phase = slot == 0 ? phase ^ 1u : phase;
+        ok = mbar_wait(empty_bar(last), last_phase, abort_flag, kWaitLimitNs, kRoleProducer, &g_device_error);
+        if (ok) issue(i - 1 + ST, last);
+      }
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(full_bar(slot), phase, abort_flag, kWaitLimitNs, kRoleMma, &g_device_error));
+      if (!ok) break;
+      if (!p.x_vec) {
+        fill_x(i, slot);
+        group_sync();
+      }
+      const uint32_t w = w_slot(slot) + w_at, x = x_slot(slot) + x_at;
+      float acc[R][NC][4];
       uint32_t zero[R][2];
       float scale[R][2];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < Plan::kBlocks; ++c) {
         if (c % GC == 0) {
-          const int j = static_cast<int>((static_cast<int64_t>(u) * kQ4Unit + c * 32) >> p.group_log2) - first_group;
-          const uint32_t *s = scales + wr * 16 * R * scale_ld + min(j, held - 1);  // blocks past K have no group; their X is 0
+          const int j = ((u * kUnit + c * 32) >> p.group_log2) - first_group;
+          const uint32_t *s = scales + wr * 16 * R * Plan::kScaleLd + min(j, held - 1);  // blocks past K have no group; their X is 0
 #pragma unroll
           for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t v = s[(r * 16 + h * 8 + g) * scale_ld];
+              const uint32_t v = s[(r * 16 + h * 8 + g) * Plan::kScaleLd];
               zero[r][h] = kMagic + (v >> 16) * 0x10001u;
               float none;
               unpack2<T>(v, scale[r][h], none);
             }
         }
-        uint32_t b[NT][4];
+        uint32_t b[NC][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int m = n * 8 + g;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (m < tokens) v = ld_shared_v4(x + static_cast<uint32_t>(m * 256 + (((c * 4 + t) ^ ((m & 1) << 2)) * 16)));
+        for (int n = 0; n < NC; ++n) {
+          const uint4 v = ld_shared_v4(NT == 0 ? x + c * 64 : (x ^ ((c & 1) * 64)) + (c >> 1) * Plan::kXBox + n * 1024);
           b[n][0] = __byte_perm(v.x, v.z, 0x5410);  // elements 0 and 4
           b[n][1] = __byte_perm(v.x, v.z, 0x7632);  // 1 and 5
           b[n][2] = __byte_perm(v.y, v.w, 0x5410);  // 2 and 6
@@ -243,13 +300,12 @@ __global__ void __launch_bounds__(32 * kQ4Warps) gemv_q4_kernel(const Q4Params p
           uint32_t a[2][4];  // [half of the block][operand register]
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int row = r * 16 + h * 8 + g;
-            const uint32_t v = ld_shared_u32(w + static_cast<uint32_t>(row * 64 + ((c ^ ((row >> 1) & 3)) * 16) + t * 4));
+            const uint32_t v = ld_shared_u32((w ^ (c * 16)) + (r * 16 + h * 8) * Plan::kWRow);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i >> 1][h + 2 * (i & 1)] = q4_sub<T>(((v >> (4 * i)) & 0x000f000fu) | kMagic, zero[r][h]);
+            for (int i = 0; i < 4; ++i) a[i >> 1][h + 2 * (i & 1)] = q4_sub<T>(q4_place(v >> (4 * i), mask, magic), zero[r][h]);
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+          for (int n = 0; n < NC; ++n) {
             const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             if (c % GC == 0)
               q4_mma<T>(acc[r][n], a[0], b[n][0], b[n][1], none);
@@ -260,19 +316,31 @@ __global__ void __launch_bounds__(32 * kQ4Warps) gemv_q4_kernel(const Q4Params p
           if (c % GC == GC - 1) {
             const float s0 = scale[r][0], s1 = scale[r][1];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              total[r][n][0] = fmaf(s0, acc[r][n][0], total[r][n][0]);
-              total[r][n][1] = fmaf(s0, acc[r][n][1], total[r][n][1]);
-              total[r][n][2] = fmaf(s1, acc[r][n][2], total[r][n][2]);
-              total[r][n][3] = fmaf(s1, acc[r][n][3], total[r][n][3]);
+            for (int n = 0; n < NC; ++n) {
+              float(&a)[4] = acc[r][n], (&d)[4] = total[r][n];
+              f2_unpack(f2_fma(f2_splat(s0), f2_pack(a[0], a[1]), f2_pack(d[0], d[1])), d[0], d[1]);
+              f2_unpack(f2_fma(f2_splat(s1), f2_pack(a[2], a[3]), f2_pack(d[2], d[3])), d[2], d[3]);
             }
           }
         }
       }
-      slot = slot == ST - 1 ? 0 : slot + 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty_bar(slot));
+      if (++slot == ST) {
+        slot = 0;
+        phase ^= 1u;
+      }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncwarp();
+  }
+  // After a wait that ran out: what was asked for lands before shared memory goes away.
+  if (!ok && issuer) {
+    for (int e = 0; e < ST && i + e < mine; ++e) {
+      mbar_wait(full_bar(slot), phase, nullptr, kWaitLimitNs, kRoleProducer, &g_device_error);
+      if (++slot == ST) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
   }
 
   // The sums of the warps that share K, added in order: [wk][token][row], in the rings' place.
@@ -281,10 +349,11 @@ __global__ void __launch_bounds__(32 * kQ4Warps) gemv_q4_kernel(const Q4Params p
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NC; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int m = n * 8 + t * 2 + (j & 1), row = wr * 16 * R + r * 16 + g + (j >> 1) * 8;
+        const int col = t * 2 + (j & 1);
+        const int m = NT == 0 ? col : n * 8 + 4 * (col & 1) + (col >> 1), row = wr * 16 * R + r * 16 + g + (j >> 1) * 8;
         if (m < tokens) sums[(wk * tokens + m) * kRows + row] = total[r][n][j];
       }
   __syncthreads();
@@ -312,38 +381,47 @@ __global__ void __launch_bounds__(32 * kQ4Warps) gemv_q4_kernel(const Q4Params p
 
 template <int T, int NT, int R, int WK, int GC>
 tlg_status launch_q4(int dev, Q4Params p, cudaStream_t s) {
+  using Plan = Q4Plan<NT, R, WK>;
   constexpr auto kernel = gemv_q4_kernel<T, NT, R, WK, GC>;
-  constexpr int kRows = kQ4Warps / WK * 16 * R, kStages = kQ4Stages<NT, WK>;
-  constexpr int kMost = WK * kStages * q4_slot(kRows, 8 * NT) + kRows * q4_scale_ld(kQ4Panel) * 4;
-  static_assert(kMost <= 232448, "shared memory per CTA exceeded");
-  static_assert(kStages * q4_slot(kRows, 1) >= kRows * 4, "a slice's sums of a token fit its ring");
   static bool ready[kMaxDevices];
   static std::mutex mutex;
   {
     std::lock_guard<std::mutex> lock(mutex);
     if (!ready[dev]) {
-      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan::kDynamicBytes) != cudaSuccess) {
         cudaGetLastError();
         return TLG_ERR_CUDA;
       }
       ready[dev] = true;
     }
   }
-  const int tokens = std::min(p.M, 8 * NT);
-  p.token_blocks = (p.M + 8 * NT - 1) / (8 * NT);
-  const int64_t tiles = (p.N + kRows - 1) / kRows;
+  p.token_blocks = (p.M + Plan::kTokens - 1) / Plan::kTokens;
+  const int64_t tiles = (p.N + Plan::kRows - 1) / Plan::kRows;
   if (tiles * p.token_blocks > kMaxExtent) return TLG_ERR_UNSUPPORTED;
+  CUtensorMap w = {}, x = {};
+  if (p.K > 0) {
+    const uint64_t row = static_cast<uint64_t>(row_bytes(TLG_MX_E2M1, p.K));
+    if (!encode_2d(&w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.Q, row, static_cast<uint64_t>(p.N),
+                   p.N > 1 ? static_cast<uint64_t>(p.ldq) : row, Plan::kWRow, Plan::kRows,
+                   Plan::kBlocks == 8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+      return TLG_ERR_CUDA;
+    if (p.x_vec && !encode_2d(&x, T == kTypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.X,
+                              static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.M),
+                              static_cast<uint64_t>(p.M > 1 ? p.ldx : (int64_t(p.K) + 7) / 8 * 8) * 2, NT == 0 ? Plan::kUnit : 64,
+                              Plan::kTokens, NT == 0 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
+      return TLG_ERR_CUDA;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.token_blocks));
   cfg.blockDim = dim3(32 * kQ4Warps);
-  cfg.dynamicSmemBytes = WK * kStages * q4_slot(kRows, tokens) + kRows * q4_scale_ld(p.groups) * 4;
+  cfg.dynamicSmemBytes = Plan::kDynamicBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, w, x, p) != cudaSuccess) {
     cudaGetLastError();
     return TLG_ERR_CUDA;
   }
@@ -358,13 +436,16 @@ tlg_status launch_q4_group(int dev, const Q4Params &p, cudaStream_t s) {
 }
 
 template <int T>
-tlg_status launch_q4_shape(int dev, const Q4Params &p, cudaStream_t s) {
-  if (p.M > 8) return launch_q4_group<T, 2, 1, 2>(dev, p, s);
-  if (p.M > 2) return launch_q4_group<T, 1, 1, 2>(dev, p, s);
-  return launch_q4_group<T, 1, 1, 8>(dev, p, s);
+tlg_status launch_q4_shape(int dev, int sms, const Q4Params &p, cudaStream_t s) {
+  if (p.M == 1) return p.N >= 64 * sms ? launch_q4_group<T, 0, 2, 8>(dev, p, s) : launch_q4_group<T, 0, 1, 8>(dev, p, s);
+  if (p.M <= 8) return p.N >= 64 * sms ? launch_q4_group<T, 1, 2, 4>(dev, p, s) : launch_q4_group<T, 1, 1, 8>(dev, p, s);
+  return p.N >= 64 * sms ? launch_q4_group<T, 2, 2, 4>(dev, p, s) : launch_q4_group<T, 2, 1, 8>(dev, p, s);
 }
 
 }  // namespace
+
+TLG_DEFINE_ERROR_WORD_READER(error_word_gemv)
+
 }  // namespace tlg
 
 using namespace tlg;
@@ -436,8 +517,8 @@ tlg_status tlg_gemv_q4(int64_t M, int64_t N, int64_t K, tlg_type type, const voi
   p.R = e.residual;
   p.ldr = e.ldr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return type == TLG_TYPE_F16 ? launch_q4_shape<kTypeF16>(dev, p, s)
-                              : launch_q4_shape<kTypeBF16>(dev, p, s);
+  return type == TLG_TYPE_F16 ? launch_q4_shape<kTypeF16>(dev, info.sm_count, p, s)
+                              : launch_q4_shape<kTypeBF16>(dev, info.sm_count, p, s);
 }
 
 }  // extern "C"

@@ -175,6 +175,7 @@ tlg_status error_word_tn(bool clear, uint32_t *out);
 tlg_status error_word_tt(bool clear, uint32_t *out);
 tlg_status error_word_mxgemm(bool clear, uint32_t *out);  // tlg_mxgemm.cu
 tlg_status error_word_grouped(bool clear, uint32_t *out);  // tlg_grouped.cu
+tlg_status error_word_gemv(bool clear, uint32_t *out);     // tlg_gemv_q4.cu
 
 #define TLG_DEFINE_ERROR_WORD_READER(NAME)                                            \
   tlg_status NAME(bool clear, uint32_t *out) {                                        \
