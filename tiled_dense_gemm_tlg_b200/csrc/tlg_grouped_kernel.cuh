@@ -163,6 +163,21 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// As tmem_load_32cols, for 16 columns.
+__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
 // Instruction descriptor as make_idesc_f16, for fp16 or bf16 operands (format 1) and without its N.
 template <int TYPE>
 __device__ __forceinline__ constexpr uint32_t grouped_idesc(int m, bool a_mn, bool b_mn) {
@@ -308,7 +323,11 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(misc);
   const int tiles = start[p.groups];
   int g0 = 0;
-  auto tile_at = [&](int t) { return grouped_tile<KIND, CG, BN>(p, start, begin, size, t, g0, lane); };
+  auto tile_at = [&](int t) {
+    GroupedTile w = grouped_tile<KIND, CG, BN>(p, start, begin, size, t, g0, lane);
+    for (int *x : {&w.g, &w.lane0, &w.col0, &w.cols, &w.n, &w.k0, &w.k}) *x = __shfl_sync(0xffffffffu, *x, 0);
+    return w;
+  };
 
   if (!LSU && warp == 0) {
     // ---------------------------------------------------------------- producer (every CTA)
@@ -573,27 +592,38 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
           mbar_arrive(release_bar0 + 8u * (j & 1u));
       }
     };
-    auto load_piece = [&](int i, uint32_t(&r)[32]) {
-      __syncwarp();
-      tmem_load_32cols(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (j & 1u) * BN +
-                           static_cast<uint32_t>(i * 32),
-                       r);
+    auto piece_at = [&](int i) {
+      return tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (j & 1u) * BN + static_cast<uint32_t>(i * 32);
     };
     for (int t = unit; t < tiles && ok; t += num_units) {
       const GroupedTile w = tile_at(t);
       const int num_kb = ceil_div(w.k, kBK);
       const uint64_t limit = p.limit_ns + static_cast<uint64_t>(num_kb) * kWaitPerKBlockNs;
-      const int at = w.lane0 + static_cast<int>(rank) * kBM + quarter * 32 + lane;  // column of C or dB
+      const unsigned at = static_cast<unsigned>(w.lane0 + static_cast<int>(rank) * kBM + quarter * 32 + lane);  // column of C or dB
       const int pieces = ceil_div(w.cols, 32);
-      auto store_piece = [&](int i, float(&v)[32]) {
-        if constexpr (!kDw) activate_lane<OUT, 32>(p.act, v);
-        if (at < p.lanes) {
+      // Piece i, 32 fp32 values or pairs of 16-bit ones.
+      auto store_piece = [&](int i, auto &v) {
+        if (at < static_cast<unsigned>(p.lanes)) {
+          // The row's address is the same in every lane (and known to be): it stays out of the lanes' registers.
           const int left = w.cols - i * 32;
-          int64_t to = static_cast<int64_t>(w.col0 + i * 32) * p.ldc + at;
-          if constexpr (kDw) to += w.g * p.stride_c;
+          int64_t row = static_cast<int64_t>(w.col0 + i * 32) * p.ldc;
+          if constexpr (kDw) row += w.g * p.stride_c;
+          char *to = static_cast<char *>(p.C) + row * kTypeBytes<OUT>;
+          const int64_t step = p.ldc * kTypeBytes<OUT>;
+          auto put = [&](int c, char *row) {
+            if constexpr (OUT == kTypeF32)
+              reinterpret_cast<float *>(row)[at] = v[c];
+            else
+              reinterpret_cast<uint16_t *>(row)[at] = static_cast<uint16_t>(v[c / 2] >> (16 * (c & 1)));
+          };
+          if (left >= 32) {  // without a bound for each (K = 64, 16-bit C: 2.8 us a 256 x 256 tile, 5 with)
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c < left) store_elem<OUT>(p.C, to + c * p.ldc, v[c]);
+            for (int c = 0; c < 32; ++c, to += step) put(c, to);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c, to += step)
+              if (c < left) put(c, to);
+          }
         }
       };
       if constexpr (kSpans) {
@@ -610,11 +640,15 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
           for (int m = 0; m < kMine; ++m) {
             const int i = side + m * kSides;
             if (i < pieces && num_kb > 0) {
-              uint32_t r[32];
-              load_piece(i, r);
 #pragma unroll
-              for (int c = 0; c < 32; c += 2)
-                f2_add_to(sum[m][c], sum[m][c + 1], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+              for (int h = 0; h < 32; h += 16) {
+                uint32_t r[16];
+                __syncwarp();
+                tmem_load_16cols(piece_at(i) + h, r);
+#pragma unroll
+                for (int c = 0; c < 16; c += 2)
+                  f2_add_to(sum[m][h + c], sum[m][h + c + 1], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+              }
             }
           }
           release();
@@ -623,22 +657,36 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
         } while (kb < num_kb);
         if (!ok) break;
 #pragma unroll
-        for (int m = 0; m < kMine; ++m)
-          if (side + m * kSides < pieces) store_piece(side + m * kSides, sum[m]);
+        for (int m = 0; m < kMine; ++m) {
+          if (side + m * kSides < pieces) {
+            if constexpr (!kDw) activate_lane<OUT, 32>(p.act, sum[m]);
+            store_piece(side + m * kSides, sum[m]);
+          }
+        }
       } else {
         wait_full(limit);
         if (!ok) break;
-        if (side >= pieces) release();
-#pragma unroll 1
-        for (int i = side; i < pieces; i += kSides) {
-          uint32_t r[32];
-          load_piece(i, r);
-          if (i + kSides >= pieces) release();
-          float v[32];
+        // All pieces are read, and rounded, before any is stored: the MMAs get the accumulator back sooner.
+        uint32_t packed[kMine][16];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) v[c] = w.k > 0 ? __uint_as_float(r[c]) : 0.0f;  // the empty sum
-          store_piece(i, v);
+        for (int m = 0; m < kMine; ++m) {
+          const int i = side + m * kSides;
+          if (i < pieces) {
+            uint32_t r[32];
+            __syncwarp();
+            tmem_load_32cols(piece_at(i), r);
+            float v[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = w.k > 0 ? __uint_as_float(r[c]) : 0.0f;  // the empty sum
+            if constexpr (!kDw) activate_lane<OUT, 32>(p.act, v);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) packed[m][c] = pack2<OUT>(v[2 * c], v[2 * c + 1]);
+          }
         }
+        release();
+#pragma unroll
+        for (int m = 0; m < kMine; ++m)
+          if (side + m * kSides < pieces) store_piece(side + m * kSides, packed[m]);
         ++j;
       }
     }
