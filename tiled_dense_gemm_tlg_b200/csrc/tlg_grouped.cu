@@ -31,7 +31,7 @@ struct GroupedVariant {
   static void fill(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int ctas, cudaStream_t s) {
     *cfg = {};
     cfg->gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg->blockDim = dim3(GroupedRoles<OUT, LSU>::kThreads);
+    cfg->blockDim = dim3(GroupedRoles<OUT, BN, LSU>::kThreads);
     cfg->dynamicSmemBytes = Plan::kDynamicBytes;
     cfg->stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -60,7 +60,7 @@ struct GroupedVariant {
           cudaGetLastError();
           return TLG_ERR_CUDA;
         }
-        st.units = sms;
+        st.units = sms * Plan::kCtasPerSm;
         if (CG > 1) {
           fill(&cfg, attr, CG * (sms / CG), nullptr);
           if (cudaOccupancyMaxActiveClusters(&st.units, kKernel, &cfg) != cudaSuccess || st.units < 1) {
@@ -184,6 +184,7 @@ tlg_status tlg_gemm_grouped(int64_t rows, int64_t N, int64_t K, int32_t groups, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   GroupedMaps m;
   const int64_t tlda = tma_ld(rows, K, lda), tldb = tma_ld(b_rows, b_cols, ldb);
+  const bool wide = rows > int64_t(groups) * 48;
   const bool tma = K > 0 && tma_ok(A, tlda) && tma_ok(B, tldb) && p.stride_w % 8 == 0;
   if (tma) {
     const CUtensorMapDataType ty =
@@ -192,11 +193,10 @@ tlg_status tlg_gemm_grouped(int64_t rows, int64_t N, int64_t K, int32_t groups, 
     const uint64_t mat_bytes = static_cast<uint64_t>(p.shared_w ? tldb : stride_b) * 2;
     if (!encode_3d(&m.w, ty, B, static_cast<uint64_t>(b_cols), static_cast<uint64_t>(b_rows), mats,
                    static_cast<uint64_t>(tldb) * 2, mat_bytes, 64, t ? 128 : 64) ||
-        !encode_2d(&m.x, ty, A, static_cast<uint64_t>(K), static_cast<uint64_t>(rows), static_cast<uint64_t>(tlda) * 2, 64, 32) ||
+        !encode_2d(&m.x, ty, A, static_cast<uint64_t>(K), static_cast<uint64_t>(rows), static_cast<uint64_t>(tlda) * 2, 64, wide ? 32 : 16) ||
         !encode_2d(&m.x128, ty, A, static_cast<uint64_t>(K), static_cast<uint64_t>(rows), static_cast<uint64_t>(tlda) * 2, 64, 128))
       return TLG_ERR_CUDA;
   }
-  const bool wide = rows > int64_t(groups) * 48;
   return with_types(type, out, [&](auto TY, auto OU) {
     constexpr int kTy = decltype(TY)::value, kOu = decltype(OU)::value;
     auto run = [&](auto kind) {
@@ -205,7 +205,7 @@ tlg_status tlg_gemm_grouped(int64_t rows, int64_t N, int64_t K, int32_t groups, 
         return GroupedVariant<kKind, 1, 128, 6, kTy, kOu, true>::launch(dev, info.sm_count, most(128, 128), m, p, s);
       if (wide)
         return GroupedVariant<kKind, 2, 256, 6, kTy, kOu, false>::launch(dev, info.sm_count, most(256, 256), m, p, s);
-      return GroupedVariant<kKind, 1, 64, 8, kTy, kOu, false>::launch(dev, info.sm_count, most(64, 128), m, p, s);
+      return GroupedVariant<kKind, 1, 64, 4, kTy, kOu, false>::launch(dev, info.sm_count, most(64, 128), m, p, s);
     };
     return t ? run(std::integral_constant<int, kGroupedT>()) : run(std::integral_constant<int, kGroupedN>());
   });

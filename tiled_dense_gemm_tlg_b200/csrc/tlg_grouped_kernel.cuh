@@ -12,9 +12,11 @@
 // a group is a bound on the columns of TMEM: rows behind a group's last are never written.
 // In the gradient the lanes are the contiguous index of dB, its other index the MMA's N.
 //
-// Sizes of the groups live on the device.  Every CTA turns them into a table of tiles in shared
+// Sizes of the groups live on the device.  Every CTA turns them into a table of first tiles in shared
 // memory (two warp scans), and the persistent work units (a CTA, or a CTA pair) walk the list of all
-// tiles with the stride of their number.
+// tiles with the stride of their number.  Finding a tile's group and place takes half a microsecond
+// (divisions, shared memory), which the MMA warp would spend between two tiles, so the warps work out the
+// unit's first kGroupedListed tiles together before the roles begin.
 //
 //   warp 0      TMA producer: a ring of slots of one k-block (64 elements) of both operands
 //   warp 1      MMA issuer (the pair's leader), owner of the TMEM allocation
@@ -37,12 +39,13 @@ namespace tlg {
 constexpr int kGroupedN = 0, kGroupedT = 1, kGroupedDw = 2;  // B stored K x N, N x K; the gradient of B
 constexpr int kGroupedMax = 1024;  // groups
 constexpr int kGroupedEpiWarp = 4;
+constexpr int kGroupedListed = 64;  // tiles of a unit worked out in advance
 constexpr int kGroupedSpan = 8;    // k-blocks summed in TMEM for an fp32 output
 
-// Warps by the type of the output: fp32 sums of 64 columns to a thread leave no room for 128.
-template <int OUT, bool LSU>
+// Warps by the type of the output: a thread has room for the fp32 sums of 64 columns, not of 128.
+template <int OUT, int BN, bool LSU>
 struct GroupedRoles {
-  static constexpr int kEpiWarps = OUT == kTypeF32 ? 16 : 8;
+  static constexpr int kEpiWarps = OUT == kTypeF32 && BN > 64 ? 16 : 8;
   static constexpr int kLoader = kGroupedEpiWarp + kEpiWarps;
   static constexpr int kThreads = 32 * (kLoader + (LSU ? kLoaderWarps : 0));
 };
@@ -78,14 +81,18 @@ struct GroupedPlan {
   static constexpr uint32_t kBeginOffset = kStartOffset + (kGroupedMax + 1) * 4;  // first row
   static constexpr uint32_t kSizeOffset = kBeginOffset + kGroupedMax * 4;         // rows
   static constexpr uint32_t kSumOffset = kSizeOffset + kGroupedMax * 4;           // tiles of 32 groups
-  static constexpr uint32_t kDynamicBytes = kSumOffset + kGroupedMax / 32 * 4 + 1024;
+  static constexpr uint32_t kListOffset = (kSumOffset + kGroupedMax / 32 * 4 + 15) / 16 * 16;  // the unit's first tiles
+  static constexpr uint32_t kDynamicBytes = kListOffset + kGroupedListed * 32 + 1024;
   static constexpr uint32_t kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
+  static constexpr int kXRows = BN == 64 ? 16 : 32;  // tokens of a small box
+  static constexpr int kCtasPerSm = BN == 64 ? 2 : 1;
+  static_assert(kCtasPerSm * (kDynamicBytes + 1024) <= 233472, "CTAs of an SM");
   static_assert(kXBytes % 1024 == 0 && BN / CG % 32 == 0 && kTmemCols <= 512, "operand tiles and accumulators");
   static_assert(kDynamicBytes <= 232448, "shared memory per CTA exceeded");
 };
 
 // What a tile computes: TMEM lanes [lane0, +128 CG) by `cols` columns.
-struct GroupedTile {
+struct alignas(16) GroupedTile {
   int g;
   int lane0;
   int col0;  // forward: row of A (and C) of column 0; gradient: row of dB_g
@@ -93,7 +100,9 @@ struct GroupedTile {
   int n;     // columns of the MMA
   int k0;    // gradient: the group's first row
   int k;     // elements summed
+  int pad;
 };
+static_assert(sizeof(GroupedTile) == 32, "two 16-byte pieces");
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -213,11 +222,11 @@ __device__ __forceinline__ void grouped_fill(uint32_t dst, const uint16_t *base,
 }
 
 template <int KIND, int CG, int BN, int STAGES, int TYPE, int OUT, bool LSU>
-__global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
+__global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedPlan<CG, BN, STAGES>::kCtasPerSm)
     grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const __grid_constant__ CUtensorMap tmX128, const GroupedParams p) {
   using Plan = GroupedPlan<CG, BN, STAGES>;
-  using Roles = GroupedRoles<OUT, LSU>;
+  using Roles = GroupedRoles<OUT, BN, LSU>;
   constexpr bool kSpans = OUT == kTypeF32;
   constexpr bool kDw = KIND == kGroupedDw;
   constexpr bool kWmn = KIND != kGroupedT, kXmn = kDw;  // MN-major operands
@@ -313,6 +322,14 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
     }
     if (threadIdx.x == 0) start[0] = 0;
   }
+  __syncthreads();
+  const int tiles = __shfl_sync(0xffffffffu, start[p.groups], 0);
+  GroupedTile *list = reinterpret_cast<GroupedTile *>(smem + Plan::kListOffset);
+  int g0 = 0;
+  for (int i = warp; i < kGroupedListed && unit + i * num_units < tiles; i += num_warps) {
+    const GroupedTile w = grouped_tile<KIND, CG, BN>(p, start, begin, size, unit + i * num_units, g0, lane);
+    if (lane == 0) list[i] = w;
+  }
   tc_fence_before_sync();
   __syncwarp();
   if constexpr (CG == 2)
@@ -321,13 +338,15 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
     __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(misc);
-  const int tiles = start[p.groups];
-  int g0 = 0;
-  auto tile_at = [&](int t) {
-    GroupedTile w = grouped_tile<KIND, CG, BN>(p, start, begin, size, t, g0, lane);
+  g0 = 0;
+  // The unit's i-th tile, the same in every lane and known to be.
+  auto tile_at = [&](int i) {
+    GroupedTile w = i < kGroupedListed ? list[i]
+                                       : grouped_tile<KIND, CG, BN>(p, start, begin, size, unit + i * num_units, g0, lane);
     for (int *x : {&w.g, &w.lane0, &w.col0, &w.cols, &w.n, &w.k0, &w.k}) *x = __shfl_sync(0xffffffffu, *x, 0);
     return w;
   };
+  const int mine = unit < tiles ? (tiles - unit + num_units - 1) / num_units : 0;
 
   if (!LSU && warp == 0) {
     // ---------------------------------------------------------------- producer (every CTA)
@@ -336,14 +355,14 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
     uint32_t issued_mask = 0, issued_parity = 0;
     uint32_t tail_mask = 0, tail_parity = 0;  // tails issued, and the parity of each slot's next one
     bool ok = true;
-    for (int t = unit; t < tiles && ok; t += num_units) {
+    for (int t = 0; t < mine && ok; ++t) {
       const GroupedTile w = tile_at(t);
       const int num_kb = ceil_div(w.k, kBK);
       const int lane0 = w.lane0 + static_cast<int>(rank) * kBM;
       const int nh = w.n / CG;  // columns of the MMA held by this CTA
       const int x0 = w.col0 + static_cast<int>(rank) * nh;
-      const int boxes = ceil_div(nh, kDw ? 64 : 32);
-      const uint32_t bytes = Plan::kWBytes + static_cast<uint32_t>(boxes) * (kDw ? 8192u : 4096u);
+      const int boxes = ceil_div(nh, kDw ? 64 : Plan::kXRows);
+      const uint32_t bytes = Plan::kWBytes + static_cast<uint32_t>(boxes) * (kDw ? 8192u : Plan::kXRows * 128u);
       for (int kb = 0; kb < num_kb; ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait_spin(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns,
                                                     kRoleProducer, &g_device_error, 4096));
@@ -389,10 +408,10 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
               load3(w_slot(stage), lane0, k);
               load3(w_slot(stage) + 8192, lane0 + 64, k);
             }
-            if (nh % 128 == 0) {
+            if (BN >= 128 && nh % 128 == 0) {
               for (int c = 0; c < nh / 128; ++c) load(x_slot(stage) + c * 16384, &tmX128, k, x0 + c * 128);
             } else {
-              for (int c = 0; c < boxes; ++c) load(x_slot(stage) + c * 4096, &tmX, k, x0 + c * 32);
+              for (int c = 0; c < boxes; ++c) load(x_slot(stage) + c * (Plan::kXRows * 128), &tmX, k, x0 + c * Plan::kXRows);
             }
           }
         }
@@ -434,7 +453,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int t = unit; t < tiles && ok; t += num_units) {
+    for (int t = 0; t < mine && ok; ++t) {
       const GroupedTile w = tile_at(t);
       const int num_kb = ceil_div(w.k, kBK);
       const uint16_t *wp, *xp;
@@ -479,7 +498,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
     uint32_t phase = 0;
     uint32_t j = 0;  // accumulators handed over
     bool ok = true;
-    for (int t = unit; t < tiles && ok; t += num_units) {
+    for (int t = 0; t < mine && ok; ++t) {
       const GroupedTile w = tile_at(t);
       const int num_kb = ceil_div(w.k, kBK);
       const uint32_t idesc = idesc0 | (static_cast<uint32_t>(w.n >> 3) << 17);
@@ -539,7 +558,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
     int stage = 0;
     uint32_t parity = 0;  // of each slot's next tail
     bool ok = true;
-    for (int t = unit; t < tiles; t += num_units) {
+    for (int t = 0; t < mine; ++t) {
       const GroupedTile w = tile_at(t);
       const int num_kb = ceil_div(w.k, kBK), valid = w.k % kBK;
       const int last = (stage + num_kb + STAGES - 1) % STAGES;
@@ -595,7 +614,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, LSU>::kThreads, 1)
     auto piece_at = [&](int i) {
       return tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (j & 1u) * BN + static_cast<uint32_t>(i * 32);
     };
-    for (int t = unit; t < tiles && ok; t += num_units) {
+    for (int t = 0; t < mine && ok; ++t) {
       const GroupedTile w = tile_at(t);
       const int num_kb = ceil_div(w.k, kBK);
       const uint64_t limit = p.limit_ns + static_cast<uint64_t>(num_kb) * kWaitPerKBlockNs;
