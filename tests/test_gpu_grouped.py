@@ -119,6 +119,20 @@ def test_forward_any_alignment(tlg, sizes, lead, extra, op_b):
     assert c.guards_kept()
 
 
+@pytest.mark.parametrize("op_b", ["N", "T"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("sizes,k,n", [([1], 4096, 96), ([0, 1, 0], 2056, 300), ([3, 0, 2], 1088, 1000), ([20, 45, 0], 600, 130),
+                                       ([1, 1], 520, 4000), ([64, 65], 4000, 200)])
+def test_forward_few_rows_and_long_sums(tlg, sizes, k, n, out, op_b):
+    """Few tiles, whose sums several CTAs share."""
+    A, B = operands(16, sum(sizes), k, n, len(sizes), op_b, torch.bfloat16)
+    want, err = forward(A, B, sizes, 0, op_b, "silu")
+    c = Strided(torch.zeros((sum(sizes), n), dtype=TYPES[out]), 4, 4)
+    tlg.tlg_gemm_grouped(A.cuda(), B.cuda(), offsets_of(sizes).cuda(), op_b=op_b, activation="silu", C=c.view, out=out)
+    check(c.view, want, err, TYPES[out])
+    assert c.guards_kept()
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("typ,out", [("f16", "f16"), ("bf16", "f32"), ("bf16", "bf16")])
 def test_forward_activation(tlg, act, typ, out):

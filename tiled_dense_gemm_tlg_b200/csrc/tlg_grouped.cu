@@ -23,12 +23,12 @@ struct GroupedMaps {
   CUtensorMap w = {}, x = {}, x128 = {};
 };
 
-template <int KIND, int CG, int BN, int STAGES, int TYPE, int OUT, bool LSU>
+template <int KIND, int CG, int BN, int STAGES, int TYPE, int OUT, bool LSU, bool KSPLIT = false>
 struct GroupedVariant {
   using Plan = GroupedPlan<CG, BN, STAGES>;
-  static constexpr auto kKernel = grouped_kernel<KIND, CG, BN, STAGES, TYPE, OUT, LSU>;
+  static constexpr auto kKernel = grouped_kernel<KIND, CG, BN, STAGES, TYPE, OUT, LSU, KSPLIT>;
 
-  static void fill(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int ctas, cudaStream_t s) {
+  static void fill(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int ctas, int cluster, cudaStream_t s) {
     *cfg = {};
     cfg->gridDim = dim3(static_cast<unsigned>(ctas));
     cfg->blockDim = dim3(GroupedRoles<OUT, BN, LSU>::kThreads);
@@ -37,15 +37,16 @@ struct GroupedVariant {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg->attrs = attr;
-    cfg->numAttrs = CG > 1 ? 2 : 1;
+    cfg->numAttrs = cluster > 1 ? 2 : 1;
   }
 
+  // ks: CTAs that share a tile (KSPLIT).
   static tlg_status launch(int dev, int sms, int64_t most_tiles, const GroupedMaps &m, const GroupedParams &p,
-                           cudaStream_t s) {
+                           cudaStream_t s, int ks = 1) {
     static LaunchState state[kMaxDevices];
     static std::mutex mutex;
     int units;
@@ -62,7 +63,7 @@ struct GroupedVariant {
         }
         st.units = sms * Plan::kCtasPerSm;
         if (CG > 1) {
-          fill(&cfg, attr, CG * (sms / CG), nullptr);
+          fill(&cfg, attr, CG * (sms / CG), CG, nullptr);
           if (cudaOccupancyMaxActiveClusters(&st.units, kKernel, &cfg) != cudaSuccess || st.units < 1) {
             cudaGetLastError();
             return TLG_ERR_CUDA;
@@ -72,7 +73,10 @@ struct GroupedVariant {
       }
       units = st.units;
     }
-    fill(&cfg, attr, CG * static_cast<int>(std::min<int64_t>(units, most_tiles)), s);
+    if (KSPLIT)
+      fill(&cfg, attr, ks * static_cast<int>(most_tiles), ks, s);
+    else
+      fill(&cfg, attr, CG * static_cast<int>(std::min<int64_t>(units, most_tiles)), CG, s);
     if (cudaLaunchKernelEx(&cfg, kKernel, m.w, m.x, m.x128, p) != cudaSuccess) {
       cudaGetLastError();
       return TLG_ERR_CUDA;
@@ -205,6 +209,13 @@ tlg_status tlg_gemm_grouped(int64_t rows, int64_t N, int64_t K, int32_t groups, 
         return GroupedVariant<kKind, 1, 128, 6, kTy, kOu, true>::launch(dev, info.sm_count, most(128, 128), m, p, s);
       if (wide)
         return GroupedVariant<kKind, 2, 256, 6, kTy, kOu, false>::launch(dev, info.sm_count, most(256, 256), m, p, s);
+      // With few tiles each CTA's ring, 64 KB in flight, sets the pace (64 tiles of K = 4096: 23 us, 15.8 with
+      // four CTAs to a tile; its bytes take 10): more CTAs to a tile while two to an SM suffice and each has
+      // a ring's worth of k-blocks.
+      int ks = 1;
+      while (ks < 8 && most(64, 128) * ks * 2 <= 2 * int64_t(info.sm_count) && K >= int64_t(ks) * 2 * 4 * kBK) ks *= 2;
+      if (ks > 1)
+        return GroupedVariant<kKind, 1, 64, 4, kTy, kOu, false, true>::launch(dev, info.sm_count, most(64, 128), m, p, s, ks);
       return GroupedVariant<kKind, 1, 64, 4, kTy, kOu, false>::launch(dev, info.sm_count, most(64, 128), m, p, s);
     };
     return t ? run(std::integral_constant<int, kGroupedT>()) : run(std::integral_constant<int, kGroupedN>());

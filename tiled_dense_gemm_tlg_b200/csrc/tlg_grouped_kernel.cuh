@@ -221,7 +221,10 @@ __device__ __forceinline__ void grouped_fill(uint32_t dst, const uint16_t *base,
   }
 }
 
-template <int KIND, int CG, int BN, int STAGES, int TYPE, int OUT, bool LSU>
+// KSPLIT: a cluster of 2, 4 or 8 CTAs (its size) shares the K range of one tile, for calls with so few tiles
+// that most SMs would have none: a unit has one tile at most.  Each CTA adds the fp32 partial sums of its
+// part of the 128 lanes in slice order, received through distributed shared memory in the ring's place.
+template <int KIND, int CG, int BN, int STAGES, int TYPE, int OUT, bool LSU, bool KSPLIT>
 __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedPlan<CG, BN, STAGES>::kCtasPerSm)
     grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const __grid_constant__ CUtensorMap tmX128, const GroupedParams p) {
@@ -231,6 +234,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
   constexpr bool kDw = KIND == kGroupedDw;
   constexpr bool kWmn = KIND != kGroupedT, kXmn = kDw;  // MN-major operands
   static_assert(!LSU || CG == 1, "the plain-load path is built for one-CTA tiles");
+  static_assert(!KSPLIT || (CG == 1 && BN == 64 && !LSU && !kDw), "the K split is built for tiles of few rows");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -255,8 +259,15 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
   const int lane = threadIdx.x & 31;
   const uint32_t rank = (CG == 2) ? __shfl_sync(0xffffffffu, cluster_ctarank(), 0) : 0u;
   const bool leader = rank == 0;
-  const int unit = CG == 2 ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
-  const int num_units = CG == 2 ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+  constexpr bool kCluster = CG == 2 || KSPLIT;
+  const int unit = kCluster ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int num_units = kCluster ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+  const int ks = KSPLIT ? static_cast<int>(gridDim.x) / num_units : 1;
+  const int slice = KSPLIT ? __shfl_sync(0xffffffffu, static_cast<int>(cluster_ctarank()), 0) : 0;
+  // k-blocks of this CTA
+  auto kb_begin = [&](int num_kb) { return KSPLIT ? num_kb * slice / ks : 0; };
+  auto kb_end = [&](int num_kb) { return KSPLIT ? num_kb * (slice + 1) / ks : num_kb; };
+  float part[KSPLIT ? 32 : 1];  // partial sums of an epilogue warp's lane
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -332,7 +343,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
   }
   tc_fence_before_sync();
   __syncwarp();
-  if constexpr (CG == 2)
+  if constexpr (CG == 2)  // (the K split's CTAs meet later)
     cluster_sync_all();
   else
     __syncthreads();
@@ -363,7 +374,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
       const int x0 = w.col0 + static_cast<int>(rank) * nh;
       const int boxes = ceil_div(nh, kDw ? 64 : Plan::kXRows);
       const uint32_t bytes = Plan::kWBytes + static_cast<uint32_t>(boxes) * (kDw ? 8192u : Plan::kXRows * 128u);
-      for (int kb = 0; kb < num_kb; ++kb) {
+      for (int kb = kb_begin(num_kb); kb < kb_end(num_kb); ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait_spin(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns,
                                                     kRoleProducer, &g_device_error, 4096));
         if (!ok) break;
@@ -502,7 +513,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
       const GroupedTile w = tile_at(t);
       const int num_kb = ceil_div(w.k, kBK);
       const uint32_t idesc = idesc0 | (static_cast<uint32_t>(w.n >> 3) << 17);
-      int first = 0;  // k-block of this accumulator
+      int first = kb_begin(num_kb);  // k-block of this accumulator
       auto take = [&]() {
         ok = __all_sync(0xffffffffu, mbar_wait(tempty_bar(j & 1u), ((j >> 1) & 1u) ^ 1u, abort_flag, p.limit_ns,
                                                kRoleMma, &g_device_error));
@@ -515,7 +526,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
       };
       take();
       if (!ok) break;
-      for (int kb = 0; kb < num_kb; ++kb) {
+      for (int kb = first; kb < kb_end(num_kb); ++kb) {
         if (kSpans && kb - first == kGroupedSpan) {
           hand_over();
           first = kb;
@@ -651,7 +662,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
         for (int m = 0; m < kMine; ++m)
 #pragma unroll
           for (int c = 0; c < 32; ++c) sum[m][c] = 0.0f;  // the empty sum
-        int kb = 0;
+        int kb = kb_begin(num_kb);
         do {
           wait_full(limit);
           if (!ok) break;
@@ -673,8 +684,13 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
           release();
           ++j;
           kb += kGroupedSpan;
-        } while (kb < num_kb);
+        } while (kb < kb_end(num_kb));
         if (!ok) break;
+        if constexpr (KSPLIT) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) part[c] = sum[0][c];
+          continue;
+        }
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
           if (side + m * kSides < pieces) {
@@ -682,6 +698,14 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
             store_piece(side + m * kSides, sum[m]);
           }
         }
+      } else if constexpr (KSPLIT) {
+        wait_full(limit);
+        if (!ok) break;
+        uint32_t r[32];
+        __syncwarp();
+        tmem_load_32cols(piece_at(side), r);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) part[c] = __uint_as_float(r[c]);
       } else {
         wait_full(limit);
         if (!ok) break;
@@ -707,6 +731,37 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
         for (int m = 0; m < kMine; ++m)
           if (side + m * kSides < pieces) store_piece(side + m * kSides, packed[m]);
         ++j;
+      }
+    }
+  }
+
+  if constexpr (KSPLIT) {
+    __syncwarp();
+    cluster_sync_all();  // every CTA's MMAs have read its ring: partial sums may be written there
+    const int epi = warp - kGroupedEpiWarp;
+    GroupedTile w = {};
+    if (mine > 0) w = tile_at(0);
+    const int per = kBM / ks;  // lanes a CTA finishes
+    if (epi >= 0 && (epi >> 2) * 32 < w.cols && *abort_flag == 0u) {
+      const int row = (epi & 3) * 32 + lane;
+      const uint32_t to = mapa_shared(s0, static_cast<uint32_t>(row / per)) +
+                          static_cast<uint32_t>(((slice * BN + (epi >> 2) * 32) * per + row % per) * 4);
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + static_cast<uint32_t>(c * per * 4)), "f"(part[c]) : "memory");
+    }
+    __syncwarp();
+    cluster_sync_all();  // all partial sums are in place
+    if (epi >= 0 && *abort_flag == 0u) {
+      const int shift = 31 - __clz(per);
+      const float *recv = reinterpret_cast<const float *>(smem);
+      for (int e = static_cast<int>(threadIdx.x) - kGroupedEpiWarp * 32; e < w.cols << shift; e += Roles::kEpiWarps * 32) {
+        const int c = e >> shift, row = e & (per - 1), at = w.lane0 + slice * per + row;
+        if (at >= p.lanes) continue;
+        float v = 0.0f;
+        for (int q = 0; q < ks; ++q) v += recv[(q * BN + c) * per + row];
+        v = activate<OUT != kTypeF32>(p.act, v);
+        store_elem<OUT>(p.C, static_cast<int64_t>(w.col0 + c) * p.ldc + at, v);
       }
     }
   }
