@@ -5,7 +5,7 @@
 //   backward: with x^ = h s and g = dy w,  dx = s (g - x^ mean(g x^)) + dh,  dw = sum over rows of dy x^
 //
 // Both are bound by HBM traffic: a row is read once, held in registers while its sum is taken, and
-// written once.  `nw` warps share a row; each has up to U pieces of 32 lanes x 16 bytes, nw pieces apart.
+// written once.  `nw` warps share a row; each has up to U pieces of 32 lanes x 16 bytes side by side.
 // CTAs are persistent and load their next row before they wait for the sum of this one, so that the
 // reduction's latency (two barriers, shuffles) runs under the next row's loads; the weights stay in
 // registers.
@@ -48,38 +48,78 @@ NormShape norm_shape(int64_t cols, int type) {
 template <int U>
 constexpr bool kNormAhead = U <= 2;
 
-// A lane's part of one row of up to U pieces, as loaded.
+// A lane's part of one row: U pieces of 32 lanes x 16 bytes side by side, as loaded.
 template <int U>
 struct RowPart {
   uint32_t w[U][4], first[U];
 };
 
-template <int T, bool VEC, int U>
-__device__ __forceinline__ void load_row(const RowMat &m, int64_t row, int c0, int step, int cols, int lane,
-                                         RowPart<U> &part) {
-  const char *base = static_cast<const char *>(m.p) + (row * m.ld + c0) * kTypeBytes<T>;
+// Rows of one matrix from a warp's first column on: a cursor that steps from row to row.
+template <int T>
+struct RowCursor {
+  char *p;
+  int64_t step;  // bytes from one of the warp's rows to its next
+  __device__ __forceinline__ RowCursor(const RowMat &m, int64_t row, int64_t row_step, int c0)
+      : p(static_cast<char *>(const_cast<void *>(m.p)) + (row * m.ld + c0) * kTypeBytes<T>),
+        step(row_step * m.ld * kTypeBytes<T>) {}
+};
+
+// Calls f(u, full) for every piece that has columns; `left`: columns from the warp's first one on.  Whole
+// pieces, all but the last as a rule, need no check of columns.
+template <int T, int U, typename F>
+__device__ __forceinline__ void for_pieces(int left, F f) {
+  constexpr int kPiece = 32 * kLaneElems<T>;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) part.w[u][j] = 0;
-    part.first[u] = 0;
-    const int left = cols - c0 - u * step;
-    if (left > 0)
-      issue_load<T, VEC, false>(base + static_cast<int64_t>(u) * step * kTypeBytes<T>, left, lane, part.w[u], part.first[u]);
+    if (left >= (u + 1) * kPiece)
+      f(u, std::true_type());
+    else if (left > u * kPiece)
+      f(u, std::false_type());
   }
 }
 
-// Piece u's values, zeros past the last column; `base`: the piece's first byte in memory.
+template <int T, bool VEC, int U>
+__device__ __forceinline__ void load_row(const char *p, int left, int lane, RowPart<U> &part) {
+  constexpr int kPiece = 32 * kLaneElems<T>;
+  for_pieces<T, U>(left, [&](int u, auto full) {
+    part.first[u] = 0;
+    issue_load<T, VEC, decltype(full)::value>(p + u * 512, left - u * kPiece, lane, part.w[u], part.first[u]);
+  });
+}
+
+// Piece u's values, zeros past the last column.
 template <int T, bool VEC, int U, int E>
-__device__ __forceinline__ void row_values(RowPart<U> &part, int u, const char *base, int lane, uint32_t *stage,
-                                           float (&v)[E]) {
-  finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(base), part.first[u], stage, part.w[u]);
+__device__ __forceinline__ void row_values(RowPart<U> &part, int u, const char *p, int lane, uint32_t *stage, float (&v)[E]) {
+  finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(p + u * 512), part.first[u], stage, part.w[u]);
   to_floats<T, E>(part.w[u], v);
 }
 
-template <int T, bool VEC, int U>
-__device__ __forceinline__ const char *piece_at(const RowMat &m, int64_t row, int c0, int u, int step) {
-  return static_cast<const char *>(m.p) + (row * m.ld + c0 + static_cast<int64_t>(u) * step) * kTypeBytes<T>;
+// d[j] = a[j] * b[j] and so on, two at a time.
+template <int E>
+__device__ __forceinline__ void mul_to(float (&d)[E], const float (&a)[E], const float (&b)[E]) {
+#pragma unroll
+  for (int j = 0; j < E; j += 2) f2_unpack(f2_mul(f2_pack(a[j], a[j + 1]), f2_pack(b[j], b[j + 1])), d[j], d[j + 1]);
+}
+
+template <int E>
+__device__ __forceinline__ void scale_to(float (&d)[E], const float (&a)[E], float c) {
+#pragma unroll
+  for (int j = 0; j < E; j += 2) f2_unpack(f2_mul(f2_pack(a[j], a[j + 1]), f2_splat(c)), d[j], d[j + 1]);
+}
+
+template <int E>
+__device__ __forceinline__ void add_to(float (&d)[E], const float (&a)[E]) {
+#pragma unroll
+  for (int j = 0; j < E; j += 2) f2_add_to(d[j], d[j + 1], a[j], a[j + 1]);
+}
+
+// (lo, hi) += sums of a[j] * b[j] over even and odd j.
+template <int E>
+__device__ __forceinline__ void dot_to(float &lo, float &hi, const float (&a)[E], const float (&b)[E]) {
+  uint64_t s = f2_pack(lo, hi);
+#pragma unroll
+  for (int j = 0; j < E; j += 2) s = f2_fma(f2_pack(a[j], a[j + 1]), f2_pack(b[j], b[j + 1]), s);
+  f2_unpack(s, lo, hi);
 }
 
 // The sum of x over the nw warps of a row, in every lane of them.  part: an entry for each warp; the same
@@ -90,11 +130,13 @@ __device__ __forceinline__ float row_sum(float x, int warp, int lane, int nw, fl
   if (nw == 1) return x;
   if (lane == 0) part[warp] = x;
   __syncthreads();
-  x = lane < nw ? part[(warp & ~(nw - 1)) + lane] : 0.0f;
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+  x = part[(warp & ~(nw - 1)) + (lane & (nw - 1))];
+  for (int d = nw / 2; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
   return x;
 }
+
+// CTAs of an SM: what the registers of a row, and of the next, allow.
+constexpr int norm_ctas(int u, int warps) { return warps == 8 ? 4 : u <= 2 ? 2 : 1; }
 
 struct NormArgs {
   RowMat x, r, h, y;  // r.p, h.p: may be nullptr
@@ -108,101 +150,104 @@ struct NormArgs {
 
 // FMT: kE2M1 or kE4M3 for an MX matrix, -1 for Y in the inputs' type.
 template <int T, bool VEC, int U, int WARPS, int FMT>
-__global__ void __launch_bounds__(32 * WARPS) norm_forward_kernel(const NormArgs a) {
-  constexpr int E = kLaneElems<T>, B = kTypeBytes<T>;
+__global__ void __launch_bounds__(32 * WARPS, VEC ? norm_ctas(U, WARPS) : 1) norm_forward_kernel(const NormArgs a) {
+  constexpr int E = kLaneElems<T>, kPiece = 32 * E;
   __shared__ __align__(16) uint32_t stage_all[VEC ? 1 : WARPS][128];
   __shared__ float sums[2][WARPS];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   uint32_t *stage = stage_all[VEC ? 0 : warp];
   const int at_once = WARPS / a.nw;  // rows of a CTA
-  const int c0 = (warp & (a.nw - 1)) * 32 * E, step = a.nw * 32 * E;
+  const int c0 = (warp & (a.nw - 1)) * kPiece * U, left = a.cols - c0;
   grid_dependency_wait();
   grid_launch_dependents();
   int64_t row = static_cast<int64_t>(blockIdx.x) * at_once + warp / a.nw;
   const int64_t row_step = static_cast<int64_t>(gridDim.x) * at_once;
-  const int64_t rounds = (a.rows - static_cast<int64_t>(blockIdx.x) * at_once + row_step - 1) / row_step;
+  const int rounds = static_cast<int>((a.rows - static_cast<int64_t>(blockIdx.x) * at_once + row_step - 1) / row_step);
+  RowCursor<T> x(a.x, row, row_step, c0), r(a.r, row, row_step, c0), h(a.h, row, row_step, c0), y(a.y, row, row_step, c0);
+  const bool has_r = a.r.p != nullptr, has_h = a.h.p != nullptr;
   RowPart<U> nx, nr, wp;
-  const RowMat wm = {a.w, 0};
-  load_row<T, VEC, U>(wm, 0, c0, step, a.cols, lane, wp);
-  auto fetch = [&](int64_t r) {
-    if (r < a.rows) {
-      load_row<T, VEC, U>(a.x, r, c0, step, a.cols, lane, nx);
-      if (a.r.p != nullptr) load_row<T, VEC, U>(a.r, r, c0, step, a.cols, lane, nr);
+  const char *w0 = static_cast<const char *>(a.w) + static_cast<int64_t>(c0) * kTypeBytes<T>;
+  load_row<T, VEC, U>(w0, left, lane, wp);
+  const char *fx = x.p, *fr = r.p;  // of the row to fetch
+  auto fetch = [&](int64_t at) {
+    if (at < a.rows) {
+      load_row<T, VEC, U>(fx, left, lane, nx);
+      if (has_r) load_row<T, VEC, U>(fr, left, lane, nr);
     }
+    fx += x.step;
+    fr += r.step;
   };
   if (kNormAhead<U>) fetch(row);
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(piece_at<T, VEC, U>(wm, 0, c0, u, step)), wp.first[u], stage, wp.w[u]);
-  for (int64_t i = 0; i < rounds; ++i, row += row_step) {
+  for_pieces<T, U>(left, [&](int u, auto) {
+    finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(w0 + u * 512), wp.first[u], stage, wp.w[u]);
+  });
+  for (int i = 0; i < rounds; ++i, row += row_step) {
     const bool in = row < a.rows;
     if (!kNormAhead<U>) fetch(row);
     float v[U][E];
-    float sum = 0.0f;
+    float lo = 0.0f, hi = 0.0f;
     if (in) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        row_values<T, VEC, U, E>(nx, u, piece_at<T, VEC, U>(a.x, row, c0, u, step), lane, stage, v[u]);
-        if (a.r.p != nullptr) {
+      for_pieces<T, U>(left, [&](int u, auto) {
+        row_values<T, VEC, U, E>(nx, u, x.p, lane, stage, v[u]);
+        if (has_r) {
           float b[E];
-          row_values<T, VEC, U, E>(nr, u, piece_at<T, VEC, U>(a.r, row, c0, u, step), lane, stage, b);
-#pragma unroll
-          for (int j = 0; j < E; j += 2) f2_add_to(v[u][j], v[u][j + 1], b[j], b[j + 1]);
+          row_values<T, VEC, U, E>(nr, u, r.p, lane, stage, b);
+          add_to<E>(v[u], b);
         }
-      }
+      });
     }
     if (kNormAhead<U>) fetch(row + row_step);
     if (in) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int j = 0; j < E; ++j) sum = fmaf(v[u][j], v[u][j], sum);
-        const int left = a.cols - c0 - u * step;
-        if (a.h.p != nullptr && left > 0) {
+      for_pieces<T, U>(left, [&](int u, auto full) {
+        dot_to<E>(lo, hi, v[u], v[u]);
+        if (has_h) {
           uint32_t o[4];
           from_floats<T, E>(v[u], o);
-          store_lane<T, VEC, false>(const_cast<char *>(piece_at<T, VEC, U>(a.h, row, c0, u, step)), left, lane, stage, o);
+          store_lane<T, VEC, decltype(full)::value>(h.p + u * 512, left - u * kPiece, lane, stage, o);
         }
-      }
+      });
     }
-    sum = row_sum(sum, warp, lane, a.nw, sums[i & 1]);
-    if (!in) continue;
-    const float s = __frsqrt_rn(sum / static_cast<float>(a.cols) + a.eps);
-    if (a.rstd != nullptr && c0 == 0 && lane == 0) a.rstd[row] = s;
+    const float sum = row_sum(lo + hi, warp, lane, a.nw, sums[i & 1]);
+    if (in) {
+      const float s = __frsqrt_rn(sum / static_cast<float>(a.cols) + a.eps);
+      if (a.rstd != nullptr && c0 == 0 && lane == 0) a.rstd[row] = s;
+      for_pieces<T, U>(left, [&](int u, auto full) {
+        constexpr bool kFull = decltype(full)::value;
+        float w[E], o[E];
+        to_floats<T, E>(wp.w[u], w);
+        scale_to<E>(o, v[u], s);
+        mul_to<E>(o, o, w);
+        if constexpr (FMT < 0) {
+          uint32_t b[4];
+          from_floats<T, E>(o, b);
+          store_lane<T, VEC, kFull>(y.p + u * 512, left - u * kPiece, lane, stage, b);
+        } else {
+          constexpr int kFmt = FMT < 0 ? 0 : FMT;
+          constexpr int kLanesPerBlock = kMxBlock / E;
+          uint32_t m = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int left = a.cols - c0 - u * step;
-      if (left <= 0) continue;
-      float w[E], y[E];
-      to_floats<T, E>(wp.w[u], w);
+          for (int j = 0; j < E; ++j) {
+            if (!kFull && lane * E + j >= left - u * kPiece) o[j] = 0.0f;  // also where the row's factor is not finite
+            m = max(m, __float_as_uint(o[j]) & 0x7fffffffu);
+          }
 #pragma unroll
-      for (int j = 0; j < E; ++j) y[j] = v[u][j] * s * w[j];
-      if constexpr (FMT < 0) {
-        uint32_t o[4];
-        from_floats<T, E>(y, o);
-        store_lane<T, VEC, false>(const_cast<char *>(piece_at<T, VEC, U>(a.y, row, c0, u, step)), left, lane, stage, o);
-      } else {
-        constexpr int kFmt = FMT < 0 ? 0 : FMT;
-        constexpr int kLanesPerBlock = kMxBlock / E;
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          if (lane * E + j >= left) y[j] = 0.0f;  // also where the row's factor is not finite
-          m = max(m, __float_as_uint(y[j]) & 0x7fffffffu);
+          for (int d = 1; d < kLanesPerBlock; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+          const uint32_t byte = scale_byte<kFmt>(m);
+          uint32_t q[kQWords<kFmt, E>];
+          encode<kFmt, E>(o, inverse_scale(byte), q);
+          const int at = c0 + u * kPiece;
+          const int block = at / kMxBlock + lane * E / kMxBlock;
+          if (kFull || block < a.q.blocks)
+            store_q<kFmt, E>(const_cast<uint8_t *>(a.q.q) + row * a.q.ldq + (at / E + lane) * kQBytes<kFmt, E>, q);
+          if (lane % kLanesPerBlock == 0 && (kFull || (block >> 2) < a.q.tiles_x))
+            const_cast<uint8_t *>(a.q.s)[scale_offset(row, block, a.q.tiles_x)] = static_cast<uint8_t>(byte);
         }
-#pragma unroll
-        for (int d = 1; d < kLanesPerBlock; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const uint32_t byte = scale_byte<kFmt>(m);
-        uint32_t q[kQWords<kFmt, E>];
-        encode<kFmt, E>(y, inverse_scale(byte), q);
-        const int first = c0 + u * step;
-        const int block = first / kMxBlock + lane * E / kMxBlock;
-        if (block < a.q.blocks)
-          store_q<kFmt, E>(const_cast<uint8_t *>(a.q.q) + row * a.q.ldq + (first / E + lane) * kQBytes<kFmt, E>, q);
-        if (lane % kLanesPerBlock == 0 && (block >> 2) < a.q.tiles_x)
-          const_cast<uint8_t *>(a.q.s)[scale_offset(row, block, a.q.tiles_x)] = static_cast<uint8_t>(byte);
-      }
+      });
     }
+    x.p += x.step;
+    r.p += r.step;
+    h.p += h.step;
+    y.p += y.step;
   }
 }
 
@@ -215,89 +260,102 @@ struct NormBackArgs {
   int cols, nw;
 };
 
+constexpr int norm_back_ctas(int u, int warps) { return u == 1 ? 3 : warps == 8 ? 2 : 1; }
+
 // The sums for dw stay in registers, row after row in order; CTAs leave their sums in `part`, which
 // column_sum_kernel adds in order, so the result does not depend on timing.
 template <int T, bool VEC, int U, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) norm_backward_kernel(const NormBackArgs a) {
-  constexpr int E = kLaneElems<T>;
+__global__ void __launch_bounds__(32 * WARPS, VEC ? norm_back_ctas(U, WARPS) : 1) norm_backward_kernel(const NormBackArgs a) {
+  constexpr int E = kLaneElems<T>, kPiece = 32 * E;
   __shared__ __align__(16) uint32_t stage_all[VEC ? 1 : WARPS][128];
   __shared__ float sums[2][WARPS];
-  __shared__ __align__(16) float columns[U == 1 ? WARPS : 1][U == 1 ? 32 * E : 4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ __align__(16) float columns[U == 1 ? WARPS : 1][U == 1 ? kPiece : 4];
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   uint32_t *stage = stage_all[VEC ? 0 : warp];
   const int at_once = WARPS / a.nw;
-  const int c0 = (warp & (a.nw - 1)) * 32 * E, step = a.nw * 32 * E;
+  const int c0 = (warp & (a.nw - 1)) * kPiece * U, left = a.cols - c0;
   grid_dependency_wait();
   grid_launch_dependents();
   int64_t row = static_cast<int64_t>(blockIdx.x) * at_once + warp / a.nw;
   const int64_t row_step = static_cast<int64_t>(gridDim.x) * at_once;
-  const int64_t rounds = (a.rows - static_cast<int64_t>(blockIdx.x) * at_once + row_step - 1) / row_step;
+  const int rounds = static_cast<int>((a.rows - static_cast<int64_t>(blockIdx.x) * at_once + row_step - 1) / row_step);
+  RowCursor<T> y(a.dy, row, row_step, c0), h(a.h, row, row_step, c0), d(a.dh, row, row_step, c0), x(a.dx, row, row_step, c0);
+  const bool has_d = a.dh.p != nullptr;
   RowPart<U> ny, nh, nd, wp;
   float ns = 0.0f;
-  const RowMat wm = {a.w, 0};
-  load_row<T, VEC, U>(wm, 0, c0, step, a.cols, lane, wp);
-  auto fetch = [&](int64_t r) {
-    if (r < a.rows) {
-      load_row<T, VEC, U>(a.dy, r, c0, step, a.cols, lane, ny);
-      load_row<T, VEC, U>(a.h, r, c0, step, a.cols, lane, nh);
-      if (a.dh.p != nullptr) load_row<T, VEC, U>(a.dh, r, c0, step, a.cols, lane, nd);
-      ns = a.rstd[r];
+  const char *w0 = static_cast<const char *>(a.w) + static_cast<int64_t>(c0) * kTypeBytes<T>;
+  load_row<T, VEC, U>(w0, left, lane, wp);
+  const char *fy = y.p, *fh = h.p, *fd = d.p;
+  auto fetch = [&](int64_t at) {
+    if (at < a.rows) {
+      load_row<T, VEC, U>(fy, left, lane, ny);
+      load_row<T, VEC, U>(fh, left, lane, nh);
+      ns = a.rstd[at];
     }
+    fy += y.step;
+    fh += h.step;
   };
-  if (kNormAhead<U>) fetch(row);
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(piece_at<T, VEC, U>(wm, 0, c0, u, step)), wp.first[u], stage, wp.w[u]);
+  auto fetch_d = [&](int64_t at) {
+    if (has_d && at < a.rows) load_row<T, VEC, U>(fd, left, lane, nd);
+    fd += d.step;
+  };
+  if (kNormAhead<U>) {
+    fetch(row);
+    fetch_d(row);
+  }
+  for_pieces<T, U>(left, [&](int u, auto) {
+    finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(w0 + u * 512), wp.first[u], stage, wp.w[u]);
+  });
   float acc[U][E];
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int j = 0; j < E; ++j) acc[u][j] = 0.0f;
-  for (int64_t i = 0; i < rounds; ++i, row += row_step) {
+  for (int i = 0; i < rounds; ++i, row += row_step) {
     const bool in = row < a.rows;
-    if (!kNormAhead<U>) fetch(row);
+    if (!kNormAhead<U>) {
+      fetch(row);
+      fetch_d(row);
+    }
     const float s = ns;
-    float dot = 0.0f;
-    RowPart<U> y = ny, h = nh, d = nd;
+    float lo = 0.0f, hi = 0.0f;
+    float g[U][E], xh[U][E];  // dy w and h s
     if (in) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float vy[E], vh[E], w[E];
-        row_values<T, VEC, U, E>(y, u, piece_at<T, VEC, U>(a.dy, row, c0, u, step), lane, stage, vy);
-        row_values<T, VEC, U, E>(h, u, piece_at<T, VEC, U>(a.h, row, c0, u, step), lane, stage, vh);
+      for_pieces<T, U>(left, [&](int u, auto) {
+        float w[E], t[E];
+        row_values<T, VEC, U, E>(ny, u, y.p, lane, stage, g[u]);
+        row_values<T, VEC, U, E>(nh, u, h.p, lane, stage, xh[u]);
         to_floats<T, E>(wp.w[u], w);
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const float t = vy[j] * (vh[j] * s);
-          acc[u][j] += t;
-          dot = fmaf(t, w[j], dot);
-        }
-        if (a.dh.p != nullptr)
-          finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(piece_at<T, VEC, U>(a.dh, row, c0, u, step)), d.first[u], stage, d.w[u]);
-      }
+        scale_to<E>(xh[u], xh[u], s);
+        mul_to<E>(t, g[u], xh[u]);
+        add_to<E>(acc[u], t);
+        mul_to<E>(g[u], g[u], w);
+        dot_to<E>(lo, hi, g[u], xh[u]);
+      });
     }
     if (kNormAhead<U>) fetch(row + row_step);
-    dot = row_sum(dot, warp, lane, a.nw, sums[i & 1]) / static_cast<float>(a.cols);
-    if (!in) continue;
+    const float dot = row_sum(lo + hi, warp, lane, a.nw, sums[i & 1]) / static_cast<float>(a.cols);
+    if (in) {
+      for_pieces<T, U>(left, [&](int u, auto full) {
+        float b[E];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int left = a.cols - c0 - u * step;
-      if (left <= 0) continue;
-      float vy[E], vh[E], w[E];
-      to_floats<T, E>(y.w[u], vy);
-      to_floats<T, E>(h.w[u], vh);
-      to_floats<T, E>(wp.w[u], w);
-#pragma unroll
-      for (int j = 0; j < E; ++j) vy[j] = s * fmaf(-dot, vh[j] * s, vy[j] * w[j]);
-      if (a.dh.p != nullptr) {
-        to_floats<T, E>(d.w[u], vh);
-#pragma unroll
-        for (int j = 0; j < E; ++j) vy[j] += vh[j];
-      }
-      uint32_t o[4];
-      from_floats<T, E>(vy, o);
-      store_lane<T, VEC, false>(const_cast<char *>(piece_at<T, VEC, U>(a.dx, row, c0, u, step)), left, lane, stage, o);
+        for (int j = 0; j < E; j += 2)
+          f2_unpack(f2_fma(f2_splat(-dot), f2_pack(xh[u][j], xh[u][j + 1]), f2_pack(g[u][j], g[u][j + 1])), g[u][j], g[u][j + 1]);
+        scale_to<E>(g[u], g[u], s);
+        if (has_d) {
+          row_values<T, VEC, U, E>(nd, u, d.p, lane, stage, b);
+          add_to<E>(g[u], b);
+        }
+        uint32_t o[4];
+        from_floats<T, E>(g[u], o);
+        store_lane<T, VEC, decltype(full)::value>(x.p + u * 512, left - u * kPiece, lane, stage, o);
+      });
     }
+    if (kNormAhead<U>) fetch_d(row + row_step);
+    y.p += y.step;
+    h.p += h.step;
+    d.p += d.step;
+    x.p += x.step;
   }
   if (a.part == nullptr) return;
   float *part = a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
@@ -307,7 +365,7 @@ __global__ void __launch_bounds__(32 * WARPS) norm_backward_kernel(const NormBac
     __syncthreads();
     for (int c = threadIdx.x; c < a.cols; c += 32 * WARPS) {
       float t = 0.0f;
-      for (int g = 0; g < at_once; ++g) t += columns[g * a.nw + c / (32 * E)][c % (32 * E)];
+      for (int q = 0; q < at_once; ++q) t += columns[q * a.nw + c / kPiece][c % kPiece];
       part[c] = t;
     }
   } else {
@@ -315,8 +373,8 @@ __global__ void __launch_bounds__(32 * WARPS) norm_backward_kernel(const NormBac
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const int c = c0 + u * step + lane * E + j;
-        if (c < a.cols) part[c] = acc[u][j];
+        const int c = u * kPiece + lane * E + j;
+        if (c < left) part[c0 + c] = acc[u][j];
       }
   }
 }
@@ -344,7 +402,7 @@ unsigned norm_grid(const NormShape &n, int64_t rows, int sms, int per_sm) {
 // CTAs of the backward kernel, each of which leaves a row of partial sums.
 unsigned backward_ctas(int64_t rows, int64_t cols, int type, int sms) {
   const NormShape n = norm_shape(cols, type);
-  return norm_grid(n, rows, sms, n.warps == 8 ? 3 : 1);
+  return norm_grid(n, rows, sms, norm_back_ctas(n.u, n.warps));
 }
 
 tlg_status check_norm(int64_t rows, int64_t cols, int type) {
@@ -405,7 +463,7 @@ tlg_status norm_forward(int64_t rows, int64_t cols, int type, const void *X, int
                 static_cast<int>(cols), n.nw};
   const bool vec = aligned16(weight) && vec_rows(X, rows, ldx, type) && vec_or_none(R, rows, ldr, type) &&
                    vec_or_none(H, rows, ldh, type) && vec_or_none(Y, rows, ldy, type);
-  const unsigned grid = norm_grid(n, rows, info.sm_count, n.warps == 8 ? 4 : 2);
+  const unsigned grid = norm_grid(n, rows, info.sm_count, norm_ctas(n.u, n.warps));
   return with_type(type, [&](auto T) {
     constexpr int kT = decltype(T)::value;
     return with_flag(vec, [&](auto V) {
