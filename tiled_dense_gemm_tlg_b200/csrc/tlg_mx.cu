@@ -583,14 +583,14 @@ tlg_status tlg_mx_quantize(tlg_mx_format format, int64_t rows, int64_t cols, tlg
         const int64_t tiles_r = (rows + 127) / 128, tiles = tiles_r * o.tiles_x;
         const int pairs = reinterpret_cast<uintptr_t>(X) % 4 == 0 && ldx * type_bytes(type) % 4 == 0 ? 1 : 0;
         return launch(quantize_cols_kernel<kT, kF>, dim3(static_cast<unsigned>(std::min<int64_t>(tiles, 1 << 30))),
-                      kT == kTypeF32 ? 512 : 256, s, X, ldx, pairs, o, rows, cols, tiles_r, tiles);
+                      kT == kTypeF32 ? 512 : 256, s, 0, X, ldx, pairs, o, rows, cols, tiles_r, tiles);
       }
       const bool vec = vec_rows(X, rows, ldx, type);
       const RowGrid g = quantize_grid(rows, cols, type, vec, info.sm_count);
       return with_flag(vec, [&](auto V) {
         return with_width<quantize_width(kT, decltype(V)::value)>(g.u, [&](auto U) {
           return launch(quantize_rows_kernel<kT, kF, false, decltype(V)::value, decltype(U)::value>, g.grid,
-                        kRowThreads, s, RowMat{X, ldx}, o, RowMat{}, 0, rows, cols, g.rows_per, g.across);
+                        kRowThreads, s, 0, RowMat{X, ldx}, o, RowMat{}, 0, rows, cols, g.rows_per, g.across);
         });
       });
     });
@@ -620,7 +620,7 @@ tlg_status tlg_mx_dequantize(tlg_mx_format format, int64_t rows, int64_t cols, c
         return with_width<kWide>(g.u, [&](auto U) {
           return launch(
               dequantize_rows_kernel<decltype(T)::value, decltype(F)::value, decltype(V)::value, decltype(U)::value>,
-              g.grid, kRowThreads, static_cast<cudaStream_t>(stream), in, RowMat{X, ldx}, rows, cols, g.rows_per, g.across);
+              g.grid, kRowThreads, static_cast<cudaStream_t>(stream), 0, in, RowMat{X, ldx}, rows, cols, g.rows_per, g.across);
         });
       });
     });
@@ -651,7 +651,7 @@ tlg_status tlg_act_forward_mx(int64_t rows, int64_t cols, tlg_activation activat
     return with_flag(vec, [&](auto V) {
       return with_width<quantize_width(decltype(T)::value, decltype(V)::value)>(g.u, [&](auto U) {
         return launch(quantize_rows_kernel<decltype(T)::value, kE4M3, true, decltype(V)::value, decltype(U)::value>,
-                      g.grid, kRowThreads, static_cast<cudaStream_t>(stream), RowMat{Z, ldz}, o, RowMat{Y, ldy},
+                      g.grid, kRowThreads, static_cast<cudaStream_t>(stream), 0, RowMat{Z, ldz}, o, RowMat{Y, ldy},
                       static_cast<int>(activation), rows, cols, g.rows_per, g.across);
       });
     });
@@ -731,7 +731,7 @@ tlg_status tlg_act_backward_mx(int64_t rows, int64_t cols, tlg_activation activa
       return with_flag(vec, [&](auto V) {
         return with_width<kWideBackward>(g.u, [&](auto U) {
           return launch(act_backward_kernel<kT, decltype(SUM)::value, decltype(V)::value, decltype(U)::value>, g.grid,
-                        kRowThreads, s, RowMat{dY, lddy}, z, RowMat{dZ, lddz}, static_cast<int>(activation), rows,
+                        kRowThreads, s, 0, RowMat{dY, lddy}, z, RowMat{dZ, lddz}, static_cast<int>(activation), rows,
                         cols, g.rows_per, g.across, part);
         });
       });
@@ -739,8 +739,8 @@ tlg_status tlg_act_backward_mx(int64_t rows, int64_t cols, tlg_activation activa
   });
   if (st != TLG_OK || part == dbias) return st;
   const dim3 sum_grid(static_cast<unsigned>((cols + 31) / 32));
-  return splits > 128 ? launch(column_sum_kernel<32>, sum_grid, 1024, s, part, splits, cols, dbias)
-                      : launch(column_sum_kernel<8>, sum_grid, 256, s, part, splits, cols, dbias);
+  return splits > 128 ? launch(column_sum_kernel<32>, sum_grid, 1024, s, 0, part, splits, cols, dbias)
+                      : launch(column_sum_kernel<8>, sum_grid, 256, s, 0, part, splits, cols, dbias);
 }
 
 }  // extern "C"

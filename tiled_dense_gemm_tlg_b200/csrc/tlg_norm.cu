@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include "tlg.h"
@@ -260,18 +261,207 @@ struct NormBackArgs {
   int cols, nw;
 };
 
-constexpr int norm_back_ctas(int u, int warps) { return u == 1 ? 3 : warps == 8 ? 2 : 1; }
-
-// The sums for dw stay in registers, row after row in order; CTAs leave their sums in `part`, which
-// column_sum_kernel adds in order, so the result does not depend on timing.
-template <int T, bool VEC, int U, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, VEC ? norm_back_ctas(U, WARPS) : 1) norm_backward_kernel(const NormBackArgs a) {
+// The end of both backward kernels: a CTA's row of partial sums for dw.  acc: the lane's sums, piece u of it at
+// column c0 + u * kPiece; where a CTA takes several rows at once (U == 1) its warps' sums are added in order.
+template <int T, int U, int WARPS>
+__device__ __forceinline__ void leave_sums(const NormBackArgs &a, const float (&acc)[U][kLaneElems<T>], int c0, int left,
+                                           int warp, int lane) {
   constexpr int E = kLaneElems<T>, kPiece = 32 * E;
-  __shared__ __align__(16) uint32_t stage_all[VEC ? 1 : WARPS][128];
-  __shared__ float sums[2][WARPS];
   __shared__ __align__(16) float columns[U == 1 ? WARPS : 1][U == 1 ? kPiece : 4];
+  if (a.part == nullptr) return;
+  float *part = a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
+  if constexpr (U == 1) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) columns[warp][lane * E + j] = acc[0][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += 32 * WARPS) {
+      float t = 0.0f;
+      for (int q = 0; q < WARPS / a.nw; ++q) t += columns[q * a.nw + c / kPiece][c % kPiece];
+      part[c] = t;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int c = u * kPiece + lane * E + j;
+        if (c < left) part[c0 + c] = acc[u][j];
+      }
+  }
+}
+
+// dX of one piece: g = dy w, xh = h s, and dh, or nullptr.
+template <int E>
+__device__ __forceinline__ void finish_dx(float (&g)[E], const float (&xh)[E], float dot, float s) {
+#pragma unroll
+  for (int j = 0; j < E; j += 2)
+    f2_unpack(f2_fma(f2_splat(-dot), f2_pack(xh[j], xh[j + 1]), f2_pack(g[j], g[j + 1])), g[j], g[j + 1]);
+  scale_to<E>(g, g, s);
+}
+
+// Backward kernel.  Three streams, the sums for dw and the row between its two uses leave no registers for
+// loads in flight, and one row ahead is too little of them (16384 x 4096 bf16: 122 us), so rows come through
+// shared memory: a ring of SLOTS rows to a warp, copied asynchronously, each lane's 16 bytes its own.  WORDS:
+// rows that are aligned to 4 bytes only are copied by words, neighbouring lanes on neighbouring ones, which
+// rearranges them on the way.  The sums for dw stay in registers, row after row in order; CTAs leave their
+// sums in `part`, which column_sum_kernel adds in order, so the result does not depend on timing.
+template <int T, int U, int WARPS>
+struct NormRing {
+  static constexpr int kSlots = U == 8 ? 1 : U == 4 || WARPS * U > 24 ? 2 : 3;
+  static constexpr int kStream = U * 512;                      // bytes of a warp's part of a row
+  static constexpr int kSlot = 3 * kStream;                    // dY, H, dH
+  static constexpr int kWarp = kSlots * kSlot;
+  static constexpr int kDynamicBytes = WARPS * (kWarp + kSlots * 4 + (16 - kSlots * 4 % 16) % 16);
+  static constexpr int kCtas = WARPS == 8 ? (U == 1 ? 4 : 2) : 1;
+  static constexpr int kStaticBytes = WARPS * (512 + 8 + (U == 1 ? 1024 : 2));
+  static_assert(kCtas * (kDynamicBytes + kStaticBytes + 1024) <= 233472, "CTAs of an SM");
+};
+
+template <int T, bool WORDS, int U, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, NormRing<T, U, WARPS>::kCtas) norm_backward_ring_kernel(const NormBackArgs a) {
+  using Ring = NormRing<T, U, WARPS>;
+  constexpr int E = kLaneElems<T>, B = kTypeBytes<T>, kPiece = 32 * E, ST = Ring::kSlots;
+  constexpr bool kKeep = U <= 2;  // dy w and h s stay in registers between their uses
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ __align__(16) uint32_t stage_all[WORDS ? WARPS : 1][128];
+  __shared__ float sums[2][WARPS];
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
-  uint32_t *stage = stage_all[VEC ? 0 : warp];
+  uint32_t *stage = stage_all[WORDS ? warp : 0];
+  uint8_t *ring = ring_smem + warp * Ring::kWarp;
+  float *factors = reinterpret_cast<float *>(ring_smem + WARPS * Ring::kWarp) + warp * ST;
+  const int at_once = WARPS / a.nw;
+  const int c0 = (warp & (a.nw - 1)) * kPiece * U, left = a.cols - c0;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  int64_t row = static_cast<int64_t>(blockIdx.x) * at_once + warp / a.nw;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * at_once;
+  const int rounds = static_cast<int>((a.rows - static_cast<int64_t>(blockIdx.x) * at_once + row_step - 1) / row_step);
+  RowCursor<T> y(a.dy, row, row_step, c0), h(a.h, row, row_step, c0), d(a.dh, row, row_step, c0), x(a.dx, row, row_step, c0);
+  const bool has_d = a.dh.p != nullptr;
+  const char *w0 = static_cast<const char *>(a.w) + static_cast<int64_t>(c0) * B;
+  RowPart<U> wp;
+  load_row<T, !WORDS, U>(w0, left, lane, wp);
+
+  auto copy = [&](uint8_t *to, const char *from) {
+    for_pieces<T, U>(left, [&](int u, auto full) {
+      const int have = (left - u * kPiece) * B;  // bytes of the piece's columns
+      if constexpr (!WORDS) {
+        const int size = decltype(full)::value ? 16 : min(max(have - lane * 16, 0), 16);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to + u * 512 + lane * 16)),
+                     "l"(size > 0 ? from + u * 512 + lane * 16 : from), "r"(size)
+                     : "memory");
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = (j * 32 + lane) * 4;
+          const int size = decltype(full)::value ? 4 : min(max(have - at, 0), 4);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to + u * 512 + at)),
+                       "l"(size > 0 ? from + u * 512 + at : from), "r"(size)
+                       : "memory");
+        }
+      }
+    });
+  };
+  int64_t next = row;  // to fetch
+  auto fetch = [&](int slot) {
+    if (next < a.rows) {
+      uint8_t *to = ring + slot * Ring::kSlot;
+      copy(to, y.p);
+      copy(to + Ring::kStream, h.p);
+      if (has_d) copy(to + 2 * Ring::kStream, d.p);
+      if (lane == 0)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(factors + slot)), "l"(a.rstd + next) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    next += row_step;
+    y.p += y.step;
+    h.p += h.step;
+    d.p += d.step;
+  };
+#pragma unroll
+  for (int q = 0; q < ST - 1; ++q) fetch(q);
+  for_pieces<T, U>(left, [&](int u, auto) {
+    finish_load<T, !WORDS>(lane, starts_inside_word<T, !WORDS>(w0 + u * 512), wp.first[u], stage, wp.w[u]);
+  });
+  float acc[U][E];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int j = 0; j < E; ++j) acc[u][j] = 0.0f;
+  int slot = 0;
+  for (int i = 0; i < rounds; ++i, row += row_step) {
+    const bool in = row < a.rows;
+    if constexpr (ST == 1) {
+      __syncwarp();
+      fetch(0);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncwarp();
+    } else {
+      asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
+      __syncwarp();  // every lane's copies of this row have landed, and the row before is read
+      fetch(slot == 0 ? ST - 1 : slot - 1);
+    }
+    const uint8_t *at = ring + slot * Ring::kSlot + lane * 16;
+    auto values = [&](int u, int stream, float(&v)[E]) {
+      const uint4 q = *reinterpret_cast<const uint4 *>(at + stream * Ring::kStream + u * 512);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      to_floats<T, E>(w, v);
+    };
+    const float s = factors[slot];
+    float lo = 0.0f, hi = 0.0f;
+    float g[kKeep ? U : 1][E], xh[kKeep ? U : 1][E];
+    if (in) {
+      for_pieces<T, U>(left, [&](int u, auto) {
+        const int k = kKeep ? u : 0;
+        float w[E], t[E];
+        values(u, 0, g[k]);
+        values(u, 1, xh[k]);
+        to_floats<T, E>(wp.w[u], w);
+        scale_to<E>(xh[k], xh[k], s);
+        mul_to<E>(t, g[k], xh[k]);
+        add_to<E>(acc[u], t);
+        mul_to<E>(g[k], g[k], w);
+        dot_to<E>(lo, hi, g[k], xh[k]);
+      });
+    }
+    const float dot = row_sum(lo + hi, warp, lane, a.nw, sums[i & 1]) / static_cast<float>(a.cols);
+    if (in) {
+      for_pieces<T, U>(left, [&](int u, auto full) {
+        const int k = kKeep ? u : 0;
+        float b[E];
+        if constexpr (!kKeep) {
+          values(u, 0, g[k]);
+          values(u, 1, xh[k]);
+          to_floats<T, E>(wp.w[u], b);
+          mul_to<E>(g[k], g[k], b);
+          scale_to<E>(xh[k], xh[k], s);
+        }
+        finish_dx<E>(g[k], xh[k], dot, s);
+        if (has_d) {
+          values(u, 2, b);
+          add_to<E>(g[k], b);
+        }
+        uint32_t o[4];
+        from_floats<T, E>(g[k], o);
+        store_lane<T, !WORDS, decltype(full)::value>(x.p + u * 512, left - u * kPiece, lane, stage, o);
+      });
+    }
+    x.p += x.step;
+    slot = slot == ST - 1 ? 0 : slot + 1;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  leave_sums<T, U, WARPS>(a, acc, c0, left, warp, lane);
+}
+
+// The same for 16-bit rows at odd places, which no asynchronous copy takes: loaded to registers, a row ahead
+// where they hold two.
+template <int T, int U, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) norm_backward_odd_kernel(const NormBackArgs a) {
+  constexpr int E = kLaneElems<T>, kPiece = 32 * E;
+  __shared__ __align__(16) uint32_t stage_all[WARPS][128];
+  __shared__ float sums[2][WARPS];
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  uint32_t *stage = stage_all[warp];
   const int at_once = WARPS / a.nw;
   const int c0 = (warp & (a.nw - 1)) * kPiece * U, left = a.cols - c0;
   grid_dependency_wait();
@@ -284,19 +474,19 @@ __global__ void __launch_bounds__(32 * WARPS, VEC ? norm_back_ctas(U, WARPS) : 1
   RowPart<U> ny, nh, nd, wp;
   float ns = 0.0f;
   const char *w0 = static_cast<const char *>(a.w) + static_cast<int64_t>(c0) * kTypeBytes<T>;
-  load_row<T, VEC, U>(w0, left, lane, wp);
+  load_row<T, false, U>(w0, left, lane, wp);
   const char *fy = y.p, *fh = h.p, *fd = d.p;
   auto fetch = [&](int64_t at) {
     if (at < a.rows) {
-      load_row<T, VEC, U>(fy, left, lane, ny);
-      load_row<T, VEC, U>(fh, left, lane, nh);
+      load_row<T, false, U>(fy, left, lane, ny);
+      load_row<T, false, U>(fh, left, lane, nh);
       ns = a.rstd[at];
     }
     fy += y.step;
     fh += h.step;
   };
   auto fetch_d = [&](int64_t at) {
-    if (has_d && at < a.rows) load_row<T, VEC, U>(fd, left, lane, nd);
+    if (has_d && at < a.rows) load_row<T, false, U>(fd, left, lane, nd);
     fd += d.step;
   };
   if (kNormAhead<U>) {
@@ -304,7 +494,7 @@ __global__ void __launch_bounds__(32 * WARPS, VEC ? norm_back_ctas(U, WARPS) : 1
     fetch_d(row);
   }
   for_pieces<T, U>(left, [&](int u, auto) {
-    finish_load<T, VEC>(lane, starts_inside_word<T, VEC>(w0 + u * 512), wp.first[u], stage, wp.w[u]);
+    finish_load<T, false>(lane, starts_inside_word<T, false>(w0 + u * 512), wp.first[u], stage, wp.w[u]);
   });
   float acc[U][E];
 #pragma unroll
@@ -323,8 +513,8 @@ __global__ void __launch_bounds__(32 * WARPS, VEC ? norm_back_ctas(U, WARPS) : 1
     if (in) {
       for_pieces<T, U>(left, [&](int u, auto) {
         float w[E], t[E];
-        row_values<T, VEC, U, E>(ny, u, y.p, lane, stage, g[u]);
-        row_values<T, VEC, U, E>(nh, u, h.p, lane, stage, xh[u]);
+        row_values<T, false, U, E>(ny, u, y.p, lane, stage, g[u]);
+        row_values<T, false, U, E>(nh, u, h.p, lane, stage, xh[u]);
         to_floats<T, E>(wp.w[u], w);
         scale_to<E>(xh[u], xh[u], s);
         mul_to<E>(t, g[u], xh[u]);
@@ -337,18 +527,15 @@ __global__ void __launch_bounds__(32 * WARPS, VEC ? norm_back_ctas(U, WARPS) : 1
     const float dot = row_sum(lo + hi, warp, lane, a.nw, sums[i & 1]) / static_cast<float>(a.cols);
     if (in) {
       for_pieces<T, U>(left, [&](int u, auto full) {
-        float b[E];
-#pragma unroll
-        for (int j = 0; j < E; j += 2)
-          f2_unpack(f2_fma(f2_splat(-dot), f2_pack(xh[u][j], xh[u][j + 1]), f2_pack(g[u][j], g[u][j + 1])), g[u][j], g[u][j + 1]);
-        scale_to<E>(g[u], g[u], s);
+        finish_dx<E>(g[u], xh[u], dot, s);
         if (has_d) {
-          row_values<T, VEC, U, E>(nd, u, d.p, lane, stage, b);
+          float b[E];
+          row_values<T, false, U, E>(nd, u, d.p, lane, stage, b);
           add_to<E>(g[u], b);
         }
         uint32_t o[4];
         from_floats<T, E>(g[u], o);
-        store_lane<T, VEC, decltype(full)::value>(x.p + u * 512, left - u * kPiece, lane, stage, o);
+        store_lane<T, false, decltype(full)::value>(x.p + u * 512, left - u * kPiece, lane, stage, o);
       });
     }
     if (kNormAhead<U>) fetch_d(row + row_step);
@@ -357,26 +544,7 @@ __global__ void __launch_bounds__(32 * WARPS, VEC ? norm_back_ctas(U, WARPS) : 1
     d.p += d.step;
     x.p += x.step;
   }
-  if (a.part == nullptr) return;
-  float *part = a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
-  if constexpr (U == 1) {  // the rows taken at once
-#pragma unroll
-    for (int j = 0; j < E; ++j) columns[warp][lane * E + j] = acc[0][j];
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.cols; c += 32 * WARPS) {
-      float t = 0.0f;
-      for (int q = 0; q < at_once; ++q) t += columns[q * a.nw + c / kPiece][c % kPiece];
-      part[c] = t;
-    }
-  } else {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int c = u * kPiece + lane * E + j;
-        if (c < left) part[c0 + c] = acc[u][j];
-      }
-  }
+  leave_sums<T, U, WARPS>(a, acc, c0, left, warp, lane);
 }
 
 // ------------------------------------------------------------------ host side
@@ -399,10 +567,65 @@ unsigned norm_grid(const NormShape &n, int64_t rows, int sms, int per_sm) {
   return static_cast<unsigned>(std::min<int64_t>((rows + at_once - 1) / at_once, int64_t(sms) * per_sm));
 }
 
-// CTAs of the backward kernel, each of which leaves a row of partial sums.
-unsigned backward_ctas(int64_t rows, int64_t cols, int type, int sms) {
-  const NormShape n = norm_shape(cols, type);
-  return norm_grid(n, rows, sms, norm_back_ctas(n.u, n.warps));
+// The backward pass through the ring: fewer warps with more pieces, two CTAs to an SM where they fit.
+NormShape ring_shape(int64_t cols, int type) {
+  const int64_t piece = 32 * 16 / type_bytes(type);
+  const int pieces = static_cast<int>((cols + piece - 1) / piece);
+  if (pieces <= 8) return norm_shape(cols, type);
+  if (pieces <= 32) return {(pieces + 7) / 8, 8, 8};
+  return {pieces <= 48 ? 3 : pieces <= 64 ? 4 : 8, 16, 16};
+}
+
+template <int T, typename F>
+tlg_status with_ring_shape(const NormShape &n, F f) {
+  using W8 = std::integral_constant<int, 8>;
+  using W16 = std::integral_constant<int, 16>;
+  using U1 = std::integral_constant<int, 1>;
+  using U2 = std::integral_constant<int, 2>;
+  using U3 = std::integral_constant<int, 3>;
+  using U4 = std::integral_constant<int, 4>;
+  if (n.warps == 8) return n.u == 1 ? f(U1(), W8()) : n.u == 2 ? f(U2(), W8()) : n.u == 3 ? f(U3(), W8()) : f(U4(), W8());
+  if constexpr (T == kTypeF32) {
+    if (n.u == 8) return f(std::integral_constant<int, 8>(), W16());
+  }
+  return n.u == 3 ? f(U3(), W16()) : f(U4(), W16());
+}
+
+// CTAs of the backward kernels, each of which leaves a row of partial sums.
+unsigned ring_ctas(const NormShape &n, int64_t rows, int sms) {
+  return norm_grid(n, rows, sms, n.warps != 8 ? 1 : n.u == 1 ? 4 : 2);
+}
+
+unsigned odd_ctas(const NormShape &n, int64_t rows, int sms) { return norm_grid(n, rows, sms, n.warps == 8 ? 2 : 1); }
+
+// Workspace bytes of their partial sums; the caller does not know which matrices will be aligned.
+size_t norm_workspace(int64_t rows, int64_t cols, int type, int sms) {
+  const unsigned ctas = std::max(ring_ctas(ring_shape(cols, type), rows, sms), odd_ctas(norm_shape(cols, type), rows, sms));
+  return ctas > 1 ? static_cast<size_t>(ctas) * static_cast<size_t>(cols) * 4 : 0;
+}
+
+template <int T, bool WORDS, int U, int WARPS>
+tlg_status launch_ring(int dev, unsigned ctas, cudaStream_t s, const NormBackArgs &a) {
+  constexpr auto kernel = norm_backward_ring_kernel<T, WORDS, U, WARPS>;
+  constexpr int kBytes = NormRing<T, U, WARPS>::kDynamicBytes;
+  static bool ready[kMaxDevices];
+  static std::mutex mutex;
+  {
+    std::lock_guard<std::mutex> lock(mutex);
+    if (!ready[dev]) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess) {
+        cudaGetLastError();
+        return TLG_ERR_CUDA;
+      }
+      ready[dev] = true;
+    }
+  }
+  return launch(kernel, dim3(ctas), 32 * WARPS, s, kBytes, a);
+}
+
+// Whether every row starts on 4 bytes.
+bool word_rows(const void *p, int64_t rows, int64_t ld, int type) {
+  return reinterpret_cast<uintptr_t>(p) % 4 == 0 && (rows == 1 || (ld * type_bytes(type)) % 4 == 0);
 }
 
 tlg_status check_norm(int64_t rows, int64_t cols, int type) {
@@ -471,9 +694,9 @@ tlg_status norm_forward(int64_t rows, int64_t cols, int type, const void *X, int
         constexpr int kU = decltype(U)::value, kW = decltype(W)::value;
         constexpr bool kV = decltype(V)::value;
         cudaStream_t s = static_cast<cudaStream_t>(stream);
-        if (format < 0) return launch(norm_forward_kernel<kT, kV, kU, kW, -1>, dim3(grid), 32 * kW, s, a);
-        if (format == TLG_MX_E2M1) return launch(norm_forward_kernel<kT, kV, kU, kW, kE2M1>, dim3(grid), 32 * kW, s, a);
-        return launch(norm_forward_kernel<kT, kV, kU, kW, kE4M3>, dim3(grid), 32 * kW, s, a);
+        if (format < 0) return launch(norm_forward_kernel<kT, kV, kU, kW, -1>, dim3(grid), 32 * kW, s, 0, a);
+        if (format == TLG_MX_E2M1) return launch(norm_forward_kernel<kT, kV, kU, kW, kE2M1>, dim3(grid), 32 * kW, s, 0, a);
+        return launch(norm_forward_kernel<kT, kV, kU, kW, kE4M3>, dim3(grid), 32 * kW, s, 0, a);
       });
     });
   });
@@ -508,8 +731,7 @@ tlg_status tlg_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols, tlg_t
   DeviceInfo info;
   const tlg_status ds = current_device(&dev, &info);
   if (ds != TLG_OK) return ds;
-  const unsigned ctas = backward_ctas(rows, cols, type, info.sm_count);
-  *bytes = ctas > 1 ? static_cast<size_t>(ctas) * static_cast<size_t>(cols) * 4 : 0;
+  *bytes = norm_workspace(rows, cols, type, info.sm_count);
   return TLG_OK;
 }
 
@@ -558,30 +780,42 @@ tlg_status tlg_rmsnorm_backward(int64_t rows, int64_t cols, tlg_type type, const
   if (meets(rw, rk)) return TLG_ERR_INVALID_ARG;
   st = device_ready({dY, H, weight, rstd, dH, dX, dweight, workspace}, &info);
   if (st != TLG_OK) return st;
-  const unsigned ctas = backward_ctas(rows, cols, type, info.sm_count);
+  int dev = 0;
+  st = current_device(&dev, &info);
+  if (st != TLG_OK) return st;
+  auto rows_are = [&](bool (*fit)(const void *, int64_t, int64_t, int), const void *w) {
+    return fit(w, 1, 0, type) && fit(dY, rows, lddy, type) && fit(H, rows, ldh, type) &&
+           (dH == nullptr || fit(dH, rows, lddh, type)) && fit(dX, rows, lddx, type);
+  };
+  const bool vec = rows_are(vec_rows, weight), words = rows_are(word_rows, weight);
+  const NormShape n = vec || words ? ring_shape(cols, type) : norm_shape(cols, type);
+  const unsigned ctas = vec || words ? ring_ctas(n, rows, info.sm_count) : odd_ctas(n, rows, info.sm_count);
   float *part = dweight;
   if (dweight != nullptr && ctas > 1) {
-    if (workspace == nullptr || workspace_bytes < static_cast<size_t>(ctas) * static_cast<size_t>(cols) * 4)
-      return TLG_ERR_INVALID_ARG;
+    if (workspace == nullptr || workspace_bytes < norm_workspace(rows, cols, type, info.sm_count)) return TLG_ERR_INVALID_ARG;
     part = static_cast<float *>(workspace);
   }
-  const NormShape n = norm_shape(cols, type);
   const NormBackArgs a = {{dY, lddy}, {H, ldh}, {dH, lddh}, {dX, lddx}, weight, rstd, part, rows, static_cast<int>(cols), n.nw};
-  const bool vec = aligned16(weight) && vec_rows(dY, rows, lddy, type) && vec_rows(H, rows, ldh, type) &&
-                   vec_or_none(dH, rows, lddh, type) && vec_rows(dX, rows, lddx, type);
   st = with_type(type, [&](auto T) {
     constexpr int kT = decltype(T)::value;
-    return with_flag(vec, [&](auto V) {
+    if (vec || words) {
+      return with_ring_shape<kT>(n, [&](auto U, auto W) {
+        constexpr int kU = decltype(U)::value, kW = decltype(W)::value;
+        return vec ? launch_ring<kT, false, kU, kW>(dev, ctas, s, a) : launch_ring<kT, true, kU, kW>(dev, ctas, s, a);
+      });
+    }
+    if constexpr (kT != kTypeF32) {
       return with_shape<kT>(n, [&](auto U, auto W) {
         constexpr int kU = decltype(U)::value, kW = decltype(W)::value;
-        return launch(norm_backward_kernel<kT, decltype(V)::value, kU, kW>, dim3(ctas), 32 * kW, s, a);
+        return launch(norm_backward_odd_kernel<kT, kU, kW>, dim3(ctas), 32 * kW, s, 0, a);
       });
-    });
+    }
+    return TLG_ERR_ALIGNMENT;  // fp32 rows are aligned to words
   });
   if (st != TLG_OK || part == dweight) return st;
   const dim3 sum_grid(static_cast<unsigned>((cols + 31) / 32));
-  return ctas > 128 ? launch(column_sum_kernel<32>, sum_grid, 1024, s, part, static_cast<int>(ctas), cols, dweight)
-                    : launch(column_sum_kernel<8>, sum_grid, 256, s, part, static_cast<int>(ctas), cols, dweight);
+  return ctas > 128 ? launch(column_sum_kernel<32>, sum_grid, 1024, s, 0, part, static_cast<int>(ctas), cols, dweight)
+                    : launch(column_sum_kernel<8>, sum_grid, 256, s, 0, part, static_cast<int>(ctas), cols, dweight);
 }
 
 }  // extern "C"

@@ -255,10 +255,11 @@ MxMat mx_mat(const void *Q, int64_t ldq, const void *S, int64_t cols) {
 // here waits for that one to complete before it touches memory, so only launch latency and
 // set-up overlap.
 template <typename... P, typename... A>
-tlg_status launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
+tlg_status launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, int smem, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
