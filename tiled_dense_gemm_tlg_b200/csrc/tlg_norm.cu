@@ -32,6 +32,8 @@ struct NormShape {
   int u, warps, nw;
 };
 
+// Eight warps with more pieces rather than sixteen, so that an SM has several CTAs whose barriers do not meet
+// (1000 x 3001 fp32, forward: 17.8 us with sixteen warps of two pieces).
 NormShape norm_shape(int64_t cols, int type) {
   const int64_t piece = 32 * 16 / type_bytes(type);
   const int pieces = static_cast<int>((cols + piece - 1) / piece);
@@ -40,14 +42,13 @@ NormShape norm_shape(int64_t cols, int type) {
     while (nw < pieces) nw *= 2;
     return {1, 8, nw};
   }
-  if (pieces <= 16) return {2, 8, 8};
-  if (pieces <= 32) return {2, 16, 16};
-  return {pieces <= 64 ? 4 : 8, 16, 16};
+  if (pieces <= 32) return {(pieces + 7) / 8, 8, 8};
+  return {pieces <= 48 ? 3 : pieces <= 64 ? 4 : 8, 16, 16};
 }
 
 // Rows are loaded a row ahead where the registers hold two.
 template <int U>
-constexpr bool kNormAhead = U <= 2;
+constexpr bool kNormAhead = U <= 4;
 
 // A lane's part of one row: U pieces of 32 lanes x 16 bytes side by side, as loaded.
 template <int U>
@@ -137,7 +138,7 @@ __device__ __forceinline__ float row_sum(float x, int warp, int lane, int nw, fl
 }
 
 // CTAs of an SM: what the registers of a row, and of the next, allow.
-constexpr int norm_ctas(int u, int warps) { return warps == 8 ? 4 : u <= 2 ? 2 : 1; }
+constexpr int norm_ctas(int u, int warps, bool vec) { return warps != 8 ? 1 : u <= 2 && vec ? 4 : 2; }
 
 struct NormArgs {
   RowMat x, r, h, y;  // r.p, h.p: may be nullptr
@@ -151,7 +152,7 @@ struct NormArgs {
 
 // FMT: kE2M1 or kE4M3 for an MX matrix, -1 for Y in the inputs' type.
 template <int T, bool VEC, int U, int WARPS, int FMT>
-__global__ void __launch_bounds__(32 * WARPS, VEC ? norm_ctas(U, WARPS) : 1) norm_forward_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(32 * WARPS, norm_ctas(U, WARPS, VEC)) norm_forward_kernel(const NormArgs a) {
   constexpr int E = kLaneElems<T>, kPiece = 32 * E;
   __shared__ __align__(16) uint32_t stage_all[VEC ? 1 : WARPS][128];
   __shared__ float sums[2][WARPS];
@@ -272,7 +273,8 @@ __device__ __forceinline__ void leave_sums(const NormBackArgs &a, const float (&
   float *part = a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
   if constexpr (U == 1) {
 #pragma unroll
-    for (int j = 0; j < E; ++j) columns[warp][lane * E + j] = acc[0][j];
+    for (int j = 0; j < E; j += 4)
+      *reinterpret_cast<float4 *>(&columns[warp][lane * E + j]) = make_float4(acc[0][j], acc[0][j + 1], acc[0][j + 2], acc[0][j + 3]);
     __syncthreads();
     for (int c = threadIdx.x; c < a.cols; c += 32 * WARPS) {
       float t = 0.0f;
@@ -283,9 +285,15 @@ __device__ __forceinline__ void leave_sums(const NormBackArgs &a, const float (&
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
+      for (int j = 0; j < E; j += 4) {
         const int c = u * kPiece + lane * E + j;
-        if (c < left) part[c0 + c] = acc[u][j];
+        if (a.cols % 4 == 0 && reinterpret_cast<uintptr_t>(a.part) % 16 == 0) {
+          if (c < left) *reinterpret_cast<float4 *>(part + c0 + c) = make_float4(acc[u][j], acc[u][j + 1], acc[u][j + 2], acc[u][j + 3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (c + k < left) part[c0 + c + k] = acc[u][j + k];
+        }
       }
   }
 }
@@ -554,32 +562,6 @@ template <int T, typename F>
 tlg_status with_shape(const NormShape &n, F f) {
   using W8 = std::integral_constant<int, 8>;
   using W16 = std::integral_constant<int, 16>;
-  if (n.u == 1) return f(std::integral_constant<int, 1>(), W8());
-  if (n.u == 2) return n.warps == 8 ? f(std::integral_constant<int, 2>(), W8()) : f(std::integral_constant<int, 2>(), W16());
-  if constexpr (T == kTypeF32) {
-    if (n.u == 8) return f(std::integral_constant<int, 8>(), W16());
-  }
-  return f(std::integral_constant<int, 4>(), W16());
-}
-
-unsigned norm_grid(const NormShape &n, int64_t rows, int sms, int per_sm) {
-  const int64_t at_once = n.warps / n.nw;
-  return static_cast<unsigned>(std::min<int64_t>((rows + at_once - 1) / at_once, int64_t(sms) * per_sm));
-}
-
-// The backward pass through the ring: fewer warps with more pieces, two CTAs to an SM where they fit.
-NormShape ring_shape(int64_t cols, int type) {
-  const int64_t piece = 32 * 16 / type_bytes(type);
-  const int pieces = static_cast<int>((cols + piece - 1) / piece);
-  if (pieces <= 8) return norm_shape(cols, type);
-  if (pieces <= 32) return {(pieces + 7) / 8, 8, 8};
-  return {pieces <= 48 ? 3 : pieces <= 64 ? 4 : 8, 16, 16};
-}
-
-template <int T, typename F>
-tlg_status with_ring_shape(const NormShape &n, F f) {
-  using W8 = std::integral_constant<int, 8>;
-  using W16 = std::integral_constant<int, 16>;
   using U1 = std::integral_constant<int, 1>;
   using U2 = std::integral_constant<int, 2>;
   using U3 = std::integral_constant<int, 3>;
@@ -591,6 +573,11 @@ tlg_status with_ring_shape(const NormShape &n, F f) {
   return n.u == 3 ? f(U3(), W16()) : f(U4(), W16());
 }
 
+unsigned norm_grid(const NormShape &n, int64_t rows, int sms, int per_sm) {
+  const int64_t at_once = n.warps / n.nw;
+  return static_cast<unsigned>(std::min<int64_t>((rows + at_once - 1) / at_once, int64_t(sms) * per_sm));
+}
+
 // CTAs of the backward kernels, each of which leaves a row of partial sums.
 unsigned ring_ctas(const NormShape &n, int64_t rows, int sms) {
   return norm_grid(n, rows, sms, n.warps != 8 ? 1 : n.u == 1 ? 4 : 2);
@@ -600,7 +587,8 @@ unsigned odd_ctas(const NormShape &n, int64_t rows, int sms) { return norm_grid(
 
 // Workspace bytes of their partial sums; the caller does not know which matrices will be aligned.
 size_t norm_workspace(int64_t rows, int64_t cols, int type, int sms) {
-  const unsigned ctas = std::max(ring_ctas(ring_shape(cols, type), rows, sms), odd_ctas(norm_shape(cols, type), rows, sms));
+  const NormShape n = norm_shape(cols, type);
+  const unsigned ctas = std::max(ring_ctas(n, rows, sms), odd_ctas(n, rows, sms));
   return ctas > 1 ? static_cast<size_t>(ctas) * static_cast<size_t>(cols) * 4 : 0;
 }
 
@@ -686,7 +674,9 @@ tlg_status norm_forward(int64_t rows, int64_t cols, int type, const void *X, int
                 static_cast<int>(cols), n.nw};
   const bool vec = aligned16(weight) && vec_rows(X, rows, ldx, type) && vec_or_none(R, rows, ldr, type) &&
                    vec_or_none(H, rows, ldh, type) && vec_or_none(Y, rows, ldy, type);
-  const unsigned grid = norm_grid(n, rows, info.sm_count, norm_ctas(n.u, n.warps));
+  // Few rows: a CTA for each, which loads no row ahead of its own (1000 x 3000 fp32: 8.7 us, 13.6 with 296).
+  const int per_sm = norm_ctas(n.u, n.warps, vec);
+  const unsigned grid = norm_grid(n, rows, info.sm_count, (vec || type == TLG_TYPE_F32) && rows * n.nw <= 64 * int64_t(info.sm_count) ? 64 : per_sm);
   return with_type(type, [&](auto T) {
     constexpr int kT = decltype(T)::value;
     return with_flag(vec, [&](auto V) {
@@ -788,7 +778,7 @@ tlg_status tlg_rmsnorm_backward(int64_t rows, int64_t cols, tlg_type type, const
            (dH == nullptr || fit(dH, rows, lddh, type)) && fit(dX, rows, lddx, type);
   };
   const bool vec = rows_are(vec_rows, weight), words = rows_are(word_rows, weight);
-  const NormShape n = vec || words ? ring_shape(cols, type) : norm_shape(cols, type);
+  const NormShape n = norm_shape(cols, type);
   const unsigned ctas = vec || words ? ring_ctas(n, rows, info.sm_count) : odd_ctas(n, rows, info.sm_count);
   float *part = dweight;
   if (dweight != nullptr && ctas > 1) {
@@ -799,7 +789,7 @@ tlg_status tlg_rmsnorm_backward(int64_t rows, int64_t cols, tlg_type type, const
   st = with_type(type, [&](auto T) {
     constexpr int kT = decltype(T)::value;
     if (vec || words) {
-      return with_ring_shape<kT>(n, [&](auto U, auto W) {
+      return with_shape<kT>(n, [&](auto U, auto W) {
         constexpr int kU = decltype(U)::value, kW = decltype(W)::value;
         return vec ? launch_ring<kT, false, kU, kW>(dev, ctas, s, a) : launch_ring<kT, true, kU, kW>(dev, ctas, s, a);
       });
