@@ -24,7 +24,7 @@
 //               fills with zeros only past the end of the whole matrix; a product with 0 would keep
 //               a NaN) in both operands before the MMAs read them
 //   warps 4-    epilogue: two (fp32: four) to a quarter of the lanes, taking its 32-column pieces in turn
-//   the last 4  plain-load builds only: loads for operands that TMA cannot describe
+//   the last 8  plain-load builds only: loads for operands that TMA cannot describe
 //
 // The tensor core's adder truncates: over a long sum the accumulator falls short by about 2e-8 of its
 // size per MMA (1.2e-6 at K = 1000, 2e-5 at 16384), more than an fp32 result should lose.  Builds
@@ -39,6 +39,7 @@ namespace tlg {
 constexpr int kGroupedN = 0, kGroupedT = 1, kGroupedDw = 2;  // B stored K x N, N x K; the gradient of B
 constexpr int kGroupedMax = 1024;  // groups
 constexpr int kGroupedEpiWarp = 4;
+constexpr int kGroupedLoaders = 8;  // warps of the plain-load builds
 constexpr int kGroupedListed = 64;  // tiles of a unit worked out in advance
 constexpr int kGroupedSpan = 8;    // k-blocks summed in TMEM for an fp32 output
 
@@ -47,7 +48,7 @@ template <int OUT, int BN, bool LSU>
 struct GroupedRoles {
   static constexpr int kEpiWarps = OUT == kTypeF32 && BN > 64 ? 16 : 8;
   static constexpr int kLoader = kGroupedEpiWarp + kEpiWarps;
-  static constexpr int kThreads = 32 * (kLoader + (LSU ? kLoaderWarps : 0));
+  static constexpr int kThreads = 32 * (kLoader + (LSU ? kGroupedLoaders : 0));
 };
 
 struct GroupedParams {
@@ -193,32 +194,75 @@ __device__ __forceinline__ constexpr uint32_t grouped_idesc(int m, bool a_mn, bo
   return make_idesc_f16(m, 0, a_mn, b_mn) | (TYPE == kTypeBF16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
-// Fills one operand tile of a slot with plain loads: `count` (a multiple of 4) M or N indices by 64 k,
-// zeros past the limits.  K-major: a warp takes a row of 64 k at a time; MN-major: a k's row, 64 at a time.
-template <bool MN>
-__device__ __forceinline__ void grouped_fill(uint32_t dst, const uint16_t *base, int64_t ld, int count, int mn_left,
-                                             int k_left, int warp, int lane) {
-  constexpr int kBatch = 8;
-  const int items = MN ? ceil_div(count, 64) * 64 : count;  // rows of 64 elements, 2 to a lane
-  const int inner = lane * 2;
-  for (int i0 = warp; i0 < items; i0 += kLoaderWarps * kBatch) {
-    uint32_t w[kBatch];
+// Predicated read-only global load of a 32-bit word (0 when !pred).
+__device__ __forceinline__ uint32_t ld_u32_pred(const void *ptr, bool pred) {
+  uint32_t x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "@p ld.global.nc.u32 %0, [%1];\n\t}"
+      : "=r"(x)
+      : "l"(ptr), "r"(static_cast<uint32_t>(pred)));
+  return x;
+}
+
+// Fills one operand tile of a slot with plain loads: `count` M or N indices by 64 k, zeros past the limits.
+// A warp takes rows of 64 consecutive elements, two to a lane (K-major: an index's 64 k; MN-major: a k's 64
+// indices), sixteen rows' loads in flight at once.  Words are read whole: in a row that starts in the middle
+// of one, word l holds elements 2l - 1 and 2l, and lane 0 reads the row's first and last element one by one.
+// EVEN: every row starts on a word and is a whole number of words.
+template <bool MN, bool EVEN>
+__device__ __forceinline__ void grouped_fill_rows(uint32_t dst, const uint16_t *base, int64_t ld, int items, int mn_left,
+                                                  int k_left, int warp, int lane) {
+  constexpr int kBatch = EVEN ? 16 : 8;
+  for (int i0 = warp; i0 < items; i0 += kGroupedLoaders * kBatch) {
+    uint32_t w[kBatch], l[EVEN ? 1 : kBatch], h[EVEN ? 1 : kBatch], odd = 0;
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + b * kLoaderWarps;
-      const int k = MN ? i & 63 : inner, mn = MN ? (i >> 6) * 64 + inner : i;
-      const bool lo = i < items && mn < mn_left && k < k_left;
-      const bool hi = i < items && (MN ? mn + 1 < mn_left && k < k_left : mn < mn_left && k + 1 < k_left);
-      const uint16_t *q = base + (lo ? (MN ? k * ld + mn : mn * ld + k) : 0);
-      w[b] = ld_u16_pred(q, lo) | ld_u16_pred(q + (hi ? 1 : 0), hi) << 16;
+      const int i = i0 + b * kGroupedLoaders;
+      const int at = MN ? i & 63 : i;                     // row of the operand
+      const int first = MN ? (i >> 6) * 64 : 0;           // its first element
+      const bool in = i < items && at < (MN ? k_left : mn_left);
+      const int left = in ? (MN ? mn_left : k_left) - first : 0;
+      const uint16_t *q = base + (in ? at * ld + first : 0);
+      w[b] = 0;
+      if constexpr (EVEN) {
+        if (2 * lane < left) w[b] = __ldg(reinterpret_cast<const uint32_t *>(q) + lane);
+      } else {
+        const bool inside = (reinterpret_cast<uintptr_t>(q) & 2) != 0;
+        odd |= static_cast<uint32_t>(inside) << b;
+        const int e = 2 * lane - (inside ? 1 : 0);
+        const bool apart = inside && lane == 0;
+        // predicated, not branched around: the batch's loads stay in flight together
+        w[b] = ld_u32_pred(q + e, !apart && e + 1 < left);
+        l[b] = ld_u16_pred(q + (apart ? 63 : e), apart ? 63 < left : e + 1 == left);
+        h[b] = ld_u16_pred(q, apart && left > 0);
+      }
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + b * kLoaderWarps;
-      const int k = MN ? i & 63 : inner, mn = MN ? (i >> 6) * 64 + inner : i;
+      const int i = i0 + b * kGroupedLoaders;
+      if constexpr (!EVEN) {
+        w[b] |= l[b] | h[b] << 16;
+        const uint32_t next = __shfl_sync(0xffffffffu, w[b], (lane + 1) & 31);
+        w[b] = (odd >> b & 1u) != 0 ? __funnelshift_r(w[b], next, 16) : w[b];
+      }
+      const int at = MN ? i & 63 : i, first = MN ? (i >> 6) * 64 : 0;
+      const int k = MN ? at : 2 * lane, mn = MN ? first + 2 * lane : at;
       if (i < items) st_shared_u32(dst + (MN ? mnmajor_offset(mn, k) : kmajor_offset(mn, k)), w[b]);
     }
   }
+}
+
+template <bool MN>
+__device__ __forceinline__ void grouped_fill(uint32_t dst, const uint16_t *base, int64_t ld, int count, int mn_left,
+                                             int k_left, int warp, int lane) {
+  const int items = MN ? ceil_div(count, 64) * 64 : count;
+  if ((reinterpret_cast<uintptr_t>(base) & 2) == 0 && ld % 2 == 0 && (MN ? mn_left : k_left) % 2 == 0)
+    grouped_fill_rows<MN, true>(dst, base, ld, items, mn_left, k_left, warp, lane);
+  else
+    grouped_fill_rows<MN, false>(dst, base, ld, items, mn_left, k_left, warp, lane);
 }
 
 // KSPLIT: a cluster of 2, 4 or 8 CTAs (its size) shares the K range of one tile, for calls with so few tiles
@@ -272,7 +316,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       // The gradient's tail is announced by each CTA's tail warp, so its other slots take as many arrivals.
-      mbar_init(full_bar(s), LSU ? kLoaderWarps : kDw ? CG : 1);
+      mbar_init(full_bar(s), LSU ? kGroupedLoaders : kDw ? CG : 1);
       mbar_init(empty_bar(s), 1);
       mbar_init(tail_bar(s), 1);
     }
