@@ -3,7 +3,7 @@
 //   C = act(X . W^T + bias) + residual,  W[n, k] = (q[n, k] - z[n, k / group]) s[n, k / group]
 //
 // Reading the weights (half a byte each) is all the work there is for one token, so the kernel is built
-// around a stream of weights: a CTA takes a block of W's rows, its eight warps share K in units of 256
+// around a stream of weights: a CTA takes a block of W's rows, its warps share K in units of 256
 // or 128, and TMA brings their units (128 or 64 bytes of a row, and the tokens' elements) into a ring of each
 // group of warps, without any barrier across the CTA until the groups' sums are added at the end.
 //
@@ -238,15 +238,16 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
     // scales and zero points of the panel, 0 past the last row: a warp takes an eighth of the rows, all
     // loads of 32 groups in flight at once
     const int held = min(p.groups - first_group, kQ4Panel);
-    for (int j = lane; j < held; j += 32) {
+    for (int j = lane; j < kQ4Panel; j += 32) {
+      if (j >= (held + 7) / 8 * 8) break;  // a unit's blocks past K have no group: their scale is 0
       constexpr int kMine = kRows / kQ4Warps;
       uint32_t v[kMine], z[kMine];
 #pragma unroll
       for (int r = 0; r < kMine; ++r) {
         const int n = n0 + warp * kMine + r;
         const int64_t at = static_cast<int64_t>(n) * p.groups + first_group + j;
-        v[r] = n < p.N ? p.S[at] : 0u;
-        z[r] = n < p.N && p.Z != nullptr ? p.Z[at] : 8u;
+        v[r] = n < p.N && j < held ? p.S[at] : 0u;
+        z[r] = n < p.N && j < held && p.Z != nullptr ? p.Z[at] : 8u;
       }
 #pragma unroll
       for (int r = 0; r < kMine; ++r) scales[(warp * kMine + r) * Plan::kScaleLd + j] = v[r] | (z[r] & 15u) << 16;
@@ -268,19 +269,19 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
         group_sync();
       }
       const uint32_t w = w_slot(slot) + w_at, x = x_slot(slot) + x_at;
+      const uint32_t *unit_scales = scales + (wr * 16 * R + g) * Plan::kScaleLd + ((u * kUnit) >> p.group_log2) - first_group;
       float acc[R][NC][4];
       uint32_t zero[R][2];
       float scale[R][2];
 #pragma unroll
       for (int c = 0; c < Plan::kBlocks; ++c) {
         if (c % GC == 0) {
-          const int j = ((u * kUnit + c * 32) >> p.group_log2) - first_group;
-          const uint32_t *s = scales + wr * 16 * R * Plan::kScaleLd + min(j, held - 1);  // blocks past K have no group; their X is 0
+          const uint32_t *s = unit_scales + (GC < 4 ? c / GC : (c * 32) >> p.group_log2);
 #pragma unroll
           for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t v = s[(r * 16 + h * 8 + g) * Plan::kScaleLd];
+              const uint32_t v = s[(r * 16 + h * 8) * Plan::kScaleLd];
               zero[r][h] = kMagic + (v >> 16) * 0x10001u;
               float none;
               unpack2<T>(v, scale[r][h], none);
@@ -437,9 +438,10 @@ tlg_status launch_q4_group(int dev, const Q4Params &p, cudaStream_t s) {
 
 template <int T>
 tlg_status launch_q4_shape(int dev, int sms, const Q4Params &p, cudaStream_t s) {
-  if (p.M == 1) return p.N >= 64 * sms ? launch_q4_group<T, 0, 2, 8>(dev, p, s) : launch_q4_group<T, 0, 1, 8>(dev, p, s);
-  if (p.M <= 8) return p.N >= 64 * sms ? launch_q4_group<T, 1, 2, 4>(dev, p, s) : launch_q4_group<T, 1, 1, 8>(dev, p, s);
-  return p.N >= 64 * sms ? launch_q4_group<T, 2, 2, 4>(dev, p, s) : launch_q4_group<T, 2, 1, 8>(dev, p, s);
+  const bool wide = p.N >= 64 * sms;
+  if (p.M == 1) return wide ? launch_q4_group<T, 0, 2, 4>(dev, p, s) : launch_q4_group<T, 0, 1, 8>(dev, p, s);
+  if (p.M <= 8) return wide ? launch_q4_group<T, 1, 2, 4>(dev, p, s) : launch_q4_group<T, 1, 1, 8>(dev, p, s);
+  return wide ? launch_q4_group<T, 2, 2, 4>(dev, p, s) : launch_q4_group<T, 2, 1, 8>(dev, p, s);
 }
 
 }  // namespace
