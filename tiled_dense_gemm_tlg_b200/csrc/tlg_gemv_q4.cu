@@ -47,7 +47,8 @@ struct Q4Params {
   int64_t ldx;
   int M, N, K;
   int group_log2, groups;
-  int x_vec;  // X may be copied 16 bytes at a time
+  int x_vec;  // X may be read 16 bytes at a time
+  int x_tma;  // and comes by TMA
   int token_blocks;
   void *C;
   int64_t ldc;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
     if (warp == 0) *abort_flag = 0u;
     fence_mbar_init();
     if (p.K > 0) tma_prefetch_desc(&tmW);
-    if (p.K > 0 && p.x_vec) tma_prefetch_desc(&tmX);
+    if (p.K > 0 && p.x_tma) tma_prefetch_desc(&tmX);
   }
   __syncthreads();
   grid_dependency_wait();
@@ -162,13 +163,15 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
 
   const int units = (p.K + kUnit - 1) / kUnit;
   const int mine = units > wk ? (units - wk + WK - 1) / WK : 0;  // units wk, wk + WK, ..
+  // X comes by TMA where it may and the unit is whole.
+  auto tma_x = [&](int i) { return p.x_tma != 0 && (wk + i * WK + 1) * kUnit <= p.K; };
   // One lane of the group asks for its i-th unit; TMA fills with zeros what lies outside the matrices.
   auto issue = [&](int i, int slot) {
     const int k = (wk + i * WK) * kUnit;
     const uint32_t bar = full_bar(slot);
-    mbar_arrive_expect_tx(bar, Plan::kWBytes + (p.x_vec ? Plan::kXBytes : 0u));
+    mbar_arrive_expect_tx(bar, Plan::kWBytes + (tma_x(i) ? Plan::kXBytes : 0u));
     tma_load_2d(w_slot(slot), &tmW, bar, k / 2, n0);
-    if (p.x_vec) {
+    if (tma_x(i)) {
       if constexpr (NT == 0) {
         tma_load_2d(x_slot(slot), &tmX, bar, k, token0);
       } else {
@@ -182,26 +185,42 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
   if (issuer) {
     for (int i = 0; i < min(ST, mine); ++i) issue(i, i);
   }
-  // Without TMA (X at odd places): the group's lanes write the unit's X as TMA would have.
+  // Without TMA: the group's lanes write the unit's X as TMA would have.
   auto fill_x = [&](int i, int slot) {
     constexpr int kPieces = kUnit / 8;  // of 16 bytes, of a token
+    constexpr int kMine = (Plan::kTokens * kPieces + WR * 32 - 1) / (WR * 32), kBatch = kMine < 8 ? kMine : 8;
     const uint32_t x = x_slot(slot);
     const int k0 = (wk + i * WK) * kUnit;
-#pragma unroll 2
-    for (int e = wr * 32 + lane; e < Plan::kTokens * kPieces; e += WR * 32) {
-      const int m = e / kPieces, q = e % kPieces, k = k0 + q * 8;
-      const uint16_t *from = p.X + static_cast<int64_t>(token0 + m) * p.ldx + k;
-      const int left = m < tokens ? min(max(p.K - k, 0), 8) : 0;
-      uint32_t v[4];
+    for (int b0 = 0; b0 < kMine; b0 += kBatch) {
+      uint4 v[kBatch];  // a batch's loads are in flight together
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = ld_u16_pred(from + 2 * j, 2 * j < left) | ld_u16_pred(from + 2 * j + 1, 2 * j + 1 < left) << 16;
-      const uint32_t to = NT == 0 ? x + q * 16
-                                  : x + (q >> 3) * Plan::kXBox + static_cast<uint32_t>(m * 128 + (((q & 7) ^ (m & 7)) * 16));
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                   : "memory");
+      for (int b = 0; b < kBatch; ++b) {
+        const int e = (b0 + b) * WR * 32 + wr * 32 + lane, m = e / kPieces, k = k0 + e % kPieces * 8;
+        const uint16_t *from = p.X + static_cast<int64_t>(token0 + m) * p.ldx + k;
+        const int left = m < tokens ? min(max(p.K - k, 0), 8) : 0;
+        v[b] = make_uint4(0, 0, 0, 0);
+        if (p.x_vec && left == 8) {
+          v[b] = __ldg(reinterpret_cast<const uint4 *>(from));
+        } else if (left > 0) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = ld_u16_pred(from + 2 * j, 2 * j < left) | ld_u16_pred(from + 2 * j + 1, 2 * j + 1 < left) << 16;
+          v[b] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int e = (b0 + b) * WR * 32 + wr * 32 + lane, m = e / kPieces, q = e % kPieces;
+        const uint32_t to = NT == 0 ? x + q * 16
+                                    : x + (q >> 3) * Plan::kXBox + static_cast<uint32_t>(m * 128 + (((q & 7) ^ (m & 7)) * 16));
+        if (e < Plan::kTokens * kPieces)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[b].x), "r"(v[b].y), "r"(v[b].z), "r"(v[b].w)
+                       : "memory");
+      }
     }
   };
+  if (mine > 0 && mine <= ST && !tma_x(mine - 1)) fill_x(mine - 1, mine - 1);  // under the wait for the scales
   auto group_sync = [&]() {
     if constexpr (WR == 1)
       __syncwarp();
@@ -264,7 +283,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
       }
       ok = __all_sync(0xffffffffu, ok && mbar_wait(full_bar(slot), phase, abort_flag, kWaitLimitNs, kRoleMma, &g_device_error));
       if (!ok) break;
-      if (!p.x_vec) {
+      if (!tma_x(i) && !(mine <= ST && i == mine - 1)) {
         fill_x(i, slot);
         group_sync();
       }
@@ -406,7 +425,7 @@ tlg_status launch_q4(int dev, Q4Params p, cudaStream_t s) {
                    p.N > 1 ? static_cast<uint64_t>(p.ldq) : row, Plan::kWRow, Plan::kRows,
                    Plan::kBlocks == 8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
       return TLG_ERR_CUDA;
-    if (p.x_vec && !encode_2d(&x, T == kTypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.X,
+    if (p.x_tma && !encode_2d(&x, T == kTypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.X,
                               static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.M),
                               static_cast<uint64_t>(p.M > 1 ? p.ldx : (int64_t(p.K) + 7) / 8 * 8) * 2, NT == 0 ? Plan::kUnit : 64,
                               Plan::kTokens, NT == 0 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
@@ -511,6 +530,9 @@ tlg_status tlg_gemv_q4(int64_t M, int64_t N, int64_t K, tlg_type type, const voi
   p.groups = static_cast<int>(groups);
   while ((int64_t(1) << p.group_log2) < group) ++p.group_log2;
   p.x_vec = aligned16(X) && (M == 1 || ldx % 8 == 0);
+  // Of few tokens TMA is slow to fetch rows that are not whole lines apart (two, 3000 x 1000 weights: 5.0 us, 3.0
+  // with plain loads); of more than eight the plain loads take longer (16, 16384 x 16392: 72 us against 60).
+  p.x_tma = p.x_vec && (M == 1 || M > 8 || ldx % 64 == 0);
   p.C = C;
   p.ldc = ldc;
   p.out_f32 = out == TLG_TYPE_F32;
