@@ -235,6 +235,11 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
   const uint32_t w_at = static_cast<uint32_t>((wr * 16 * R + g) * Plan::kWRow + (Plan::kBlocks == 8 ? g : (g >> 1) & 3) * 16 + t * 4);
   const uint32_t x_at = NT == 0 ? t * 16 : static_cast<uint32_t>(col_token * 128 + (t ^ col_token) * 16);
 
+  // The row whose sums this thread finishes, and its bias, loaded ahead of their use.
+  static_assert(32 * kQ4Warps % kRows == 0, "a thread keeps its row");
+  const int last_row = static_cast<int>(threadIdx.x) % kRows;
+  const float bias = p.bias != nullptr && n0 + last_row < p.N ? load_elem<T>(p.bias, n0 + last_row) : 0.0f;
+
   float total[R][NC][4];
 #pragma unroll
   for (int r = 0; r < R; ++r)
@@ -257,8 +262,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
     // scales and zero points of the panel, 0 past the last row: a warp takes an eighth of the rows, all
     // loads of 32 groups in flight at once
     const int held = min(p.groups - first_group, kQ4Panel);
-    for (int j = lane; j < kQ4Panel; j += 32) {
-      if (j >= (held + 7) / 8 * 8) break;  // a unit's blocks past K have no group: their scale is 0
+    for (int j = lane; j < (held + 7) / 8 * 8; j += 32) {  // a unit's blocks past K have no group: their scale is 0
       constexpr int kMine = kRows / kQ4Warps;
       uint32_t v[kMine], z[kMine];
 #pragma unroll
@@ -266,7 +270,14 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
         const int n = n0 + warp * kMine + r;
         const int64_t at = static_cast<int64_t>(n) * p.groups + first_group + j;
         v[r] = n < p.N && j < held ? p.S[at] : 0u;
-        z[r] = n < p.N && j < held && p.Z != nullptr ? p.Z[at] : 8u;
+        z[r] = 8;
+      }
+      if (p.Z != nullptr) {
+#pragma unroll
+        for (int r = 0; r < kMine; ++r) {
+          const int n = n0 + warp * kMine + r;
+          if (n < p.N && j < held) z[r] = p.Z[static_cast<int64_t>(n) * p.groups + first_group + j];
+        }
       }
 #pragma unroll
       for (int r = 0; r < kMine; ++r) scales[(warp * kMine + r) * Plan::kScaleLd + j] = v[r] | (z[r] & 15u) << 16;
@@ -377,13 +388,13 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
         if (m < tokens) sums[(wk * tokens + m) * kRows + row] = total[r][n][j];
       }
   __syncthreads();
-  for (int i = threadIdx.x; i < tokens * kRows; i += 32 * kQ4Warps) {
-    const int m = i / kRows, row = i - m * kRows, n = n0 + row;
-    if (n >= p.N) continue;
+  const int n = n0 + last_row;
+  if (n >= p.N) return;
+  for (int m = static_cast<int>(threadIdx.x) / kRows; m < tokens; m += 32 * kQ4Warps / kRows) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < WK; ++w) v += sums[(w * tokens + m) * kRows + row];
-    if (p.bias != nullptr) v += load_elem<T>(p.bias, n);
+    for (int w = 0; w < WK; ++w) v += sums[(w * tokens + m) * kRows + last_row];
+    v += bias;
     const int64_t token = token0 + m;
     if (p.out_f32) {
       v = activate<false>(p.act, v);
