@@ -544,8 +544,9 @@ tlg_status tlg_act_backward_mx_workspace_size(int64_t rows, int64_t cols, tlg_ty
  * once after the activation, whose accuracy is tlg_gemm_fused's.
  *
  * offsets: groups + 1 int32 values in device memory, read by the kernel (0 <= groups <= 1024).  They
- * must not decrease; values outside [0, rows] are held to it, and a group that ends before it begins
- * has no rows.  Rows of C before offsets[0] and from offsets[groups] on are left as they were.  K == 0
+ * should not decrease: values outside [0, rows] are held to it, and one that is less than an earlier one
+ * counts as that one.  Rows of C before offsets[0] and from offsets[groups] on are left as they were, and
+ * may hold anything in A.  K == 0
  * gives C = act(0) in the groups' rows.  The input gradient is the same call: dA_g = dC_g . op(B_g)^T
  * takes dC for A and the other op.  A pipeline wait past its time limit is reported by
  * tlg_device_error().

@@ -181,25 +181,32 @@ def test_one_matrix_for_all_groups(tlg):
     check(got, want, err, torch.float16)
 
 
-@pytest.mark.parametrize("offsets", [[0, 50, 30, 64], [-5, 10, 64, 1 << 30], [64, 0, 0, 0], [70, 80, 90, 100]])
-def test_bad_offsets_stay_inside(tlg, offsets):
-    """Values outside [0, rows] are held to it; a group that ends before it begins has no rows."""
+@pytest.mark.parametrize("offsets", [[0, 50, 30, 64], [-5, 10, 64, 1 << 30], [64, 0, 0, 0], [70, 80, 90, 100],
+                                     [9, 3, 20, 15], [-(1 << 31), 1, (1 << 31) - 1, 7]])
+@pytest.mark.parametrize("many", [False, True])
+def test_bad_offsets_stay_inside(tlg, offsets, many):
+    """Values outside [0, rows] are held to it, and one less than an earlier one counts as that one; also where the
+    groups are so many that several warps look at them."""
     rows, k, n = 64, 64, 128
-    A, B = operands(7, rows, k, n, 3, "N", torch.float16)
+    if many:
+        offsets = offsets[:2] * 40 + offsets[2:] + [o - 1 for o in offsets[2:]] * 20
+        offsets = [max(o, -(1 << 31)) for o in offsets]
+    groups = len(offsets) - 1
+    A, B = operands(7, rows, k, n, groups, "N", torch.float16)
     c = Strided(torch.full((rows, n), -7.0, dtype=torch.float16))
     tlg.tlg_gemm_grouped(A.cuda(), B.cuda(), torch.tensor(offsets, dtype=torch.int32).cuda(), C=c.view)
     assert c.guards_kept()
-    held = [min(max(o, 0), rows) for o in offsets]
-    got = c.view.double().cpu()
-    mine = torch.zeros(rows, dtype=torch.bool)
-    for g in range(3):
-        a, e = held[g], held[g + 1]
-        if a < e:
-            mine[a:e] = True
-            want = A[a:e].double() @ B[g].double()
-            if not any(h[0] < e and a < h[1] for i, h in enumerate(zip(held, held[1:])) if i != g and h[0] < h[1]):
-                check(got[a:e], want, 0 * want + 1e-4, torch.float16)
-    assert (got[~mine] == -7).all()
+    held = []
+    for o in offsets:
+        held.append(max(min(max(o, 0), rows), held[-1] if held else 0))
+    sizes = [b - a for a, b in zip(held, held[1:])]
+    want, err = forward(A, B, sizes, held[0], "N", "none")
+    check(c.view[held[0]:held[-1]], want[held[0]:held[-1]], err[held[0]:held[-1]], torch.float16)
+    got = c.view.cpu()
+    assert (got[:held[0]] == -7).all() and (got[held[-1]:] == -7).all()
+    dB = tlg.tlg_gemm_grouped_dw(A.cuda(), A.cuda(), torch.tensor(offsets, dtype=torch.int32).cuda(), out="f32")
+    want, err = backward(A, A, sizes, held[0], "N")
+    check(dB, want, err, torch.float32)
 
 
 def test_many_groups(tlg):

@@ -17,6 +17,7 @@ namespace tlg {
 namespace {
 
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s per pipeline wait
+constexpr int64_t kMostTiles = int64_t(1) << 30;
 constexpr int64_t kMaxStackStride = int64_t(1) << 38;
 
 struct GroupedMaps {
@@ -184,7 +185,7 @@ tlg_status tlg_gemm_grouped(int64_t rows, int64_t N, int64_t K, int32_t groups, 
   p.stride_w = p.shared_w ? 0 : stride_b;
   // At most this many tiles of `bn` rows by `bl` columns.
   auto most = [&](int64_t bn, int64_t bl) { return (rows / bn + std::min<int64_t>(groups, rows)) * ((N + bl - 1) / bl); };
-  if (most(64, 128) > kMaxExtent) return TLG_ERR_UNSUPPORTED;
+  if (most(64, 128) > kMostTiles) return TLG_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   GroupedMaps m;
   const int64_t tlda = tma_ld(rows, K, lda), tldb = tma_ld(b_rows, b_cols, ldb);
@@ -274,7 +275,7 @@ tlg_status tlg_gemm_grouped_dw(int64_t rows, int64_t N, int64_t K, int32_t group
   auto most = [&](int64_t bn, int64_t bl) {
     return int64_t(groups) * ((b_rows + bn - 1) / bn) * ((b_cols + bl - 1) / bl);
   };
-  if (most(128, 128) > kMaxExtent) return TLG_ERR_UNSUPPORTED;
+  if (most(128, 128) > kMostTiles) return TLG_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   GroupedMaps m;
   const int64_t tldw = tma_ld(rows, b_cols, ldw), tldx = tma_ld(rows, b_rows, ldx);

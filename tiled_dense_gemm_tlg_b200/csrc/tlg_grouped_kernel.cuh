@@ -13,7 +13,7 @@
 // In the gradient the lanes are the contiguous index of dB, its other index the MMA's N.
 //
 // Sizes of the groups live on the device.  Every CTA turns them into a table of first tiles in shared
-// memory (two warp scans), and the persistent work units (a CTA, or a CTA pair) walk the list of all
+// memory (warp scans), and the persistent work units (a CTA, or a CTA pair) walk the list of all
 // tiles with the stride of their number.  Finding a tile's group and place takes half a microsecond
 // (divisions, shared memory), which the MMA warp would spend between two tiles, so the warps work out the
 // unit's first kGroupedListed tiles together before the roles begin.
@@ -81,8 +81,8 @@ struct GroupedPlan {
   static constexpr uint32_t kStartOffset = kMiscOffset + 16;                      // first tile of each group
   static constexpr uint32_t kBeginOffset = kStartOffset + (kGroupedMax + 1) * 4;  // first row
   static constexpr uint32_t kSizeOffset = kBeginOffset + kGroupedMax * 4;         // rows
-  static constexpr uint32_t kSumOffset = kSizeOffset + kGroupedMax * 4;           // tiles of 32 groups
-  static constexpr uint32_t kListOffset = (kSumOffset + kGroupedMax / 32 * 4 + 15) / 16 * 16;  // the unit's first tiles
+  static constexpr uint32_t kSumOffset = kSizeOffset + kGroupedMax * 4;           // tiles, and last rows, of 32 groups
+  static constexpr uint32_t kListOffset = (kSumOffset + 2 * kGroupedMax / 32 * 4 + 15) / 16 * 16;  // the unit's first tiles
   static constexpr uint32_t kDynamicBytes = kListOffset + kGroupedListed * 32 + 1024;
   static constexpr uint32_t kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
   static constexpr int kXRows = BN == 64 ? 16 : 32;  // tokens of a small box
@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
   int *begin = reinterpret_cast<int *>(smem + Plan::kBeginOffset);
   int *size = reinterpret_cast<int *>(smem + Plan::kSizeOffset);
   int *sums = reinterpret_cast<int *>(smem + Plan::kSumOffset);
+  int *ends = sums + kGroupedMax / 32;
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
@@ -340,42 +341,71 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
   grid_dependency_wait();  // global memory is touched only after this
   grid_launch_dependents();
 
-  // The table of tiles.  Offsets are held to [0, rows], and a group that ends before it begins has no
-  // rows, so that no offsets lead outside the matrices.
+  // The table of tiles.  Offsets are held to [0, rows], and one that is less than an earlier one counts as
+  // that one: whatever they are, the groups lie in the matrices, do not overlap, and have no more tiles than
+  // the host counted on.  Scans of 32 groups to a warp, then of the warps' results.
   const int lane_tiles = ceil_div(p.lanes, kBM * CG);
   const int blocks = ceil_div(p.groups, 32), num_warps = static_cast<int>(blockDim.x >> 5);
-  for (int b = warp; b < blocks; b += num_warps) {
+  auto held = [&](int i) { return min(max(p.offsets[i], 0), p.rows); };
+  const int first_row = held(0);
+  // The largest end so far among block b's groups.
+  auto scan_ends = [&](int b) {
     const int g = b * 32 + lane;
+    int end = g < p.groups ? held(g + 1) : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) end = max(end, __shfl_up_sync(0xffffffffu, end, d));  // (lane < d: its own)
+    return end;
+  };
+  // Block b's rows and tiles; from: where its first group begins, end: scan_ends.  Returns the sum of tiles.
+  auto place = [&](int b, int from, int end) {
+    const int g = b * 32 + lane;
+    end = max(from, end);
+    int lo = __shfl_up_sync(0xffffffffu, end, 1);
+    if (lane == 0) lo = from;
     int tiles = 0;
     if (g < p.groups) {
-      const int lo = min(max(p.offsets[g], 0), p.rows), hi = min(max(p.offsets[g + 1], 0), p.rows);
       begin[g] = lo;
-      size[g] = max(hi - lo, 0);
-      tiles = grouped_col_tiles<KIND, BN>(p, max(hi - lo, 0)) * lane_tiles;
+      size[g] = end - lo;
+      tiles = grouped_col_tiles<KIND, BN>(p, end - lo) * lane_tiles;
     }
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
       const int v = __shfl_up_sync(0xffffffffu, tiles, d);
       if (lane >= d) tiles += v;
     }
-    if (g < p.groups) start[g + 1] = tiles;  // of this block of 32
-    if (lane == 31) sums[b] = tiles;
-  }
-  __syncthreads();
-  {
-    int before = lane < blocks ? sums[lane] : 0;
-    const int own = before;
+    if (g < p.groups) start[g + 1] = tiles;  // of this block
+    return tiles;
+  };
+  if (threadIdx.x == 0) start[0] = 0;
+  if (blocks == 1) {
+    if (warp == 0) place(0, first_row, scan_ends(0));
+  } else {
+    for (int b = warp; b < blocks; b += num_warps) {
+      const int end = scan_ends(b);
+      if (lane == 31) ends[b] = end;
+    }
+    __syncthreads();
+    int before = lane < blocks ? ends[lane] : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) before = max(before, __shfl_up_sync(0xffffffffu, before, d));
+    for (int b = warp; b < blocks; b += num_warps) {
+      const int from = max(first_row, b > 0 ? __shfl_sync(0xffffffffu, before, b - 1) : 0);
+      const int tiles = place(b, from, scan_ends(b));
+      if (lane == 31) sums[b] = tiles;
+    }
+    __syncthreads();
+    const int own = lane < blocks ? sums[lane] : 0;
+    int add = own;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
-      const int v = __shfl_up_sync(0xffffffffu, before, d);
-      if (lane >= d) before += v;
+      const int v = __shfl_up_sync(0xffffffffu, add, d);
+      if (lane >= d) add += v;
     }
-    before -= own;  // tiles of the blocks before block `lane`
+    add -= own;  // tiles of the blocks before block `lane`
     for (int b = warp; b < blocks; b += num_warps) {
-      const int add = __shfl_sync(0xffffffffu, before, b);
-      if (b * 32 + lane < p.groups) start[b * 32 + lane + 1] += add;
+      const int more = __shfl_sync(0xffffffffu, add, b);
+      if (b * 32 + lane < p.groups) start[b * 32 + lane + 1] += more;
     }
-    if (threadIdx.x == 0) start[0] = 0;
   }
   __syncthreads();
   const int tiles = __shfl_sync(0xffffffffu, start[p.groups], 0);
