@@ -1220,6 +1220,6 @@ const char *tlg_status_string(tlg_status status) {
   return "unknown tlg_status";
 }
 
-int32_t tlg_version(void) { return 200; }
+int32_t tlg_version(void) { return 300; }
 
 }  // extern "C"

@@ -18,6 +18,10 @@
 // A lane holds word t of a 32-element block of rows g and g + 8 (t = lane % 4, g = lane / 4), so a word's eight
 // elements i and i + 4 are pairs of one mma operand register: the k order of the operands is a permutation,
 // the same for X, whose pairs are put together by byte permutes.
+//
+// What bounds it: issue slots, about 50 instructions for 512 weights (16 rows by 32 k), 22 of them the conversion, at
+// 1.8 to 2 a cycle.  bf16, groups of 128, back to back in a graph: one token 4096 x 4096 4.6 us, 16384 x 4096 11.4 us
+// (2.9 TB/s of weights), eight tokens 12.1, sixteen 16.0.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

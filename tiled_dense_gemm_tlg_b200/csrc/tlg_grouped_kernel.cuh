@@ -30,6 +30,12 @@
 // size per MMA (1.2e-6 at K = 1000, 2e-5 at 16384), more than an fp32 result should lose.  Builds
 // with an fp32 output therefore sum at most kGroupedSpan k-blocks in TMEM, and the epilogue warps add
 // those partial sums, rounding to nearest, in registers.  For a 16-bit output it is far below the rounding.
+//
+// What bounds it: at full size operands from L2, 64 KB a pair and k-block at 9 to 10 TB/s (8192 rows, 8 groups of
+// 4096 x 4096, fp16: 212 us, 1.29 PFLOP/s back to back in a graph, the tensor pipe at 92 % of active cycles;
+// under the power cap 253 us); with few rows a group HBM (64 rows over 64 groups of 2048 x 2048: 80 us,
+// 6.7 TB/s).  Stores straight from the registers: a 256 x 256 tile takes 2.8 us of epilogue, beside the next
+// tile's main loop.
 #pragma once
 
 #include "tlg_mxgemm_kernel.cuh"
