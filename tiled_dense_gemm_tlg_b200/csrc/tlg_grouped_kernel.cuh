@@ -344,6 +344,9 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
     tmem_alloc<CG>(smem_u32(misc), Plan::kTmemCols);
     tmem_relinquish<CG>();
   }
+  // The next kernel may start, and take tensor memory, only once this CTA has its own: were it to come first, each
+  // would wait for the other.
+  __syncthreads();
   grid_dependency_wait();  // global memory is touched only after this
   grid_launch_dependents();
 
