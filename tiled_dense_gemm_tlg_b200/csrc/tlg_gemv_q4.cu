@@ -225,6 +225,8 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
     }
   };
   if (mine > 0 && mine <= ST && !tma_x(mine - 1)) fill_x(mine - 1, mine - 1);  // under the wait for the scales
+  // Whether the i-th unit's X is written by the lanes when its turn comes.
+  auto by_lanes = [&](int i) { return !tma_x(i) && !(mine <= ST && i == mine - 1); };
   auto group_sync = [&]() {
     if constexpr (WR == 1)
       __syncwarp();
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
   uint32_t mask = 0x000f000fu, magic = kMagic;
   asm volatile("" : "+r"(mask), "+r"(magic));
   bool ok = true;
-  int slot = 0, i = 0, lost = 0;
+  int slot = 0, i = 0;
   uint32_t phase = 0;
   for (int u0 = 0; u0 < units; u0 += panel_units) {
     const int u1 = min(units, u0 + panel_units);
@@ -287,12 +289,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
       for (int r = 0; r < kMine; ++r) scales[(warp * kMine + r) * Plan::kScaleLd + j] = v[r] | (z[r] & 15u) << 16;
     }
     __syncthreads();
-    for (; wk + i * WK < u1; ++i) {
-      const bool by_lanes = !tma_x(i) && !(mine <= ST && i == mine - 1);
-      if (!ok) {  // warps that share a ring still meet where the others of it may wait
-        if (WR > 1 && by_lanes) group_sync();
-        continue;
-      }
+    for (; ok && wk + i * WK < u1; ++i) {
       const int u = wk + i * WK;
       // Refills the slot of the unit before this one, which the group has had time to leave.
       if (issuer && i > 0 && i - 1 + ST < mine) {
@@ -302,13 +299,10 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
         if (ok) issue(i - 1 + ST, last);
       }
       ok = __all_sync(0xffffffffu, ok && mbar_wait(full_bar(slot), phase, abort_flag, kWaitLimitNs, kRoleMma, &g_device_error));
-      if (by_lanes) {
-        if (ok) fill_x(i, slot);
+      if (!ok) break;
+      if (by_lanes(i)) {
+        fill_x(i, slot);
         group_sync();
-      }
-      if (!ok) {
-        lost = i;
-        continue;
       }
       const uint32_t w = w_slot(slot) + w_at, x = x_slot(slot) + x_at;
       const uint32_t *unit_scales = scales + (wr * 16 * R + g) * Plan::kScaleLd + ((u * kUnit) >> p.group_log2) - first_group;
@@ -374,10 +368,15 @@ __global__ void __launch_bounds__(32 * kQ4Warps, 2)
         phase ^= 1u;
       }
     }
+    if constexpr (WR > 1) {  // after a wait that ran out: warps that share a ring still meet where the others may wait
+      if (!ok)
+        for (int e = max(i, u0 > wk ? (u0 - wk + WK - 1) / WK : 0); wk + e * WK < u1; ++e)
+          if (by_lanes(e)) group_sync();
+    }
   }
   // After a wait that ran out: what was asked for lands before shared memory goes away.
   if (!ok && issuer) {
-    for (int e = 0; e < ST && lost + e < mine; ++e) {
+    for (int e = 0; e < ST && i + e < mine; ++e) {
       mbar_wait(full_bar(slot), phase, nullptr, kWaitLimitNs, kRoleProducer, &g_device_error);
       if (++slot == ST) {
         slot = 0;
