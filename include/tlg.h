@@ -541,7 +541,9 @@ tlg_status tlg_act_backward_mx_workspace_size(int64_t rows, int64_t cols, tlg_ty
  * with B_g the matrix at B + g * stride_b elements, K x N (TLG_OP_N, ldb >= N) or N x K (TLG_OP_T,
  * ldb >= K), as tlg_gemm_op.  stride_b may be 0: every group has the same B.  type is the type of A and
  * B (TLG_TYPE_F16 or TLG_TYPE_BF16), out that of C: the same, or TLG_TYPE_F32.  Sums are fp32, rounded
- * once after the activation, whose accuracy is tlg_gemm_fused's.
+ * once after the activation, whose accuracy is tlg_gemm_fused's: at most 1024 terms (512 for an fp32 C) at a
+ * time by the tensor core, whose adder truncates, and those parts added with rounding to nearest, so that
+ * a long sum loses no more of its size than a short one.
  *
  * offsets: groups + 1 int32 values in device memory, read by the kernel (0 <= groups <= 1024).  They
  * should not decrease: values outside [0, rows] are held to it, and one that is less than an earlier one
@@ -561,7 +563,7 @@ tlg_status tlg_gemm_grouped(int64_t rows, int64_t N, int64_t K, int32_t groups, 
  * Its weight gradient: dB_g = A_g^T . dC_g (K x N) or, for TLG_OP_T, its transpose (N x K), in the
  * layout of B: lddb and stride_db (not 0 for more than one group; the matrices must not overlap) in
  * elements.  dC has A's type; out is that type or TLG_TYPE_F32.  A group without rows gets dB_g = 0, and
- * every dB_g is overwritten.  Sums run over a group's rows in order, in fp32, rounded once; what other
+ * every dB_g is overwritten.  Sums run over a group's rows in order, in fp32 as above, rounded once; what other
  * rows hold (NaN, infinities) does not matter.
  */
 tlg_status tlg_gemm_grouped_dw(int64_t rows, int64_t N, int64_t K, int32_t groups, const int32_t *offsets,

@@ -26,10 +26,13 @@
 //   warps 4-    epilogue: two (fp32: four) to a quarter of the lanes, taking its 32-column pieces in turn
 //   the last 8  plain-load builds only: loads for operands that TMA cannot describe
 //
-// The tensor core's adder truncates: over a long sum the accumulator falls short by about 2e-8 of its
-// size per MMA (1.2e-6 at K = 1000, 2e-5 at 16384), more than an fp32 result should lose.  Builds
-// with an fp32 output therefore sum at most kGroupedSpan k-blocks in TMEM, and the epilogue warps add
-// those partial sums, rounding to nearest, in registers.  For a 16-bit output it is far below the rounding.
+// The tensor core's adder truncates: a step of 16 k cuts every term, and the accumulator, two bits below the last
+// place of the largest, and then the sum.  Over a long sum that adds up, always towards zero: of random signs a sum of
+// 1000 terms loses 1.2e-6 of its size, of 16384 2e-5; of positive fp16 terms up to five times that, and there is no
+// limit to the length.  So no accumulator sums more than a span, 512 k for an fp32 output (5e-7 lost) and 1024 for a
+// 16-bit one (1e-6, half a unit being 2.4e-4 or more), and the epilogue warps add the spans, rounding to nearest, in
+// registers.  (One accumulator for all of a 16-bit sum: 16384 rows of 4096 x 4096, 8 groups, weight gradient bf16 420
+// us, 426 with spans; more spans cost more of TMEM's bandwidth, 431 with 512.)
 //
 // What bounds it: at full size operands from L2, 64 KB a pair and k-block at 9 to 10 TB/s (8192 rows, 8 groups of
 // 4096 x 4096, fp16: 212 us, 1.29 PFLOP/s back to back in a graph, the tensor pipe at 92 % of active cycles;
@@ -47,9 +50,11 @@ constexpr int kGroupedMax = 1024;  // groups
 constexpr int kGroupedEpiWarp = 4;
 constexpr int kGroupedLoaders = 8;  // warps of the plain-load builds
 constexpr int kGroupedListed = 64;  // tiles of a unit worked out in advance
-constexpr int kGroupedSpan = 8;    // k-blocks summed in TMEM for an fp32 output
+template <int OUT>
+constexpr int kGroupedSpan = OUT == kTypeF32 ? 8 : 16;  // k-blocks summed in TMEM
 
-// Warps by the type of the output: a thread has room for the fp32 sums of 64 columns, not of 128.
+// Epilogue warps: a thread of eight holds the sums of 128 columns (168 registers, no spills); fp32 values, which take
+// twice as long to store, are left to sixteen.
 template <int OUT, int BN, bool LSU>
 struct GroupedRoles {
   static constexpr int kEpiWarps = OUT == kTypeF32 && BN > 64 ? 16 : 8;
@@ -179,17 +184,17 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// As tmem_load_32cols, for 16 columns.
-__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+// As tmem_load_32cols, 16 columns of fp32 values.
+__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, float (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32"
       " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
                :
                : "memory");
 }
@@ -280,7 +285,6 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
                    const __grid_constant__ CUtensorMap tmX128, const GroupedParams p) {
   using Plan = GroupedPlan<CG, BN, STAGES>;
   using Roles = GroupedRoles<OUT, BN, LSU>;
-  constexpr bool kSpans = OUT == kTypeF32;
   constexpr bool kDw = KIND == kGroupedDw;
   constexpr bool kWmn = KIND != kGroupedT, kXmn = kDw;  // MN-major operands
   static_assert(!LSU || CG == 1, "the plain-load path is built for one-CTA tiles");
@@ -318,7 +322,9 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
   // k-blocks of this CTA
   auto kb_begin = [&](int num_kb) { return KSPLIT ? num_kb * slice / ks : 0; };
   auto kb_end = [&](int num_kb) { return KSPLIT ? num_kb * (slice + 1) / ks : num_kb; };
-  float part[KSPLIT ? 32 : 1];  // partial sums of an epilogue warp's lane
+  constexpr int kSides = Roles::kEpiWarps / 4;             // epilogue warps to a quarter of the lanes
+  constexpr int kMine = (BN / 32 + kSides - 1) / kSides;  // 32-column pieces of one
+  float sum[kMine][32];                                    // a lane's sums of them
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -596,51 +602,42 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
       const GroupedTile w = tile_at(t);
       const int num_kb = ceil_div(w.k, kBK);
       const uint32_t idesc = idesc0 | (static_cast<uint32_t>(w.n >> 3) << 17);
-      int first = kb_begin(num_kb);  // k-block of this accumulator
-      auto take = [&]() {
+      int kb = kb_begin(num_kb);
+      do {  // a span
         ok = __all_sync(0xffffffffu, mbar_wait(tempty_bar(j & 1u), ((j >> 1) & 1u) ^ 1u, abort_flag, p.limit_ns,
                                                kRoleMma, &g_device_error));
+        if (!ok) break;
         tc_fence_after_sync();
-      };
-      auto hand_over = [&]() {
+        const uint32_t d_tmem = tmem_base + (j & 1u) * BN;
+        const int first = kb, end = min(kb + kGroupedSpan<OUT>, kb_end(num_kb));
+        for (; kb < end; ++kb) {
+          const bool tail = kDw && (kb + 1) * kBK > w.k;
+          // the tail's last writes come from the pair's other CTA, so they are acquired at cluster scope
+          const bool got = CG == 2 && tail
+                               ? mbar_wait_cluster(full_bar(stage), phase, abort_flag, p.limit_ns, kRoleMma, &g_device_error)
+                               : mbar_wait_spin(full_bar(stage), phase, abort_flag, p.limit_ns, kRoleMma, &g_device_error, 4096);
+          ok = __all_sync(0xffffffffu, got);
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (elect_one()) {
+            const uint64_t wd = smem_desc_sw128(w_slot(stage), kWmn ? 8192 : 16, 1024);
+            const uint64_t xd = smem_desc_sw128(x_slot(stage), kXmn ? 8192 : 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              mma_f16_ss<CG>(d_tmem, wd + kk * kWStep, xd + kk * kXStep, idesc, (kb > first || kk > 0) ? 1u : 0u);
+            mma_commit<CG>(empty_bar(stage));
+          }
+          __syncwarp();
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
         if (elect_one()) mma_commit<CG>(tfull_bar(j & 1u));
         __syncwarp();
         ++j;
-      };
-      take();
-      if (!ok) break;
-      for (int kb = first; kb < kb_end(num_kb); ++kb) {
-        if (kSpans && kb - first == kGroupedSpan) {
-          hand_over();
-          first = kb;
-          take();
-          if (!ok) break;
-        }
-        const uint32_t d_tmem = tmem_base + (j & 1u) * BN;
-        const bool tail = kDw && (kb + 1) * kBK > w.k;
-        // the tail's last writes come from the pair's other CTA, so they are acquired at cluster scope
-        const bool got = CG == 2 && tail
-                             ? mbar_wait_cluster(full_bar(stage), phase, abort_flag, p.limit_ns, kRoleMma, &g_device_error)
-                             : mbar_wait_spin(full_bar(stage), phase, abort_flag, p.limit_ns, kRoleMma, &g_device_error, 4096);
-        ok = __all_sync(0xffffffffu, got);
-        if (!ok) break;
-        tc_fence_after_sync();
-        if (elect_one()) {
-          const uint64_t wd = smem_desc_sw128(w_slot(stage), kWmn ? 8192 : 16, 1024);
-          const uint64_t xd = smem_desc_sw128(x_slot(stage), kXmn ? 8192 : 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            mma_f16_ss<CG>(d_tmem, wd + kk * kWStep, xd + kk * kXStep, idesc, (kb > first || kk > 0) ? 1u : 0u);
-          mma_commit<CG>(empty_bar(stage));
-        }
-        __syncwarp();
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      if (!ok) break;
-      hand_over();
+      } while (kb < kb_end(num_kb));
     }
     if (!ok) {
       if (elect_one()) mma_commit_local<CG>(drain_bar);
@@ -683,8 +680,6 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
     // ---------------------------------------------------------------- epilogue (every CTA)
     const int quarter = warp & 3;
     const int side = (warp - kGroupedEpiWarp) >> 2;
-    constexpr int kSides = Roles::kEpiWarps / 4;
-    constexpr int kMine = (BN / 32 + kSides - 1) / kSides;  // pieces of a warp
     const uint32_t release_bar0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
     uint32_t j = 0;
     bool ok = true;
@@ -739,81 +734,47 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
           }
         }
       };
-      if constexpr (kSpans) {
-        float sum[kMine][32];
+      int kb = kb_begin(num_kb);
 #pragma unroll
-        for (int m = 0; m < kMine; ++m)
+      for (int m = 0; m < kMine; ++m)
 #pragma unroll
-          for (int c = 0; c < 32; ++c) sum[m][c] = 0.0f;  // the empty sum
-        int kb = kb_begin(num_kb);
-        do {
-          wait_full(limit);
-          if (!ok) break;
-#pragma unroll
-          for (int m = 0; m < kMine; ++m) {
-            const int i = side + m * kSides;
-            if (i < pieces && num_kb > 0) {
-#pragma unroll
-              for (int h = 0; h < 32; h += 16) {
-                uint32_t r[16];
-                __syncwarp();
-                tmem_load_16cols(piece_at(i) + h, r);
-#pragma unroll
-                for (int c = 0; c < 16; c += 2)
-                  f2_add_to(sum[m][h + c], sum[m][h + c + 1], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
-              }
-            }
-          }
-          release();
-          ++j;
-          kb += kGroupedSpan;
-        } while (kb < kb_end(num_kb));
-        if (!ok) break;
-        if constexpr (KSPLIT) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) part[c] = sum[0][c];
-          continue;
-        }
-#pragma unroll
-        for (int m = 0; m < kMine; ++m) {
-          if (side + m * kSides < pieces) {
-            if constexpr (!kDw) activate_lane<OUT, 32>(p.act, sum[m]);
-            store_piece(side + m * kSides, sum[m]);
-          }
-        }
-      } else if constexpr (KSPLIT) {
+        for (int c = 0; c < 32; ++c) sum[m][c] = 0.0f;  // the empty sum
+      do {
         wait_full(limit);
         if (!ok) break;
-        uint32_t r[32];
-        __syncwarp();
-        tmem_load_32cols(piece_at(side), r);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) part[c] = __uint_as_float(r[c]);
-      } else {
-        wait_full(limit);
-        if (!ok) break;
-        // All pieces are read, and rounded, before any is stored: the MMAs get the accumulator back sooner.
-        uint32_t packed[kMine][16];
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
           const int i = side + m * kSides;
-          if (i < pieces) {
-            uint32_t r[32];
-            __syncwarp();
-            tmem_load_32cols(piece_at(i), r);
-            float v[32];
+          if (i < pieces && num_kb > 0) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = w.k > 0 ? __uint_as_float(r[c]) : 0.0f;  // the empty sum
-            if constexpr (!kDw) activate_lane<OUT, 32>(p.act, v);
+            for (int h = 0; h < 32; h += 16) {
+              float r[16];
+              __syncwarp();
+              tmem_load_16cols(piece_at(i) + h, r);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) packed[m][c] = pack2<OUT>(v[2 * c], v[2 * c + 1]);
+              for (int c = 0; c < 16; c += 2) f2_add_to(sum[m][h + c], sum[m][h + c + 1], r[c], r[c + 1]);
+            }
           }
         }
         release();
-#pragma unroll
-        for (int m = 0; m < kMine; ++m)
-          if (side + m * kSides < pieces) store_piece(side + m * kSides, packed[m]);
         ++j;
+        kb += kGroupedSpan<OUT>;
+      } while (kb < kb_end(num_kb));
+      if (!ok) break;
+      if constexpr (KSPLIT) break;  // the sums are exchanged below
+#pragma unroll
+      for (int m = 0; m < kMine; ++m) {
+        const int i = side + m * kSides;
+        if (i >= pieces) break;
+        if constexpr (!kDw) activate_lane<OUT, 32>(p.act, sum[m]);
+        if constexpr (OUT == kTypeF32) {
+          store_piece(i, sum[m]);
+        } else {
+          uint32_t packed[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) packed[c] = pack2<OUT>(sum[m][2 * c], sum[m][2 * c + 1]);
+          store_piece(i, packed);
+        }
       }
     }
   }
@@ -831,7 +792,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
                           static_cast<uint32_t>(((slice * BN + (epi >> 2) * 32) * per + row % per) * 4);
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + static_cast<uint32_t>(c * per * 4)), "f"(part[c]) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + static_cast<uint32_t>(c * per * 4)), "f"(sum[0][c]) : "memory");
     }
     __syncwarp();
     cluster_sync_all();  // all partial sums are in place
