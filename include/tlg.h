@@ -580,7 +580,9 @@ tlg_status tlg_gemm_grouped_dw(int64_t rows, int64_t N, int64_t K, int32_t group
  * that type, rstd rows fp32 values.  R may be NULL (H = X); H and rstd may be NULL where they are not
  * needed.  H and Y may each be X or R itself (same base and row stride).  Computed in fp32 from the
  * unrounded H and rounded once; the sum of a row does not depend on timing.  eps >= 0 and finite.
- * cols <= 16384 (TLG_ERR_UNSUPPORTED beyond).
+ * cols <= 16384 (TLG_ERR_UNSUPPORTED beyond).  A row that holds a NaN has rstd and Y NaN.  Of a row whose
+ * sum of squares is infinite in fp32 (it holds an infinity, or squares that add up to one) rstd is 0, and Y is
+ * 0 but for NaN where H is infinite.
  */
 tlg_status tlg_rmsnorm_forward(int64_t rows, int64_t cols, tlg_type type,
                                const void *X, int64_t ldx, const void *R, int64_t ldr,
@@ -589,8 +591,8 @@ tlg_status tlg_rmsnorm_forward(int64_t rows, int64_t cols, tlg_type type,
 
 /*
  * The same with Y written as an MX matrix, quantised from the fp32 values as tlg_mx_quantize does:
- * TLG_MX_E2M1 for the A operand of tlg_gemm_mxfp4, TLG_MX_E4M3 in 8 bits.  A row that holds a NaN or an
- * infinity reads back as NaN.
+ * TLG_MX_E2M1 for the A operand of tlg_gemm_mxfp4, TLG_MX_E4M3 in 8 bits.  So a row that holds a
+ * NaN reads back as NaN, and of a row with an infinity its blocks of 32 with one do, the others as 0.
  */
 tlg_status tlg_rmsnorm_forward_mx(int64_t rows, int64_t cols, tlg_type type,
                                   const void *X, int64_t ldx, const void *R, int64_t ldr,

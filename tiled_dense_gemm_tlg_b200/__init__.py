@@ -597,7 +597,8 @@ def tlg_rmsnorm_forward_mx(X: torch.Tensor, weight: torch.Tensor, residual: torc
                            Q: torch.Tensor | None = None, S: torch.Tensor | None = None,
                            rstd: torch.Tensor | None = None, stream=None):
     """(Q, S, H, rstd): ``tlg_rmsnorm_forward`` with Y as an MX matrix, "e4m3" (8 bits) or "e2m1" (4 bits, the
-    operand of ``tlg_gemm_mxfp4``)."""
+    operand of ``tlg_gemm_mxfp4``). A row with a NaN reads back as NaN; of a row with an infinity, whose rstd is 0,
+    the blocks of 32 that hold one do, the others as 0."""
     return _result(_binding.rmsnorm_forward(X, weight, residual, eps, H, None, _format(format), Q, S, rstd,
                                             _handle(stream)), "tlg_rmsnorm_forward_mx")
 
