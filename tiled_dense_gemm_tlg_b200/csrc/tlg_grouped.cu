@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 #include <type_traits>
@@ -17,6 +18,8 @@ namespace tlg {
 namespace {
 
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s per pipeline wait
+// What the next launches are given; tests make waits run out with less.
+std::atomic<uint64_t> wait_limit_ns{kWaitLimitNs}, wait_limit_kb_ns{kWaitPerKBlockNs};
 constexpr int64_t kMostTiles = int64_t(1) << 30;
 constexpr int64_t kMaxStackStride = int64_t(1) << 38;
 
@@ -139,6 +142,13 @@ using namespace tlg;
 
 extern "C" {
 
+// Not part of the interface, for tests: the limit of the pipeline waits of the grouped products launched from here on,
+// and what a k-block adds to it.  A limit of 0 restores both.
+void tlg_internal_grouped_wait_limit(uint64_t limit_ns, uint64_t per_k_block_ns) {
+  wait_limit_ns = limit_ns != 0 ? limit_ns : kWaitLimitNs;
+  wait_limit_kb_ns = limit_ns != 0 ? per_k_block_ns : kWaitPerKBlockNs;
+}
+
 tlg_status tlg_gemm_grouped(int64_t rows, int64_t N, int64_t K, int32_t groups, const int32_t *offsets, tlg_type type,
                             const void *A, int64_t lda, tlg_op op_b, const void *B, int64_t ldb, int64_t stride_b,
                             tlg_activation activation, void *C, int64_t ldc, tlg_type out, void *stream) {
@@ -177,7 +187,8 @@ tlg_status tlg_gemm_grouped(int64_t rows, int64_t N, int64_t K, int32_t groups, 
   p.raster = 8;
   p.act = activation;
   p.shared_w = groups == 1 || stride_b == 0;
-  p.limit_ns = kWaitLimitNs;
+  p.limit_ns = wait_limit_ns;
+  p.limit_kb_ns = wait_limit_kb_ns;
   p.W = static_cast<const uint16_t *>(B);
   p.X = static_cast<const uint16_t *>(A);
   p.ldw = ldb;
@@ -267,7 +278,8 @@ tlg_status tlg_gemm_grouped_dw(int64_t rows, int64_t N, int64_t K, int32_t group
   p.ldc = lddb;
   p.stride_c = stride_db;
   p.raster = 8;
-  p.limit_ns = kWaitLimitNs;
+  p.limit_ns = wait_limit_ns;
+  p.limit_kb_ns = wait_limit_kb_ns;
   p.W = static_cast<const uint16_t *>(W);
   p.X = static_cast<const uint16_t *>(X);
   p.ldw = ldw;

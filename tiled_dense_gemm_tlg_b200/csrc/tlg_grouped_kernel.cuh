@@ -74,7 +74,8 @@ struct GroupedParams {
   int raster;    // lane tiles walked together
   int act;
   int shared_w;  // every group has the same B
-  uint64_t limit_ns;
+  uint64_t limit_ns;     // of a wait, and what a k-block of the tiles that it spans adds
+  uint64_t limit_kb_ns;
   // plain loads: the M and N operands as stored
   const uint16_t *W, *X;
   int64_t ldw, ldx, stride_w;
@@ -648,17 +649,19 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
     // ---------------------------------------------------------------- the groups' last k-blocks (every CTA)
     int stage = 0;
     uint32_t parity = 0;  // of each slot's next tail
+    uint64_t skipped = 0;  // k-blocks, and tiles, since the last tail: whole groups pass without a wait
     bool ok = true;
     for (int t = 0; t < mine; ++t) {
       const GroupedTile w = tile_at(t);
       const int num_kb = ceil_div(w.k, kBK), valid = w.k % kBK;
       const int last = (stage + num_kb + STAGES - 1) % STAGES;
       stage = (stage + num_kb) % STAGES;
+      skipped += num_kb + 1;
       if (valid == 0) continue;
-      const uint64_t limit = p.limit_ns + static_cast<uint64_t>(num_kb) * kWaitPerKBlockNs;
-      ok = __all_sync(0xffffffffu, mbar_wait(tail_bar(last), (parity >> last) & 1u, abort_flag, limit,
-                                                   kRoleProducer, &g_device_error));
+      ok = __all_sync(0xffffffffu, mbar_wait(tail_bar(last), (parity >> last) & 1u, abort_flag,
+                                             p.limit_ns + skipped * p.limit_kb_ns, kRoleProducer, &g_device_error));
       if (!ok) break;
+      skipped = 0;
       parity ^= 1u << last;
       // rows [valid, 64) of each 64-element block are consecutive bytes
       const int x_blocks = w.n / CG / 64;
@@ -683,9 +686,10 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
     const uint32_t release_bar0 = (CG == 2) ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
     uint32_t j = 0;
     bool ok = true;
-    auto wait_full = [&](uint64_t limit) {
+    auto wait_full = [&](int num_kb) {
       ok = ok && *abort_flag == 0u;
-      if (ok && !mbar_wait(tfull_bar(j & 1u), (j >> 1) & 1u, abort_flag, limit, kRoleEpilogue, &g_device_error))
+      if (ok && !mbar_wait(tfull_bar(j & 1u), (j >> 1) & 1u, abort_flag,
+                           p.limit_ns + static_cast<uint64_t>(num_kb) * p.limit_kb_ns, kRoleEpilogue, &g_device_error))
         ok = false;
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after_sync();
@@ -706,7 +710,6 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
     for (int t = 0; t < mine && ok; ++t) {
       const GroupedTile w = tile_at(t);
       const int num_kb = ceil_div(w.k, kBK);
-      const uint64_t limit = p.limit_ns + static_cast<uint64_t>(num_kb) * kWaitPerKBlockNs;
       const unsigned at = static_cast<unsigned>(w.lane0 + static_cast<int>(rank) * kBM + quarter * 32 + lane);  // column of C or dB
       const int pieces = ceil_div(w.cols, 32);
       // Piece i, 32 fp32 values or pairs of 16-bit ones.
@@ -740,7 +743,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
 #pragma unroll
         for (int c = 0; c < 32; ++c) sum[m][c] = 0.0f;  // the empty sum
       do {
-        wait_full(limit);
+        wait_full(num_kb);
         if (!ok) break;
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
