@@ -200,9 +200,12 @@ tlg_status tlg_gemm_grouped(int64_t rows, int64_t N, int64_t K, int32_t groups, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   GroupedMaps m;
   const int64_t tlda = tma_ld(rows, K, lda), tldb = tma_ld(b_rows, b_cols, ldb);
-  // Tiles of 128 lanes by up to 64 rows, two CTAs to an SM, for few rows to a group; but 256 x 256 pairs from
-  // 16 rows on average on, where they are 5 % slower (64 rows over 8 groups of 4096 x 4096: 50 us against 47.6)
-  // and do not mind a group that has most of the rows.  Where the small tiles are few, clusters share their K.
+  // Tiles of 128 lanes by up to 64 rows, two CTAs to an SM, up to 16 rows a group on average, then pairs with 256 x 256.
+  // 8 groups of 4096 x 4096, bf16, small tiles against pairs: 16 rows a group 46.4 us against 49.3, 20 rows 46.7 against
+  // 49.6.  As long as no group takes a second small tile the pairs are 5 % slower; where one does, the small tiles read
+  // its weights again: 32 rows a group on average, most of them in one group, 57.0 us against 52.9, 48 rows spread
+  // unevenly 61.7 against 50.9.  The sizes are on the device, so the average has to decide, and 16 is on the side that
+  // loses little.  Where the small tiles are few, clusters share their K.
   const bool few = most(64, 128) * 2 <= 2 * int64_t(info.sm_count) && K >= 2 * 4 * kBK;
   const bool wide = !few && rows > int64_t(groups) * 16;
   const bool tma = K > 0 && tma_ok(A, tlda) && tma_ok(B, tldb) && p.stride_w % 8 == 0;
