@@ -19,9 +19,13 @@
 // elements i and i + 4 are pairs of one mma operand register: the k order of the operands is a permutation,
 // the same for X, whose pairs are put together by byte permutes.
 //
-// What bounds it: issue slots, about 50 instructions for 512 weights (16 rows by 32 k), 22 of them the conversion, at
-// 1.8 to 2 a cycle.  bf16, groups of 128, back to back in a graph: one token 4096 x 4096 4.6 us, 16384 x 4096 11.4 us
-// (2.9 TB/s of weights), eight tokens 12.1, sixteen 16.0.
+// What bounds it: latency with few warps.  127 registers a thread and the rings leave 14 warps to an SM; they issue 1.8 of
+// 4 instructions a cycle (16 tokens, 16384 x 4096), tensor pipe, shared memory and DRAM are at a fifth to a third.  Of
+// the 7.7 cycles from one instruction of a warp to its next 1.6 go to memory (units that have not landed, the panel's
+// scales), 1.4 to the latency of the instruction before, 1.0 to a busy pipe, 0.6 to barriers; the rest is issue.  And 256
+// tiles on 296 places leave some SMs with one where others have two.  About 50 instructions stand for 512 weights (16
+// rows by 32 k), 22 of them the conversion.  bf16, groups of 128, back to back in a graph: one token 4096 x 4096 4.6 us,
+// 16384 x 4096 11.4 us (2.9 TB/s of weights), eight tokens 12.1, sixteen 16.0.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
