@@ -607,7 +607,8 @@ tlg_status tlg_rmsnorm_forward_mx(int64_t rows, int64_t cols, tlg_type type,
  *
  * dX is the gradient of X and of R alike.  dH, what arrives on the residual stream behind the norm, may
  * be NULL, and so may dweight (cols fp32 values).  dX may be dY or dH itself (same base and row stride).
- * Sums are fp32, in an order that does not depend on timing.  rows of 0: dweight = 0.  cols <= 16384.
+ * Sums are fp32, in an order that does not depend on timing; dweight's parts, sums of some rows each, are
+ * added in 64 bits.  rows of 0: dweight = 0.  cols <= 16384.
  * workspace: tlg_rmsnorm_backward_workspace_size() bytes of device memory, 256-byte aligned, needed when
  * dweight is not NULL (TLG_ERR_INVALID_ARG when too small; the size may be 0).  Its contents on entry do
  * not matter; calls that overlap in time must not share one.

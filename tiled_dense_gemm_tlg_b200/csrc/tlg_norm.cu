@@ -313,7 +313,8 @@ __device__ __forceinline__ void finish_dx(float (&g)[E], const float (&xh)[E], f
 // shared memory: a ring of SLOTS rows to a warp, copied asynchronously, each lane's 16 bytes its own.  WORDS:
 // rows that are aligned to 4 bytes only are copied by words, neighbouring lanes on neighbouring ones, which
 // rearranges them on the way.  The sums for dw stay in registers, row after row in order; CTAs leave their
-// sums in `part`, which column_sum_kernel adds in order, so the result does not depend on timing.
+// sums in `part`, which column_sum_kernel adds in order, so the result does not depend on timing, and in 64 bits, which
+// costs nothing: 1000 x 3001 fp32 13.9 us with both, dw 5e-8 of its size off, 1.3e-7 with fp32.
 template <int T, int U, int WARPS>
 struct NormRing {
   static constexpr int kSlots = U == 8 ? 1 : U == 4 || WARPS * U > 24 ? 2 : 3;
@@ -805,8 +806,8 @@ tlg_status tlg_rmsnorm_backward(int64_t rows, int64_t cols, tlg_type type, const
   });
   if (st != TLG_OK || part == dweight) return st;
   const dim3 sum_grid(static_cast<unsigned>((cols + 31) / 32));
-  return ctas > 128 ? launch(column_sum_kernel<32>, sum_grid, 1024, s, 0, part, static_cast<int>(ctas), cols, dweight)
-                    : launch(column_sum_kernel<8>, sum_grid, 256, s, 0, part, static_cast<int>(ctas), cols, dweight);
+  return ctas > 128 ? launch(column_sum_kernel<32, double>, sum_grid, 1024, s, 0, part, static_cast<int>(ctas), cols, dweight)
+                    : launch(column_sum_kernel<8, double>, sum_grid, 256, s, 0, part, static_cast<int>(ctas), cols, dweight);
 }
 
 }  // extern "C"

@@ -217,15 +217,15 @@ __device__ __forceinline__ int64_t scale_row(uint32_t row, int64_t tile_row_byte
 // columns, and their sums are added in order.  W = 32 where a narrow matrix has hundreds of
 // row splits and a warp's chain of loads takes the time (16384 x 1000 fp16, 592 splits, the whole
 // backward call: 24.7 us, 30.5 with 8), else 8, which find room beside the kernel before sooner
-// (2000 x 5000: 18.3 us, 20.3 with 32).
-template <int W>
+// (2000 x 5000: 18.3 us, 20.3 with 32).  T: the type they are added in.
+template <int W, typename T = float>
 __global__ void __launch_bounds__(32 * W) column_sum_kernel(const float *part, int parts, int64_t cols, float *dbias) {
-  __shared__ float sums[W][32];
+  __shared__ T sums[W][32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  float s = 0.0f;
+  T s = 0;
   if (c < cols) {
 #pragma unroll 8
     for (int i = warp; i < parts; i += W) s += part[i * cols + c];
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(32 * W) column_sum_kernel(const float *part, i
   if (warp == 0 && c < cols) {
 #pragma unroll
     for (int i = 1; i < W; ++i) s += sums[i][lane];
-    dbias[c] = s;
+    dbias[c] = static_cast<float>(s);
   }
 }
 
