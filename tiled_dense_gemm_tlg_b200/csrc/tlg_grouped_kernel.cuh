@@ -29,10 +29,11 @@
 // The tensor core's adder truncates: a step of 16 k cuts every term, and the accumulator, two bits below the last
 // place of the largest, and then the sum.  Over a long sum that adds up, always towards zero: of random signs a sum of
 // 1000 terms loses 1.2e-6 of its size, of 16384 2e-5; of positive fp16 terms up to five times that, and there is no
-// limit to the length.  So no accumulator sums more than a span, 512 k for an fp32 output (5e-7 lost) and 1024 for a
-// 16-bit one (1e-6, half a unit being 2.4e-4 or more), and the epilogue warps add the spans, rounding to nearest, in
-// registers.  (One accumulator for all of a 16-bit sum: 16384 rows of 4096 x 4096, 8 groups, weight gradient bf16 420
-// us, 426 with spans; more spans cost more of TMEM's bandwidth, 431 with 512.)
+// limit to the length.  So no accumulator sums more than a span, 512 k for an fp32 output or in small tiles (5e-7 lost)
+// and 1024 for a 16-bit output of large ones (1e-6, half a unit being 2.4e-4 or more), and the epilogue warps add the
+// spans, rounding to nearest, in registers.  (One accumulator for all of a 16-bit sum: 16384 rows of 4096 x 4096, 8
+// groups, weight gradient bf16 420 us, 426 with spans; more spans cost more of TMEM's bandwidth, 431 with 512.  Small
+// tiles wait for HBM: 16 rows over 32 groups of 2048 x 1024 9.3 us with one accumulator, 9.5 with 1024, 9.7 with 512.)
 //
 // What bounds it: at full size operands from L2, 64 KB a pair and k-block at 9 to 10 TB/s (8192 rows, 8 groups of
 // 4096 x 4096, fp16: 212 us, 1.29 PFLOP/s back to back in a graph, the tensor pipe at 92 % of active cycles;
@@ -50,8 +51,8 @@ constexpr int kGroupedMax = 1024;  // groups
 constexpr int kGroupedEpiWarp = 4;
 constexpr int kGroupedLoaders = 8;  // warps of the plain-load builds
 constexpr int kGroupedListed = 64;  // tiles of a unit worked out in advance
-template <int OUT>
-constexpr int kGroupedSpan = OUT == kTypeF32 ? 8 : 16;  // k-blocks summed in TMEM
+template <int OUT, int BN>
+constexpr int kGroupedSpan = OUT == kTypeF32 || BN == 64 ? 8 : 16;  // k-blocks summed in TMEM
 
 // Epilogue warps: a thread of eight holds the sums of 128 columns (168 registers, no spills); fp32 values, which take
 // twice as long to store, are left to sixteen.
@@ -610,7 +611,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + (j & 1u) * BN;
-        const int first = kb, end = min(kb + kGroupedSpan<OUT>, kb_end(num_kb));
+        const int first = kb, end = min(kb + kGroupedSpan<OUT, BN>, kb_end(num_kb));
         for (; kb < end; ++kb) {
           const bool tail = kDw && (kb + 1) * kBK > w.k;
           // the tail's last writes come from the pair's other CTA, so they are acquired at cluster scope
@@ -761,7 +762,7 @@ __global__ void __launch_bounds__(GroupedRoles<OUT, BN, LSU>::kThreads, GroupedP
         }
         release();
         ++j;
-        kb += kGroupedSpan<OUT>;
+        kb += kGroupedSpan<OUT, BN>;
       } while (kb < kb_end(num_kb));
       if (!ok) break;
       if constexpr (KSPLIT) break;  // the sums are exchanged below
