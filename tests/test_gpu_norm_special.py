@@ -20,7 +20,7 @@ def tlg():
 
 
 def rows_of(typ):
-    """Finite rows, 0 and 5, around one with a NaN, one with infinities, and two that are so by their sum alone."""
+    """Finite rows, 0 and 5, around two with a NaN, one with infinities, and one that is so by its sum alone."""
     X = torch.randn((6, COLS), generator=torch.Generator().manual_seed(1)).to(TYPES[typ])
     R = torch.randn((6, COLS), generator=torch.Generator().manual_seed(2)).to(TYPES[typ])
     X[1, 70] = float("nan")
