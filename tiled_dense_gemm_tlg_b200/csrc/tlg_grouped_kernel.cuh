@@ -37,7 +37,7 @@
 //
 // What bounds it: at full size operands from L2, 64 KB a pair and k-block at 9 to 10 TB/s (8192 rows, 8 groups of
 // 4096 x 4096, fp16: 210 us, 1.31 PFLOP/s back to back in a graph, the tensor pipe at 92 % of active cycles;
-// under the power cap 247 us); with few rows a group HBM (64 rows over 64 groups of 2048 x 2048: 80 us,
+// under the power cap 247 to 253 us); with few rows a group HBM (64 rows over 64 groups of 2048 x 2048: 80 us,
 // 6.7 TB/s).  Stores straight from the registers: a 256 x 256 tile takes 2.8 us of epilogue, beside the next
 // tile's main loop.
 #pragma once
